@@ -234,8 +234,8 @@ def run(s):
 
 def _own_conv(s, c):
     from speculative_decoding_mamba2_gb300 import Dims, ssm_prompt_conv
-    ssm_prompt_conv(Dims(n_heads=c["H"], ring_cap=R), s["params"], 0, s["cu"], s["xBC"], s["ring"], s["head"], s["out"],
-                    slots=s["slots"])
+    ssm_prompt_conv(Dims(n_heads=c["H"], ring_cap=R), s["params"], 0, s["cu"], s["max_len"], s["xBC"], s["ring"], s["head"],
+                    s["out"], slots=s["slots"])
     return dict(out=s["out"], ring=_window(s), head=s["head"])
 
 
