@@ -24,3 +24,9 @@ from .block_oracle import (  # noqa: F401
     gated_rmsnorm,
     block_verify,
 )
+from .prompt_oracle import (  # noqa: F401
+    prompt_conv,
+    prompt_scan,
+    tree_attention,
+    kv_commit,
+)

@@ -1,4 +1,4 @@
-"""ctypes binding of libssmtree (include/ssm_tree.h), same names as the C ABI.
+"""ctypes binding of libssmtree (include/*.h), same names as the C ABI.
 
 Argument marshalling only: each wrapper checks that the torch tensors it is
 given have the dtype, device, contiguity and element count the C signature
@@ -29,6 +29,7 @@ SSM_STATUS_PATH_RANGE = 2
 SSM_STATUS_K_RANGE = 4
 SSM_STATUS_WALK_TRUNCATED = 8
 SSM_STATUS_TIMEOUT = 16
+SSM_STATUS_SEQ_RANGE = 32
 SSM_MAX_NODES = 64
 SSM_MAX_DEPTH = 15
 SSM_MAX_PATH = 256
@@ -484,3 +485,178 @@ def ssm_gated_rmsnorm(y, z, w, eps: float, out, stream=None):
         raise ValueError("z, out: M rows")
     _check(lib().ssm_gated_rmsnorm(M, C, py, ldy, pz, ldz, _dev(w, "w", torch.float32, C), float(eps), po, ldo,
                                    _stream(stream, y)))
+
+
+# ---------------------------------------------------------------------------
+# prompts and single tokens (include/ssm_prompt.h)
+# ---------------------------------------------------------------------------
+_L = ctypes.c_int64
+_SIGS.update({
+    "ssm_prompt_conv": (ctypes.c_int, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _L, _P, _P, _P, _L, _P, _P]),
+    "ssm_prompt_scan": (ctypes.c_int, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _L, _P, _L, _P, _L, _P, _L, _P, _P,
+                                       _P, _L, _P, ctypes.c_size_t, _P, _P]),
+    "ssm_prompt_scan_workspace_size": (ctypes.c_size_t, [_P, _I, _I, _I, _I]),
+    "ssm_scan_step": (ctypes.c_int, [_P, _P, _I, _I, _I, _I, _P, _P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _P, _L, _P,
+                                     _P]),
+    "ssm_tree_attention": (ctypes.c_int, [_I, _I, _I, _I, _I, _P, _P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _P, _I, _P,
+                                          _I, ctypes.c_float, _P, _L, _P, ctypes.c_size_t, _P, _P]),
+    "ssm_tree_attention_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
+    "ssm_kv_commit": (ctypes.c_int, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _P]),
+})
+
+
+def _slots_of(cache, name: str, per_slot: int) -> int:
+    """Slots of a [n_slots][L]... cache tensor with per_slot elements each."""
+    if not isinstance(cache, torch.Tensor) or cache.numel() % per_slot:
+        raise ValueError(f"{name}: not a whole number of slots of {per_slot} elements")
+    return cache.numel() // per_slot
+
+
+def _tok_rows(t, name: str, cols: int | None = None):
+    """_rows of a bf16 tensor that may have no rows (whose strides then say nothing)."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.size(0) == 0 and t.dtype == torch.bfloat16 \
+            and cols in (None, t.size(1)):
+        return None, 0, (t.size(1) + 7) // 8 * 8
+    return _rows(t, name, torch.bfloat16, cols)
+
+
+def _opt_slots(slots, n_seq: int):
+    return None if slots is None else _dev(slots, "slots", torch.int32, n_seq)
+
+
+def ssm_prompt_conv(dims: Dims, params: dict, layer: int, cu_seqlens, max_len: int, xBC, ring, ring_head, out,
+                    slots=None, status=None, stream=None):
+    """Causal conv + SiLU of ragged prompts (xBC, out: bf16 [n_tok, conv_dim], any row stride); the ring's rows
+    before each prompt are read, its last three rows and the head written."""
+    d = dims
+    px, T, ldx = _tok_rows(xBC, "xBC", d.conv_dim)
+    po, To, ldo = _tok_rows(out, "out", d.conv_dim)
+    if To != T:
+        raise ValueError("out: as many rows as xBC")
+    n_seq = cu_seqlens.numel() - 1
+    n_slots = _slots_of(ring, "ring", d.n_layers * d.ring_cap * d.conv_dim)
+    cd = d.c()
+    cp = ssm_params(_ptr(params["conv_w"], "conv_w", torch.float32, d.n_layers * d.conv_dim * d.conv_width),
+                    _ptr(params["conv_b"], "conv_b", torch.float32, d.n_layers * d.conv_dim), None, None, None)
+    _check(lib().ssm_prompt_conv(
+        ctypes.byref(cd), ctypes.byref(cp), int(layer), n_seq, n_slots, T, int(max_len),
+        _dev(cu_seqlens, "cu_seqlens", torch.int32, n_seq + 1), _opt_slots(slots, n_seq), px, ldx,
+        _dev(ring, "ring", torch.bfloat16), _dev(ring_head, "ring_head", torch.int32, n_slots * d.n_layers), po, ldo,
+        _opt_status(status), _stream(stream, xBC)))
+
+
+def _scan_params(prm: dict, d: Dims) -> ssm_params:
+    lh = d.n_layers * d.n_heads
+    return ssm_params(None, None, _ptr(prm["dt_bias"], "dt_bias", torch.float32, lh),
+                      _ptr(prm["A_log"], "A_log", torch.float32, lh), _ptr(prm["D"], "D", torch.float32, lh))
+
+
+def _scan_tensors(d: Dims, x, B, C, dt, h_in, h_out, y):
+    """(rows, groups, slots, the (pointer, stride) pairs of x, B, C, dt, h_in, h_out, (y, stride))."""
+    px, T, ldx = _tok_rows(x, "x", d.d_inner)
+    if B.dim() != 2 or B.size(1) < d.d_state or B.size(1) % d.d_state:
+        raise ValueError("B: [rows, n_groups * d_state]")
+    pb, Tb, ldb = _tok_rows(B, "B")
+    pc, Tc, ldc = _tok_rows(C, "C", B.size(1))
+    pd, Td, ldd = _tok_rows(dt, "dt", d.n_heads)
+    py, Ty, ldy = _tok_rows(y, "y", d.d_inner)
+    if not T == Tb == Tc == Td == Ty:
+        raise ValueError("x, B, C, dt and y: as many rows each")
+    n_slots = _slots_of(h_out, "h_out", d.n_layers * d.n_heads * d.head_dim * d.d_state)
+    hi = None if h_in is None else _dev(h_in, "h_in", torch.float32, h_out.numel())
+    return T, B.size(1) // d.d_state, n_slots, (px, ldx, pb, ldb, pc, ldc, pd, ldd, hi,
+                                                _dev(h_out, "h_out", torch.float32), py, ldy)
+
+
+def ssm_prompt_scan_workspace_size(dims: Dims, n_seq: int, n_tok: int, max_len: int, n_groups: int = 1) -> int:
+    """Bytes of device workspace ssm_prompt_scan needs (host call)."""
+    cd = dims.c()
+    b = lib().ssm_prompt_scan_workspace_size(ctypes.byref(cd), n_seq, n_tok, max_len, n_groups)
+    if b == 0:
+        raise SSMError(SSM_ERR_INVALID_ARG, ssm_last_error())
+    return int(b)
+
+
+def ssm_prompt_scan(dims: Dims, params: dict, layer: int, cu_seqlens, max_len: int, x, B, C, dt, h_in, h_out, y,
+                    workspace, slots=None, status=None, stream=None):
+    """Linear attention with a decay for each head over ragged prompts: y (bf16) and the state after each prompt.
+    x, B, C, dt: bf16 [n_tok, .], any row stride (n_groups = columns of B / d_state); h_in: fp32
+    [n_slots, L, H, P, N] or None (zero states); h_out may be h_in."""
+    T, G, n_slots, t = _scan_tensors(dims, x, B, C, dt, h_in, h_out, y)
+    n_seq = cu_seqlens.numel() - 1
+    cd, cp = dims.c(), _scan_params(params, dims)
+    _check(lib().ssm_prompt_scan(
+        ctypes.byref(cd), ctypes.byref(cp), int(layer), G, n_seq, n_slots, T, int(max_len),
+        _dev(cu_seqlens, "cu_seqlens", torch.int32, n_seq + 1), _opt_slots(slots, n_seq), *t,
+        _dev(workspace, "workspace", torch.uint8), ctypes.c_size_t(workspace.numel()), _opt_status(status),
+        _stream(stream, x)))
+
+
+def ssm_scan_step(dims: Dims, params: dict, layer: int, x, B, C, dt, h_in, h_out, y, slots=None, status=None,
+                  stream=None):
+    """The recurrent form of ssm_prompt_scan for one token of each sequence (row s of every tensor: sequence s)."""
+    S, G, n_slots, t = _scan_tensors(dims, x, B, C, dt, h_in, h_out, y)
+    cd, cp = dims.c(), _scan_params(params, dims)
+    if slots is None and S > n_slots:
+        raise ValueError(f"h_out: {n_slots} slots for {S} sequences")
+    _check(lib().ssm_scan_step(ctypes.byref(cd), ctypes.byref(cp), int(layer), G, S, n_slots, _opt_slots(slots, S), *t,
+                               _opt_status(status), _stream(stream, x)))
+
+
+# ---------------------------------------------------------------------------
+# attention blocks (include/ssm_attention.h)
+# ---------------------------------------------------------------------------
+def ssm_tree_attention_workspace_size(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, max_cache_len: int) -> int:
+    """Bytes of device workspace ssm_tree_attention needs (host call)."""
+    b = lib().ssm_tree_attention_workspace_size(n_seq, n_nodes, Hq, Hkv, D, max_cache_len)
+    if b == 0:
+        raise SSMError(SSM_ERR_INVALID_ARG, ssm_last_error())
+    return int(b)
+
+
+def _pages(k_pages, v_pages, lead: int, Hkv: int, D: int):
+    """(n_pages, page_size) of page tensors [..lead.., n_pages, Hkv, page_size, D]."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != lead + 4 or k_pages.size(-3) != Hkv or k_pages.size(-1) != D:
+        raise ValueError("k_pages: [" + "n_layers, " * lead + "n_pages, Hkv, page_size, D]")
+    return k_pages.size(-4), k_pages.size(-2)
+
+
+def ssm_tree_attention(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, layout, q, k, v, k_pages, v_pages, page_table,
+                       cache_len, max_cache_len: int, scale: float, o, workspace, status=None, stream=None):
+    """Attention of every node of the draft trees over its sequence's paged cache and its ancestors.  q, o: bf16
+    [S * n, Hq * D], k, v: bf16 [S * n, Hkv * D] (any row stride); k_pages, v_pages: bf16
+    [n_pages, Hkv, page_size, D]; page_table: int32 [S, max_pages]."""
+    S, n = n_seq, n_nodes
+    rows = [_tok_rows(t, nm, h * D) for t, nm, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv), (o, "o", Hq))]
+    if any(r[1] != S * n for r in rows):
+        raise ValueError("q, k, v and o: n_seq * n_nodes rows each")
+    n_pages, page = _pages(k_pages, v_pages, 0, Hkv, D)
+    if page_table.dim() != 2 or page_table.size(0) != S:
+        raise ValueError("page_table: [n_seq, max_pages]")
+    (pq, _, ldq), (pk, _, ldk), (pv, _, ldv), (po, _, ldo) = rows
+    _check(lib().ssm_tree_attention(
+        S, n, Hq, Hkv, D, _dev(layout, "layout", torch.int32, S * n * NODE_WORDS), pq, ldq, pk, ldk, pv, ldv,
+        _dev(k_pages, "k_pages", torch.bfloat16), _dev(v_pages, "v_pages", torch.bfloat16, k_pages.numel()), n_pages, page,
+        _dev(page_table, "page_table", torch.int32), page_table.size(1), _dev(cache_len, "cache_len", torch.int32, S),
+        int(max_cache_len), float(scale), po, ldo, _dev(workspace, "workspace", torch.uint8),
+        ctypes.c_size_t(workspace.numel()), _opt_status(status), _stream(stream, q)))
+
+
+def ssm_kv_commit(n_seq: int, n_nodes: int, path, path_len, k, v, k_pages, v_pages, page_table, cache_len, len_out,
+                  status=None, stream=None):
+    """The accepted paths' K and V rows behind the cached rows, all layers: k, v bf16 [L, S * n, Hkv * D], pages bf16
+    [L, n_pages, Hkv, page_size, D]; len_out (may be cache_len) = cache_len + the rows committed."""
+    S, n = n_seq, n_nodes
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 5:
+        raise ValueError("k_pages: [n_layers, n_pages, Hkv, page_size, D]")
+    L, Hkv, D = k_pages.size(0), k_pages.size(2), k_pages.size(4)
+    n_pages, page = _pages(k_pages, v_pages, 1, Hkv, D)
+    for nm, t in (("path", path), ("page_table", page_table)):
+        if t.dim() != 2 or t.size(0) != S:
+            raise ValueError(f"{nm}: a row for each sequence")
+    _check(lib().ssm_kv_commit(
+        L, S, n, Hkv, D, path.size(1), _dev(path, "path", torch.int32), _dev(path_len, "path_len", torch.int32, S),
+        _dev(k, "k", torch.bfloat16, L * S * n * Hkv * D), _dev(v, "v", torch.bfloat16, L * S * n * Hkv * D),
+        _dev(k_pages, "k_pages", torch.bfloat16), _dev(v_pages, "v_pages", torch.bfloat16, k_pages.numel()), n_pages, page,
+        _dev(page_table, "page_table", torch.int32), page_table.size(1), _dev(cache_len, "cache_len", torch.int32, S),
+        _dev(len_out, "len_out", torch.int32, S), _opt_status(status), _stream(stream, k_pages)))
