@@ -132,25 +132,24 @@ __global__ void __launch_bounds__(ATHREADS, 2) attend_kernel(AttendArgs a) {
     m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
   }
 
+#pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     cp_async_wait<0>();
     __syncthreads();  // the tile is there; the other stage's readers are done
     if (i + 1 < i1) load(i + 1);
     const uint32_t kt = sb + Sh::OFF_KV + (i & 1) * 2 * Sh::KV, vt = kt + Sh::KV;
     const bool tree = i == ct;
-    unsigned long long odd = 0;  // tree rows with a value of v that is not finite: zero in the tile, added by themselves
+    unsigned long long odd = 0;  // tree rows with values of v that are not finite: zero in the tile, added by themselves
     if (tree) {
       if (tid < a.n) {
         bool f = false;
+#pragma unroll 1
         for (int ch = 0; ch < CH; ++ch) {
           uint4* v = reinterpret_cast<uint4*>(smem + (vt - sb) + tile_off(tid, ch, ROWB));
           const uint4 x = *v;
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          for (int k = 0; k < 4; ++k) f |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+          const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+          if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) f = true, *v = y;
         }
-        if (f)
-          for (int ch = 0; ch < CH; ++ch)
-            *reinterpret_cast<uint4*>(smem + (vt - sb) + tile_off(tid, ch, ROWB)) = make_uint4(0, 0, 0, 0);
         link[tid] = f ? -2 : -1;
       } else if (tid < 64) {
         link[tid] = -1;
@@ -192,6 +191,7 @@ __global__ void __launch_bounds__(ATHREADS, 2) attend_kernel(AttendArgs a) {
           wa = ra < rows ? anc[ra / a.g] : 0ull;
           wb = ra + 8 < rows ? anc[(ra + 8) / a.g] : 0ull;
         } else if (*no_page) {  // rows on such pages are absent
+#pragma unroll 1
           for (int key = 0; key < min(left, KT); ++key) {
             const int pg = table[(i * KT + key) >> a.page_shift];
             if (pg < 0 || pg >= a.n_pages) wa &= ~(1ull << key);
@@ -243,27 +243,26 @@ __global__ void __launch_bounds__(ATHREADS, 2) attend_kernel(AttendArgs a) {
           mma16816(o[t][2 * d + 1], pa, b[2], b[3]);
         }
       }
-    if (odd) {
+    // what the values left out add, in the rows that see them, is not finite whatever its weight
+    const unsigned long long mine = WN == 1 ? odd : odd >> (wn * KW) << (wn * KW) & (wn + 1 < WN ? (1ull << (wn + 1) * KW) - 1 : ~0ull);
+    if (mine) {  // each by the warp whose key it is
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const int ra = r0 + (wm * MT + t) * 16 + g8;
         const unsigned long long wa = ra < rows ? anc[ra / a.g] : 0ull, wb = ra + 8 < rows ? anc[(ra + 8) / a.g] : 0ull;
+#pragma unroll 1
+        for (unsigned long long left = mine & (wa | wb); left; left &= left - 1) {
+          const int key = __ffsll((long long)left) - 1;
+          const bool sa = wa >> key & 1, sb2 = wb >> key & 1;
+          const uint16_t* v = a.v + ((long long)s * a.n + key) * a.ldv + kvh * D + 2 * q4;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          for (int kk = 0; kk < 8; ++kk) {
-            const int key = wn * KW + 8 * j + kk, from = (lane & ~3) | (kk >> 1);
-            if (!(odd >> key & 1)) continue;
-            const uint32_t ua = __shfl_sync(0xffffffffu, pf[t][j][0], from);
-            const uint32_t ub = __shfl_sync(0xffffffffu, pf[t][j][1], from);
-            const float pa = kk & 1 ? bf16_hi(ua) : bf16_lo(ua), pb = kk & 1 ? bf16_hi(ub) : bf16_lo(ub);
-            const uint16_t* v = a.v + ((long long)s * a.n + key) * a.ldv + kvh * D + 2 * q4;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              const uint32_t x = *reinterpret_cast<const uint32_t*>(v + 8 * d);
-              if (wa >> key & 1) o[t][d][0] = fmaf(pa, bf16_lo(x), o[t][d][0]), o[t][d][1] = fmaf(pa, bf16_hi(x), o[t][d][1]);
-              if (wb >> key & 1) o[t][d][2] = fmaf(pb, bf16_lo(x), o[t][d][2]), o[t][d][3] = fmaf(pb, bf16_hi(x), o[t][d][3]);
-            }
+          for (int d = 0; d < DT; ++d) {
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(v + 8 * d), out = x ^ finite_or_zero(x);
+            const float x0 = out & 0xffffu ? bf16_lo(x) : 0.f, x1 = out & 0xffff0000u ? bf16_hi(x) : 0.f;
+            o[t][d][0] += sa ? x0 : 0.f, o[t][d][1] += sa ? x1 : 0.f;
+            o[t][d][2] += sb2 ? x0 : 0.f, o[t][d][3] += sb2 ? x1 : 0.f;
           }
+        }
       }
     }
   }

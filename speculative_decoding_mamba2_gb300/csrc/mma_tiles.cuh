@@ -58,6 +58,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// a pair of bf16 values, 0 in the place of one that is not finite
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t v) {
+  return ((v & 0x7f80u) == 0x7f80u ? 0u : v & 0xffffu) | ((v & 0x7f800000u) == 0x7f800000u ? 0u : v & 0xffff0000u);
+}
+
 // 2^x on the special-function unit (relative error about 2^-22; 2^-inf = 0)
 __device__ __forceinline__ float exp2_sfu(float x) {
   float r;

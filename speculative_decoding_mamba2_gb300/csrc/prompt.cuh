@@ -50,8 +50,12 @@ struct ScanArgs {
   int nseg;         // segments of a sequence (set by launch_prompt_scan)
   float* seg_state;  // workspace: what segments 0 .. nseg-2 add to the state, and their decay
 };
-size_t prompt_scan_workspace_bytes(int H, int n_seq, int max_len);
+size_t prompt_scan_workspace_bytes(int H, int G, int n_seq, int n_tok, int max_len);
 cudaError_t launch_prompt_scan(const ScanArgs& a, void* workspace, cudaStream_t s);
+// the same on tcgen05 (prompt_scan_tc.cu)
+bool prompt_scan_tc_fits(int H, int G, int n_seq, int max_len);
+size_t prompt_scan_tc_workspace_bytes(int H, int G, int n_seq, int n_tok, int max_len);
+cudaError_t launch_prompt_scan_tc(const ScanArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
 
 struct AttendArgs {

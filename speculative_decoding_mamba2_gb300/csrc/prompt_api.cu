@@ -138,7 +138,7 @@ extern "C" size_t ssm_prompt_scan_workspace_size(const ssm_dims* dims, int32_t n
     return 0;
   }
   set_error("");
-  return prompt_scan_workspace_bytes(dims->n_heads, n_seq, max_len < n_tok ? max_len : n_tok);
+  return prompt_scan_workspace_bytes(dims->n_heads, n_groups, n_seq, n_tok, max_len < n_tok ? max_len : n_tok);
 }
 
 extern "C" int ssm_prompt_scan(const ssm_dims* dims, const ssm_params* prm, int32_t layer, int32_t n_groups,
@@ -154,7 +154,7 @@ extern "C" int ssm_prompt_scan(const ssm_dims* dims, const ssm_params* prm, int3
   if (n_seq > 0 && !cu_seqlens) return pfail(SSM_ERR_INVALID_ARG, fn, "cu_seqlens is NULL");
   if (max_len > n_tok) max_len = n_tok;  // no sequence is longer than that
   if (!workspace || ((uintptr_t)workspace & 255)) return pfail(SSM_ERR_INVALID_ARG, fn, "workspace must be 256-byte aligned");
-  if (workspace_bytes < prompt_scan_workspace_bytes(dims->n_heads, n_seq, max_len))
+  if (workspace_bytes < prompt_scan_workspace_bytes(dims->n_heads, n_groups, n_seq, n_tok, max_len))
     return pfail(SSM_ERR_CAPACITY, fn, "workspace too small (ssm_prompt_scan_workspace_size)");
   ScanArgs a = scan_args(dims, prm, layer, n_groups, x, ldx, B, ldb, C, ldc, dt, lddt, h_in, h_out, y, ldy);
   a.q = SeqArgs{n_seq, n_slots, n_tok, max_len, cu_seqlens, slots, dev_status};

@@ -31,11 +31,6 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t& hi, uint32_
   lo = pack_bf16x2(r0 - bf16_lo(mid), r1 - bf16_hi(mid));
 }
 
-// a pair of bf16 values, 0 in the place of one that is not finite
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t v) {
-  return ((v & 0x7f80u) == 0x7f80u ? 0u : v & 0xffffu) | ((v & 0x7f800000u) == 0x7f800000u ? 0u : v & 0xffff0000u);
-}
-
 // STATE_ONLY: what the segment adds to a zero state, and its decay, into the workspace
 template <bool STATE_ONLY>
 __global__ void __launch_bounds__(THREADS, 2) prompt_scan_kernel(ScanArgs a) {
@@ -92,6 +87,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_scan_kernel(ScanArgs a) {
       hi = *reinterpret_cast<const float2*>(a.h_in + hbase + (16 * warp + g + 8) * kN + n);
     }
     if (!STATE_ONLY) {
+#pragma unroll 1
       for (int i = 0; i < seg; ++i) {
         const float* r = ws + i * wrec;
         const float d = r[kP * kN];
@@ -117,6 +113,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_scan_kernel(ScanArgs a) {
   float* sS = reinterpret_cast<float*>(smem + OFF_T) + warp * 3 * Q;
   float *sW = sS + Q, *sD = sW + Q;
   float seg_sum = 0.f;  // of the exponents of the whole segment
+#pragma unroll 1
   for (int c = c0; c < c1; ++c) {
     const uint32_t st = sb + (c & 1) * STAGE;
     // each warp by itself: exponents of the chunk's tokens 2 lane, 2 lane + 1, their prefix and suffix sums
@@ -186,6 +183,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_scan_kernel(ScanArgs a) {
       for (int i = 0; i < 8; ++i) acc[i][0] *= ea, acc[i][1] *= ea, acc[i][2] *= eb, acc[i][3] *= eb;
       const bool any_odd = __syncthreads_or(odd);  // and: every warp has read the state
       // the chunk's own tokens, 16 at a time
+#pragma unroll 1
       for (int jb = 0; jb <= warp; ++jb) {
         float gs[2][4];
 #pragma unroll
@@ -221,6 +219,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_scan_kernel(ScanArgs a) {
         if (any_odd) {  // the values left out, each only in the rows at or after its token
 #pragma unroll
           for (int i = 0; i < 4; ++i)  // pa[i]: rows g + 8 (i & 1), tokens 8 (i >> 1) + 2 q4, + 1
+#pragma unroll 1
             for (int k = 0; k < 8; ++k) {
               const int u = 16 * jb + 8 * (i >> 1) + k, t = i & 1 ? tb : ta;
               const uint32_t w = __shfl_sync(0xffffffffu, pa[i], (lane & ~3) | (k >> 1));
@@ -306,13 +305,15 @@ int plan_segments(int H, int n_seq, int max_len) {
 
 }  // namespace
 
-size_t prompt_scan_workspace_bytes(int H, int n_seq, int max_len) {
+size_t prompt_scan_workspace_bytes(int H, int G, int n_seq, int n_tok, int max_len) {
+  if (prompt_scan_tc_fits(H, G, n_seq, max_len)) return prompt_scan_tc_workspace_bytes(H, G, n_seq, n_tok, max_len);
   const int nseg = plan_segments(H, n_seq, max_len);
   return 256 + (size_t)n_seq * H * (nseg - 1) * (kP * kN + 32) * sizeof(float);
 }
 
 cudaError_t launch_prompt_scan(const ScanArgs& args, void* workspace, cudaStream_t s) {
   if (args.q.n_seq == 0) return cudaSuccess;
+  if (prompt_scan_tc_fits(args.H, args.G, args.q.n_seq, args.q.max_len)) return launch_prompt_scan_tc(args, workspace, s);
   ScanArgs a = args;
   a.nseg = plan_segments(a.H, a.q.n_seq, a.q.max_len);
   a.seg_state = static_cast<float*>(workspace);

@@ -135,6 +135,15 @@ def test_prompt_scan_long_axis(H, G, lens):
     check_scan(c, y, h)
 
 
+@pytest.mark.parametrize("H,G,lens", [(2, 1, [65 * k + 3 for k in range(1, 9)]), (24, 2, [300 + 17 * k for k in range(13)])])
+def test_prompt_scan_many_chunks(H, G, lens):
+    """Enough (sequence, head) pairs that a sequence's chunks follow each other in one block."""
+    c = scan_case(14, H, G, lens)
+    y, h, status = run_scan(c)
+    assert status == 0
+    check_scan(c, y, h)
+
+
 def test_prompt_scan_layers_in_place_and_loose_bound():
     c = scan_case(3, 4, 2, [70, 0, 5], L=3, layer=1)
     y, h, status = run_scan(c, in_place=True, max_len=1000)
