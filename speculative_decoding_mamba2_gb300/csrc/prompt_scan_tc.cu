@@ -7,12 +7,13 @@
 //     Y2 [128 x 64]  = h [128 x n] . C^T                       h rounded to bf16, in tensor memory
 //     Y1 [128 x 64]  = x^T [128 x 64] . P^T                    for each head of the pair, P = scores with their decays
 //     y = Y1 + e^{S_t} Y2 + D x,   h' = decay h + S            (h in fp32 registers for the whole walk)
-// The scores C.B^T are the same for every head: scores_kernel computes them once, chunk by chunk, into the workspace.
-//
-// Warps by role, each waiting only for what it needs, so that the chunks overlap: 4 make Xw, 4 make P, 4 finish y, 8
-// carry the state, one issues copies (TMA, three stages), one the MMAs, two the decays of their head.  MMAs run in the
-// order they are issued: S, Y2, Y1.  Every wait is bounded: on a time-out all roles leave, the copies and MMAs in
-// flight are waited for (bounded again) and the tensor memory is freed.
+// // Scores and decays of the chunks are the same for every walk of them, so prep_kernel makes them first, into the
+// workspace.  16 warps then walk through a chunk's steps together -- h' from S, Xw of the next chunk, y, h for the tensor
+// cores, P of the next chunk -- while one warp issues the MMAs that the steps hand over and one the copies (TMA, three
+// stages): the 128 rows of tensor memory are four warps, and the four groups of four share out tokens or columns.  (Warps
+// specialised by step, tried first, each ran their own code: 4000 cycles a chunk, most of them waiting for instructions.)
+// MMAs run in the order they are issued: S, Y2, Y1.  Every wait is bounded: on a time-out all warps leave, the copies and
+// MMAs in flight are waited for (bounded again) and the tensor memory is freed.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -23,7 +24,7 @@
 namespace ssmtree {
 namespace {
 
-constexpr int Q = 64, NT = 768, STAGES = 3;
+constexpr int Q = 64, WARPS = 16, NT = 32 * WARPS + 64, STAGES = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast2 = -120.f * kLog2e;  // as kLeast of prompt_scan.cu, in powers of two
 
@@ -33,8 +34,9 @@ constexpr int ST_BYTES = 6 * BLK, OFF_TB = 2 * BLK, OFF_TX = 4 * BLK;
 constexpr int OFF_P = STAGES * ST_BYTES;   // [2][head][BLK]
 constexpr int OFF_Y = OFF_P + 4 * BLK;     // [2][64][256]
 constexpr int OFF_D = OFF_Y + 4 * BLK;     // [STAGES][head] decay records
-constexpr int OFF_ODD = OFF_D + STAGES * 2 * 320 * 4;  // [2][128] tokens whose x is not finite
-constexpr int OFF_BAR = OFF_ODD + 2 * 128 * 8;
+constexpr int REC = 1280;                  // bytes of one
+constexpr int OFF_ODD = OFF_D + STAGES * 2 * REC;  // [2][group][128] tokens whose x is not finite | chunk << 16
+constexpr int OFF_BAR = OFF_ODD + 2 * 4 * 128 * 4;
 constexpr int TC_SMEM = OFF_BAR + 256 + 1024 /* alignment */;
 
 // tensor memory columns
@@ -48,14 +50,17 @@ struct Decays {  // of one head and chunk (exponents in powers of two)
   float e[64];   // 2^(sum up to the token)
   float total, pad[31];  // 2^(sum of the chunk)
 };
-static_assert(sizeof(Decays) == 320 * 4, "record size");
+static_assert(sizeof(Decays) == REC, "record size");
 
 struct Bars {
-  unsigned long long full[STAGES], free_[STAGES], dt_full[STAGES], dt_free[STAGES];
-  unsigned long long xw_full[2], xw_free, s_full, s_free, h_ready, y2_done, p_full[2], p_free[2], y_full, y_free, drain;
+  unsigned long long full[STAGES], free_[STAGES], s_full, y_full, drain;
   uint32_t tmem;
   int stop;
+  int odd_chunk[2];  // the last chunk of each parity with an x that is not finite
 };
+// named barriers: 1 .. 4 a group's y, then all workers, and what they hand to the MMA warp
+constexpr int B_ALL = 5, B_XW = 6, B_H = 7, B_P = 8, HANDED = 32 * WARPS + 32;
+__device__ __forceinline__ void hand_over(int id) { asm volatile("bar.arrive %0, %1;\n" ::"r"(id), "n"(HANDED) : "memory"); }
 static_assert(sizeof(Bars) <= 256, "barrier space");
 
 // Descriptors: 128-byte swizzled tiles of 64-column blocks (rows of 128 bytes, groups of 8 rows 1024 bytes apart).
@@ -118,6 +123,12 @@ __device__ __forceinline__ void tmem_wait_ld8(float (&v)[8], float (&w)[8]) {
                :
                : "memory");
 }
+// a 64 x 64 block of a tile stored by a bulk tensor copy
+__device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(tmap), "r"(c0), "r"(c1),
+               "r"(src)
+               : "memory");
+}
 // four 8 x 8 fragments stored transposed, row addresses as frag_a_t's
 __device__ __forceinline__ void stsm4_t(uint32_t addr, const uint32_t (&r)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(r[0]),
@@ -141,50 +152,74 @@ __device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
                : "memory");
 }
 
-// The warp waits together, suspended for up to 20 us at a time (spinning took 40 % of the SM's issue slots from the warps
-// at work).  False once kTries of those have passed or another role has given up.
-constexpr int kTries = 50000;
-__device__ __forceinline__ bool try_wait_20us(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return __all_sync(0xffffffffu, done);
-}
+// The warp waits together.  False once kWaitLimit tries (seconds) have passed or another role has given up.
 __device__ __forceinline__ bool wait_bar(unsigned long long* bar, uint32_t parity, volatile int* stop) {
   const uint32_t b = smem_u32(bar);
-  if (try_wait_20us(b, parity)) return true;
-#pragma unroll 1
-  for (int it = 0; it < kTries && !*stop; ++it)
-    if (try_wait_20us(b, parity)) return true;
-  *stop = 1;
-  return false;
-}
-__device__ __forceinline__ void arrive_warp(unsigned long long* bar, int lane) {
+  unsigned it = 0;
+  while (!mbar_try_wait(b, parity)) {
+    if ((++it & 1023) == 0 && (*stop || it > kWaitLimit)) {
+      *stop = 1;
+      break;
+    }
+  }
   __syncwarp();
-  if (lane == 0) mbar_arrive(smem_u32(bar));
+  return (it & 1023) != 0 || it == 0 || !*stop;
 }
 
-// x = hi + mid + lo in bf16 (an infinity: hi alone), pairs of values
-__device__ __forceinline__ void split3_pair(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  hi = pack_bf16x2(x0, x1);
-  const float r0 = x0 - bf16_lo(hi), r1 = x1 - bf16_hi(hi);
-  mid = pack_bf16x2(r0, r1);
-  lo = pack_bf16x2(r0 - bf16_lo(mid), r1 - bf16_hi(mid));
+// x w = hi + mid + lo in bf16 (an infinity: hi alone), for a pair of bf16 values x
+__device__ __forceinline__ void scale_split3(uint32_t x, unsigned long long w, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  const unsigned long long minus1 = 0xbf800000bf800000ull;
+  const unsigned long long u = fmul2(pack2(bf16_lo(x), bf16_hi(x)), w);
+  const float2 a = unpack2(u);
+  hi = pack_bf16x2(a.x, a.y);
+  const unsigned long long r = ffma2(pack2(bf16_lo(hi), bf16_hi(hi)), minus1, u);
+  const float2 b = unpack2(r);
+  mid = pack_bf16x2(b.x, b.y);
+  const float2 c = unpack2(ffma2(pack2(bf16_lo(mid), bf16_hi(mid)), minus1, r));
+  lo = pack_bf16x2(c.x, c.y);
 }
 
-// Scores C_t . B_s of every chunk and group, once for all heads: [record][s / 4][t][s % 4] fp32.
-__device__ __forceinline__ long long score_record(int first, int s, int chunk, int G, int grp) {
-  return ((long long)(first / Q) + s + chunk) * G + grp;
-}
-__global__ void __launch_bounds__(128) scores_kernel(ScanArgs a, float* scores) {
+// Once for all walks: grid z < G: scores C_t . B_s of a chunk and group, [record][s / 4][t][s % 4] fp32; then the decays
+// of a chunk and four heads, a warp each.
+__device__ __forceinline__ long long chunk_record(int first, int s, int chunk) { return (long long)(first / Q) + s + chunk; }
+__global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, Decays* decays) {
   __shared__ __align__(128) unsigned char sm[2 * Q * kN * 2];
   launch_dependents();
   const int c = blockIdx.x, s = blockIdx.y, grp = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int first, len, slot;
   if (!seq_range(a.q, s, first, len, slot) || c * Q >= len) return;
+  if (grp >= a.G) {
+    const int h = (grp - a.G) * 4 + warp;
+    if (h >= a.H) return;
+    const float A2 = neg_exp(a.A_log[h]) * kLog2e, bias = a.dt_bias[h];
+    const int t = c * Q + 2 * lane;  // tokens 2 lane, 2 lane + 1
+    const uint16_t* q = a.dt + (long long)(first + t) * a.lddt + h;
+    const float d0 = t < len ? softplus_f(bf16f(q[0]) + bias) : 0.f;
+    const float d1 = t + 1 < len ? softplus_f(bf16f(q[a.lddt]) + bias) : 0.f;
+    const float e0 = fmaxf(d0 * A2, kLeast2), e1 = fmaxf(d1 * A2, kLeast2);
+    float pre = e0 + e1, suf = pre;  // sums within the lane's half of the chunk
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      const float u = __shfl_up_sync(0xffffffffu, pre, o, 16), v = __shfl_down_sync(0xffffffffu, suf, o, 16);
+      if ((lane & 15) >= o) pre += u;
+      if ((lane & 15) + o < 16) suf += v;
+    }
+    const float sum0 = __shfl_sync(0xffffffffu, pre, 15), sum1 = __shfl_sync(0xffffffffu, pre, 31);
+    float before = __shfl_up_sync(0xffffffffu, pre, 1, 16), after = __shfl_down_sync(0xffffffffu, suf, 1, 16);
+    if ((lane & 15) == 0) before = 0.f;
+    if ((lane & 15) == 15) after = 0.f;
+    const bool low = lane < 16;
+    Decays& d = decays[chunk_record(first, s, c) * a.H + h];
+    const float base = low ? 0.f : sum0, rest = low ? sum1 : 0.f, S0 = before + e0;
+    *reinterpret_cast<float2*>(&d.S[2 * lane]) = make_float2(S0, pre);
+    *reinterpret_cast<float2*>(&d.D[2 * lane]) = make_float2(d0, d1);
+    const float a0 = after + e1;  // after token 2 lane, in its half
+    if (low) *reinterpret_cast<float2*>(&d.E1[2 * lane]) = make_float2(exp2_sfu(a0) * d0, exp2_sfu(after) * d1);
+    *reinterpret_cast<float2*>(&d.w[2 * lane]) = make_float2(exp2_sfu(a0 + rest) * d0, exp2_sfu(after + rest) * d1);
+    *reinterpret_cast<float2*>(&d.e[2 * lane]) = make_float2(exp2_sfu(base + S0), exp2_sfu(base + pre));
+    if (lane == 0) d.total = exp2_sfu(sum0 + sum1);
+    return;
+  }
   const uint32_t sb = smem_u32(sm);
   for (int i = tid; i < Q * 16; i += 128) {
     const int row = i >> 4, ch = i & 15;
@@ -213,7 +248,7 @@ __global__ void __launch_bounds__(128) scores_kernel(ScanArgs a, float* scores) 
         mma16816(acc[2 * np + 1], cf, b[2], b[3]);
       }
   }
-  float* out = scores + score_record(first, s, c, a.G, grp) * (Q * Q);
+  float* out = scores + (chunk_record(first, s, c) * a.G + grp) * (Q * Q);
   const int t = 16 * warp + (lane >> 2);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -225,309 +260,80 @@ __global__ void __launch_bounds__(128) scores_kernel(ScanArgs a, float* scores) 
     }
 }
 
-// Registers per thread by role: launched with 80, 6 x 80 = 72 + 96 + 80 + 88 + 88 + 56.
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
-
 template <bool STATE_ONLY>
 __global__ void __launch_bounds__(NT, 1)
     scan_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
-                   const __grid_constant__ CUtensorMap tcm, ScanArgs a, const float* scores) {
+                   const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap ty, ScanArgs a,
+                   const float* scores, const Decays* decays) {
   extern __shared__ unsigned char smem_raw[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+  // (shuffles tell the compiler what is the same for a warp: it then keeps it in uniform registers)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int pair = blockIdx.x, nseg = STATE_ONLY ? a.nseg - 1 : a.nseg;
   const int s = blockIdx.y / nseg, seg = blockIdx.y % nseg;
   int first, len, slot;
-  if (!seq_range(a.q, s, first, len, slot)) {
-    if (pair == 0 && seg == 0 && tid == 0) flag(a.q.status, SSM_STATUS_SEQ_RANGE);
-    grid_dependency_wait();
-    return;
-  }
+  const bool there = seq_range(a.q, s, first, len, slot);
+  first = __shfl_sync(0xffffffffu, first, 0), len = __shfl_sync(0xffffffffu, len, 0), slot = __shfl_sync(0xffffffffu, slot, 0);
   const int nch = (len + Q - 1) / Q, per = (nch + a.nseg - 1) / a.nseg;
   const int c0 = seg * per, c1 = min(nch, c0 + per), n = max(0, c1 - c0);
-  if (STATE_ONLY ? c1 >= nch : (n == 0 && seg > 0)) {
+  if (!there || (STATE_ONLY ? c1 >= nch : (n == 0 && seg > 0))) {
+    if (!there && pair == 0 && seg == 0 && tid == 0) flag(a.q.status, SSM_STATUS_SEQ_RANGE);
     grid_dependency_wait();  // the grid does not end before the one it depends on
     return;
   }
   unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // stays a shared-memory pointer to the compiler
   const uint32_t sb = smem_u32(smem);
-  Decays* dec = reinterpret_cast<Decays*>(smem + OFF_D);
   Bars* bar = reinterpret_cast<Bars*>(smem + OFF_BAR);
   volatile int* stop = &bar->stop;
 
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(smem_u32(&bar->full[i]), 1);
-      mbar_init(smem_u32(&bar->free_[i]), 1 + 4);
-      mbar_init(smem_u32(&bar->dt_full[i]), 2);
-      mbar_init(smem_u32(&bar->dt_free[i]), STATE_ONLY ? 12 : 20);
+      mbar_init(smem_u32(&bar->free_[i]), 2);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bar->xw_full[i]), 4);
-      mbar_init(smem_u32(&bar->p_full[i]), 4);
-      mbar_init(smem_u32(&bar->p_free[i]), 4);
-    }
-    mbar_init(smem_u32(&bar->xw_free), 1);
     mbar_init(smem_u32(&bar->s_full), 1);
-    mbar_init(smem_u32(&bar->s_free), 8);
-    mbar_init(smem_u32(&bar->h_ready), 8);
-    mbar_init(smem_u32(&bar->y2_done), 1);
     mbar_init(smem_u32(&bar->y_full), 1);
-    mbar_init(smem_u32(&bar->y_free), 4);
     mbar_init(smem_u32(&bar->drain), 1);
+    bar->odd_chunk[0] = bar->odd_chunk[1] = -1;
     bar->stop = 0;
     fence_barrier_init();
   }
   if (!STATE_ONLY)  // P's entries after their token stay zero for the whole walk
     for (int i = tid; i < 4 * BLK / 16; i += NT) reinterpret_cast<uint4*>(smem + OFF_P)[i] = make_uint4(0, 0, 0, 0);
-  if (warp == 21) tmem_alloc_warp(smem_u32(&bar->tmem), 512);
+  if (warp == WARPS) tmem_alloc_warp(smem_u32(&bar->tmem), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar->tmem;
-  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;  // this warp's rows of tensor memory
-  const int row = (warp & 3) * 32 + lane;                    // (head of the pair, p) of a thread
-  const int hd = row >> 6, p = row & 63, head = 2 * pair + hd;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar->tmem, 0);
+  grid_dependency_wait();  // scores, decays, what the segments before add
 
-  const uint32_t xcol = (uint32_t)(OFF_TX + hd * BLK + (p & 7) * 2);  // column p of head hd in a tile of x
-  // x of token t in it: the 16-byte chunk of row t is (p >> 3) ^ (t & 7)
-  auto x_at = [&](unsigned char* stage, int t) {
-    return reinterpret_cast<uint16_t*>(stage + xcol + t * 128 + (((p >> 3) ^ (t & 7)) << 4));
-  };
-  unsigned long long* odd_tokens = reinterpret_cast<unsigned long long*>(smem + OFF_ODD);
-  const int q4 = lane & 3, p0 = (warp & 1) * 32;  // p0: this warp's first column of its head's x
-  if (wg == 0) {
-    // ---- Xw ----
-    if (!STATE_ONLY) regs_dec<72>();
-    bool ok = true;
-#pragma unroll 1
-    for (int i = 0; i < n && ok; ++i) {
-      const int st = i % STAGES, valid = min(Q, len - (c0 + i) * Q);
-      unsigned char* sp = smem + st * ST_BYTES;
-      ok = wait_bar(&bar->full[st], (i / STAGES) & 1, stop) && wait_bar(&bar->dt_full[st], (i / STAGES) & 1, stop);
-      if (!ok) break;
-      if (valid < Q) {  // rows after the sequence's last belong to another one
-        for (int k = tid; k < (Q - valid) * 32; k += 128) {
-          const int r = valid + (k >> 5), blk = (k >> 3) & 3, ch = k & 7;  // blocks of B, then of x
-          *reinterpret_cast<uint4*>(sp + OFF_TB + blk * BLK + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_smem();
-        named_sync(1, 128);
-      }
-      const Decays& d = dec[st * 2 + hd];
-      const uint32_t tile = sb + st * ST_BYTES + OFF_TX + hd * BLK;
-      uint32_t chk = 0;  // sum of 0 x, in pairs: NaN once an x is not finite
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (i > 0) {
-          ok = wait_bar(half ? &bar->s_full : &bar->xw_free, (i - 1) & 1, stop);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        bool odd_half = false;
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {  // 16 tokens, 16 rows.  (Rolled up: the roles' loops share the instruction caches)
-          const int t0 = 32 * half + 16 * (b >> 1), rh = b & 1;
-          uint32_t xf[4], hi[4], mid[4], lo[4];
-          frag_a_t(xf, tile, 128, p0 + 16 * rh, t0, lane);
-          const float2 w0 = *reinterpret_cast<const float2*>(&d.w[t0 + 2 * q4]);
-          const float2 w1 = *reinterpret_cast<const float2*>(&d.w[t0 + 8 + 2 * q4]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 w = j < 2 ? w0 : w1;
-            split3_pair(bf16_lo(xf[j]) * w.x, bf16_hi(xf[j]) * w.y, hi[j], mid[j], lo[j]);
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(chk) : "r"(xf[j]), "r"(0u));
-          }
-          if (odd_half) {  // an infinity is its own first part
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if ((hi[j] & 0x7f80u) == 0x7f80u) mid[j] &= 0xffff0000u, lo[j] &= 0xffff0000u;
-              if ((hi[j] & 0x7f800000u) == 0x7f800000u) mid[j] &= 0xffffu, lo[j] &= 0xffffu;
-            }
-          }
-          const uint32_t at = tmem + T_XW + lanes + ((uint32_t)(16 * rh) << 16) + (t0 >> 1);
-          tmem_st_frag(at, lo);
-          tmem_st_frag(at + 32, mid);
-          tmem_st_frag(at + 64, hi);
-          if (b == 3 && !odd_half && __any_sync(0xffffffffu, chk & 0x7fff7fffu)) odd_half = true, b = -1;  // once more
-        }
-        if (half == 1 && !STATE_ONLY) {
-          unsigned long long odd = 0;
-          if (__any_sync(0xffffffffu, chk & 0x7fff7fffu)) {
-            // such values leave the tile (each thread its row's): the product with a zero of P would spread them
-#pragma unroll 1
-            for (int t = 0; t < Q; ++t) {
-              uint16_t* v = x_at(sp, t);
-              if ((*v & 0x7f80u) == 0x7f80u) odd |= 1ull << t, *v = 0;
-            }
-            fence_async_smem();
-          }
-          odd_tokens[(i & 1) * 128 + row] = odd;
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive_warp(&bar->xw_full[half], lane);
-      }
-      if (!ok) break;
-      if (STATE_ONLY) arrive_warp(&bar->free_[st], lane);
-      arrive_warp(&bar->dt_free[st], lane);
-    }
-    // a warp that gives up still takes part in the barrier that the other three may be waiting at
-    if (!ok) asm volatile("bar.arrive 1, 128;\n" ::: "memory");
-  } else if (wg == 1) {
-    // ---- P ----
-    if (!STATE_ONLY) {
-      regs_inc<96>();
-      const int ph = (warp >> 1) & 1, t = (warp & 1) * 32 + lane;  // head and token of this thread's row of P
-      const bool late = (warp & 1) != 0;                           // the second half of the chunk
-      const int grp = 2 * pair / (a.H / a.G);
-      grid_dependency_wait();  // the scores
-      float4 gq[16];
-      auto fetch = [&](int i) {
-        const float4* g = reinterpret_cast<const float4*>(scores + score_record(first, s, c0 + i, a.G, grp) * (Q * Q)) + t;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j < 8 || late) gq[j] = g[j * Q];
-      };
-      if (n > 0) fetch(0);
-#pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int st = i % STAGES;
-        if (!wait_bar(&bar->dt_full[st], (i / STAGES) & 1, stop)) break;
-        if (i >= 2 && !wait_bar(&bar->p_free[i & 1], (i / 2 - 1) & 1, stop)) break;
-        const Decays& d = dec[st * 2 + ph];
-        unsigned char* pr = smem + OFF_P + ((i & 1) * 2 + ph) * BLK + t * 128;
-        const float St = d.S[t];
-        auto put = [&](int j8, const uint32_t (&v)[4]) {
-          *reinterpret_cast<uint4*>(pr + ((j8 ^ (t & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-        };
-        if (late) {  // the first half's tokens: their factor times this token's
-          const float E2 = exp2_sfu(St);
-#pragma unroll
-          for (int j8 = 0; j8 < 4; ++j8) {
-            uint32_t v[4];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const float4 g = gq[2 * j8 + m], f = *reinterpret_cast<const float4*>(&d.E1[8 * j8 + 4 * m]);
-              v[2 * m] = pack_bf16x2(g.x * (f.x * E2), g.y * (f.y * E2));
-              v[2 * m + 1] = pack_bf16x2(g.z * (f.z * E2), g.w * (f.w * E2));
-            }
-            put(j8, v);
-          }
-        }
-        const int s0 = late ? 32 : 0;
-#pragma unroll
-        for (int j8 = 0; j8 < 4; ++j8) {  // the token's own half
-          uint32_t v[4];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const int u = 8 * j8 + 4 * m;
-            const float4 g = late ? gq[8 + 2 * j8 + m] : gq[2 * j8 + m];
-            const float4 S = *reinterpret_cast<const float4*>(&d.S[s0 + u]), D = *reinterpret_cast<const float4*>(&d.D[s0 + u]);
-            const float w0 = u <= lane ? g.x * (exp2_sfu(St - S.x) * D.x) : 0.f;
-            const float w1 = u + 1 <= lane ? g.y * (exp2_sfu(St - S.y) * D.y) : 0.f;
-            const float w2 = u + 2 <= lane ? g.z * (exp2_sfu(St - S.z) * D.z) : 0.f;
-            const float w3 = u + 3 <= lane ? g.w * (exp2_sfu(St - S.w) * D.w) : 0.f;
-            v[2 * m] = pack_bf16x2(w0, w1), v[2 * m + 1] = pack_bf16x2(w2, w3);
-          }
-          put((s0 >> 3) + j8, v);
-        }
-        fence_async_smem();
-        arrive_warp(&bar->p_full[i & 1], lane);
-        arrive_warp(&bar->dt_free[st], lane);
-        if (i + 1 < n) fetch(i + 1);
-      }
-    }
-  } else if (wg == 2) {
-    // ---- y ----
-    if (!STATE_ONLY) {
-      const int wt = tid - 256;
-      const float Dh = a.D[head];
-      bool ok = true;
-#pragma unroll 1
-      for (int i = 0; i < n && ok; ++i) {
-        const int st = i % STAGES, c = c0 + i, valid = min(Q, len - c * Q);
-        unsigned char* ys = smem + OFF_Y + (i & 1) * 2 * BLK;
-        const Decays& d = dec[st * 2 + hd];
-        const uint32_t tile = sb + st * ST_BYTES + OFF_TX + hd * BLK, yb = sb + OFF_Y + (i & 1) * 2 * BLK;
-        ok = wait_bar(&bar->y_full, i & 1, stop);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int b = 0; b < 8; ++b) {  // 16 tokens, 16 rows
-          const int t0 = 16 * (b >> 1), rh = b & 1;
-          const uint32_t at = tmem + lanes + ((uint32_t)(16 * rh) << 16) + t0;
-          float y1[8], y2[8];
-          uint32_t xf[4], o[4];
-          tmem_ld_frag_async(at + T_Y1 + hd * 64, y1);
-          tmem_ld_frag_async(at + T_Y2, y2);
-          frag_a_t(xf, tile, 128, p0 + 16 * rh, t0, lane);
-          const float2 e0 = *reinterpret_cast<const float2*>(&d.e[t0 + 2 * q4]);
-          const float2 e1 = *reinterpret_cast<const float2*>(&d.e[t0 + 8 + 2 * q4]);
-          tmem_wait_ld8(y1, y2);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 e = j < 2 ? e0 : e1;
-            o[j] = pack_bf16x2(fmaf(Dh, bf16_lo(xf[j]), fmaf(e.x, y2[2 * j], y1[2 * j])),
-                               fmaf(Dh, bf16_hi(xf[j]), fmaf(e.y, y2[2 * j + 1], y1[2 * j + 1])));
-          }
-          const int r = t0 + (lane & 7) + ((lane >> 4) << 3);
-          stsm4_t(yb + tile_off(r, hd * 8 + ((p0 + 16 * rh) >> 3) + ((lane >> 3) & 1), 256), o);
-        }
-        const unsigned long long odd = odd_tokens[(i & 1) * 128 + row];
-        if (__any_sync(0xffffffffu, odd != 0)) {  // what those values add is not finite, so it can be added to the rounded y
-          __syncwarp();
-          const unsigned char* pt = smem + OFF_P + ((i & 1) * 2 + hd) * BLK;
-#pragma unroll 1
-          for (int u = 0; u < Q; ++u) {
-            if (!(odd >> u & 1)) continue;
-            const float xv = bf16f(a.x[(long long)(first + c * Q + u) * a.ldx + head * kP + p]);
-#pragma unroll 1
-            for (int r = u; r < Q; ++r) {
-              uint16_t* y = reinterpret_cast<uint16_t*>(ys + tile_off(r, row >> 3, 256) + (row & 7) * 2);
-              const uint16_t w = *reinterpret_cast<const uint16_t*>(pt + r * 128 + (((u >> 3) ^ (r & 7)) << 4) + (u & 7) * 2);
-              float v = fmaf(bf16f(w), xv, bf16f(*y));
-              if (r == u) v = fmaf(Dh, xv, v);
-              *y = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
-            }
-          }
-        }
-        tc_fence_before();
-        arrive_warp(&bar->y_free, lane);
-        arrive_warp(&bar->free_[st], lane);
-        arrive_warp(&bar->dt_free[st], lane);
-        arrive_warp(&bar->p_free[i & 1], lane);
-        named_sync(2, 128);  // y of the chunk is in shared memory
-        uint16_t* yo = a.y + (long long)(first + c * Q) * a.ldy + pair * 2 * kP;
-#pragma unroll 2
-        for (int k = 0; k < 8; ++k) {
-          const int r = k * 8 + (wt >> 4), ch = wt & 15;
-          if (r < valid)
-            *reinterpret_cast<uint4*>(yo + (long long)r * a.ldy + ch * 8) =
-                *reinterpret_cast<const uint4*>(ys + tile_off(r, ch, 256));
-        }
-      }
-      if (!ok) asm volatile("bar.arrive 2, 128;\n" ::: "memory");
-    }
-  } else if (wg < 5) {
-    // ---- the state: 64 of a row's 128 columns ----
-    if (!STATE_ONLY) regs_inc<88>();
-    const int n0 = (wg - 3) * 64;
+  if (warp < WARPS) {
+    const int w4 = warp & 3, grp4 = warp >> 2;        // rows 32 w4 .. of tensor memory; this group's share
+    const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+    const int row = w4 * 32 + lane, hd = row >> 6, p = row & 63, head = 2 * pair + hd;  // (head of the pair, p) of a thread
+    const int q4 = lane & 3, p0 = (w4 & 1) * 32;      // the warp's first column of its head's x
+    const int tg = 16 * grp4;                         // the group's first token of a chunk
+    const int n0 = 32 * grp4;                         // its first column of the state
+    uint32_t* odd_tokens = reinterpret_cast<uint32_t*>(smem + OFF_ODD) + row;
+    auto x_at = [&](unsigned char* stage, int t) {    // x of token t in column p: chunk (p >> 3) ^ (t & 7) of the tile's row
+      return reinterpret_cast<uint16_t*>(stage + OFF_TX + hd * BLK + t * 128 + (((p >> 3) ^ (t & 7)) << 4) + (p & 7) * 2);
+    };
+    // this lane's row of the 8 x 8 matrices of 16 tokens x 16 columns, in a stage's x and in a buffer of y
+    const int fr = tg + (lane & 7) + ((lane >> 4) << 3), fc = (p0 >> 3) + ((lane >> 3) & 1);
+    const uint32_t f_off[2] = {(uint32_t)(hd * BLK) + tile_off(fr, fc, 128), (uint32_t)(hd * BLK) + tile_off(fr, fc + 2, 128)};
+
+    // the state: columns n0 .. n0 + 31 of the thread's row
     const long long at = (((long long)slot * a.L + a.layer) * a.H + head) * (kP * kN) + p * kN + n0;
     const long long wrec = kP * kN + 32;
     float* ws = a.seg_state + ((long long)s * a.H + head) * (a.nseg - 1) * wrec;
-    float h[64];
+    float h[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) h[j] = 0.f;
     if (!STATE_ONLY && a.h_in) {
 #pragma unroll
-      for (int j = 0; j < 64; j += 4) {
+      for (int j = 0; j < 32; j += 4) {
         const float4 v = *reinterpret_cast<const float4*>(a.h_in + at + j);
         h[j] = v.x, h[j + 1] = v.y, h[j + 2] = v.z, h[j + 3] = v.w;
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 64; ++j) h[j] = 0.f;
     }
     if (!STATE_ONLY)
 #pragma unroll 1
@@ -536,62 +342,261 @@ __global__ void __launch_bounds__(NT, 1)
         const float dk = r[kP * kN];
         r += p * kN + n0;
 #pragma unroll
-        for (int j = 0; j < 64; j += 4) {
+        for (int j = 0; j < 32; j += 4) {
           const float4 v = *reinterpret_cast<const float4*>(r + j);
           h[j] = fmaf(dk, h[j], v.x), h[j + 1] = fmaf(dk, h[j + 1], v.y);
           h[j + 2] = fmaf(dk, h[j + 2], v.z), h[j + 3] = fmaf(dk, h[j + 3], v.w);
         }
       }
-    auto put_h = [&]() {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(h[16 * k + 2 * j], h[16 * k + 2 * j + 1]);
-        tmem_st8(tmem + T_H + lanes + (n0 >> 1) + 8 * k, v);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      arrive_warp(&bar->h_ready, lane);
-    };
-    if (!STATE_ONLY) put_h();
     float seg_decay = 1.f;
+    const float Dh = a.D[head];
+    const unsigned long long D2 = pack2(Dh, Dh);
+
+    // P: row (head ph, token t), the group's 16 tokens s: in the same half of the chunk, in the one before, or none
+    const int ph = w4 >> 1, t = (w4 & 1) * 32 + lane, sh = grp4 >> 1;
+    const bool own_half = (w4 & 1) == sh, has_p = (w4 & 1) >= sh;
+    float4 gq[4];
+    const float4* gp = reinterpret_cast<const float4*>(scores + (chunk_record(first, s, c0) * a.G + 2 * pair / (a.H / a.G)) * (Q * Q)) +
+                       (tg >> 2) * Q + t;
+    auto fetch = [&]() {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) gq[j] = gp[j * Q];
+      gp += (long long)a.G * (Q * Q / 4);
+    };
+    if (!STATE_ONLY && has_p && n > 0) fetch();
+    const uint32_t p_off = (uint32_t)(OFF_P + ph * BLK + t * 128);
+    const uint32_t p_ch[2] = {(uint32_t)(((2 * grp4) ^ (t & 7)) << 4), (uint32_t)(((2 * grp4 + 1) ^ (t & 7)) << 4)};
+
     bool ok = true;
+    uint32_t cur = 0, nxt = 0, nd = OFF_D, cd = OFF_D, full_par = 0;  // stages (and decays) of chunks i and i + 1
+    unsigned long long* full = bar->full;
+    int left = len - c0 * Q;                                         // tokens from chunk i + 1 on
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const int st = i % STAGES;
-      ok = wait_bar(&bar->dt_full[st], (i / STAGES) & 1, stop) && wait_bar(&bar->s_full, i & 1, stop);
-      if (!ok) break;
-      const float f = dec[st * 2 + hd].total;
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float v[16];
-        tmem_ld16_async(tmem + T_S + lanes + n0 + 16 * k, v);
-        tmem_wait_ld16(v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) h[16 * k + j] = fmaf(f, h[16 * k + j], v[j]);
-      }
-      seg_decay *= f;
-      tc_fence_before();
-      arrive_warp(&bar->s_free, lane);
-      arrive_warp(&bar->dt_free[st], lane);
-      if (!STATE_ONLY && i + 1 < n) {
-        ok = wait_bar(&bar->y2_done, i & 1, stop);
+    for (int i = -1; i < n; ++i) {
+      // ---- h' = decay h + S of chunk i ----
+      if (i >= 0) {
+        ok = wait_bar(&bar->s_full, i & 1, stop);
         if (!ok) break;
         tc_fence_after();
-        put_h();
+        float v0[16], v1[16];
+        tmem_ld16_async(tmem + T_S + lanes + n0, v0);
+        tmem_ld16_async(tmem + T_S + lanes + n0 + 16, v1);
+        const float f = reinterpret_cast<const Decays*>(smem + cd)[hd].total;
+        const unsigned long long f2 = pack2(f, f);
+        if (STATE_ONLY) seg_decay *= f;
+        tmem_wait_ld16(v0);
+        tmem_wait_ld16(v1);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float2 u = unpack2(ffma2(f2, pack2(h[j], h[j + 1]), pack2(v0[j], v0[j + 1])));
+          const float2 z = unpack2(ffma2(f2, pack2(h[16 + j], h[17 + j]), pack2(v1[j], v1[j + 1])));
+          h[j] = u.x, h[j + 1] = u.y, h[16 + j] = z.x, h[17 + j] = z.y;
+        }
       }
+      // ---- Xw of chunk i + 1 (the MMAs that read the last one are done) ----
+      if (i + 1 < n) {
+        ok = wait_bar(full, full_par, stop);
+        if (!ok) break;
+        if (left < Q) {  // rows of B and x after the sequence's last belong to another one
+          for (int k = tid; k < (Q - left) * 32; k += 32 * WARPS) {
+            const int r = left + (k >> 5), blk = (k >> 3) & 3, ch = k & 7;
+            *reinterpret_cast<uint4*>(smem + nxt + OFF_TB + blk * BLK + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+          named_sync(B_ALL, 32 * WARPS);
+        }
+        const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[hd];
+        const unsigned long long w0 = *reinterpret_cast<const unsigned long long*>(&d.w[tg + 2 * q4]);
+        const unsigned long long w1 = *reinterpret_cast<const unsigned long long*>(&d.w[tg + 8 + 2 * q4]);
+        uint32_t chk = 0;  // sum of 0 x, in pairs: NaN once an x is not finite
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh) {  // 16 rows, 16 tokens
+          uint32_t xf[4], hi[4], mid[4], lo[4];
+          ldsm4_t(xf, sb + nxt + OFF_TX + f_off[rh]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            scale_split3(xf[j], j < 2 ? w0 : w1, hi[j], mid[j], lo[j]);
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(chk) : "r"(xf[j]), "r"(0u));
+          }
+          const uint32_t to = tmem + T_XW + lanes + ((uint32_t)(16 * rh) << 16) + (tg >> 1);
+          tmem_st_frag(to, lo);
+          tmem_st_frag(to + 32, mid);
+          tmem_st_frag(to + 64, hi);
+        }
+        if (__any_sync(0xffffffffu, chk & 0x7fff7fffu)) {  // seldom: an infinity is its own first part
+#pragma unroll 1
+          for (int rh = 0; rh < 2; ++rh) {
+            uint32_t xf[4], hi[4], mid[4], lo[4];
+            ldsm4_t(xf, sb + nxt + OFF_TX + (rh ? f_off[1] : f_off[0]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              scale_split3(xf[j], j < 2 ? w0 : w1, hi[j], mid[j], lo[j]);
+              if ((hi[j] & 0x7f80u) == 0x7f80u) mid[j] &= 0xffff0000u, lo[j] &= 0xffff0000u;
+              if ((hi[j] & 0x7f800000u) == 0x7f800000u) mid[j] &= 0xffffu, lo[j] &= 0xffffu;
+            }
+            const uint32_t to = tmem + T_XW + lanes + ((uint32_t)(16 * rh) << 16) + (tg >> 1);
+            tmem_st_frag(to, lo);
+            tmem_st_frag(to + 32, mid);
+            tmem_st_frag(to + 64, hi);
+          }
+          // such values leave the tile (each thread its row's): the product with a zero of P would spread them
+          uint32_t odd = 0;
+#pragma unroll 1
+          for (int u = 0; u < 16; ++u) {
+            uint16_t* v = x_at(smem + nxt, tg + u);
+            if ((*v & 0x7f80u) == 0x7f80u) odd |= 1u << u, *v = 0;
+          }
+          fence_async_smem();
+          odd_tokens[(((i + 1) & 1) * 4 + grp4) * 128] = odd | (uint32_t)(i + 1) << 16;
+          bar->odd_chunk[(i + 1) & 1] = i + 1;
+        }
+        // the store of the chunk before this one's y has read its buffer
+        if (!STATE_ONLY && w4 == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+        tmem_wait_st();
+        tc_fence_before();
+        hand_over(B_XW);
+      }
+      // ---- y of chunk i ----
+      if (!STATE_ONLY && i >= 0) {
+        const Decays& d = reinterpret_cast<const Decays*>(smem + cd)[hd];
+        const uint32_t yb = OFF_Y + (uint32_t)(i & 1) * 2 * BLK;
+        const unsigned long long e0 = *reinterpret_cast<const unsigned long long*>(&d.e[tg + 2 * q4]);
+        const unsigned long long e1 = *reinterpret_cast<const unsigned long long*>(&d.e[tg + 8 + 2 * q4]);
+        uint32_t xf[2][4];
+        ldsm4_t(xf[0], sb + cur + OFF_TX + f_off[0]);
+        ldsm4_t(xf[1], sb + cur + OFF_TX + f_off[1]);
+        ok = wait_bar(&bar->y_full, i & 1, stop);
+        if (!ok) break;
+        tc_fence_after();
+        float y1[2][8], y2[2][8];
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh) {  // 16 rows, 16 tokens
+          const uint32_t from = tmem + lanes + ((uint32_t)(16 * rh) << 16) + tg;
+          tmem_ld_frag_async(from + T_Y1 + hd * 64, y1[rh]);
+          tmem_ld_frag_async(from + T_Y2, y2[rh]);
+        }
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh) {
+          uint32_t o[4];
+          tmem_wait_ld8(y1[rh], y2[rh]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = unpack2(ffma2(D2, pack2(bf16_lo(xf[rh][j]), bf16_hi(xf[rh][j])),
+                                           ffma2(j < 2 ? e0 : e1, pack2(y2[rh][2 * j], y2[rh][2 * j + 1]),
+                                                 pack2(y1[rh][2 * j], y1[rh][2 * j + 1]))));
+            o[j] = pack_bf16x2(y.x, y.y);
+          }
+          stsm4_t(sb + yb + f_off[rh], o);
+        }
+        if (bar->odd_chunk[i & 1] == i) {  // what those values add is not finite, so it can be added to the rounded y
+          __syncwarp();
+          const int c = c0 + i;
+          unsigned long long odd = 0;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t v = odd_tokens[((i & 1) * 4 + k) * 128];
+            if (v >> 16 == (uint32_t)(i & 0xffff)) odd |= (unsigned long long)(v & 0xffffu) << (16 * k);
+          }
+          const unsigned char* pt = smem + OFF_P + ((i & 1) * 2 + hd) * BLK;
+#pragma unroll 1
+          for (int u = 0; u < tg + 16; ++u) {
+            if (!(odd >> u & 1)) continue;
+            const float xv = bf16f(a.x[(long long)(first + c * Q + u) * a.ldx + head * kP + p]);
+#pragma unroll 1
+            for (int r = max(u, tg); r < tg + 16; ++r) {
+              uint16_t* y = reinterpret_cast<uint16_t*>(smem + yb + hd * BLK + tile_off(r, p >> 3, 128) + (p & 7) * 2);
+              const uint16_t w = *reinterpret_cast<const uint16_t*>(pt + r * 128 + (((u >> 3) ^ (r & 7)) << 4) + (u & 7) * 2);
+              float v = fmaf(bf16f(w), xv, bf16f(*y));
+              if (r == u) v = fmaf(Dh, xv, v);
+              *y = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
+            }
+          }
+        }
+        tc_fence_before();
+        fence_async_smem();
+        named_sync(1 + grp4, 128);  // the group's 16 rows of y are in shared memory
+        const int valid = left + Q - tg;  // of the group's tokens
+        if (valid >= 16) {
+          if (w4 == 0 && lane == 0) {
+            tma_store_2d(&ty, sb + yb + tg * 128, 2 * pair * kP, first + (c0 + i) * Q + tg);
+            tma_store_2d(&ty, sb + yb + BLK + tg * 128, 2 * pair * kP + 64, first + (c0 + i) * Q + tg);
+            asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+          }
+        } else {  // the rows after the last are another sequence's
+          uint16_t* yo = a.y + (long long)(first + (c0 + i) * Q) * a.ldy + pair * 2 * kP;
+#pragma unroll 1
+          for (int k = tid & 127; k < valid * 16; k += 128) {
+            const int r = tg + (k >> 4), ch = k & 15;
+            *reinterpret_cast<uint4*>(yo + (long long)r * a.ldy + ch * 8) =
+                *reinterpret_cast<const uint4*>(smem + yb + (ch >> 3) * BLK + tile_off(r, ch & 7, 128));
+          }
+        }
+      }
+      if (i + 1 >= n) break;
+      if (!STATE_ONLY) {
+        // ---- the state for the next chunk's y, rounded to bf16 (y2 of this chunk, which read the last, is done) ----
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(h[16 * k + 2 * j], h[16 * k + 2 * j + 1]);
+          tmem_st8(tmem + T_H + lanes + (n0 >> 1) + 8 * k, v);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        hand_over(B_H);
+        // ---- P of chunk i + 1 ----
+        if (has_p) {
+          const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[ph];
+          unsigned char* pr = smem + p_off + ((i + 1) & 1) * 2 * BLK;
+          const float St = d.S[t];
+#pragma unroll
+          for (int j8 = 0; j8 < 2; ++j8) {
+            uint32_t v[4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const float4 g = gq[2 * j8 + m];
+              const int u = tg + 8 * j8 + 4 * m;
+              float w[4];
+              if (own_half) {  // 2^(S_t - S_u) D_u
+                const float4 S = *reinterpret_cast<const float4*>(&d.S[u]), D = *reinterpret_cast<const float4*>(&d.D[u]);
+                w[0] = u <= t ? g.x * (exp2_sfu(St - S.x) * D.x) : 0.f;
+                w[1] = u + 1 <= t ? g.y * (exp2_sfu(St - S.y) * D.y) : 0.f;
+                w[2] = u + 2 <= t ? g.z * (exp2_sfu(St - S.z) * D.z) : 0.f;
+                w[3] = u + 3 <= t ? g.w * (exp2_sfu(St - S.w) * D.w) : 0.f;
+              } else {  // to the end of the first half, and from there
+                const float4 f = *reinterpret_cast<const float4*>(&d.E1[u]);
+                const float E2 = exp2_sfu(St);
+                w[0] = g.x * (f.x * E2), w[1] = g.y * (f.y * E2), w[2] = g.z * (f.z * E2), w[3] = g.w * (f.w * E2);
+              }
+              v[2 * m] = pack_bf16x2(w[0], w[1]), v[2 * m + 1] = pack_bf16x2(w[2], w[3]);
+            }
+            *reinterpret_cast<uint4*>(pr + p_ch[j8]) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          fence_async_smem();
+        }
+        hand_over(B_P);
+        if (has_p && i + 2 < n) fetch();
+      }
+      cur = nxt, cd = nd, left -= Q;
+      nxt += ST_BYTES, nd += 2 * REC, ++full;
+      if (nxt == STAGES * ST_BYTES) nxt = 0, nd = OFF_D, full = bar->full, full_par ^= 1;
+    }
+    if (!STATE_ONLY && w4 == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+    if (!ok) {  // a warp that gives up still takes part in the barriers that others may be waiting at
+      asm volatile("bar.arrive %0, %1;\n" ::"r"(1 + grp4), "n"(128) : "memory");
+      asm volatile("bar.arrive %0, %1;\n" ::"n"(B_ALL), "n"(32 * WARPS) : "memory");
+      hand_over(B_XW);
+      hand_over(B_H);
+      hand_over(B_P);
     }
     if (ok && (STATE_ONLY || c1 == nch)) {
       float* out = STATE_ONLY ? ws + seg * wrec + p * kN + n0 : a.h_out + at;
 #pragma unroll
-      for (int j = 0; j < 64; j += 4) *reinterpret_cast<float4*>(out + j) = make_float4(h[j], h[j + 1], h[j + 2], h[j + 3]);
+      for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(out + j) = make_float4(h[j], h[j + 1], h[j + 2], h[j + 3]);
       if (STATE_ONLY && p == 0 && n0 == 0) ws[seg * wrec + kP * kN] = seg_decay;
     }
-  } else {
-    if (!STATE_ONLY) regs_dec<56>();
-  if (warp == 20) {
+  } else if (warp == WARPS + 1) {
     // ---- copies ----
     int issued = 0;
 #pragma unroll 1
@@ -601,9 +606,10 @@ __global__ void __launch_bounds__(NT, 1)
       if (lane == 0) {
         const uint32_t f = smem_u32(&bar->full[st]), d = sb + st * ST_BYTES;
         const int t = first + (c0 + i) * Q, bn = 2 * pair / (a.H / a.G) * kN;
-        mbar_arrive_expect_tx(f, STATE_ONLY ? 4 * BLK : 6 * BLK);
+        mbar_arrive_expect_tx(f, (STATE_ONLY ? 4 * BLK : 6 * BLK) + 2 * REC);
         tma_load_2d(d + OFF_TX, &tx, 2 * pair * kP, t, f);
         tma_load_2d(d + OFF_TX + BLK, &tx, 2 * pair * kP + 64, t, f);
+        bulk_load(sb + OFF_D + st * 2 * REC, decays + chunk_record(first, s, c0 + i) * a.H + 2 * pair, 2 * REC, f);
         tma_load_2d(d + OFF_TB, &tb, bn, t, f);
         tma_load_2d(d + OFF_TB + BLK, &tb, bn + 64, t, f);
         if (!STATE_ONLY) {
@@ -617,116 +623,72 @@ __global__ void __launch_bounds__(NT, 1)
       for (int i = max(0, issued - STAGES); i < issued; ++i)
         mbar_poll_ns(smem_u32(&bar->full[i % STAGES]), (i / STAGES) & 1, kWaitLimitNs);
     }
-  } else if (warp == 21) {
+  } else {
     // ---- MMAs ----
     constexpr uint32_t id_s = idesc_major(128, 128, false, true), id_y2 = idesc_major(128, 64, false, false),
                        id_y1 = idesc_major(128, 64, true, false);
     const bool leader = elect_one();
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    bool ok = true;
+    uint32_t tile = sb, pd = desc_lo(sb + OFF_P, 16);
+    unsigned long long *fr = bar->free_, *last = nullptr;  // stages of this chunk and the one before
 #pragma unroll 1
-    for (int i = 0; i < n && ok; ++i) {
-      const int st = i % STAGES;
-      const uint32_t tile = sb + st * ST_BYTES;
-      ok = wait_bar(&bar->full[st], (i / STAGES) & 1, stop) && (i == 0 || wait_bar(&bar->s_free, (i - 1) & 1, stop));
-#pragma unroll 1
-      for (int half = 0; half < 2 && ok; ++half) {
-        ok = wait_bar(&bar->xw_full[half], i & 1, stop);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint32_t bd = desc_lo(tile + OFF_TB + half * 4096, BLK), xw = tm + T_XW + half * 16;
+    for (int i = 0; i < n; ++i) {
+      named_sync(B_XW, HANDED);  // Xw of this chunk; S of the last has been read
+      if (*stop) break;
+      tc_fence_after();
+      if (leader) {
+        if (STATE_ONLY && i > 0) mbar_arrive(smem_u32(last));
+        const uint32_t bd = desc_lo(tile + OFF_TB, BLK);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)  // 16 tokens: two groups of 8 rows
+        for (int k = 0; k < 4; ++k)  // 16 tokens: two groups of 8 rows
 #pragma unroll
-            for (int part = 0; part < 3; ++part)
-              mma_ts<id_s>(tm + T_S, xw + part * 32 + k * 8, bd + k * (2048 >> 4), k + part > 0 || half > 0);
-          mma_commit(smem_u32(half ? &bar->s_full : &bar->xw_free));
-        }
-        __syncwarp();
+          for (int part = 0; part < 3; ++part)
+            mma_ts<id_s>(tmem + T_S, tmem + T_XW + part * 32 + k * 8, bd + k * (2048 >> 4), k + part > 0);
+        mma_commit(smem_u32(&bar->s_full));
       }
+      __syncwarp();
       if (!STATE_ONLY) {
-        ok = ok && wait_bar(&bar->h_ready, i & 1, stop) && (i == 0 || wait_bar(&bar->y_free, (i - 1) & 1, stop));
-        if (!ok) break;
+        named_sync(B_H, HANDED);  // h; y of the last chunk has been read
+        if (*stop) break;
         tc_fence_after();
         if (leader) {
+          if (i > 0) mbar_arrive(smem_u32(last));
           const uint32_t cd = desc_lo(tile, 16);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ts<id_y2>(tm + T_Y2, tm + T_H + k * 8, cd + ((k >> 2) * (BLK >> 4) + (k & 3) * 2), k != 0);
-          mma_commit(smem_u32(&bar->y2_done));
+            mma_ts<id_y2>(tmem + T_Y2, tmem + T_H + k * 8, cd + ((k >> 2) * (BLK >> 4) + (k & 3) * 2), k != 0);
         }
         __syncwarp();
-        ok = wait_bar(&bar->p_full[i & 1], (i / 2) & 1, stop);
-        if (!ok) break;
+        named_sync(B_P, HANDED);
+        if (*stop) break;
         tc_fence_after();
         if (leader) {
-          const uint32_t xd = desc_lo(tile + OFF_TX, BLK), pd = desc_lo(sb + OFF_P + (i & 1) * 2 * BLK, 16);
+          const uint32_t xd = desc_lo(tile + OFF_TX, BLK);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ss<id_y1>(tm + T_Y1 + e * 64, xd + k * (2048 >> 4), pd + e * (BLK >> 4) + k * 2, k != 0);
+              mma_ss<id_y1>(tmem + T_Y1 + e * 64, xd + k * (2048 >> 4), pd + e * (BLK >> 4) + k * 2, k != 0);
           mma_commit(smem_u32(&bar->y_full));
         }
         __syncwarp();
       }
-      if (ok && leader) mma_commit(smem_u32(&bar->free_[st]));
+      if (leader) mma_commit(smem_u32(fr));
       __syncwarp();
+      last = fr;
+      pd ^= desc_lo(sb + OFF_P, 16) ^ desc_lo(sb + OFF_P + 2 * BLK, 16);
+      tile += ST_BYTES, ++fr;
+      if (fr == bar->free_ + STAGES) fr = bar->free_, tile = sb;
     }
     if (leader) {
       mma_commit(smem_u32(&bar->drain));
       mbar_poll_ns(smem_u32(&bar->drain), 0, kWaitLimitNs);
     }
     __syncwarp();
-  } else {
-    // ---- the decays of one head: tokens 2 lane, 2 lane + 1 ----
-    const int dh = warp - 22, hh = 2 * pair + dh;
-    const float A2 = neg_exp(a.A_log[hh]) * kLog2e, bias = a.dt_bias[hh];
-    auto fetch = [&](int i, uint32_t& v0, uint32_t& v1) {
-      const int t = (c0 + i) * Q + 2 * lane;
-      const uint16_t* q = a.dt + (long long)(first + t) * a.lddt + hh;
-      v0 = t < len ? q[0] : 0u, v1 = t + 1 < len ? q[a.lddt] : 0u;
-    };
-    uint32_t r0 = 0, r1 = 0;
-    if (n > 0) fetch(0, r0, r1);
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const int st = i % STAGES, t = (c0 + i) * Q + 2 * lane;
-      if (i >= STAGES && !wait_bar(&bar->dt_free[st], (i / STAGES - 1) & 1, stop)) break;
-      const float d0 = t < len ? softplus_f(bf16f((uint16_t)r0) + bias) : 0.f;
-      const float d1 = t + 1 < len ? softplus_f(bf16f((uint16_t)r1) + bias) : 0.f;
-      if (i + 1 < n) fetch(i + 1, r0, r1);
-      const float e0 = fmaxf(d0 * A2, kLeast2), e1 = fmaxf(d1 * A2, kLeast2);
-      float pre = e0 + e1, suf = pre;  // sums within the lane's half of the chunk
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, pre, o, 16), v = __shfl_down_sync(0xffffffffu, suf, o, 16);
-        if ((lane & 15) >= o) pre += u;
-        if ((lane & 15) + o < 16) suf += v;
-      }
-      const float sum0 = __shfl_sync(0xffffffffu, pre, 15), sum1 = __shfl_sync(0xffffffffu, pre, 31);
-      float before = __shfl_up_sync(0xffffffffu, pre, 1, 16), after = __shfl_down_sync(0xffffffffu, suf, 1, 16);
-      if ((lane & 15) == 0) before = 0.f;
-      if ((lane & 15) == 15) after = 0.f;
-      const bool low = lane < 16;
-      Decays& d = dec[st * 2 + dh];
-      const float base = low ? 0.f : sum0, rest = low ? sum1 : 0.f, S0 = before + e0;
-      *reinterpret_cast<float2*>(&d.S[2 * lane]) = make_float2(S0, pre);
-      *reinterpret_cast<float2*>(&d.D[2 * lane]) = make_float2(d0, d1);
-      const float a0 = after + e1;  // after token 2 lane, in its half
-      if (low) *reinterpret_cast<float2*>(&d.E1[2 * lane]) = make_float2(exp2_sfu(a0) * d0, exp2_sfu(after) * d1);
-      *reinterpret_cast<float2*>(&d.w[2 * lane]) = make_float2(exp2_sfu(a0 + rest) * d0, exp2_sfu(after + rest) * d1);
-      *reinterpret_cast<float2*>(&d.e[2 * lane]) = make_float2(exp2_sfu(base + S0), exp2_sfu(base + pre));
-      if (lane == 0) d.total = exp2_sfu(sum0 + sum1);
-      arrive_warp(&bar->dt_full[st], lane);
-    }
-  }
   }
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *stop) flag(a.q.status, SSM_STATUS_TIMEOUT);
-  if (warp == 21) {
+  if (warp == WARPS) {
     __syncwarp();
     tc_fence_after();
     tmem_free_warp(tmem, 512);
@@ -744,12 +706,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   }
   return fn;
 }
-bool encode(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld) {
+bool encode(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows = Q) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t gstride[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, Q};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   const cuuint32_t estride[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gdim, gstride, box, estride,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -766,36 +728,16 @@ int plan_segments_tc(int H, int n_seq, int max_len) {
   return nseg < 2 ? 1 : nseg;
 }
 
-size_t score_bytes(int n_seq, int n_tok, int G) { return ((size_t)(n_tok / Q) + n_seq + 1) * G * Q * Q * sizeof(float); }
+// workspace: scores, decays, then what segments add to the state; chunks of all sequences at most n_tok / Q + n_seq
+size_t chunk_count(int n_seq, int n_tok) { return (size_t)(n_tok / Q) + n_seq + 1; }
+size_t score_bytes(int n_seq, int n_tok, int G) { return chunk_count(n_seq, n_tok) * G * Q * Q * sizeof(float); }
+size_t decay_bytes(int n_seq, int n_tok, int H) { return chunk_count(n_seq, n_tok) * H * REC; }
 
-}  // namespace
-
-bool prompt_scan_tc_fits(int H, int G, int n_seq, int max_len) { return (H / G) % 2 == 0 && max_len > 64; }
-
-size_t prompt_scan_tc_workspace_bytes(int H, int G, int n_seq, int n_tok, int max_len) {
-  const int nseg = plan_segments_tc(H, n_seq, max_len);
-  return 256 + score_bytes(n_seq, n_tok, G) + (size_t)n_seq * H * (nseg - 1) * (kP * kN + 32) * sizeof(float);
-}
-
-cudaError_t launch_prompt_scan_tc(const ScanArgs& args, void* workspace, cudaStream_t s) {
-  ScanArgs a = args;
-  a.nseg = plan_segments_tc(a.H, a.q.n_seq, a.q.max_len);
-  float* scores = static_cast<float*>(workspace);
-  a.seg_state = scores + score_bytes(a.q.n_seq, a.q.n_tok, a.G) / sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(scan_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM);
-  if (e != cudaSuccess) return e;
-  CUtensorMap tx, tb, tcm;
-  if (!encode(&tx, a.x, a.q.n_tok, (long long)a.H * kP, a.ldx) || !encode(&tb, a.B, a.q.n_tok, (long long)a.G * kN, a.ldb) ||
-      !encode(&tcm, a.C, a.q.n_tok, (long long)a.G * kN, a.ldc))
-    return cudaErrorInvalidValue;
-  if (a.nseg > 1)
-    scan_tc_kernel<true><<<dim3((unsigned)(a.H / 2), (unsigned)(a.q.n_seq * (a.nseg - 1))), NT, TC_SMEM, s>>>(tx, tb, tcm, a, scores);
-  scores_kernel<<<dim3((unsigned)((a.q.max_len + Q - 1) / Q), (unsigned)a.q.n_seq, (unsigned)a.G), 128, 0, s>>>(a, scores);
-  // the walk starts while the scores are made; its P warps wait for them
+// the second grid of a pair, whose blocks start while the first one's end
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.H / 2), (unsigned)(a.q.n_seq * a.nseg));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = TC_SMEM;
   cfg.stream = s;
@@ -804,7 +746,45 @@ cudaError_t launch_prompt_scan_tc(const ScanArgs& args, void* workspace, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, scan_tc_kernel<false>, tx, tb, tcm, a, (const float*)scores);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+bool prompt_scan_tc_fits(int H, int G, int n_seq, int max_len) { return (H / G) % 2 == 0 && max_len > 64; }
+
+size_t prompt_scan_tc_workspace_bytes(int H, int G, int n_seq, int n_tok, int max_len) {
+  const int nseg = plan_segments_tc(H, n_seq, max_len);
+  return 256 + score_bytes(n_seq, n_tok, G) + decay_bytes(n_seq, n_tok, H) +
+         (size_t)n_seq * H * (nseg - 1) * (kP * kN + 32) * sizeof(float);
+}
+
+cudaError_t launch_prompt_scan_tc(const ScanArgs& args, void* workspace, cudaStream_t s) {
+  ScanArgs a = args;
+  a.nseg = plan_segments_tc(a.H, a.q.n_seq, a.q.max_len);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  float* scores = reinterpret_cast<float*>(ws);
+  ws += score_bytes(a.q.n_seq, a.q.n_tok, a.G);
+  Decays* decays = reinterpret_cast<Decays*>(ws);
+  ws += decay_bytes(a.q.n_seq, a.q.n_tok, a.H);
+  a.seg_state = reinterpret_cast<float*>(ws);
+  cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(scan_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tx, tb, tcm, ty;
+  if (!encode(&tx, a.x, a.q.n_tok, (long long)a.H * kP, a.ldx) || !encode(&tb, a.B, a.q.n_tok, (long long)a.G * kN, a.ldb) ||
+      !encode(&tcm, a.C, a.q.n_tok, (long long)a.G * kN, a.ldc) || !encode(&ty, a.y, a.q.n_tok, (long long)a.H * kP, a.ldy, 16))
+    return cudaErrorInvalidValue;
+  prep_kernel<<<dim3((unsigned)((a.q.max_len + Q - 1) / Q), (unsigned)a.q.n_seq, (unsigned)(a.G + (a.H + 3) / 4)), 128, 0, s>>>(
+      a, scores, decays);
+  const dim3 grid((unsigned)(a.H / 2), (unsigned)(a.q.n_seq * a.nseg));
+  if (a.nseg > 1) {
+    e = launch_dependent(scan_tc_kernel<true>, dim3(grid.x, (unsigned)(a.q.n_seq * (a.nseg - 1))), s, tx, tb, tcm, ty, a,
+                         (const float*)scores, (const Decays*)decays);
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_dependent(scan_tc_kernel<false>, grid, s, tx, tb, tcm, ty, a, (const float*)scores, (const Decays*)decays);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
