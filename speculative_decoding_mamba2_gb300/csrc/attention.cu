@@ -1,347 +1,435 @@
 // Attention of a draft tree's nodes over a paged cache and their ancestors, and the commit of the accepted
 // path into the cache (ssm_attention.h).
 //
-// attend_kernel.  The query rows of one key/value head -- n nodes x g query heads -- share its keys, so a CTA
-// takes up to RT of them and walks tiles of 64 keys once, with the running maximum and sum of each row's
-// softmax: s = q.k, m' = max(m, s), p = 2^(s - m'), l' = l 2^(m - m') + sum p, o' = o 2^(m - m') + p v.
-// One tile more than the cache has holds the tree's own rows; there a row keeps its node's ancestors only,
-// read from a 64-bit word per node.  Few rows share a tile (n g operations for each byte of the cache), so the
-// keys are split over the SMs where the (sequence, head, row tile) triples leave SMs idle; the partial sums
-// are then joined by combine_kernel.
-#include "mma_tiles.cuh"
+// attend_kernel.  The query rows of one key/value head -- n nodes x g query heads -- share its keys, so a CTA takes up to
+// 128 of them (the rows of tensor memory) and walks tiles of 64 keys once, on tcgen05:
+//     S [128 x 64] = Q . K^T,   P = 2^(S - m),   O [128 x D] += P . V        (P, O in tensor memory, V read MN-major)
+// with the running maximum m and sum of each row's softmax in the row's thread.  O is rescaled only when a maximum has
+// grown by more than 2^8 (P then stays below 2^8, and its rounding to bf16 is relative).  S of the next tile is made while
+// the softmax of this one runs, and two CTAs to an SM overlap the rest; K and V tiles come by TMA from their pages.
+// Where there are at most 64 (32) rows they stand in tensor memory twice (four times), each copy for its half (quarter)
+// of a tile's keys, so that all 128 threads have exponentials to do; the copies' sums are joined at the end.
+// One tile more than the cache has holds the tree's own rows; there a row keeps its node's ancestors only, read from a
+// 64-bit word per node.  Few rows share a tile (n g operations for each byte of the cache), so the keys are split over the
+// SMs where the (sequence, head, row tile) triples leave SMs idle; the partial sums are then joined by combine_kernel.
+// Rows of V that no key of the tile owns, and values of V in tree rows that are not finite, are zeroed in shared memory
+// (a weight of 0 would spread them); the latter are added to the rows that see them at the end.
 #include "prompt.cuh"
+#include "umma.cuh"
 
 namespace ssmtree {
 namespace {
 
-constexpr int KT = 64;  // keys per tile
-constexpr int ATHREADS = 128;
+constexpr int KT = 64;          // keys per tile
+constexpr int ATHREADS = 192;   // 4 softmax warps, one for copies, one for MMAs
+constexpr int STAGES = 2;
+constexpr int BLK = KT * 128;   // 64 rows x 64 columns of bf16
 
-// WM warps along the rows, MT m16 tiles each; 4 / WM warps along the keys of a tile
-template <int D, int WM, int MT>
-struct AttendShape {
-  static constexpr int RT = WM * MT * 16, WN = 4 / WM;
-  static constexpr int STAGES = 2;
-  static constexpr int OFF_KV = RT * D * 2;                      // after q
-  static constexpr int KV = KT * D * 2;
-  static constexpr int OFF_ANC = OFF_KV + STAGES * 2 * KV;       // 64 ancestor words, 64 links
-  static constexpr int SMEM = OFF_ANC + 64 * 8 + 64 * 4 + 16;
+constexpr int A_S = 0, A_P = 64, A_O = 128, A_COLS = 256;  // tensor memory columns: S, P (two buffers of 32), O
+
+template <int D>
+struct AttendSmem {
+  static constexpr int OFF_KV = (D / 64) * 2 * BLK;          // after Q: D / 64 blocks of 128 rows
+  static constexpr int TILE = (D / 64) * BLK;                // K or V of a tile
+  static constexpr int OFF_MISC = OFF_KV + STAGES * 2 * TILE;
+  static constexpr int BYTES = OFF_MISC + 64 * 8 + 128 * 8 + 256 + 1024 /* alignment */;
 };
+struct AttendMisc {
+  unsigned long long anc[64];  // ancestors and self of each node
+  float2 ml[128];
+  unsigned long long k_full[STAGES], v_full[STAGES], k_free[STAGES], v_free[STAGES], q_full, s_full, s_free, p_full[2], o_done, drain;
+  unsigned int odd[2];         // tree rows with a value of v that is not finite
+  uint32_t tmem;
+  int stop;
+  int no_page[4];              // whether a page of tile i (at i % 4) is out of range
+};
+static_assert(sizeof(AttendMisc) <= 64 * 8 + 128 * 8 + 256, "space");
 
-template <int D, int WM, int MT>
-__global__ void __launch_bounds__(ATHREADS, 2) attend_kernel(AttendArgs a) {
-  using Sh = AttendShape<D, WM, MT>;
-  constexpr int RT = Sh::RT, WN = Sh::WN, ROWB = D * 2, CH = D / 8;
-  constexpr int KW = KT / WN, NT = KW / 8, DT = D / 8;  // keys, score and output n-tiles of a warp
-  extern __shared__ __align__(128) unsigned char smem[];
-  unsigned long long* anc = reinterpret_cast<unsigned long long*>(smem + Sh::OFF_ANC);
-  volatile int* link = reinterpret_cast<volatile int*>(smem + Sh::OFF_ANC + 64 * 8);
-  volatile int* no_page = link + 64;  // whether a row's page is out of range
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, q4 = lane & 3;
-  const int wm = warp % WM, wn = warp / WM;
-  const int rows = a.n * a.g, rt = (rows + RT - 1) / RT;
-  const int sp = blockIdx.x, kvh = blockIdx.y, s = blockIdx.z / rt, r0 = (blockIdx.z % rt) * RT;
-  int len = a.cache_len[s];
+__device__ __forceinline__ float max3f(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+template <int D, int DUP>
+__global__ void __launch_bounds__(ATHREADS, 2)
+    attend_kernel(const __grid_constant__ CUtensorMap tkp, const __grid_constant__ CUtensorMap tvp,
+                  const __grid_constant__ CUtensorMap tkt, const __grid_constant__ CUtensorMap tvt, AttendArgs a) {
+  using Sh = AttendSmem<D>;
+  constexpr int RG = 128 / DUP, KK = KT / DUP, DB = D / 64;  // rows of a copy, its keys of a tile, 64-column blocks
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  AttendMisc* ms = reinterpret_cast<AttendMisc*>(smem + Sh::OFF_MISC);
+  volatile int* stop = &ms->stop;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int rows = a.n * a.g, rt = (rows + 127) / 128;
+  const int r0 = (blockIdx.x % rt) * 128, sp = blockIdx.x / rt, kvh = blockIdx.y, s = blockIdx.z;
+  launch_dependents();
+  int len = __shfl_sync(0xffffffffu, a.cache_len[s], 0);
   if (len < 0 || len > a.max_len || (long long)len > ((long long)a.max_pages << a.page_shift)) {
     if (sp == 0 && kvh == 0 && r0 == 0 && tid == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
     len = 0;
   }
-  const int ct = (len + KT - 1) / KT, nt = ct + 1;  // tiles: the cache's, then the tree's
-  const int i0 = sp * a.tps, i1 = min(nt, i0 + a.tps);
-  if (i0 >= i1) return;
-  const uint32_t sb = smem_u32(smem);
-  const int32_t* table = a.table + (long long)s * a.max_pages;
-  const int pmask = (1 << a.page_shift) - 1;
+  const int ct = (len + KT - 1) / KT;  // tiles of the cache; one more is the tree's
+  const int i0 = sp * a.tps, n = min(ct + 1, i0 + a.tps) - i0;
+  if (n <= 0) return;
+  const bool has_tree = i0 + n == ct + 1;
 
-  if (tid == 0) *no_page = 0;
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&ms->k_full[i]), 1);
+      mbar_init(smem_u32(&ms->v_full[i]), 1);
+      mbar_init(smem_u32(&ms->k_free[i]), 1);
+      mbar_init(smem_u32(&ms->v_free[i]), 1);
+    }
+    mbar_init(smem_u32(&ms->q_full), 4);
+    mbar_init(smem_u32(&ms->s_full), 1);
+    mbar_init(smem_u32(&ms->s_free), 4);
+    mbar_init(smem_u32(&ms->p_full[0]), 4);  // two: a warp may be done with a tile before another is with the last one
+    mbar_init(smem_u32(&ms->p_full[1]), 4);
+    mbar_init(smem_u32(&ms->o_done), 1);
+    mbar_init(smem_u32(&ms->drain), 1);
+    ms->stop = 0;
+    ms->odd[0] = ms->odd[1] = 0;
+    fence_barrier_init();
+  }
+  if (warp == 5) tmem_alloc_warp(smem_u32(&ms->tmem), A_COLS);
+  tc_fence_before();
   __syncthreads();
-  // q rows (zero beyond the last)
-  for (int i = tid; i < RT * CH; i += ATHREADS) {
-    const int r = i / CH, ch = i % CH, row = r0 + r;
-    const bool there = row < rows;
-    const int node = there ? row / a.g : 0, j = there ? row % a.g : 0;
-    cp_async16_or_zero(sb + tile_off(r, ch, ROWB),
-                       a.q + ((long long)s * a.n + node) * a.ldq + (kvh * a.g + j) * D + ch * 8, there);
-  }
-  auto load = [&](int i) {
-    const uint32_t st = sb + Sh::OFF_KV + (i & 1) * 2 * Sh::KV;
-#pragma unroll 4
-    for (int u = tid; u < KT * CH; u += ATHREADS) {
-      const int r = u / CH, ch = u % CH;
-      const uint16_t *kr = a.kp, *vr = a.vp;
-      bool there;
-      if (i < ct) {
-        const int at = i * KT + r;
-        there = at < len;
-        const int pg = there ? table[at >> a.page_shift] : 0;
-        if (pg < 0 || pg >= a.n_pages) {
-          flag(a.status, SSM_STATUS_SEQ_RANGE);
-          *no_page = 1;
-          there = false;
-        }
-        if (there) {
-          const long long off = ((((long long)pg * a.Hkv + kvh) << a.page_shift) + (at & pmask)) * D + ch * 8;
-          kr += off, vr += off;
-        }
-      } else {
-        there = r < a.n;
-        const long long row = (long long)s * a.n + (there ? r : 0);
-        kr = a.k + row * a.ldk + kvh * D + ch * 8;
-        vr = a.v + row * a.ldv + kvh * D + ch * 8;
-      }
-      cp_async16_or_zero(st + tile_off(r, ch, ROWB), kr, there);
-      cp_async16_or_zero(st + Sh::KV + tile_off(r, ch, ROWB), vr, there);
-    }
-    cp_async_commit();
-  };
-  load(i0);
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ms->tmem, 0);
 
-  // ancestor words: a node's own bit, then its parent's word, its grandparent's, ... by doubling
-  if (i1 == nt && warp == 0) {
-    unsigned long long w[2];
-    int p[2];
-    bool bad = false;
+  if (warp < 4) {
+    const int r = tid % RG, dg = tid / RG, row = r0 + r;  // this thread's row, and which copy of it
+    const int node = row < rows ? row / a.g : 0, qh = row < rows ? row % a.g : 0;
+    {  // q (zero beyond the last row)
+      const uint4* q = reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + node) * a.ldq + (kvh * a.g + qh) * D);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int v = lane + 32 * k;
-      p[k] = -1;
-      if (v > 0 && v < a.n) {
-        p[k] = a.layout[(long long)s * a.n + v].parent;
-        if (p[k] < 0 || p[k] >= v) p[k] = -1, bad = true;
-      }
-      w[k] = 1ull << v;
-      anc[v] = w[k], link[v] = p[k];
-    }
-    if (bad && kvh == 0 && r0 == 0) flag(a.status, SSM_STATUS_BAD_LAYOUT);
-    for (int step = 0; step < 6; ++step) {
+      for (int c = 0; c < D / 8; ++c)
+        *reinterpret_cast<uint4*>(smem + (c >> 3) * 2 * BLK + tile_off(tid, c & 7, 128)) = row < rows ? q[c] : make_uint4(0, 0, 0, 0);
+      fence_async_smem();
       __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
+    }
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    if (DUP > 1) {  // the other copies' keys have weight 0
+      const uint32_t z[8] = {};
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (p[k] >= 0) w[k] |= reinterpret_cast<volatile unsigned long long*>(anc)[p[k]], p[k] = link[p[k]];
+      for (int c = 0; c < 64; c += 8) tmem_st8(tmem + A_P + lanes + c, z);
+      tmem_wait_st();
+    }
+    // ancestor words: a node's own bit, then its parent's word, its grandparent's, ... by doubling
+    if (has_tree && warp == 0) {
+      volatile int* link = reinterpret_cast<volatile int*>(ms->ml);
+      volatile unsigned long long* anc = ms->anc;
+      unsigned long long w[2];
+      int p[2];
+      bool bad = false;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int v = lane + 32 * k;
+        p[k] = -1;
+        if (v > 0 && v < a.n) {
+          p[k] = a.layout[(long long)s * a.n + v].parent;
+          if (p[k] < 0 || p[k] >= v) p[k] = -1, bad = true;
+        }
+        w[k] = 1ull << v;
+        anc[v] = w[k], link[v] = p[k];
+      }
+      if (bad && kvh == 0 && r0 == 0) flag(a.status, SSM_STATUS_BAD_LAYOUT);
+#pragma unroll 1
+      for (int step = 0; step < 6; ++step) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (p[k] >= 0) w[k] |= anc[p[k]], p[k] = link[p[k]];
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) anc[lane + 32 * k] = w[k], link[lane + 32 * k] = p[k];
+      }
+    }
+
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int ti = i0 + i;
+      const bool tree = ti == ct;
+      const int left = tree ? a.n : len - ti * KT;
+      ok = wait_bar(&ms->s_full, i & 1, stop);
+      if (!ok) break;
+      tc_fence_after();
+      float sv[KK];
+#pragma unroll
+      for (int c = 0; c < KK; c += 16) tmem_ld16_async(tmem + A_S + lanes + dg * KK + c, reinterpret_cast<float(&)[16]>(sv[c]));
+#pragma unroll
+      for (int c = 0; c < KK; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
+      const bool no_page = *(volatile int*)&ms->no_page[i & 3];  // (read before s_free: the copies are three tiles on at most)
+      tc_fence_before();
       __syncwarp();
-#pragma unroll
-      for (int k = 0; k < 2; ++k) anc[lane + 32 * k] = w[k], link[lane + 32 * k] = p[k];
-    }
-  }
-
-  float o[MT][DT][4], m[MT][2], l[MT][2];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-#pragma unroll
-    for (int d = 0; d < DT; ++d) o[t][d][0] = o[t][d][1] = o[t][d][2] = o[t][d][3] = 0.f;
-    m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
-  }
-
+      if (lane == 0) mbar_arrive(smem_u32(&ms->s_free));
+      if (tree || left < KT || no_page) {  // masks, and rows of V that are not to be multiplied
+        const int32_t* table = a.table + (long long)s * a.max_pages;
+        unsigned long long rowsv = left < KT ? (1ull << left) - 1 : ~0ull;  // the tile's rows that there are
+        if (!tree && no_page) {
 #pragma unroll 1
-  for (int i = i0; i < i1; ++i) {
-    cp_async_wait<0>();
-    __syncthreads();  // the tile is there; the other stage's readers are done
-    if (i + 1 < i1) load(i + 1);
-    const uint32_t kt = sb + Sh::OFF_KV + (i & 1) * 2 * Sh::KV, vt = kt + Sh::KV;
-    const bool tree = i == ct;
-    unsigned long long odd = 0;  // tree rows with values of v that are not finite: zero in the tile, added by themselves
-    if (tree) {
-      if (tid < a.n) {
-        bool f = false;
-#pragma unroll 1
-        for (int ch = 0; ch < CH; ++ch) {
-          uint4* v = reinterpret_cast<uint4*>(smem + (vt - sb) + tile_off(tid, ch, ROWB));
-          const uint4 x = *v;
-          const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
-          if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) f = true, *v = y;
-        }
-        link[tid] = f ? -2 : -1;
-      } else if (tid < 64) {
-        link[tid] = -1;
-      }
-      __syncthreads();
-      odd = (unsigned long long)__ballot_sync(0xffffffffu, link[lane] == -2) |
-            (unsigned long long)__ballot_sync(0xffffffffu, link[lane + 32] == -2) << 32;
-    }
-    // scores of this warp's keys
-    float sc[MT][NT][4];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) sc[t][j][0] = sc[t][j][1] = sc[t][j][2] = sc[t][j][3] = 0.f;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      uint32_t qf[MT][4];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) frag_a(qf[t], sb, ROWB, (wm * MT + t) * 16, 16 * k, lane);
-#pragma unroll
-      for (int j = 0; j < NT / 2; ++j) {
-        uint32_t b[4];
-        frag_b2(b, kt, ROWB, wn * KW + 16 * j, 16 * k, lane);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          mma16816(sc[t][2 * j], qf[t], b[0], b[1]);
-          mma16816(sc[t][2 * j + 1], qf[t], b[2], b[3]);
-        }
-      }
-    }
-    const int left = tree ? a.n : len - i * KT;
-    uint32_t pf[MT][NT][2];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int ra = r0 + (wm * MT + t) * 16 + g8;
-      if (tree || left < KT || *no_page) {
-        unsigned long long wa = ~0ull, wb = ~0ull;
-        if (tree) {
-          wa = ra < rows ? anc[ra / a.g] : 0ull;
-          wb = ra + 8 < rows ? anc[(ra + 8) / a.g] : 0ull;
-        } else if (*no_page) {  // rows on such pages are absent
-#pragma unroll 1
-          for (int key = 0; key < min(left, KT); ++key) {
-            const int pg = table[(i * KT + key) >> a.page_shift];
-            if (pg < 0 || pg >= a.n_pages) wa &= ~(1ull << key);
-          }
-          wb = wa;
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int key = wn * KW + 8 * j + 2 * q4 + e;
-            if (key >= left || !(wa >> key & 1)) sc[t][j][e] = -INFINITY;
-            if (key >= left || !(wb >> key & 1)) sc[t][j][2 + e] = -INFINITY;
-          }
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float mx = m[t][half];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mx = fmaxf(mx, fmaxf(sc[t][j][2 * half], sc[t][j][2 * half + 1]) * a.scale_log2);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float ref = mx == -INFINITY ? 0.f : mx;  // a row none of whose keys so far counts
-        const float f = exp2_sfu(m[t][half] - ref);
-        m[t][half] = mx;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const float p0 = exp2_sfu(fmaf(sc[t][j][2 * half], a.scale_log2, -ref));
-          const float p1 = exp2_sfu(fmaf(sc[t][j][2 * half + 1], a.scale_log2, -ref));
-          sum += p0 + p1;
-          pf[t][j][half] = pack_bf16x2(p0, p1);
-        }
-        l[t][half] = fmaf(l[t][half], f, sum);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[t][d][2 * half] *= f, o[t][d][2 * half + 1] *= f;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < NT / 2; ++j)
-#pragma unroll
-      for (int d = 0; d < DT / 2; ++d) {
-        uint32_t b[4];
-        frag_b2_t(b, vt, ROWB, 16 * d, wn * KW + 16 * j, lane);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          const uint32_t pa[4] = {pf[t][2 * j][0], pf[t][2 * j][1], pf[t][2 * j + 1][0], pf[t][2 * j + 1][1]};
-          mma16816(o[t][2 * d], pa, b[0], b[1]);
-          mma16816(o[t][2 * d + 1], pa, b[2], b[3]);
-        }
-      }
-    // what the values left out add, in the rows that see them, is not finite whatever its weight
-    const unsigned long long mine = WN == 1 ? odd : odd >> (wn * KW) << (wn * KW) & (wn + 1 < WN ? (1ull << (wn + 1) * KW) - 1 : ~0ull);
-    if (mine) {  // each by the warp whose key it is
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int ra = r0 + (wm * MT + t) * 16 + g8;
-        const unsigned long long wa = ra < rows ? anc[ra / a.g] : 0ull, wb = ra + 8 < rows ? anc[(ra + 8) / a.g] : 0ull;
-#pragma unroll 1
-        for (unsigned long long left = mine & (wa | wb); left; left &= left - 1) {
-          const int key = __ffsll((long long)left) - 1;
-          const bool sa = wa >> key & 1, sb2 = wb >> key & 1;
-          const uint16_t* v = a.v + ((long long)s * a.n + key) * a.ldv + kvh * D + 2 * q4;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const uint32_t x = *reinterpret_cast<const uint32_t*>(v + 8 * d), out = x ^ finite_or_zero(x);
-            const float x0 = out & 0xffffu ? bf16_lo(x) : 0.f, x1 = out & 0xffff0000u ? bf16_hi(x) : 0.f;
-            o[t][d][0] += sa ? x0 : 0.f, o[t][d][1] += sa ? x1 : 0.f;
-            o[t][d][2] += sb2 ? x0 : 0.f, o[t][d][3] += sb2 ? x1 : 0.f;
+          for (int k = 0; k < min(left, KT); ++k) {
+            const int pg = table[(ti * KT + k) >> a.page_shift];
+            if (pg < 0 || pg >= a.n_pages) rowsv &= ~(1ull << k);
           }
         }
+        ok = wait_bar(&ms->v_full[i % STAGES], (i / STAGES) & 1, stop);
+        if (!ok) break;
+        unsigned char* vt = smem + Sh::OFF_KV + (i % STAGES) * 2 * Sh::TILE + Sh::TILE;
+#pragma unroll 1
+        for (int k = tid; k < KT * D / 8; k += 128) {
+          const int vr = k / (D / 8), c = k % (D / 8);
+          uint4* v = reinterpret_cast<uint4*>(vt + (c >> 3) * BLK + tile_off(vr, c & 7, 128));
+          if (!(rowsv >> vr & 1)) {
+            *v = make_uint4(0, 0, 0, 0);
+          } else if (tree) {
+            const uint4 x = *v;
+            const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+            if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *v = y, atomicOr(&ms->odd[vr >> 5], 1u << (vr & 31));
+          }
+        }
+        fence_async_smem();
+        named_sync(1, 128);  // (and: the ancestor words are there)
+        if (tree) rowsv &= ms->anc[node];
+        rowsv >>= dg * KK;
+#pragma unroll
+        for (int j = 0; j < KK; ++j)
+          if (!((j < 32 ? (uint32_t)rowsv : (uint32_t)(rowsv >> 32)) >> (j & 31) & 1)) sv[j] = -INFINITY;
       }
-    }
-  }
-  // row sums over the four lanes of a row
+      float mx = fmaxf(sv[0], sv[1]);
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      l[t][half] += __shfl_xor_sync(0xffffffffu, l[t][half], 1);
-      l[t][half] += __shfl_xor_sync(0xffffffffu, l[t][half], 2);
-    }
-  if (WN > 1) {  // the key groups' sums joined through shared memory (q and the tiles are no longer needed)
-    float* ml = reinterpret_cast<float*>(smem);  // [WN][RT][2], then o [RT][D]
-    float* os = ml + WN * RT * 2;
-    __syncthreads();
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = wm * 16 + g8 + 8 * half;
-      if (q4 == 0) ml[(wn * RT + r) * 2] = m[0][half], ml[(wn * RT + r) * 2 + 1] = l[0][half];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = wm * 16 + g8 + 8 * half;
-      float mx = -INFINITY, sum = 0.f;
-      for (int w = 0; w < WN; ++w) mx = fmaxf(mx, ml[(w * RT + r) * 2]);
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      for (int w = 0; w < WN; ++w) sum = fmaf(ml[(w * RT + r) * 2 + 1], exp2_sfu(ml[(w * RT + r) * 2] - ref), sum);
-      const float f = exp2_sfu(m[0][half] - ref);
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[0][d][2 * half] *= f, o[0][d][2 * half + 1] *= f;
-      m[0][half] = mx, l[0][half] = sum;
-    }
-    for (int w = 0; w < WN; ++w) {
-      if (wn == w)
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
+      for (int j = 2; j < KK; j += 2) mx = max3f(mx, sv[j], sv[j + 1]);
+      mx *= a.scale_log2;
+      if (i == 0) {
+        m = mx;
+      } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+        const float to = fmaxf(m, mx), f = to == m ? 1.f : exp2_sfu(m - to);
+        ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          uint32_t u[8];
+          tmem_ld16_async(tmem + A_O + lanes + c, o);
+          tmem_wait_ld16(o);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            float2* p = reinterpret_cast<float2*>(os + (wm * 16 + g8 + 8 * half) * D + 8 * d + 2 * q4);
-            float2 x = make_float2(o[0][d][2 * half], o[0][d][2 * half + 1]);
-            if (w > 0) x.x += p->x, x.y += p->y;
-            if (w + 1 < WN)
-              *p = x;
-            else
-              o[0][d][2 * half] = x.x, o[0][d][2 * half + 1] = x.y;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(o[8 * half + j] * f);
+            tmem_st8(tmem + A_O + lanes + c + 8 * half, u);
           }
-      __syncthreads();
+        }
+        l *= f, m = to;
+      }
+      const float ref = m == -INFINITY ? 0.f : m;  // a row none of whose keys so far counts
+      const unsigned long long sc2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
+      float sum0 = 0.f, sum1 = 0.f;
+      const uint32_t pt = tmem + A_P + (i & 1) * 32 + lanes + dg * (KK / 2);
+#pragma unroll
+      for (int c = 0; c < KK; c += 16) {
+        uint32_t u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 e = unpack2(ffma2(pack2(sv[c + 2 * j], sv[c + 2 * j + 1]), sc2, ref2));
+          const float p0 = exp2_sfu(e.x), p1 = exp2_sfu(e.y);
+          sum0 += p0, sum1 += p1;
+          u[j] = pack_bf16x2(p0, p1);
+        }
+        tmem_st8(pt + c / 2, u);
+      }
+      l += sum0 + sum1;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[i & 1]));
     }
-    if (wn != WN - 1) return;
-  }
+    // S of the last tile was made after P . V of the last but two: two phases are left, one after the other
+    ok = ok && (n < 2 || wait_bar(&ms->o_done, (n - 2) & 1, stop)) && wait_bar(&ms->o_done, (n - 1) & 1, stop);
+    // a warp that gives up still takes part in the barriers that others may be waiting at
+    if (!ok) asm volatile("bar.arrive 1, 128;\nbar.arrive 2, 128;\nbar.arrive 2, 128;\n" ::: "memory");
+    tc_fence_after();
+    float f = 1.f;
+    if (DUP > 1 && ok) {  // the copies' maxima and sums joined
+      ms->ml[tid] = make_float2(m, l);
+      named_sync(2, 128);
+      float to = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+      for (int k = 0; k < DUP; ++k) to = fmaxf(to, ms->ml[k * RG + r].x);
+      const float ref = to == -INFINITY ? 0.f : to;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = r0 + (wm * MT + t) * 16 + g8 + 8 * half;
-      if (row >= rows) continue;
-      const int node = row / a.g, j = row % a.g;
-      const long long qrow = ((long long)s * a.n + node) * a.Hq + kvh * a.g + j;
-      if (a.splits == 1) {
-        const float inv = 1.f / l[t][half];
-        uint16_t* p = a.o + ((long long)s * a.n + node) * a.ldo + (kvh * a.g + j) * D + 2 * q4;
+      for (int k = 0; k < DUP; ++k) sum = fmaf(ms->ml[k * RG + r].y, exp2_sfu(ms->ml[k * RG + r].x - ref), sum);
+      f = exp2_sfu(m - ref);
+      m = to, l = sum;
+      if (dg > 0) {  // the tiles' space is free: their MMAs are done
+        float* os = reinterpret_cast<float*>(smem + Sh::OFF_KV) + ((dg - 1) * RG + r) * (D + 4);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          tmem_ld16_async(tmem + A_O + lanes + c, o);
+          tmem_wait_ld16(o);
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-          *reinterpret_cast<uint32_t*>(p + 8 * d) = pack_bf16x2(o[t][d][2 * half] * inv, o[t][d][2 * half + 1] * inv);
-      } else {
-        float* p = a.part + (qrow * a.splits + sp) * D + 2 * q4;
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<float4*>(os + c + j) = make_float4(o[j] * f, o[j + 1] * f, o[j + 2] * f, o[j + 3] * f);
+        }
+      }
+      named_sync(2, 128);
+    }
+    if (ok && dg == 0) {
+      const unsigned long long odd = has_tree ? (ms->odd[0] | (unsigned long long)ms->odd[1] << 32) & ms->anc[node] : 0ull;
+      const long long tok = (long long)s * a.n + node;
+      const int head = kvh * a.g + qh;
+      const float inv = 1.f / l;
+      const float* os = reinterpret_cast<const float*>(smem + Sh::OFF_KV) + r * (D + 4);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float o[16];
+        __syncwarp();
+        tmem_ld16_async(tmem + A_O + lanes + c, o);
+        tmem_wait_ld16(o);
+        if (DUP > 1) {
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-          *reinterpret_cast<float2*>(p + 8 * d) = make_float2(o[t][d][2 * half], o[t][d][2 * half + 1]);
-        if (q4 == 0)
-          *reinterpret_cast<float2*>(a.part_ml + (qrow * a.splits + sp) * 2) = make_float2(m[t][half], l[t][half]);
+          for (int j = 0; j < 16; ++j) o[j] *= f;
+#pragma unroll
+          for (int k = 1; k < DUP; ++k)
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(os + (k - 1) * RG * (D + 4) + c + j);
+              o[j] += v.x, o[j + 1] += v.y, o[j + 2] += v.z, o[j + 3] += v.w;
+            }
+        }
+#pragma unroll 1
+        for (unsigned long long todo = odd; todo; todo &= todo - 1) {  // not finite whatever its weight
+          const uint32_t* v = reinterpret_cast<const uint32_t*>(
+              a.v + ((long long)s * a.n + __ffsll((long long)todo) - 1) * a.ldv + kvh * D + c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t x = v[j], out = x ^ finite_or_zero(x);
+            if (out & 0xffffu) o[2 * j] += bf16_lo(x);
+            if (out & 0xffff0000u) o[2 * j + 1] += bf16_hi(x);
+          }
+        }
+        if (row >= rows) {
+        } else if (a.splits == 1) {
+          uint32_t u[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+          uint4* p = reinterpret_cast<uint4*>(a.o + tok * a.ldo + head * D + c);
+          p[0] = make_uint4(u[0], u[1], u[2], u[3]), p[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        } else {
+          float4* p = reinterpret_cast<float4*>(a.part + ((tok * a.Hq + head) * a.splits + sp) * D + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      }
+      if (row < rows && a.splits > 1)
+        *reinterpret_cast<float2*>(a.part_ml + ((tok * a.Hq + head) * a.splits + sp) * 2) = make_float2(m, l);
+    }
+  } else if (warp == 4) {
+    // ---- copies: lane b the b-th page piece of a tile ----
+    const int32_t* table = a.table + (long long)s * a.max_pages;
+    const int shift = min(a.page_shift, 6), box = 1 << shift, pieces = KT >> shift, pmask = (1 << a.page_shift) - 1;
+    auto lookup = [&](int ti) {  // the piece's page; -1: no such row; -2: out of range
+      const int at = ti * KT + lane * box;
+      if (lane >= pieces || ti >= ct || at >= len) return -1;
+      const int pg = table[at >> a.page_shift];
+      return pg < 0 || pg >= a.n_pages ? -2 : pg;
+    };
+    int issued = 0, pg = lookup(i0);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int st = i % STAGES, par = (i / STAGES - 1) & 1, ti = i0 + i;
+      const int mine = pg;
+      pg = lookup(ti + 1);
+      const bool bad = __any_sync(0xffffffffu, mine == -2);
+      if (bad && lane == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
+      const bool tree = ti == ct;
+      const uint32_t bytes = (tree ? KT : __popc(__ballot_sync(0xffffffffu, mine >= 0)) * box) * D * 2;
+      const int crd = ((mine * a.Hkv + kvh) << a.page_shift) + ((ti * KT + lane * box) & pmask);
+      bool ok = true;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        unsigned long long* full = kv ? &ms->v_full[st] : &ms->k_full[st];
+        const uint32_t dst = sb + Sh::OFF_KV + st * 2 * Sh::TILE + kv * Sh::TILE;
+        ok = ok && (i < STAGES || wait_bar(kv ? &ms->v_free[st] : &ms->k_free[st], par, stop));
+        if (!ok) break;
+        if (kv == 0 && lane == 0) *(volatile int*)&ms->no_page[i & 3] = bad;
+        if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), bytes);
+        __syncwarp();
+        if (tree) {
+          if (lane < DB) tma_load_2d(dst + lane * BLK, kv ? &tvt : &tkt, kvh * D + lane * 64, s * a.n, smem_u32(full));
+        } else if (mine >= 0) {
+#pragma unroll
+          for (int c = 0; c < DB; ++c)
+            tma_load_2d(dst + c * BLK + lane * box * 128, kv ? &tvp : &tkp, c * 64, crd, smem_u32(full));
+        }
+        issued = 2 * i + kv + 1;
+      }
+      if (!ok) break;
+    }
+    if (lane == 0 && *stop) {  // copies in flight land before the shared memory is given up
+      for (int k = max(0, issued - 2 * STAGES); k < issued; ++k)
+        mbar_poll_ns(smem_u32(k & 1 ? &ms->v_full[k / 2 % STAGES] : &ms->k_full[k / 2 % STAGES]), (k / 2 / STAGES) & 1, kWaitLimitNs);
+    }
+  } else {
+    // ---- MMAs: S of a tile, then P . V of the one before ----
+    constexpr uint32_t id_s = idesc_major(128, KT, false, false), id_o = idesc_major(128, D, false, true);
+    const bool leader = elect_one();
+    bool ok = wait_bar(&ms->q_full, 0, stop);
+#pragma unroll 1
+    for (int i = 0; i <= n && ok; ++i) {
+      if (i < n) {
+        ok = wait_bar(&ms->k_full[i % STAGES], (i / STAGES) & 1, stop) && (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t qd = desc_lo(sb, 16), kd = desc_lo(sb + Sh::OFF_KV + (i % STAGES) * 2 * Sh::TILE, 16);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss<id_s>(tmem + A_S, qd + (((k >> 2) * 2 * BLK + (k & 3) * 32) >> 4), kd + (((k >> 2) * BLK + (k & 3) * 32) >> 4), k > 0);
+          mma_commit(smem_u32(&ms->k_free[i % STAGES]));
+          mma_commit(smem_u32(&ms->s_full));
+        }
+        __syncwarp();
+      }
+      if (i > 0) {
+        const int j = i - 1;
+        ok = wait_bar(&ms->v_full[j % STAGES], (j / STAGES) & 1, stop) && wait_bar(&ms->p_full[j & 1], (j / 2) & 1, stop);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t vd = desc_lo(sb + Sh::OFF_KV + (j % STAGES) * 2 * Sh::TILE + Sh::TILE, BLK);
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)  // 16 keys: two groups of 8 rows
+            mma_ts<id_o>(tmem + A_O, tmem + A_P + (j & 1) * 32 + k * 8, vd + k * (2048 >> 4), j + k > 0);
+          mma_commit(smem_u32(&ms->v_free[j % STAGES]));
+          mma_commit(smem_u32(&ms->o_done));
+        }
+        __syncwarp();
       }
     }
+    if (leader) {
+      mma_commit(smem_u32(&ms->drain));
+      mbar_poll_ns(smem_u32(&ms->drain), 0, kWaitLimitNs);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *stop) flag(a.status, SSM_STATUS_TIMEOUT);
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free_warp(tmem, A_COLS);
+  }
 }
 
 // o = sum over the splits of 2^(m_i - m) o_i / sum of 2^(m_i - m) l_i; a warp per query row, D / 32 columns a lane
 template <int D>
 __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a) {
+  grid_dependency_wait();
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);  // (s, node, head)
   const int lane = threadIdx.x & 31;
   if (row >= (long long)a.S * a.n * a.Hq) return;
@@ -374,49 +462,63 @@ __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a) {
   for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(o + v) = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
 }
 
-// Rows per CTA and splits of the keys.
+// Copies of the rows, row tiles and splits of the keys.
 struct AttendPlan {
-  int rt, row_tiles, tps, splits;
+  int dup, row_tiles, tps, splits;
 };
 AttendPlan plan_attend(int S, int n, int Hq, int Hkv, int max_len) {
   AttendPlan p;
   const int rows = n * (Hq / Hkv);
-  p.rt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  p.row_tiles = (rows + p.rt - 1) / p.rt;
+  p.dup = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+  p.row_tiles = (rows + 127) / 128;
   const int nt = (max_len + KT - 1) / KT + 1;
   const long long items = (long long)S * Hkv * p.row_tiles, slots = 2 * kSMs;
-  // tiles per split so that the waves of CTAs take least, a split costing about three tiles beside its own
+  // tiles per split so that the waves of CTAs take least, a split costing about four tiles beside its own
   double best = 1e300;
   p.tps = nt, p.splits = 1;
   for (int sp = 1; sp <= 64 && sp <= nt; ++sp) {
     const int tps = (nt + sp - 1) / sp, used = (nt + tps - 1) / tps;
     const long long waves = (items * used + slots - 1) / slots;
-    const double est = (double)waves * (tps + 3.0) + (used > 1 ? 2.0 + 0.1 * used : 0.0);
+    const double est = (double)waves * (tps + 4.0) + (used > 1 ? 2.0 + 0.1 * used : 0.0);
     if (est < best * 0.999) best = est, p.tps = tps, p.splits = used;
   }
   return p;
 }
 
-template <int D, int WM, int MT>
-cudaError_t run_attend(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  using Sh = AttendShape<D, WM, MT>;
-  cudaError_t e =
-      cudaFuncSetAttribute(attend_kernel<D, WM, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+template <int D, int DUP>
+cudaError_t run_attend(const AttendArgs& a, const AttendPlan& p, const CUtensorMap (&m)[4], cudaStream_t s) {
+  using Sh = AttendSmem<D>;
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::BYTES);
   if (e != cudaSuccess) return e;
-  attend_kernel<D, WM, MT>
-      <<<dim3((unsigned)p.splits, (unsigned)a.Hkv, (unsigned)(a.S * p.row_tiles)), ATHREADS, Sh::SMEM, s>>>(a);
+  attend_kernel<D, DUP><<<dim3((unsigned)(p.splits * p.row_tiles), (unsigned)a.Hkv, (unsigned)a.S), ATHREADS, Sh::BYTES, s>>>(
+      m[0], m[1], m[2], m[3], a);
   return cudaGetLastError();
 }
 template <int D>
 cudaError_t run_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  cudaError_t e = p.rt == 16   ? run_attend<D, 1, 1>(a, p, s)
-                  : p.rt == 32 ? run_attend<D, 2, 1>(a, p, s)
-                  : p.rt == 64 ? run_attend<D, 4, 1>(a, p, s)
-                               : run_attend<D, 4, 2>(a, p, s);
+  CUtensorMap m[4];
+  const long long page_rows = ((long long)a.n_pages * a.Hkv) << a.page_shift, cols = (long long)a.Hkv * D;
+  const int box = a.page_shift < 6 ? 1 << a.page_shift : KT;
+  // a call without cached rows reads no page: any matrix will do
+  const bool none = a.max_len == 0 || page_rows == 0;
+  if (!encode_tiles(&m[0], none ? a.k : a.kp, none ? 1 : page_rows, D, none ? a.ldk : D, box) ||
+      !encode_tiles(&m[1], none ? a.v : a.vp, none ? 1 : page_rows, D, none ? a.ldv : D, box) ||
+      !encode_tiles(&m[2], a.k, (long long)a.S * a.n, cols, a.ldk, KT) ||
+      !encode_tiles(&m[3], a.v, (long long)a.S * a.n, cols, a.ldv, KT))
+    return cudaErrorInvalidValue;
+  cudaError_t e = p.dup == 4 ? run_attend<D, 4>(a, p, m, s) : p.dup == 2 ? run_attend<D, 2>(a, p, m, s) : run_attend<D, 1>(a, p, m, s);
   if (e != cudaSuccess || p.splits == 1) return e;
-  const long long rows = (long long)a.S * a.n * a.Hq;
-  combine_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};  // its blocks are placed while the last of the splits run
+  cfg.gridDim = dim3((unsigned)(((long long)a.S * a.n * a.Hq + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, combine_kernel<D>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // A cluster of 8 CTAs for each sequence: together they copy its path's rows; its length is written by one of them

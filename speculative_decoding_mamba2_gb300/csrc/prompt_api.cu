@@ -84,7 +84,7 @@ ScanArgs scan_args(const ssm_dims* d, const ssm_params* p, int32_t layer, int32_
 }
 
 int check_attend_shape(const char* fn, int32_t S, int32_t n, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_len) {
-  if (S < 0 || S > 4095) return pfail(SSM_ERR_INVALID_ARG, fn, "n_seq must be in [0, 4095]");
+  if (S < 0 || S > 65535) return pfail(SSM_ERR_INVALID_ARG, fn, "n_seq must be in [0, 65535]");
   if (n < 1) return pfail(SSM_ERR_INVALID_ARG, fn, "n_nodes must be >= 1");
   if (n > SSM_MAX_NODES) return pfail(SSM_ERR_CAPACITY, fn, "n_nodes above SSM_MAX_NODES");
   if (Hkv < 1 || Hq < 1 || Hq % Hkv) return pfail(SSM_ERR_INVALID_ARG, fn, "Hkv must divide Hq");
@@ -194,6 +194,8 @@ extern "C" int ssm_tree_attention(int32_t n_seq, int32_t n_nodes, int32_t Hq, in
   const int shift = page_shift(page_size);
   if (shift < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "page_size must be a power of two in [8, 1024]");
   if (n_pages < 0 || max_pages < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "n_pages and max_pages must be >= 0");
+  if ((long long)n_pages * Hkv * page_size > INT32_MAX || (long long)n_seq * n_nodes > INT32_MAX)
+    return pfail(SSM_ERR_CAPACITY, fn, "more than 2^31 - 1 rows of pages");
   if (!(scale > 0.f) || isinf(scale)) return pfail(SSM_ERR_RANGE, fn, "scale must be positive and finite");
   if (n_seq > 0 && (!layout || !q || !k || !v || !o || !cache_len)) return pfail(SSM_ERR_INVALID_ARG, fn, "a pointer is NULL");
   if (max_cache_len > 0 && (!k_pages || !v_pages || !page_table))

@@ -54,7 +54,7 @@ BAD += [("ssm_prompt_scan", SCAN, kw, code) for kw, code in [
     (dict(cu=None), INV), (dict(ws=None), INV), (dict(ws=ctypes.c_void_p(4096 + 16)), INV), (dict(ws_bytes=255), CAP),
     (dict(n_tok=100000, max_len=100000, ws_bytes=1 << 16), CAP)]]
 BAD += [("ssm_tree_attention", ATTEND, kw, code) for kw, code in [
-    (dict(S=-1), INV), (dict(S=4096), INV), (dict(n=0), INV), (dict(n=65), CAP), (dict(Hkv=3), INV), (dict(Hkv=0), INV),
+    (dict(S=-1), INV), (dict(S=65536), INV), (dict(n_pages=1 << 30), CAP), (dict(n=0), INV), (dict(n=65), CAP), (dict(Hkv=3), INV), (dict(Hkv=0), INV),
     (dict(Hq=66, ldq=1 << 14, ldo=1 << 14), CAP), (dict(D=96), INV), (dict(max_len=-1), INV), (dict(page=12), INV),
     (dict(page=4), INV), (dict(page=2048), INV), (dict(n_pages=-1), INV), (dict(scale=0.0), RANGE), (dict(scale=-1.0), RANGE),
     (dict(scale=float("nan")), RANGE), (dict(scale=float("inf")), RANGE), (dict(layout=None), INV), (dict(q=ODD), INV),
