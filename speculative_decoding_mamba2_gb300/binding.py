@@ -72,7 +72,12 @@ class Dims:
         return self.d_inner + 2 * self.d_state
 
     def c(self) -> ssm_dims:
-        return ssm_dims(self.n_heads, self.head_dim, self.d_state, self.conv_width, self.n_layers, self.ring_cap)
+        """The C struct (made once; the library only reads it)."""
+        d = self.__dict__.get("_c")
+        if d is None:
+            d = ssm_dims(self.n_heads, self.head_dim, self.d_state, self.conv_width, self.n_layers, self.ring_cap)
+            object.__setattr__(self, "_c", d)
+        return d
 
 
 _LIB = None
@@ -145,6 +150,9 @@ def _check(rc: int):
 # marshalling helpers
 # ---------------------------------------------------------------------------
 def _dev(t: torch.Tensor, name: str, dtype, numel: int | None = None):
+    """The address of a contiguous CUDA tensor of this dtype (and element count)."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous() and numel in (None, t.numel()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -153,14 +161,10 @@ def _dev(t: torch.Tensor, name: str, dtype, numel: int | None = None):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
-    return ctypes.c_void_p(t.data_ptr())
+    raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
 
 
-def _ptr(t: torch.Tensor, name: str, dtype, numel: int):
-    """Integer address (for ctypes struct fields)."""
-    return _dev(t, name, dtype, numel).value
+_ptr = _dev  # also for ctypes struct fields
 
 
 def _opt_status(status):
@@ -169,8 +173,8 @@ def _opt_status(status):
 
 def _stream(stream, like: torch.Tensor):
     if stream is None:
-        stream = torch.cuda.current_stream(like.device)
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(like.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _params(prm: dict, d: Dims, layers: int) -> ssm_params:
@@ -434,7 +438,7 @@ def _rows(t: torch.Tensor, name: str, dtype, cols: int | None = None):
         raise ValueError(f"{name}: must be 2-D with contiguous rows")
     if cols is not None and t.size(1) != cols:
         raise ValueError(f"{name}: {t.size(1)} columns, expected {cols}")
-    return ctypes.c_void_p(t.data_ptr()), t.size(0), t.stride(0)
+    return t.data_ptr(), t.size(0), t.stride(0)
 
 
 def ssm_linear_tile_cols() -> int:
@@ -455,7 +459,7 @@ def ssm_linear(A, W, segments, residual=None, status=None, stream=None):
         p, rows, ld = _rows(out, f"segment {i}", out.dtype, end - col)
         if out.dtype not in (torch.bfloat16, torch.float32) or rows != M:
             raise ValueError(f"segment {i}: bf16 or fp32 with {M} rows")
-        segs[i] = ssm_out_segment(col, 1 if out.dtype == torch.float32 else 0, ld, p.value)
+        segs[i] = ssm_out_segment(col, 1 if out.dtype == torch.float32 else 0, ld, p)
     r, ldr = None, 0
     if residual is not None:
         r, rows, ldr = _rows(residual, "residual", torch.float32, N)

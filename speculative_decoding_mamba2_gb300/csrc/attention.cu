@@ -6,7 +6,8 @@
 //     S [128 x 64] = Q . K^T,   P = 2^(S - m),   O [128 x D] += P . V        (P, O in tensor memory, V read MN-major)
 // with the running maximum m and sum of each row's softmax in the row's thread.  O is rescaled only when a maximum has
 // grown by more than 2^8 (P then stays below 2^8, and its rounding to bf16 is relative).  S of the next tile is made while
-// the softmax of this one runs, and two CTAs to an SM overlap the rest; K and V tiles come by TMA from their pages.
+// the softmax of this one runs, and two CTAs to an SM overlap the rest (one CTA with two such streams took 15 to 25 % longer
+// on 320 rows: nothing covered its start and its end).  K and V tiles come by TMA from their pages, through a ring.
 // Where there are at most 64 (32) rows they stand in tensor memory twice (four times), each copy for its half (quarter)
 // of a tile's keys, so that all 128 threads have exponentials to do; the copies' sums are joined at the end.
 // One tile more than the cache has holds the tree's own rows; there a row keeps its node's ancestors only, read from a
@@ -22,7 +23,7 @@ namespace {
 
 constexpr int KT = 64;          // keys per tile
 constexpr int ATHREADS = 192;   // 4 softmax warps, one for copies, one for MMAs
-constexpr int STAGES = 2;
+constexpr int UNITS = 5;         // tiles of K or V in the ring: what lets two CTAs share an SM's memory
 constexpr int BLK = KT * 128;   // 64 rows x 64 columns of bf16
 
 constexpr int A_S = 0, A_P = 64, A_O = 128, A_COLS = 256;  // tensor memory columns: S, P (two buffers of 32), O
@@ -31,19 +32,19 @@ template <int D>
 struct AttendSmem {
   static constexpr int OFF_KV = (D / 64) * 2 * BLK;          // after Q: D / 64 blocks of 128 rows
   static constexpr int TILE = (D / 64) * BLK;                // K or V of a tile
-  static constexpr int OFF_MISC = OFF_KV + STAGES * 2 * TILE;
-  static constexpr int BYTES = OFF_MISC + 64 * 8 + 128 * 8 + 256 + 1024 /* alignment */;
+  static constexpr int OFF_MISC = OFF_KV + UNITS * TILE;
+  static constexpr int BYTES = OFF_MISC + 768;
+  static_assert(BYTES <= 228 * 1024 / 2 - 1024, "two to an SM");
 };
 struct AttendMisc {
   unsigned long long anc[64];  // ancestors and self of each node
-  float2 ml[128];
-  unsigned long long k_full[STAGES], v_full[STAGES], k_free[STAGES], v_free[STAGES], q_full, s_full, s_free, p_full[2], o_done, drain;
+  unsigned long long full[UNITS], free_[UNITS], q_full, s_full, s_free, p_full[2], o_done, drain;
   unsigned int odd[2];         // tree rows with a value of v that is not finite
   uint32_t tmem;
   int stop;
-  int no_page[4];              // whether a page of tile i (at i % 4) is out of range
+  int no_page[8];              // whether a page of tile i (at i % 8) is out of range
 };
-static_assert(sizeof(AttendMisc) <= 64 * 8 + 128 * 8 + 256, "space");
+static_assert(sizeof(AttendMisc) <= 768, "space");
 
 __device__ __forceinline__ float max3f(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
@@ -53,8 +54,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
                   const __grid_constant__ CUtensorMap tkt, const __grid_constant__ CUtensorMap tvt, AttendArgs a) {
   using Sh = AttendSmem<D>;
   constexpr int RG = 128 / DUP, KK = KT / DUP, DB = D / 64;  // rows of a copy, its keys of a tile, 64-column blocks
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  extern __shared__ __align__(1024) unsigned char smem[];  // (there is no room to move it: where it is not aligned, nothing runs)
   const uint32_t sb = smem_u32(smem);
   AttendMisc* ms = reinterpret_cast<AttendMisc*>(smem + Sh::OFF_MISC);
   volatile int* stop = &ms->stop;
@@ -62,6 +62,10 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   const int rows = a.n * a.g, rt = (rows + 127) / 128;
   const int r0 = (blockIdx.x % rt) * 128, sp = blockIdx.x / rt, kvh = blockIdx.y, s = blockIdx.z;
   launch_dependents();
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) flag(a.status, SSM_STATUS_TIMEOUT);
+    return;
+  }
   int len = __shfl_sync(0xffffffffu, a.cache_len[s], 0);
   if (len < 0 || len > a.max_len || (long long)len > ((long long)a.max_pages << a.page_shift)) {
     if (sp == 0 && kvh == 0 && r0 == 0 && tid == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
@@ -73,11 +77,9 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   const bool has_tree = i0 + n == ct + 1;
 
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&ms->k_full[i]), 1);
-      mbar_init(smem_u32(&ms->v_full[i]), 1);
-      mbar_init(smem_u32(&ms->k_free[i]), 1);
-      mbar_init(smem_u32(&ms->v_free[i]), 1);
+    for (int i = 0; i < UNITS; ++i) {
+      mbar_init(smem_u32(&ms->full[i]), 1);
+      mbar_init(smem_u32(&ms->free_[i]), 1);
     }
     mbar_init(smem_u32(&ms->q_full), 4);
     mbar_init(smem_u32(&ms->s_full), 1);
@@ -117,8 +119,6 @@ __global__ void __launch_bounds__(ATHREADS, 2)
     }
     // ancestor words: a node's own bit, then its parent's word, its grandparent's, ... by doubling
     if (has_tree && warp == 0) {
-      volatile int* link = reinterpret_cast<volatile int*>(ms->ml);
-      volatile unsigned long long* anc = ms->anc;
       unsigned long long w[2];
       int p[2];
       bool bad = false;
@@ -131,19 +131,24 @@ __global__ void __launch_bounds__(ATHREADS, 2)
           if (p[k] < 0 || p[k] >= v) p[k] = -1, bad = true;
         }
         w[k] = 1ull << v;
-        anc[v] = w[k], link[v] = p[k];
       }
       if (bad && kvh == 0 && r0 == 0) flag(a.status, SSM_STATUS_BAD_LAYOUT);
 #pragma unroll 1
-      for (int step = 0; step < 6; ++step) {
-        __syncwarp();
+      for (int hop = 0; hop < 6; ++hop) {
+        unsigned long long up[2];
+        int pp[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // the word and the link of node p[k], which lane p[k] % 32 holds
+          const int from = p[k] & 31;
+          const unsigned long long u0 = __shfl_sync(0xffffffffu, w[0], from), u1 = __shfl_sync(0xffffffffu, w[1], from);
+          const int q0 = __shfl_sync(0xffffffffu, p[0], from), q1 = __shfl_sync(0xffffffffu, p[1], from);
+          up[k] = p[k] < 32 ? u0 : u1, pp[k] = p[k] < 32 ? q0 : q1;
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if (p[k] >= 0) w[k] |= anc[p[k]], p[k] = link[p[k]];
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) anc[lane + 32 * k] = w[k], link[lane + 32 * k] = p[k];
+          if (p[k] >= 0) w[k] |= up[k], p[k] = pp[k];
       }
+      ms->anc[lane] = w[0], ms->anc[lane + 32] = w[1];
     }
 
     float m = -INFINITY, l = 0.f;
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       for (int c = 0; c < KK; c += 16) tmem_ld16_async(tmem + A_S + lanes + dg * KK + c, reinterpret_cast<float(&)[16]>(sv[c]));
 #pragma unroll
       for (int c = 0; c < KK; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
-      const bool no_page = *(volatile int*)&ms->no_page[i & 3];  // (read before s_free: the copies are three tiles on at most)
+      const bool no_page = *(volatile int*)&ms->no_page[i & 7];  // (read before s_free: the copies are three tiles on at most)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->s_free));
@@ -175,9 +180,10 @@ __global__ void __launch_bounds__(ATHREADS, 2)
             if (pg < 0 || pg >= a.n_pages) rowsv &= ~(1ull << k);
           }
         }
-        ok = wait_bar(&ms->v_full[i % STAGES], (i / STAGES) & 1, stop);
+        const int use = 2 * i + 1;
+        ok = wait_bar(&ms->full[use % UNITS], (use / UNITS) & 1, stop);
         if (!ok) break;
-        unsigned char* vt = smem + Sh::OFF_KV + (i % STAGES) * 2 * Sh::TILE + Sh::TILE;
+        unsigned char* vt = smem + Sh::OFF_KV + use % UNITS * Sh::TILE;
 #pragma unroll 1
         for (int k = tid; k < KT * D / 8; k += 128) {
           const int vr = k / (D / 8), c = k % (D / 8);
@@ -198,10 +204,10 @@ __global__ void __launch_bounds__(ATHREADS, 2)
         for (int j = 0; j < KK; ++j)
           if (!((j < 32 ? (uint32_t)rowsv : (uint32_t)(rowsv >> 32)) >> (j & 31) & 1)) sv[j] = -INFINITY;
       }
-      float mx = fmaxf(sv[0], sv[1]);
+      float mx = fmaxf(sv[0], sv[1]), my = fmaxf(sv[2], sv[3]);
 #pragma unroll
-      for (int j = 2; j < KK; j += 2) mx = max3f(mx, sv[j], sv[j + 1]);
-      mx *= a.scale_log2;
+      for (int j = 4; j < KK; j += 4) mx = max3f(mx, sv[j], sv[j + 1]), my = max3f(my, sv[j + 2], sv[j + 3]);
+      mx = fmaxf(mx, my) * a.scale_log2;
       if (i == 0) {
         m = mx;
       } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
@@ -226,7 +232,8 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       }
       const float ref = m == -INFINITY ? 0.f : m;  // a row none of whose keys so far counts
       const unsigned long long sc2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
-      float sum0 = 0.f, sum1 = 0.f;
+      unsigned long long sum2[2] = {0ull, 0ull};
+      const unsigned long long one2 = pack2(1.f, 1.f);
       const uint32_t pt = tmem + A_P + (i & 1) * 32 + lanes + dg * (KK / 2);
 #pragma unroll
       for (int c = 0; c < KK; c += 16) {
@@ -235,32 +242,36 @@ __global__ void __launch_bounds__(ATHREADS, 2)
         for (int j = 0; j < 8; ++j) {
           const float2 e = unpack2(ffma2(pack2(sv[c + 2 * j], sv[c + 2 * j + 1]), sc2, ref2));
           const float p0 = exp2_sfu(e.x), p1 = exp2_sfu(e.y);
-          sum0 += p0, sum1 += p1;
+          sum2[j & 1] = ffma2(one2, pack2(p0, p1), sum2[j & 1]);
           u[j] = pack_bf16x2(p0, p1);
         }
         tmem_st8(pt + c / 2, u);
       }
-      l += sum0 + sum1;
+      l += pair_sum(sum2[0]) + pair_sum(sum2[1]);
+      if (i > 0 && i == n - 1) {  // the wait after the last tile must not find o_done two phases on
+        ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
+        if (!ok) break;
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[i & 1]));
     }
-    // S of the last tile was made after P . V of the last but two: two phases are left, one after the other
-    ok = ok && (n < 2 || wait_bar(&ms->o_done, (n - 2) & 1, stop)) && wait_bar(&ms->o_done, (n - 1) & 1, stop);
+    ok = ok && wait_bar(&ms->o_done, (n - 1) & 1, stop);
     // a warp that gives up still takes part in the barriers that others may be waiting at
     if (!ok) asm volatile("bar.arrive 1, 128;\nbar.arrive 2, 128;\nbar.arrive 2, 128;\n" ::: "memory");
     tc_fence_after();
     float f = 1.f;
     if (DUP > 1 && ok) {  // the copies' maxima and sums joined
-      ms->ml[tid] = make_float2(m, l);
+      float2* ml = reinterpret_cast<float2*>(smem);  // over Q: its MMAs are done
+      ml[tid] = make_float2(m, l);
       named_sync(2, 128);
       float to = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < DUP; ++k) to = fmaxf(to, ms->ml[k * RG + r].x);
+      for (int k = 0; k < DUP; ++k) to = fmaxf(to, ml[k * RG + r].x);
       const float ref = to == -INFINITY ? 0.f : to;
 #pragma unroll
-      for (int k = 0; k < DUP; ++k) sum = fmaf(ms->ml[k * RG + r].y, exp2_sfu(ms->ml[k * RG + r].x - ref), sum);
+      for (int k = 0; k < DUP; ++k) sum = fmaf(ml[k * RG + r].y, exp2_sfu(ml[k * RG + r].x - ref), sum);
       f = exp2_sfu(m - ref);
       m = to, l = sum;
       if (dg > 0) {  // the tiles' space is free: their MMAs are done
@@ -340,8 +351,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
     int issued = 0, pg = lookup(i0);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int st = i % STAGES, par = (i / STAGES - 1) & 1, ti = i0 + i;
-      const int mine = pg;
+      const int ti = i0 + i, mine = pg;
       pg = lookup(ti + 1);
       const bool bad = __any_sync(0xffffffffu, mine == -2);
       if (bad && lane == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
@@ -351,27 +361,26 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       bool ok = true;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        unsigned long long* full = kv ? &ms->v_full[st] : &ms->k_full[st];
-        const uint32_t dst = sb + Sh::OFF_KV + st * 2 * Sh::TILE + kv * Sh::TILE;
-        ok = ok && (i < STAGES || wait_bar(kv ? &ms->v_free[st] : &ms->k_free[st], par, stop));
+        const int use = 2 * i + kv, unit = use % UNITS;
+        const uint32_t full = smem_u32(&ms->full[unit]), dst = sb + Sh::OFF_KV + unit * Sh::TILE;
+        if (use >= UNITS) ok = ok && wait_bar(&ms->free_[unit], (use / UNITS - 1) & 1, stop);
         if (!ok) break;
-        if (kv == 0 && lane == 0) *(volatile int*)&ms->no_page[i & 3] = bad;
-        if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), bytes);
+        if (kv == 0 && lane == 0) *(volatile int*)&ms->no_page[i & 7] = bad;
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
         __syncwarp();
         if (tree) {
-          if (lane < DB) tma_load_2d(dst + lane * BLK, kv ? &tvt : &tkt, kvh * D + lane * 64, s * a.n, smem_u32(full));
+          if (lane < DB) tma_load_2d(dst + lane * BLK, kv ? &tvt : &tkt, kvh * D + lane * 64, s * a.n, full);
         } else if (mine >= 0) {
 #pragma unroll
-          for (int c = 0; c < DB; ++c)
-            tma_load_2d(dst + c * BLK + lane * box * 128, kv ? &tvp : &tkp, c * 64, crd, smem_u32(full));
+          for (int c = 0; c < DB; ++c) tma_load_2d(dst + c * BLK + lane * box * 128, kv ? &tvp : &tkp, c * 64, crd, full);
         }
-        issued = 2 * i + kv + 1;
+        issued = use + 1;
       }
-      if (!ok) break;
-    }
-    if (lane == 0 && *stop) {  // copies in flight land before the shared memory is given up
-      for (int k = max(0, issued - 2 * STAGES); k < issued; ++k)
-        mbar_poll_ns(smem_u32(k & 1 ? &ms->v_full[k / 2 % STAGES] : &ms->k_full[k / 2 % STAGES]), (k / 2 / STAGES) & 1, kWaitLimitNs);
+      if (!ok) {  // copies in flight land before the shared memory is given up
+        for (int k = max(0, issued - UNITS); k < issued && lane == 0; ++k)
+          mbar_poll_ns(smem_u32(&ms->full[k % UNITS]), (k / UNITS) & 1, kWaitLimitNs);
+        break;
+      }
     }
   } else {
     // ---- MMAs: S of a tile, then P . V of the one before ----
@@ -381,31 +390,32 @@ __global__ void __launch_bounds__(ATHREADS, 2)
 #pragma unroll 1
     for (int i = 0; i <= n && ok; ++i) {
       if (i < n) {
-        ok = wait_bar(&ms->k_full[i % STAGES], (i / STAGES) & 1, stop) && (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
+        const int use = 2 * i, unit = use % UNITS;
+        ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) && (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          const uint32_t qd = desc_lo(sb, 16), kd = desc_lo(sb + Sh::OFF_KV + (i % STAGES) * 2 * Sh::TILE, 16);
+          const uint32_t qd = desc_lo(sb, 16), kd = desc_lo(sb + Sh::OFF_KV + unit * Sh::TILE, 16);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             mma_ss<id_s>(tmem + A_S, qd + (((k >> 2) * 2 * BLK + (k & 3) * 32) >> 4), kd + (((k >> 2) * BLK + (k & 3) * 32) >> 4), k > 0);
-          mma_commit(smem_u32(&ms->k_free[i % STAGES]));
           mma_commit(smem_u32(&ms->s_full));
+          mma_commit(smem_u32(&ms->free_[unit]));
         }
         __syncwarp();
       }
       if (i > 0) {
-        const int j = i - 1;
-        ok = wait_bar(&ms->v_full[j % STAGES], (j / STAGES) & 1, stop) && wait_bar(&ms->p_full[j & 1], (j / 2) & 1, stop);
+        const int j = i - 1, use = 2 * j + 1, unit = use % UNITS;
+        ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) && wait_bar(&ms->p_full[j & 1], (j / 2) & 1, stop);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          const uint32_t vd = desc_lo(sb + Sh::OFF_KV + (j % STAGES) * 2 * Sh::TILE + Sh::TILE, BLK);
+          const uint32_t vd = desc_lo(sb + Sh::OFF_KV + unit * Sh::TILE, BLK);
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)  // 16 keys: two groups of 8 rows
             mma_ts<id_o>(tmem + A_O, tmem + A_P + (j & 1) * 32 + k * 8, vd + k * (2048 >> 4), j + k > 0);
-          mma_commit(smem_u32(&ms->v_free[j % STAGES]));
           mma_commit(smem_u32(&ms->o_done));
+          mma_commit(smem_u32(&ms->free_[unit]));
         }
         __syncwarp();
       }
@@ -426,35 +436,48 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   }
 }
 
-// o = sum over the splits of 2^(m_i - m) o_i / sum of 2^(m_i - m) l_i; a warp per query row, D / 32 columns a lane
-template <int D>
+// o = sum over the splits of 2^(m_i - m) o_i / sum of 2^(m_i - m) l_i; W warps to a query row, each a part of its splits, D / 32
+// columns a lane
+template <int D, int W>
 __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a) {
+  constexpr int V = D / 32;
+  __shared__ float part_s[W > 1 ? 4 : 1][W > 1 ? D + 1 : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
+  const long long row = (long long)blockIdx.x * (4 / W) + warp / W;  // (s, node, head)
   grid_dependency_wait();
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);  // (s, node, head)
-  const int lane = threadIdx.x & 31;
-  if (row >= (long long)a.S * a.n * a.Hq) return;
+  if (row >= (long long)a.S * a.n * a.Hq) return;  // W = 4: the whole block
   const long long tok = row / a.Hq;
   const int head = (int)(row % a.Hq), s = (int)(tok / a.n);
   int len = a.cache_len[s];
   if (len < 0 || len > a.max_len || (long long)len > ((long long)a.max_pages << a.page_shift)) len = 0;
   const int ns = ((len + KT - 1) / KT + 1 + a.tps - 1) / a.tps;  // splits that had a tile
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.splits;
-  float mx = -INFINITY;
-  for (int i = lane; i < ns; i += 32) mx = fmaxf(mx, ml[i].x);
+  // two splits a lane: there are 64 at most
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2 e0 = lane < ns ? ml[lane] : none, e1 = lane + 32 < ns ? ml[lane + 32] : none;
+  float mx = fmaxf(e0.x, e1.x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float ref = mx == -INFINITY ? 0.f : mx;
-  constexpr int V = D / 32;
+  const float f0 = exp2_sfu(e0.x - ref), f1 = exp2_sfu(e1.x - ref);
+  const float sum = warp_sum(fmaf(f0, e0.y, f1 * e1.y));
   float acc[V] = {};
-  float sum = 0.f;
   const float* p = a.part + row * a.splits * D + lane * V;
-#pragma unroll 4
-  for (int i = 0; i < ns; ++i) {
-    const float2 e = ml[i];
-    const float f = exp2_sfu(e.x - ref);
-    sum = fmaf(f, e.y, sum);
+#pragma unroll 8
+  for (int i = w; i < ns; i += W) {
+    const float f = __shfl_sync(0xffffffffu, i < 32 ? f0 : f1, i & 31);
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = fmaf(f, p[(long long)i * D + v], acc[v]);
+  }
+  if (W > 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) part_s[warp][lane * V + v] = acc[v];
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int k = 1; k < W; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += part_s[warp + k][lane * V + v];
   }
   const float inv = 1.f / sum;
   uint16_t* o = a.o + tok * a.ldo + head * D + lane * V;
@@ -488,7 +511,8 @@ AttendPlan plan_attend(int S, int n, int Hq, int Hkv, int max_len) {
 template <int D, int DUP>
 cudaError_t run_attend(const AttendArgs& a, const AttendPlan& p, const CUtensorMap (&m)[4], cudaStream_t s) {
   using Sh = AttendSmem<D>;
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::BYTES);
+  static bool done[64];
+  cudaError_t e = allow_smem(attend_kernel<D, DUP>, Sh::BYTES, done);
   if (e != cudaSuccess) return e;
   attend_kernel<D, DUP><<<dim3((unsigned)(p.splits * p.row_tiles), (unsigned)a.Hkv, (unsigned)a.S), ATHREADS, Sh::BYTES, s>>>(
       m[0], m[1], m[2], m[3], a);
@@ -509,7 +533,9 @@ cudaError_t run_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream_t 
   cudaError_t e = p.dup == 4 ? run_attend<D, 4>(a, p, m, s) : p.dup == 2 ? run_attend<D, 2>(a, p, m, s) : run_attend<D, 1>(a, p, m, s);
   if (e != cudaSuccess || p.splits == 1) return e;
   cudaLaunchConfig_t cfg{};  // its blocks are placed while the last of the splits run
-  cfg.gridDim = dim3((unsigned)(((long long)a.S * a.n * a.Hq + 3) / 4));
+  const long long out_rows = (long long)a.S * a.n * a.Hq;
+  const bool wide = p.splits >= 8;  // four warps to a row: 37 splits of 32 rows 17.6 -> 4 us
+  cfg.gridDim = dim3((unsigned)(wide ? out_rows : (out_rows + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -517,7 +543,7 @@ cudaError_t run_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, combine_kernel<D>, a);
+  e = wide ? cudaLaunchKernelEx(&cfg, combine_kernel<D, 4>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<D, 1>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -9,6 +9,17 @@ namespace ssmtree {
 
 constexpr int kSMs = 152;  // streaming multiprocessors of a GB300: what the launch plans divide work over
 
+// a kernel's dynamic shared memory, asked for once per device (done: a table of the caller's, one for each kernel)
+template <typename Kernel>
+cudaError_t allow_smem(Kernel* kernel, int bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  return e;
+}
+
 // the token rows and the cache slot of sequence s; false (and the status bit) where they are out of range
 struct SeqArgs {
   int n_seq, n_slots, n_tok, max_len;

@@ -317,9 +317,9 @@ cudaError_t launch_prompt_scan(const ScanArgs& args, void* workspace, cudaStream
   ScanArgs a = args;
   a.nseg = plan_segments(a.H, a.q.n_seq, a.q.max_len);
   a.seg_state = static_cast<float*>(workspace);
-  cudaError_t e = cudaFuncSetAttribute(prompt_scan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(prompt_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  static bool done[2][64];
+  cudaError_t e = allow_smem(prompt_scan_kernel<false>, SMEM, done[0]);
+  if (e == cudaSuccess) e = allow_smem(prompt_scan_kernel<true>, SMEM, done[1]);
   if (e != cudaSuccess) return e;
   if (a.nseg > 1)
     prompt_scan_kernel<true><<<dim3((unsigned)a.H, (unsigned)(a.q.n_seq * (a.nseg - 1))), THREADS, SMEM, s>>>(a);

@@ -638,9 +638,9 @@ cudaError_t launch_prompt_scan_tc(const ScanArgs& args, void* workspace, cudaStr
   Decays* decays = reinterpret_cast<Decays*>(ws);
   ws += decay_bytes(a.q.n_seq, a.q.n_tok, a.H);
   a.seg_state = reinterpret_cast<float*>(ws);
-  cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(scan_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM);
+  static bool done[2][64];
+  cudaError_t e = allow_smem(scan_tc_kernel<false>, TC_SMEM, done[0]);
+  if (e == cudaSuccess) e = allow_smem(scan_tc_kernel<true>, TC_SMEM, done[1]);
   if (e != cudaSuccess) return e;
   CUtensorMap tx, tb, tcm, ty;
   if (!encode_tiles(&tx, a.x, a.q.n_tok, (long long)a.H * kP, a.ldx, Q) || !encode_tiles(&tb, a.B, a.q.n_tok, (long long)a.G * kN, a.ldb, Q) ||

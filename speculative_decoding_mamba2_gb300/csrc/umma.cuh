@@ -99,20 +99,20 @@ __device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
                : "memory");
 }
 
-// The warp waits together.  False once kWaitLimit tries (seconds) have passed or another role has given up.
+// The warp waits together, and all its lanes get the same answer: false once a second has passed or another warp has given
+// up.  (A waiter has to see every phase of a barrier: the parity of one that it skipped would let it through early.)
 __device__ __forceinline__ bool wait_bar(unsigned long long* bar, uint32_t parity, volatile int* stop) {
   const uint32_t b = smem_u32(bar);
-  unsigned it = 0;
-  while (!mbar_try_wait(b, parity)) {
-    if ((++it & 1023) == 0 && (*stop || it > kWaitLimit)) {
-      *stop = 1;
-      break;
-    }
+  if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+  const unsigned long long t0 = global_time_ns();
+#pragma unroll 1
+  for (unsigned it = 1; it < kWaitLimit; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+    if ((it & 63) == 0 && __any_sync(0xffffffffu, *stop || global_time_ns() - t0 > kWaitLimitNs)) break;
   }
-  __syncwarp();
-  return (it & 1023) != 0 || it == 0 || !*stop;
+  *stop = 1;
+  return false;
 }
-
 // ---- host ----
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
