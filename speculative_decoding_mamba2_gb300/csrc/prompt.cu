@@ -1,23 +1,35 @@
 // The conv of prompts and the recurrence of single tokens (ssm_prompt.h).
 //
-// prompt_conv_kernel.  post[t][c] = SiLU(b[c] + sum_k w[c][k] row[t-3+k][c]): four products and one SiLU
-// per element against 4 bytes of traffic, so HBM binds long prompts.  A CTA takes TB tokens of one
-// sequence and all channels, a thread 8 channels (16-byte loads); its rows and the three before them are
-// in flight together and the window then slides in registers, so a row is read 1 + 3/TB times, all but
-// the first time from L2.  Blocks follow the sequences (grid y), not the token rows: only a sequence's
-// first block reads its ring, and the same threads then write the ring's new rows and advance its head,
-// so one launch needs no order between CTAs.
+// prompt_conv_kernel.  post[t][c] = SiLU(b[c] + sum_k w[c][k] row[t-3+k][c]): four products and one SiLU per element against
+// 4 bytes of traffic, so HBM and the special-function unit (two results an element) bind long prompts.  A block takes TB
+// tokens of one sequence and up to CB channels: all its rows and the three before them are asked for at once (cp.async,
+// 54 KB a block, four blocks to an SM), then a thread slides over them with its pair of channels, eight
+// tokens as soon as they are there; a row is read 1 + 3/TB times, the second time from L2.  (With the rows in registers the
+// loads of a block could not run beside another's arithmetic: 60 us at best for 8209 tokens of 5376 channels.)  Tiles follow
+// the sequences (grid y), not the token rows: only a sequence's first tile reads its ring, and the same threads then write
+// the ring's new rows; the head is advanced once the channel blocks, a cluster, have read it, so one launch needs no other
+// order.
 //
 // scan_step_kernel.  h' = a h + D x (x) B, y = C h' + D x for one token: 4 operations for each 8 bytes of
 // state, HBM bound.  A CTA takes one head's 64 x 128 state, a warp 8 of its rows with their 8 row loads in
 // flight, lane l columns 4l .. 4l+3; the 8 row sums of C h' are reduced together (each shuffle halves the
 // rows a lane carries: 9 shuffles instead of 40).
+#include "mma_tiles.cuh"
 #include "prompt.cuh"
 
 namespace ssmtree {
 namespace {
 
-constexpr int TB = 8;  // tokens per conv CTA
+constexpr int TB = 32;              // tokens per conv block
+constexpr int CB = 768;             // channels at most
+constexpr int CONV_THREADS = CB / 2;
+constexpr int CONV_SMEM = (TB + 3) * CB * 2;
+
+__device__ __forceinline__ uint32_t pack2bf(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 struct Row8 {  // 8 channels of a row, fp32
   float v[8];
@@ -28,69 +40,100 @@ __device__ __forceinline__ Row8 row8(uint4 u) {
   r.v[4] = bf16_lo(u.z), r.v[5] = bf16_hi(u.z), r.v[6] = bf16_lo(u.w), r.v[7] = bf16_hi(u.w);
   return r;
 }
-__device__ __forceinline__ uint32_t pack2bf(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
+// SiLU v / (1 + 2^(-v log2 e)) on the special-function unit (relative error about 1e-6; where 2^t is infinite the quotient is 0)
+__device__ __forceinline__ float silu_sfu(float v) {
+  float e, q;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));
+  return v * q;
 }
 
-__global__ void __launch_bounds__(256) prompt_conv_kernel(ConvArgs a) {
-  const int s = blockIdx.y, t0 = blockIdx.x * TB;
+__global__ void __launch_bounds__(CONV_THREADS, 4) prompt_conv_kernel(ConvArgs a) {
+  extern __shared__ __align__(16) uint16_t rows_s[];
+  const int s = blockIdx.y, t0 = blockIdx.x * TB, tid = threadIdx.x, cb = 2 * blockDim.x;
   int first, len, slot;
   if (!seq_range(a.q, s, first, len, slot)) {
-    if (t0 == 0 && threadIdx.x == 0) flag(a.q.status, SSM_STATUS_SEQ_RANGE);
+    if (t0 == 0 && blockIdx.z == 0 && tid == 0) flag(a.q.status, SSM_STATUS_SEQ_RANGE);
     return;
   }
   if (t0 >= len) return;
   const int nt = min(TB, len - t0), cd = a.conv_dim;
   const long long inst = (long long)slot * a.L + a.layer;
   const int head = t0 == 0 ? a.ring_head[inst] : 0;
+  if (t0 == 0) asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");  // the head has been read
   uint16_t* ring = a.ring + inst * a.R * cd;
-  for (int c = 8 * threadIdx.x; c < cd; c += 8 * blockDim.x) {
-    const uint16_t* x = a.x + (long long)(first + t0) * a.ldx + c;
-    uint4 in[TB + 3];
-    if (t0 == 0) {
+#pragma unroll 1
+  for (int c0 = blockIdx.z * cb; c0 < cd; c0 += cb * gridDim.z) {  // (more than once above 8 blocks of channels)
+  if (c0 >= cb * gridDim.z) __syncthreads();  // the last rows have been read
+  {  // rows t0 - 3 .. t0 + nt - 1, four at a time, in groups of eight
+    const int chunks = cb / 8, ch = tid % chunks, r0 = tid / chunks;
+    uint16_t* dst = rows_s + r0 * cb + ch * 8;
+    const int last = c0 + ch * 8 < cd ? nt + 3 : 0;
+    const long long step = 4 * a.ldx;
+    const uint16_t* x = a.x + (long long)(first + t0 - 3 + r0) * a.ldx + c0 + ch * 8;
 #pragma unroll
-      for (int j = 0; j < 3; ++j)
-        in[j] = *reinterpret_cast<const uint4*>(ring + (long long)ring_pos(head, j - 3, a.R) * cd + c);
-    } else {
+    for (int k = 0; k < (TB + 3 + 3) / 4; ++k) {
+      if (r0 + 4 * k < last)
+        cp_async16(dst, k == 0 && t0 == 0 && r0 < 3 ? ring + (long long)ring_pos(head, r0 - 3, a.R) * cd + c0 + ch * 8 : x);
+      x += step, dst += 4 * cb;
+      if (k & 1) cp_async_commit();
+    }
+    cp_async_commit();
+  }
+  const int c = c0 + 2 * tid;
+  const bool mine = c < cd;
+  float4 u = {}, v = {};
+  float2 bb = {};
+  if (mine) {
+    u = *reinterpret_cast<const float4*>(a.conv_w + (size_t)c * 4);
+    v = *reinterpret_cast<const float4*>(a.conv_w + (size_t)c * 4 + 4);
+    bb = *reinterpret_cast<const float2*>(a.conv_b + c);
+  }
+  const uint32_t* col = reinterpret_cast<const uint32_t*>(rows_s) + tid;
+  const int pitch = cb / 2;  // words of a row
+  uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (long long)(first + t0) * a.ldo + c);
+  const long long ld = a.ldo / 2;
+  const int stores = mine ? nt : 0;
+  float l0 = 0.f, l1 = 0.f, l2 = 0.f, h0 = 0.f, h1 = 0.f, h2 = 0.f;  // the three rows before, of either channel
 #pragma unroll
-      for (int j = 0; j < 3; ++j) in[j] = *reinterpret_cast<const uint4*>(x + (j - 3) * a.ldx);
+  for (int g = 0; g < TB / 8; ++g) {  // eight tokens: their rows are in the first g + 2 groups
+    if (8 * g >= nt && g > 0) continue;  // (the same for the whole block)
+    if (g == 0)
+      cp_async_wait<TB / 8 - 1>();
+    else if (g == 1)
+      cp_async_wait<TB / 8 - 2>();
+    else if (g == 2)
+      cp_async_wait<TB / 8 - 3>();
+    else
+      cp_async_wait<0>();
+    __syncthreads();
+    if (g == 0) {
+      const uint32_t r0 = col[0], r1 = col[pitch], r2 = col[2 * pitch];
+      l0 = bf16_lo(r0), l1 = bf16_lo(r1), l2 = bf16_lo(r2), h0 = bf16_hi(r0), h1 = bf16_hi(r1), h2 = bf16_hi(r2);
+      col += 3 * pitch;
     }
 #pragma unroll
-    for (int j = 0; j < TB; ++j)
-      if (j < nt) in[3 + j] = *reinterpret_cast<const uint4*>(x + j * a.ldx);
-    float4 w[8];
-    float b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = *reinterpret_cast<const float4*>(a.conv_w + (size_t)(c + i) * 4);
-      b[i] = a.conv_b[c + i];
-    }
-    uint16_t* o = a.out + (long long)(first + t0) * a.ldo + c;
-    Row8 r0 = row8(in[0]), r1 = row8(in[1]), r2 = row8(in[2]);
-#pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      if (j < nt) {
-        const Row8 r3 = row8(in[3 + j]);
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = silu_fast(conv4_acc(w[i], b[i], r0.v[i], r1.v[i], r2.v[i], r3.v[i]));
-        *reinterpret_cast<uint4*>(o + j * a.ldo) =
-            make_uint4(pack2bf(v[0], v[1]), pack2bf(v[2], v[3]), pack2bf(v[4], v[5]), pack2bf(v[6], v[7]));
-        r0 = r1, r1 = r2, r2 = r3;
-      }
-    }
-    if (t0 == 0) {  // the sequence's last rows into the ring (this thread has read its channels of the old ones)
-      const uint16_t* xl = a.x + (long long)first * a.ldx + c;
-      for (int t = max(0, len - 3); t < len; ++t)
-        *reinterpret_cast<uint4*>(ring + (long long)ring_pos(head, t, a.R) * cd + c) =
-            *reinterpret_cast<const uint4*>(xl + t * a.ldx);
+    for (int j = 8 * g; j < 8 * g + 8; ++j) {
+      const uint32_t r = *col;  // (behind the last row: whatever stands there, for no output)
+      col += pitch;
+      const float l3 = bf16_lo(r), h3 = bf16_hi(r);
+      const uint32_t y = pack2bf(silu_sfu(conv4_acc(u, bb.x, l0, l1, l2, l3)), silu_sfu(conv4_acc(v, bb.y, h0, h1, h2, h3)));
+      if (j < stores) *o = y;
+      o += ld;  // (a pointer that moves: products j * ldo took three quarters of the instructions)
+      l0 = l1, l1 = l2, l2 = l3, h0 = h1, h1 = h2, h2 = h3;
     }
   }
+  if (t0 == 0 && mine) {  // the sequence's last rows into the ring (its old ones are in shared memory)
+    const uint16_t* xl = a.x + (long long)first * a.ldx + c;
+#pragma unroll 1
+    for (int t = max(0, len - 3); t < len; ++t)
+      *reinterpret_cast<uint32_t*>(ring + (long long)ring_pos(head, t, a.R) * cd + c) =
+          *reinterpret_cast<const uint32_t*>(xl + t * a.ldx);
+  }
+  }
   if (t0 == 0) {
-    __syncthreads();  // every thread has read the head
-    if (threadIdx.x == 0) a.ring_head[inst] = head + len;
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    if (blockIdx.z == 0 && tid == 0) a.ring_head[inst] = head + len;
   }
 }
 
@@ -158,12 +201,23 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
 
 cudaError_t launch_prompt_conv(const ConvArgs& a, cudaStream_t s) {
   if (a.q.n_seq == 0 || a.q.n_tok == 0 || a.q.max_len == 0) return cudaSuccess;
-  // channel vectors in equal passes of at most 256 threads, whole warps
-  const int nv = a.conv_dim / 8, passes = (nv + 255) / 256;
-  const int threads = ((nv + passes - 1) / passes + 31) / 32 * 32;
-  const dim3 grid((unsigned)((min(a.q.max_len, a.q.n_tok) + TB - 1) / TB), (unsigned)a.q.n_seq);
-  prompt_conv_kernel<<<grid, threads, 0, s>>>(a);
-  return cudaGetLastError();
+  // the channels over blocks of equal size, whole warps; a cluster has 8 of them at most
+  const int need = (a.conv_dim + CB - 1) / CB, blocks = min(8, need);
+  static bool done[64];
+  cudaError_t e = allow_smem(prompt_conv_kernel, CONV_SMEM, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((min(a.q.max_len, a.q.n_tok) + TB - 1) / TB), (unsigned)a.q.n_seq, (unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)(((a.conv_dim + need - 1) / need + 63) / 64 * 32));
+  cfg.dynamicSmemBytes = (size_t)(TB + 3) * cfg.blockDim.x * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = (unsigned)blocks;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, prompt_conv_kernel, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s) {

@@ -117,8 +117,8 @@ extern "C" int ssm_prompt_conv(const ssm_dims* dims, const ssm_params* prm, int3
   if (n_tok > 0 && (!xBC || !out)) return pfail(SSM_ERR_INVALID_ARG, fn, "a tensor pointer is NULL");
   if (ldx < cd || ldo < cd || ((ldx | ldo) & 7))
     return pfail(SSM_ERR_INVALID_ARG, fn, "ldx and ldo must be >= conv_dim and multiples of 8");
-  if (off16(xBC) || off16(out) || off16(ring) || off16(prm->conv_w))
-    return pfail(SSM_ERR_INVALID_ARG, fn, "xBC, out, ring and conv_w must be 16-byte aligned");
+  if (off16(xBC) || off16(out) || off16(ring) || off16(prm->conv_w) || off16(prm->conv_b))
+    return pfail(SSM_ERR_INVALID_ARG, fn, "xBC, out, ring, conv_w and conv_b must be 16-byte aligned");
   if (n_tok > 0 && xBC == out) return pfail(SSM_ERR_INVALID_ARG, fn, "out must not be xBC");
   ConvArgs a{};
   a.q = SeqArgs{n_seq, n_slots, n_tok, max_len, cu_seqlens, slots, dev_status};

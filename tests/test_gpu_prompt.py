@@ -302,7 +302,7 @@ def test_scan_steps_follow_a_prompt():
     assert (np.abs(host(h)[c["slots"][0], 0] - rh) <= 2e-5 * mh).all()
 
 
-@pytest.mark.parametrize("H,lens", [(1, [1]), (3, [1, 2, 3, 4]), (2, [7, 8, 9, 0, 25]), (24, [1, 1, 1]), (80, [19, 2])])
+@pytest.mark.parametrize("H,lens", [(1, [1]), (3, [1, 2, 3, 4]), (2, [7, 8, 9, 0, 25]), (24, [1, 1, 1]), (80, [19, 2]), (2, [35, 32, 33, 71]), (130, [37, 1])])
 def test_prompt_conv(H, lens):
     from speculative_decoding_mamba2_gb300 import Dims, ssm_prompt_conv
     rng = np.random.default_rng([21, H])
