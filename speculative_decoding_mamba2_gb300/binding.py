@@ -516,12 +516,20 @@ def _slots_of(cache, name: str, per_slot: int) -> int:
     return cache.numel() // per_slot
 
 
+_BF16 = torch.bfloat16
+
+
 def _tok_rows(t, name: str, cols: int | None = None):
     """_rows of a bf16 tensor that may have no rows (whose strides then say nothing)."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.size(0) == 0 and t.dtype == torch.bfloat16 \
-            and cols in (None, t.size(1)):
-        return None, 0, (t.size(1) + 7) // 8 * 8
-    return _rows(t, name, torch.bfloat16, cols)
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _BF16 and t.dim() == 2:
+        rows, c = t.shape
+        if cols is None or c == cols:
+            if rows == 0:
+                return None, 0, (c + 7) // 8 * 8
+            ld, inner = t.stride()
+            if inner == 1 or c <= 1:
+                return t.data_ptr(), rows, ld
+    return _rows(t, name, _BF16, cols)  # says what is wrong
 
 
 def _opt_slots(slots, n_seq: int):
@@ -558,17 +566,18 @@ def _scan_params(prm: dict, d: Dims) -> ssm_params:
 def _scan_tensors(d: Dims, x, B, C, dt, h_in, h_out, y):
     """(rows, groups, slots, the (pointer, stride) pairs of x, B, C, dt, h_in, h_out, (y, stride))."""
     px, T, ldx = _tok_rows(x, "x", d.d_inner)
-    if B.dim() != 2 or B.size(1) < d.d_state or B.size(1) % d.d_state:
-        raise ValueError("B: [rows, n_groups * d_state]")
     pb, Tb, ldb = _tok_rows(B, "B")
-    pc, Tc, ldc = _tok_rows(C, "C", B.size(1))
+    cols = B.size(1)
+    if cols < d.d_state or cols % d.d_state:
+        raise ValueError("B: [rows, n_groups * d_state]")
+    pc, Tc, ldc = _tok_rows(C, "C", cols)
     pd, Td, ldd = _tok_rows(dt, "dt", d.n_heads)
     py, Ty, ldy = _tok_rows(y, "y", d.d_inner)
     if not T == Tb == Tc == Td == Ty:
         raise ValueError("x, B, C, dt and y: as many rows each")
     n_slots = _slots_of(h_out, "h_out", d.n_layers * d.n_heads * d.head_dim * d.d_state)
     hi = None if h_in is None else _dev(h_in, "h_in", torch.float32, h_out.numel())
-    return T, B.size(1) // d.d_state, n_slots, (px, ldx, pb, ldb, pc, ldc, pd, ldd, hi,
+    return T, cols // d.d_state, n_slots, (px, ldx, pb, ldb, pc, ldc, pd, ldd, hi,
                                                 _dev(h_out, "h_out", torch.float32), py, ldy)
 
 
@@ -592,8 +601,7 @@ def ssm_prompt_scan(dims: Dims, params: dict, layer: int, cu_seqlens, max_len: i
     _check(lib().ssm_prompt_scan(
         ctypes.byref(cd), ctypes.byref(cp), int(layer), G, n_seq, n_slots, T, int(max_len),
         _dev(cu_seqlens, "cu_seqlens", torch.int32, n_seq + 1), _opt_slots(slots, n_seq), *t,
-        _dev(workspace, "workspace", torch.uint8), ctypes.c_size_t(workspace.numel()), _opt_status(status),
-        _stream(stream, x)))
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _opt_status(status), _stream(stream, x)))
 
 
 def ssm_scan_step(dims: Dims, params: dict, layer: int, x, B, C, dt, h_in, h_out, y, slots=None, status=None,
@@ -619,10 +627,18 @@ def ssm_tree_attention_workspace_size(n_seq: int, n_nodes: int, Hq: int, Hkv: in
 
 
 def _pages(k_pages, v_pages, lead: int, Hkv: int, D: int):
-    """(n_pages, page_size) of page tensors [..lead.., n_pages, Hkv, page_size, D]."""
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != lead + 4 or k_pages.size(-3) != Hkv or k_pages.size(-1) != D:
+    """(address of each, n_pages, page_size) of page tensors [..lead.., n_pages, Hkv, page_size, D]."""
+    shape = k_pages.shape if isinstance(k_pages, torch.Tensor) else ()
+    if len(shape) != lead + 4 or shape[-3] != Hkv or shape[-1] != D:
         raise ValueError("k_pages: [" + "n_layers, " * lead + "n_pages, Hkv, page_size, D]")
-    return k_pages.size(-4), k_pages.size(-2)
+    return (_dev(k_pages, "k_pages", _BF16), _dev(v_pages, "v_pages", _BF16, k_pages.numel()), shape[-4], shape[-2])
+
+
+def _table(t, name: str, n_seq: int):
+    """(address, columns) of an int32 tensor with a row for each sequence."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.size(0) != n_seq:
+        raise ValueError(f"{name}: a row for each sequence")
+    return _dev(t, name, torch.int32), t.size(1)
 
 
 def ssm_tree_attention(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, layout, q, k, v, k_pages, v_pages, page_table,
@@ -631,19 +647,18 @@ def ssm_tree_attention(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, layo
     [S * n, Hq * D], k, v: bf16 [S * n, Hkv * D] (any row stride); k_pages, v_pages: bf16
     [n_pages, Hkv, page_size, D]; page_table: int32 [S, max_pages]."""
     S, n = n_seq, n_nodes
-    rows = [_tok_rows(t, nm, h * D) for t, nm, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv), (o, "o", Hq))]
-    if any(r[1] != S * n for r in rows):
+    pq, rq, ldq = _tok_rows(q, "q", Hq * D)
+    pk, rk, ldk = _tok_rows(k, "k", Hkv * D)
+    pv, rv, ldv = _tok_rows(v, "v", Hkv * D)
+    po, ro, ldo = _tok_rows(o, "o", Hq * D)
+    if not rq == rk == rv == ro == S * n:
         raise ValueError("q, k, v and o: n_seq * n_nodes rows each")
-    n_pages, page = _pages(k_pages, v_pages, 0, Hkv, D)
-    if page_table.dim() != 2 or page_table.size(0) != S:
-        raise ValueError("page_table: [n_seq, max_pages]")
-    (pq, _, ldq), (pk, _, ldk), (pv, _, ldv), (po, _, ldo) = rows
+    kp, vp, n_pages, page = _pages(k_pages, v_pages, 0, Hkv, D)
+    table, max_pages = _table(page_table, "page_table", S)
     _check(lib().ssm_tree_attention(
-        S, n, Hq, Hkv, D, _dev(layout, "layout", torch.int32, S * n * NODE_WORDS), pq, ldq, pk, ldk, pv, ldv,
-        _dev(k_pages, "k_pages", torch.bfloat16), _dev(v_pages, "v_pages", torch.bfloat16, k_pages.numel()), n_pages, page,
-        _dev(page_table, "page_table", torch.int32), page_table.size(1), _dev(cache_len, "cache_len", torch.int32, S),
-        int(max_cache_len), float(scale), po, ldo, _dev(workspace, "workspace", torch.uint8),
-        ctypes.c_size_t(workspace.numel()), _opt_status(status), _stream(stream, q)))
+        S, n, Hq, Hkv, D, _dev(layout, "layout", torch.int32, S * n * NODE_WORDS), pq, ldq, pk, ldk, pv, ldv, kp, vp, n_pages, page,
+        table, max_pages, _dev(cache_len, "cache_len", torch.int32, S), int(max_cache_len), float(scale), po, ldo,
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _opt_status(status), _stream(stream, q)))
 
 
 def ssm_kv_commit(n_seq: int, n_nodes: int, path, path_len, k, v, k_pages, v_pages, page_table, cache_len, len_out,
@@ -654,13 +669,11 @@ def ssm_kv_commit(n_seq: int, n_nodes: int, path, path_len, k, v, k_pages, v_pag
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 5:
         raise ValueError("k_pages: [n_layers, n_pages, Hkv, page_size, D]")
     L, Hkv, D = k_pages.size(0), k_pages.size(2), k_pages.size(4)
-    n_pages, page = _pages(k_pages, v_pages, 1, Hkv, D)
-    for nm, t in (("path", path), ("page_table", page_table)):
-        if t.dim() != 2 or t.size(0) != S:
-            raise ValueError(f"{nm}: a row for each sequence")
+    kp, vp, n_pages, page = _pages(k_pages, v_pages, 1, Hkv, D)
+    paths, max_path = _table(path, "path", S)
+    table, max_pages = _table(page_table, "page_table", S)
     _check(lib().ssm_kv_commit(
-        L, S, n, Hkv, D, path.size(1), _dev(path, "path", torch.int32), _dev(path_len, "path_len", torch.int32, S),
-        _dev(k, "k", torch.bfloat16, L * S * n * Hkv * D), _dev(v, "v", torch.bfloat16, L * S * n * Hkv * D),
-        _dev(k_pages, "k_pages", torch.bfloat16), _dev(v_pages, "v_pages", torch.bfloat16, k_pages.numel()), n_pages, page,
-        _dev(page_table, "page_table", torch.int32), page_table.size(1), _dev(cache_len, "cache_len", torch.int32, S),
-        _dev(len_out, "len_out", torch.int32, S), _opt_status(status), _stream(stream, k_pages)))
+        L, S, n, Hkv, D, max_path, paths, _dev(path_len, "path_len", torch.int32, S),
+        _dev(k, "k", _BF16, L * S * n * Hkv * D), _dev(v, "v", _BF16, L * S * n * Hkv * D), kp, vp, n_pages, page, table,
+        max_pages, _dev(cache_len, "cache_len", torch.int32, S), _dev(len_out, "len_out", torch.int32, S),
+        _opt_status(status), _stream(stream, k_pages)))
