@@ -7,7 +7,7 @@
 //     Y2 [128 x 64]  = h [128 x n] . C^T                       h rounded to bf16, in tensor memory
 //     Y1 [128 x 64]  = x^T [128 x 64] . P^T                    for each head of the pair, P = scores with their decays
 //     y = Y1 + e^{S_t} Y2 + D x,   h' = decay h + S            (h in fp32 registers for the whole walk)
-// // Scores and decays of the chunks are the same for every walk of them, so prep_kernel makes them first, into the
+// Scores and decays of the chunks are the same for every walk of them, so prep_kernel makes them first, into the
 // workspace.  16 warps then walk through a chunk's steps together -- h' from S, Xw of the next chunk, y, h for the tensor
 // cores, P of the next chunk -- while one warp issues the MMAs that the steps hand over and one the copies (TMA, three
 // stages): the 128 rows of tensor memory are four warps, and the four groups of four share out tokens or columns.  (Warps
@@ -256,7 +256,6 @@ __global__ void __launch_bounds__(NT, 1)
       for (int j = 0; j < 4; ++j) gq[j] = gp[j * Q];
       gp += (long long)a.G * (Q * Q / 4);
     };
-    if (!STATE_ONLY && has_p && n > 0) fetch();
     const uint32_t p_off = (uint32_t)(OFF_P + ph * BLK + t * 128);
     const uint32_t p_ch[2] = {(uint32_t)(((2 * grp4) ^ (t & 7)) << 4), (uint32_t)(((2 * grp4 + 1) ^ (t & 7)) << 4)};
 
@@ -348,6 +347,7 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_wait_st();
         tc_fence_before();
         hand_over(B_XW);
+        if (!STATE_ONLY && has_p) fetch();  // for P below: the loads' time passes during y
       }
       // ---- y of chunk i ----
       if (!STATE_ONLY && i >= 0) {
@@ -469,7 +469,6 @@ __global__ void __launch_bounds__(NT, 1)
           fence_async_smem();
         }
         hand_over(B_P);
-        if (has_p && i + 2 < n) fetch();
       }
       cur = nxt, cd = nd, left -= Q;
       nxt += ST_BYTES, nd += 2 * REC, ++full;
@@ -621,6 +620,10 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, cudaStream_t s,
 
 }  // namespace
 
+// Pairs of heads have to share B and C.  One chunk to a sequence leaves nothing to walk: the kernel of prompt_scan.cu takes
+// it in one launch.  80 heads, event times in us, there | here:
+//   sequences x tokens   1 x 64: 13 | 19    64 x 64: 171 | 199    8 x 65: 46 | 46    64 x 65: 246 | 233    1 x 128: 17 | 21
+//                        1 x 512: 48 | 37   64 x 128: 257 | 234   8 x 512: 134 | 81  64 x 512: 797 | 440
 bool prompt_scan_tc_fits(int H, int G, int n_seq, int max_len) { return (H / G) % 2 == 0 && max_len > 64; }
 
 size_t prompt_scan_tc_workspace_bytes(int H, int G, int n_seq, int n_tok, int max_len) {
