@@ -22,7 +22,7 @@ namespace ssmtree {
 namespace {
 
 constexpr int KT = 64;          // keys per tile
-constexpr int ATHREADS = 192;   // 4 softmax warps, one for copies, one for MMAs
+constexpr int ATHREADS = 224;   // 4 softmax warps, one for copies, two for MMAs
 constexpr int UNITS = 5;         // tiles of K or V in the ring: what lets two CTAs share an SM's memory
 constexpr int BLK = KT * 128;   // 64 rows x 64 columns of bf16
 
@@ -38,7 +38,7 @@ struct AttendSmem {
 };
 struct AttendMisc {
   unsigned long long anc[64];  // ancestors and self of each node
-  unsigned long long full[UNITS], free_[UNITS], q_full, s_full, s_free, p_full[2], o_done, drain;
+  unsigned long long full[UNITS], free_[UNITS], q_full, s_full, s_free, p_full[2], o_done[2], drain[2];
   unsigned int odd[2];         // tree rows with a value of v that is not finite
   uint32_t tmem;
   int stop;
@@ -86,8 +86,10 @@ __global__ void __launch_bounds__(ATHREADS, 2)
     mbar_init(smem_u32(&ms->s_free), 4);
     mbar_init(smem_u32(&ms->p_full[0]), 4);  // two: a warp may be done with a tile before another is with the last one
     mbar_init(smem_u32(&ms->p_full[1]), 4);
-    mbar_init(smem_u32(&ms->o_done), 1);
-    mbar_init(smem_u32(&ms->drain), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ms->o_done[i]), 1);
+      mbar_init(smem_u32(&ms->drain[i]), 1);
+    }
     ms->stop = 0;
     ms->odd[0] = ms->odd[1] = 0;
     fence_barrier_init();
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
         m = mx;
       } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
         const float to = fmaxf(m, mx), f = to == m ? 1.f : exp2_sfu(m - to);
-        ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
+        ok = wait_bar(&ms->o_done[(i - 1) & 1], ((i - 1) / 2) & 1, stop);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
@@ -248,16 +250,12 @@ __global__ void __launch_bounds__(ATHREADS, 2)
         tmem_st8(pt + c / 2, u);
       }
       l += pair_sum(sum2[0]) + pair_sum(sum2[1]);
-      if (i > 0 && i == n - 1) {  // the wait after the last tile must not find o_done two phases on
-        ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
-        if (!ok) break;
-      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[i & 1]));
     }
-    ok = ok && wait_bar(&ms->o_done, (n - 1) & 1, stop);
+    ok = ok && wait_bar(&ms->o_done[(n - 1) & 1], ((n - 1) / 2) & 1, stop);
     // a warp that gives up still takes part in the barriers that others may be waiting at
     if (!ok) asm volatile("bar.arrive 1, 128;\nbar.arrive 2, 128;\nbar.arrive 2, 128;\n" ::: "memory");
     tc_fence_after();
@@ -383,15 +381,19 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       }
     }
   } else {
-    // ---- MMAs: S of a tile, then P . V of the one before ----
-    constexpr uint32_t id_s = idesc_major(128, KT, false, false), id_o = idesc_major(128, D, false, true);
+    // ---- MMAs: one warp those of S, the other P . V, each behind its own waits ----
+    // (A parity wait must find its barrier no further than the phase before: P . V of tile i - 2 done means that the ring
+    // has been through the V that shared S's next unit, that P's buffer is free, and that o_done's other phase is past.)
     const bool leader = elect_one();
-    bool ok = wait_bar(&ms->q_full, 0, stop);
+    bool ok = true;
+    if (warp == 5) {
+      constexpr uint32_t id_s = idesc_major(128, KT, false, false);
+      ok = wait_bar(&ms->q_full, 0, stop);
 #pragma unroll 1
-    for (int i = 0; i <= n && ok; ++i) {
-      if (i < n) {
+      for (int i = 0; i < n && ok; ++i) {
         const int use = 2 * i, unit = use % UNITS;
-        ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) && (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
+        ok = (i < 2 || wait_bar(&ms->o_done[i & 1], (i / 2 - 1) & 1, stop)) && wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) &&
+             (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
         if (!ok) break;
         tc_fence_after();
         if (leader) {
@@ -404,25 +406,28 @@ __global__ void __launch_bounds__(ATHREADS, 2)
         }
         __syncwarp();
       }
-      if (i > 0) {
-        const int j = i - 1, use = 2 * j + 1, unit = use % UNITS;
-        ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) && wait_bar(&ms->p_full[j & 1], (j / 2) & 1, stop);
+    } else {
+      constexpr uint32_t id_o = idesc_major(128, D, false, true);
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const int use = 2 * i + 1, unit = use % UNITS;
+        ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) && wait_bar(&ms->p_full[i & 1], (i / 2) & 1, stop);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
           const uint32_t vd = desc_lo(sb + Sh::OFF_KV + unit * Sh::TILE, BLK);
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)  // 16 keys: two groups of 8 rows
-            mma_ts<id_o>(tmem + A_O, tmem + A_P + (j & 1) * 32 + k * 8, vd + k * (2048 >> 4), j + k > 0);
-          mma_commit(smem_u32(&ms->o_done));
+            mma_ts<id_o>(tmem + A_O, tmem + A_P + (i & 1) * 32 + k * 8, vd + k * (2048 >> 4), i + k > 0);
+          mma_commit(smem_u32(&ms->o_done[i & 1]));
           mma_commit(smem_u32(&ms->free_[unit]));
         }
         __syncwarp();
       }
     }
     if (leader) {
-      mma_commit(smem_u32(&ms->drain));
-      mbar_poll_ns(smem_u32(&ms->drain), 0, kWaitLimitNs);
+      mma_commit(smem_u32(&ms->drain[warp - 5]));
+      mbar_poll_ns(smem_u32(&ms->drain[warp - 5]), 0, kWaitLimitNs);
     }
     __syncwarp();
   }
