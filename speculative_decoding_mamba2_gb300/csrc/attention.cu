@@ -23,22 +23,24 @@ namespace {
 
 constexpr int KT = 64;          // keys per tile
 constexpr int ATHREADS = 224;   // 4 softmax warps, one for copies, two for MMAs
-constexpr int UNITS = 5;         // tiles of K or V in the ring: what lets two CTAs share an SM's memory
+constexpr int UNITS = 6;        // tiles of K and V, by turns, in the ring: what lets two CTAs share an SM's memory
 constexpr int BLK = KT * 128;   // 64 rows x 64 columns of bf16
 
-constexpr int A_S = 0, A_P = 64, A_O = 128, A_COLS = 256;  // tensor memory columns: S, P (two buffers of 32), O
+constexpr int A_S = 0, A_P = 64, A_Q = 96, A_O = 128, A_COLS = 256;  // tensor memory columns: S, P, Q's first 64 columns, O
 
 template <int D>
 struct AttendSmem {
-  static constexpr int OFF_KV = (D / 64) * 2 * BLK;          // after Q: D / 64 blocks of 128 rows
+  static constexpr int OFF_KV = (D / 64 - 1) * 2 * BLK;      // after Q's other columns: 128 rows of 64
   static constexpr int TILE = (D / 64) * BLK;                // K or V of a tile
+  static constexpr int OFF_ML = OFF_KV + 5 * TILE;           // at the end, behind the copies' sums: their maxima
   static constexpr int OFF_MISC = OFF_KV + UNITS * TILE;
   static constexpr int BYTES = OFF_MISC + 768;
   static_assert(BYTES <= 228 * 1024 / 2 - 1024, "two to an SM");
+  static_assert(3 * 32 * (D + 4) * 4 <= 5 * TILE && 1024 <= TILE, "space for the copies' sums");
 };
 struct AttendMisc {
   unsigned long long anc[64];  // ancestors and self of each node
-  unsigned long long full[UNITS], free_[UNITS], q_full, s_full, s_free, p_full[2], o_done[2], drain[2];
+  unsigned long long full[UNITS], free_[UNITS], q_full, s_full, s_free, p_full, o_done, drain[2];
   unsigned int odd[2];         // tree rows with a value of v that is not finite
   uint32_t tmem;
   int stop;
@@ -84,12 +86,10 @@ __global__ void __launch_bounds__(ATHREADS, 2)
     mbar_init(smem_u32(&ms->q_full), 4);
     mbar_init(smem_u32(&ms->s_full), 1);
     mbar_init(smem_u32(&ms->s_free), 4);
-    mbar_init(smem_u32(&ms->p_full[0]), 4);  // two: a warp may be done with a tile before another is with the last one
-    mbar_init(smem_u32(&ms->p_full[1]), 4);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ms->o_done[i]), 1);
-      mbar_init(smem_u32(&ms->drain[i]), 1);
-    }
+    mbar_init(smem_u32(&ms->p_full), 4);
+    mbar_init(smem_u32(&ms->o_done), 1);
+    mbar_init(smem_u32(&ms->drain[0]), 1);
+    mbar_init(smem_u32(&ms->drain[1]), 1);
     ms->stop = 0;
     ms->odd[0] = ms->odd[1] = 0;
     fence_barrier_init();
@@ -103,20 +103,29 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   if (warp < 4) {
     const int r = tid % RG, dg = tid / RG, row = r0 + r;  // this thread's row, and which copy of it
     const int node = row < rows ? row / a.g : 0, qh = row < rows ? row % a.g : 0;
-    {  // q (zero beyond the last row)
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    {  // q (zero beyond the last row): 64 columns in tensor memory, others in shared memory
       const uint4* q = reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + node) * a.ldq + (kvh * a.g + qh) * D);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c)
-        *reinterpret_cast<uint4*>(smem + (c >> 3) * 2 * BLK + tile_off(tid, c & 7, 128)) = row < rows ? q[c] : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < 8; c += 2) {
+        const uint4 x = row < rows ? q[c] : zero, y = row < rows ? q[c + 1] : zero;
+        const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        tmem_st8(tmem + A_Q + lanes + 4 * c, u);
+      }
+#pragma unroll
+      for (int c = 8; c < D / 8; ++c)
+        *reinterpret_cast<uint4*>(smem + ((c >> 3) - 1) * 2 * BLK + tile_off(tid, c & 7, 128)) = row < rows ? q[c] : zero;
+      tmem_wait_st();
+      tc_fence_before();
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
     }
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     if (DUP > 1) {  // the other copies' keys have weight 0
       const uint32_t z[8] = {};
 #pragma unroll
-      for (int c = 0; c < 64; c += 8) tmem_st8(tmem + A_P + lanes + c, z);
+      for (int c = 0; c < 32; c += 8) tmem_st8(tmem + A_P + lanes + c, z);
       tmem_wait_st();
     }
     // ancestor words: a node's own bit, then its parent's word, its grandparent's, ... by doubling
@@ -212,11 +221,13 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       mx = fmaxf(mx, my) * a.scale_log2;
       if (i == 0) {
         m = mx;
-      } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-        const float to = fmaxf(m, mx), f = to == m ? 1.f : exp2_sfu(m - to);
-        ok = wait_bar(&ms->o_done[(i - 1) & 1], ((i - 1) / 2) & 1, stop);
+      } else {  // P . V of the last tile has read its P
+        ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
         if (!ok) break;
         tc_fence_after();
+      }
+      if (i > 0 && __any_sync(0xffffffffu, mx > m + 8.f)) {
+        const float to = fmaxf(m, mx), f = to == m ? 1.f : exp2_sfu(m - to);
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           float o[16];
@@ -236,7 +247,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       const unsigned long long sc2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
       unsigned long long sum2[2] = {0ull, 0ull};
       const unsigned long long one2 = pack2(1.f, 1.f);
-      const uint32_t pt = tmem + A_P + (i & 1) * 32 + lanes + dg * (KK / 2);
+      const uint32_t pt = tmem + A_P + lanes + dg * (KK / 2);
 #pragma unroll
       for (int c = 0; c < KK; c += 16) {
         uint32_t u[8];
@@ -253,15 +264,15 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[i & 1]));
+      if (lane == 0) mbar_arrive(smem_u32(&ms->p_full));
     }
-    ok = ok && wait_bar(&ms->o_done[(n - 1) & 1], ((n - 1) / 2) & 1, stop);
+    ok = ok && wait_bar(&ms->o_done, (n - 1) & 1, stop);
     // a warp that gives up still takes part in the barriers that others may be waiting at
     if (!ok) asm volatile("bar.arrive 1, 128;\nbar.arrive 2, 128;\nbar.arrive 2, 128;\n" ::: "memory");
     tc_fence_after();
     float f = 1.f;
     if (DUP > 1 && ok) {  // the copies' maxima and sums joined
-      float2* ml = reinterpret_cast<float2*>(smem);  // over Q: its MMAs are done
+      float2* ml = reinterpret_cast<float2*>(smem + Sh::OFF_ML);  // the tiles' space is free: their MMAs are done
       ml[tid] = make_float2(m, l);
       named_sync(2, 128);
       float to = -INFINITY, sum = 0.f;
@@ -272,7 +283,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       for (int k = 0; k < DUP; ++k) sum = fmaf(ml[k * RG + r].y, exp2_sfu(ml[k * RG + r].x - ref), sum);
       f = exp2_sfu(m - ref);
       m = to, l = sum;
-      if (dg > 0) {  // the tiles' space is free: their MMAs are done
+      if (dg > 0) {
         float* os = reinterpret_cast<float*>(smem + Sh::OFF_KV) + ((dg - 1) * RG + r) * (D + 4);
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
@@ -382,8 +393,6 @@ __global__ void __launch_bounds__(ATHREADS, 2)
     }
   } else {
     // ---- MMAs: one warp those of S, the other P . V, each behind its own waits ----
-    // (A parity wait must find its barrier no further than the phase before: P . V of tile i - 2 done means that the ring
-    // has been through the V that shared S's next unit, that P's buffer is free, and that o_done's other phase is past.)
     const bool leader = elect_one();
     bool ok = true;
     if (warp == 5) {
@@ -392,15 +401,19 @@ __global__ void __launch_bounds__(ATHREADS, 2)
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
         const int use = 2 * i, unit = use % UNITS;
-        ok = (i < 2 || wait_bar(&ms->o_done[i & 1], (i / 2 - 1) & 1, stop)) && wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) &&
-             (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
+        ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) && (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
         if (!ok) break;
         tc_fence_after();
         if (leader) {
           const uint32_t qd = desc_lo(sb, 16), kd = desc_lo(sb + Sh::OFF_KV + unit * Sh::TILE, 16);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss<id_s>(tmem + A_S, qd + (((k >> 2) * 2 * BLK + (k & 3) * 32) >> 4), kd + (((k >> 2) * BLK + (k & 3) * 32) >> 4), k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t kk = kd + (((k >> 2) * BLK + (k & 3) * 32) >> 4);
+            if (k < 4)
+              mma_ts<id_s>(tmem + A_S, tmem + A_Q + k * 8, kk, k > 0);
+            else
+              mma_ss<id_s>(tmem + A_S, qd + ((((k >> 2) - 1) * 2 * BLK + (k & 3) * 32) >> 4), kk, true);
+          }
           mma_commit(smem_u32(&ms->s_full));
           mma_commit(smem_u32(&ms->free_[unit]));
         }
@@ -411,15 +424,15 @@ __global__ void __launch_bounds__(ATHREADS, 2)
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
         const int use = 2 * i + 1, unit = use % UNITS;
-        ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) && wait_bar(&ms->p_full[i & 1], (i / 2) & 1, stop);
+        ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop) && wait_bar(&ms->p_full, i & 1, stop);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
           const uint32_t vd = desc_lo(sb + Sh::OFF_KV + unit * Sh::TILE, BLK);
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)  // 16 keys: two groups of 8 rows
-            mma_ts<id_o>(tmem + A_O, tmem + A_P + (i & 1) * 32 + k * 8, vd + k * (2048 >> 4), i + k > 0);
-          mma_commit(smem_u32(&ms->o_done[i & 1]));
+            mma_ts<id_o>(tmem + A_O, tmem + A_P + k * 8, vd + k * (2048 >> 4), i + k > 0);
+          mma_commit(smem_u32(&ms->o_done));
           mma_commit(smem_u32(&ms->free_[unit]));
         }
         __syncwarp();
