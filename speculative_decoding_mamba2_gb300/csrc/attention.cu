@@ -45,10 +45,76 @@ struct AttendMisc {
   uint32_t tmem;
   int stop;
   int no_page[8];              // whether a page of tile i (at i % 8) is out of range
+  int most[ATHREADS / 32];     // for the splits, of each warp: tiles of the longest sequence, the least estimate
+  unsigned int least[ATHREADS / 32];
 };
 static_assert(sizeof(AttendMisc) <= 768, "space");
 
 __device__ __forceinline__ float max3f(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// a sequence's cached rows; -1: not a length there is room for
+__device__ __forceinline__ int cached_rows(const AttendArgs& a, int s) {
+  const int len = a.cache_len[s];
+  return len < 0 || len > a.max_len || (long long)len > ((long long)a.max_pages << a.page_shift) ? -1 : len;
+}
+
+// Splits.  Every sequence's tiles are cut into runs of the same length, and every CTA works out that length from the lengths
+// in device memory: of 189 from the longest sequence's tiles down to a 64th of them, each tried by a thread, the one whose
+// CTAs take least, where a CTA costs about four tiles beside its own and joining about two.  (Cut by the longest sequence
+// alone, eight ragged caches of up to 8117 rows took 50 us and four of up to 40009 rows, 101 us.)
+constexpr int CANDIDATES = 189;
+__device__ __forceinline__ int choose_split(const AttendArgs& a, int per, int* tiles, AttendMisc* ms) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int most = 0;
+  for (int s = tid; s < a.S; s += ATHREADS) most = max(most, tiles[s] = (max(cached_rows(a, s), 0) + KT - 1) / KT + 1);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) ms->most[warp] = most;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < ATHREADS / 32; ++w) most = max(most, ms->most[w]);
+  unsigned int key = 0xffffffffu;
+  const unsigned int tps = (3u * most + tid + 2) / (tid + 3);
+  if (tid < CANDIDATES) {
+    unsigned int runs = 0;
+    float total = 0.f;
+    for (int s = 0; s < a.S; ++s) runs += (tiles[s] + tps - 1) / tps, total += (float)tiles[s];
+    if (runs <= (unsigned)a.max_runs) {  // (one run to a sequence always is)
+      constexpr float slots = 2 * kSMs;
+      const float ctas = (float)(runs * per), len = tps + 4.f;
+      const float waves = ceilf(ctas / slots) * len, list = (total * per + 4.f * ctas) / slots + len;
+      const float est = fminf(waves, list) + (runs > (unsigned)a.S ? 2.f : 0.f);
+      key = (unsigned int)fminf(est / most * 65536.f, 16777215.f) << 8 | tid;
+    }
+  }
+  key = __reduce_min_sync(0xffffffffu, key);
+  if (lane == 0) ms->least[warp] = key;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < ATHREADS / 32; ++w) key = min(key, ms->least[w]);
+  const unsigned int c = key & 255u;
+  return (int)((3u * most + c + 2) / (c + 3));
+}
+// the sequence of the run-th run, its first run and their number
+__device__ __forceinline__ bool find_run(int S, const int* tiles, int tps, int run, int& s, int& first, int& runs) {
+  const int lane = threadIdx.x & 31;
+  for (int b = 0, before = 0; b < S; b += 32) {
+    const int k = b + lane < S ? (tiles[b + lane] + tps - 1) / tps : 0;
+    int upto = k;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    const unsigned int past = __ballot_sync(0xffffffffu, before + upto > run);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      s = b + l, runs = __shfl_sync(0xffffffffu, k, l), first = before + __shfl_sync(0xffffffffu, upto, l) - runs;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
 
 template <int D, int DUP>
 __global__ void __launch_bounds__(ATHREADS, 2)
@@ -62,22 +128,12 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   volatile int* stop = &ms->stop;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rows = a.n * a.g, rt = (rows + 127) / 128;
-  const int r0 = (blockIdx.x % rt) * 128, sp = blockIdx.x / rt, kvh = blockIdx.y, s = blockIdx.z;
-  launch_dependents();
+  const int r0 = (blockIdx.x % rt) * 128, run = blockIdx.x / rt, kvh = blockIdx.y;
   if (smem_u32(smem) & 1023u) {
+    grid_dependency_wait();  // no grid ends before the one that it depends on
     if (tid == 0) flag(a.status, SSM_STATUS_TIMEOUT);
     return;
   }
-  int len = __shfl_sync(0xffffffffu, a.cache_len[s], 0);
-  if (len < 0 || len > a.max_len || (long long)len > ((long long)a.max_pages << a.page_shift)) {
-    if (sp == 0 && kvh == 0 && r0 == 0 && tid == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
-    len = 0;
-  }
-  const int ct = (len + KT - 1) / KT;  // tiles of the cache; one more is the tree's
-  const int i0 = sp * a.tps, n = min(ct + 1, i0 + a.tps) - i0;
-  if (n <= 0) return;
-  const bool has_tree = i0 + n == ct + 1;
-
   if (tid == 0) {
     for (int i = 0; i < UNITS; ++i) {
       mbar_init(smem_u32(&ms->full[i]), 1);
@@ -95,10 +151,34 @@ __global__ void __launch_bounds__(ATHREADS, 2)
     fence_barrier_init();
   }
   if (warp == 5) tmem_alloc_warp(smem_u32(&ms->tmem), A_COLS);
+  grid_dependency_wait();  // what the stream's kernels before this one write
+  int s = run, sp = 0, tps = 1 << 30, splits = 1;
+  bool any = true;
+  if (a.max_runs > 0) {
+    int* tiles = reinterpret_cast<int*>(smem);  // space not in use yet
+    int first;
+    tps = choose_split(a, a.Hkv * rt, tiles, ms);
+    any = find_run(a.S, tiles, tps, run, s, first, splits);
+    sp = any ? run - first : 0;
+    if (any && sp == 0 && kvh == 0 && r0 == 0 && tid == 0) a.runs[s] = make_int2(first, splits);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  launch_dependents();  // (not before the tensor memory is there: the next grid's blocks take some too, and wait for this one)
   const uint32_t tmem = __shfl_sync(0xffffffffu, ms->tmem, 0);
+  if (!any) {
+    if (warp == 5) tmem_free_warp(tmem, A_COLS);
+    return;
+  }
+  int len = __shfl_sync(0xffffffffu, cached_rows(a, s), 0);
+  if (len < 0) {
+    if (sp == 0 && kvh == 0 && r0 == 0 && tid == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
+    len = 0;
+  }
+  const int ct = (len + KT - 1) / KT;  // tiles of the cache; one more is the tree's
+  const int i0 = sp * tps, n = min(ct + 1 - i0, tps);
+  const bool has_tree = i0 + n == ct + 1;
 
   if (warp < 4) {
     const int r = tid % RG, dg = tid / RG, row = r0 + r;  // this thread's row, and which copy of it
@@ -332,20 +412,19 @@ __global__ void __launch_bounds__(ATHREADS, 2)
           }
         }
         if (row >= rows) {
-        } else if (a.splits == 1) {
+        } else if (splits == 1) {
           uint32_t u[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) u[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
           uint4* p = reinterpret_cast<uint4*>(a.o + tok * a.ldo + head * D + c);
           p[0] = make_uint4(u[0], u[1], u[2], u[3]), p[1] = make_uint4(u[4], u[5], u[6], u[7]);
         } else {
-          float4* p = reinterpret_cast<float4*>(a.part + ((tok * a.Hq + head) * a.splits + sp) * D + c);
+          float4* p = reinterpret_cast<float4*>(a.part + (((long long)run * a.Hkv + kvh) * rows + row) * D + c);
 #pragma unroll
           for (int j = 0; j < 4; ++j) p[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
       }
-      if (row < rows && a.splits > 1)
-        *reinterpret_cast<float2*>(a.part_ml + ((tok * a.Hq + head) * a.splits + sp) * 2) = make_float2(m, l);
+      if (row < rows && splits > 1) a.part_ml[((long long)run * a.Hkv + kvh) * rows + row] = make_float2(m, l);
     }
   } else if (warp == 4) {
     // ---- copies: lane b the b-th page piece of a tile ----
@@ -460,19 +539,22 @@ template <int D, int W>
 __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a) {
   constexpr int V = D / 32;
   __shared__ float part_s[W > 1 ? 4 : 1][W > 1 ? D + 1 : 1];
+  launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
   const long long row = (long long)blockIdx.x * (4 / W) + warp / W;  // (s, node, head)
   grid_dependency_wait();
   if (row >= (long long)a.S * a.n * a.Hq) return;  // W = 4: the whole block
   const long long tok = row / a.Hq;
-  const int head = (int)(row % a.Hq), s = (int)(tok / a.n);
-  int len = a.cache_len[s];
-  if (len < 0 || len > a.max_len || (long long)len > ((long long)a.max_pages << a.page_shift)) len = 0;
-  const int ns = ((len + KT - 1) / KT + 1 + a.tps - 1) / a.tps;  // splits that had a tile
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.splits;
+  const int head = (int)(row % a.Hq), s = (int)(tok / a.n), g = a.g, rows = a.n * g, kvh = head / g;
+  const int2 run = a.runs[s];  // its first, and how many
+  const int ns = run.y;
+  if (ns == 1) return;  // written already
+  const long long step = (long long)a.Hkv * rows;  // between a row's partial sums
+  const long long at = run.x * step + (long long)kvh * rows + (int)(tok % a.n) * g + head % g;
+  const float2* ml = a.part_ml + at;
   // two splits a lane: there are 64 at most
   const float2 none = make_float2(-INFINITY, 0.f);
-  const float2 e0 = lane < ns ? ml[lane] : none, e1 = lane + 32 < ns ? ml[lane + 32] : none;
+  const float2 e0 = lane < ns ? ml[lane * step] : none, e1 = lane + 32 < ns ? ml[(lane + 32) * step] : none;
   float mx = fmaxf(e0.x, e1.x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -480,12 +562,12 @@ __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a) {
   const float f0 = exp2_sfu(e0.x - ref), f1 = exp2_sfu(e1.x - ref);
   const float sum = warp_sum(fmaf(f0, e0.y, f1 * e1.y));
   float acc[V] = {};
-  const float* p = a.part + row * a.splits * D + lane * V;
+  const float* p = a.part + at * D + lane * V;
 #pragma unroll 8
   for (int i = w; i < ns; i += W) {
     const float f = __shfl_sync(0xffffffffu, i < 32 ? f0 : f1, i & 31);
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = fmaf(f, p[(long long)i * D + v], acc[v]);
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(f, p[i * step * D + v], acc[v]);
   }
   if (W > 1) {
 #pragma unroll
@@ -503,28 +585,21 @@ __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a) {
   for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(o + v) = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
 }
 
-// Copies of the rows, row tiles and splits of the keys.
+// Copies of the rows, row tiles, and the most runs that the sequences are cut into (0: they are not cut, where the CTAs
+// fill the SMs twice over or the longest sequence is too short for what joining costs).
 struct AttendPlan {
-  int dup, row_tiles, tps, splits;
+  int dup, row_tiles, max_runs;
 };
 AttendPlan plan_attend(int S, int n, int Hq, int Hkv, int max_len) {
   AttendPlan p;
   const int rows = n * (Hq / Hkv);
   p.dup = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
   p.row_tiles = (rows + 127) / 128;
-  const int nt = (max_len + KT - 1) / KT + 1;
-  const long long items = (long long)S * Hkv * p.row_tiles, slots = 2 * kSMs;
-  // tiles per split so that the waves of CTAs take least, a split costing about four tiles beside its own
-  double best = 1e300;
-  p.tps = nt, p.splits = 1;
-  for (int sp = 1; sp <= 64 && sp <= nt; ++sp) {
-    const int tps = (nt + sp - 1) / sp, used = (nt + tps - 1) / tps;
-    const long long waves = (items * used + slots - 1) / slots;
-    const double est = (double)waves * (tps + 4.0) + (used > 1 ? 2.0 + 0.1 * used : 0.0);
-    if (est < best * 0.999) best = est, p.tps = tps, p.splits = used;
-  }
+  const long long per = (long long)Hkv * p.row_tiles, slots = 2 * kSMs;
+  p.max_runs = max_len > 5 * KT && S * per < 2 * slots ? S + (int)((slots + per - 1) / per) : 0;
   return p;
 }
+static_assert(2 * 2 * kSMs * 4 <= 6 * 64 * 64 * 2, "the lengths stand in the ring's space");
 
 template <int D, int DUP>
 cudaError_t run_attend(const AttendArgs& a, const AttendPlan& p, const CUtensorMap (&m)[4], cudaStream_t s) {
@@ -532,9 +607,8 @@ cudaError_t run_attend(const AttendArgs& a, const AttendPlan& p, const CUtensorM
   static bool done[64];
   cudaError_t e = allow_smem(attend_kernel<D, DUP>, Sh::BYTES, done);
   if (e != cudaSuccess) return e;
-  attend_kernel<D, DUP><<<dim3((unsigned)(p.splits * p.row_tiles), (unsigned)a.Hkv, (unsigned)a.S), ATHREADS, Sh::BYTES, s>>>(
-      m[0], m[1], m[2], m[3], a);
-  return cudaGetLastError();
+  return launch_early(attend_kernel<D, DUP>, dim3((unsigned)((p.max_runs ? p.max_runs : a.S) * p.row_tiles), (unsigned)a.Hkv),
+                      ATHREADS, Sh::BYTES, s, m[0], m[1], m[2], m[3], a);
 }
 template <int D>
 cudaError_t run_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
@@ -549,20 +623,11 @@ cudaError_t run_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream_t 
       !encode_tiles(&m[3], a.v, (long long)a.S * a.n, cols, a.ldv, KT))
     return cudaErrorInvalidValue;
   cudaError_t e = p.dup == 4 ? run_attend<D, 4>(a, p, m, s) : p.dup == 2 ? run_attend<D, 2>(a, p, m, s) : run_attend<D, 1>(a, p, m, s);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  cudaLaunchConfig_t cfg{};  // its blocks are placed while the last of the splits run
+  if (e != cudaSuccess || p.max_runs == 0) return e;
   const long long out_rows = (long long)a.S * a.n * a.Hq;
-  const bool wide = p.splits >= 8;  // four warps to a row: 37 splits of 32 rows 17.6 -> 4 us
-  cfg.gridDim = dim3((unsigned)(wide ? out_rows : (out_rows + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = wide ? cudaLaunchKernelEx(&cfg, combine_kernel<D, 4>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<D, 1>, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const bool wide = p.max_runs >= 8 * a.S;  // four warps to a row: 37 splits of 32 rows 17.6 -> 4 us
+  const dim3 grid((unsigned)(wide ? out_rows : (out_rows + 3) / 4));
+  return wide ? launch_early(combine_kernel<D, 4>, grid, 128, 0, s, a) : launch_early(combine_kernel<D, 1>, grid, 128, 0, s, a);
 }
 
 // A cluster of 8 CTAs for each sequence: together they copy its path's rows; its length is written by one of them
@@ -628,16 +693,18 @@ __global__ void __cluster_dims__(CCTAS, 1, 1) __launch_bounds__(CTHREADS) kv_com
 
 size_t tree_attention_workspace_bytes(int S, int n, int Hq, int Hkv, int D, int max_len) {
   const AttendPlan p = plan_attend(S, n, Hq, Hkv, max_len);
-  return 256 + (p.splits > 1 ? (size_t)S * n * Hq * p.splits * (D + 2) * sizeof(float) : 0);
+  return 256 + (p.max_runs ? (size_t)p.max_runs * Hkv * n * (Hq / Hkv) * (D + 2) * sizeof(float) + S * sizeof(int2) : 0);
 }
 
 cudaError_t launch_tree_attention(const AttendArgs& args, void* workspace, cudaStream_t s) {
   if (args.S == 0) return cudaSuccess;
   AttendArgs a = args;
   const AttendPlan p = plan_attend(a.S, a.n, a.Hq, a.Hkv, a.max_len);
-  a.tps = p.tps, a.splits = p.splits;
+  const size_t parts = (size_t)p.max_runs * a.Hkv * a.n * a.g;
+  a.max_runs = p.max_runs;
   a.part = static_cast<float*>(workspace);
-  a.part_ml = a.part + (size_t)a.S * a.n * a.Hq * p.splits * a.D;
+  a.part_ml = reinterpret_cast<float2*>(a.part + parts * a.D);
+  a.runs = reinterpret_cast<int2*>(a.part_ml + parts);
   return a.D == 64 ? run_attend_d<64>(a, p, s) : run_attend_d<128>(a, p, s);
 }
 

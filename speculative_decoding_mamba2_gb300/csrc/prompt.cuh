@@ -84,9 +84,10 @@ struct AttendArgs {
   uint16_t* o;
   long long ldo;
   int32_t* status;
-  int tps, splits;  // key tiles per split, splits (set by launch_tree_attention)
-  float* part;      // workspace: partial o, then (maximum, sum) pairs
-  float* part_ml;
+  int max_runs;     // runs of key tiles that the sequences are cut into at most, 0: not cut (set by launch_tree_attention)
+  float* part;      // workspace: partial o, (maximum, sum) pairs, each sequence's first run and their number
+  float2* part_ml;
+  int2* runs;
 };
 size_t tree_attention_workspace_bytes(int S, int n, int Hq, int Hkv, int D, int max_len);
 cudaError_t launch_tree_attention(const AttendArgs& a, void* workspace, cudaStream_t s);

@@ -602,22 +602,6 @@ size_t chunk_count(int n_seq, int n_tok) { return (size_t)(n_tok / Q) + n_seq + 
 size_t score_bytes(int n_seq, int n_tok, int G) { return chunk_count(n_seq, n_tok) * G * Q * Q * sizeof(float); }
 size_t decay_bytes(int n_seq, int n_tok, int H) { return chunk_count(n_seq, n_tok) * H * REC; }
 
-// the second grid of a pair, whose blocks start while the first one's end
-template <typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = TC_SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace
 
 // Pairs of heads have to share B and C.  One chunk to a sequence leaves nothing to walk: the kernel of prompt_scan.cu takes
@@ -653,11 +637,11 @@ cudaError_t launch_prompt_scan_tc(const ScanArgs& args, void* workspace, cudaStr
       a, scores, decays);
   const dim3 grid((unsigned)(a.H / 2), (unsigned)(a.q.n_seq * a.nseg));
   if (a.nseg > 1) {
-    e = launch_dependent(scan_tc_kernel<true>, dim3(grid.x, (unsigned)(a.q.n_seq * (a.nseg - 1))), s, tx, tb, tcm, ty, a,
+    e = launch_early(scan_tc_kernel<true>, dim3(grid.x, (unsigned)(a.q.n_seq * (a.nseg - 1))), NT, TC_SMEM, s, tx, tb, tcm, ty, a,
                          (const float*)scores, (const Decays*)decays);
     if (e != cudaSuccess) return e;
   }
-  e = launch_dependent(scan_tc_kernel<false>, grid, s, tx, tb, tcm, ty, a, (const float*)scores, (const Decays*)decays);
+  e = launch_early(scan_tc_kernel<false>, grid, NT, TC_SMEM, s, tx, tb, tcm, ty, a, (const float*)scores, (const Decays*)decays);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -114,6 +114,23 @@ __device__ __forceinline__ bool wait_bar(unsigned long long* bar, uint32_t parit
   return false;
 }
 // ---- host ----
+// a grid whose blocks may be placed while the stream's kernel before it ends; they call grid_dependency_wait before they
+// touch what others write
+template <typename... Args, typename... Given>
+cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t s, const Given&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
