@@ -30,7 +30,7 @@ constexpr int ST_BYTES = 6 * BLK, OFF_TB = 2 * BLK, OFF_TX = 4 * BLK;
 constexpr int OFF_P = STAGES * ST_BYTES;   // [2][head][BLK]
 constexpr int OFF_Y = OFF_P + 4 * BLK;     // [2][64][256]
 constexpr int OFF_D = OFF_Y + 4 * BLK;     // [STAGES][head] decay records
-constexpr int REC = 1280;                  // bytes of one
+constexpr int REC = 1408;                  // bytes of one
 constexpr int OFF_ODD = OFF_D + STAGES * 2 * REC;  // [2][group][128] tokens whose x is not finite | chunk << 16
 constexpr int OFF_BAR = OFF_ODD + 2 * 4 * 128 * 4;
 constexpr int TC_SMEM = OFF_BAR + 256 + 1024 /* alignment */;
@@ -39,9 +39,9 @@ constexpr int TC_SMEM = OFF_BAR + 256 + 1024 /* alignment */;
 constexpr int T_S = 0, T_Y2 = 128, T_Y1 = 192, T_XW = 320, T_H = 416;
 
 struct Decays {  // of one head and chunk (exponents in powers of two)
-  float S[64];   // sum from the start of the token's half of the chunk
+  float S[64];   // sum from the start of the token's block of 16 up to it
   float D[64];   // step size
-  float E1[32];  // 2^(sum after the token in the first half) D
+  float b[64];   // 2^(sum after the token in its block) D
   float w[64];   // 2^(sum after the token) D
   float e[64];   // 2^(sum up to the token)
   float total, pad[31];  // 2^(sum of the chunk)
@@ -90,27 +90,33 @@ __global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, De
     const float d0 = t < len ? softplus_f(bf16f(q[0]) + bias) : 0.f;
     const float d1 = t + 1 < len ? softplus_f(bf16f(q[a.lddt]) + bias) : 0.f;
     const float e0 = fmaxf(d0 * A2, kLeast2), e1 = fmaxf(d1 * A2, kLeast2);
-    float pre = e0 + e1, suf = pre;  // sums within the lane's half of the chunk
+    float pre = e0 + e1, suf = pre;  // sums within the lane's block
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-      const float u = __shfl_up_sync(0xffffffffu, pre, o, 16), v = __shfl_down_sync(0xffffffffu, suf, o, 16);
-      if ((lane & 15) >= o) pre += u;
-      if ((lane & 15) + o < 16) suf += v;
+    for (int o = 1; o < 8; o <<= 1) {
+      const float u = __shfl_up_sync(0xffffffffu, pre, o, 8), v = __shfl_down_sync(0xffffffffu, suf, o, 8);
+      if ((lane & 7) >= o) pre += u;
+      if ((lane & 7) + o < 8) suf += v;
     }
-    const float sum0 = __shfl_sync(0xffffffffu, pre, 15), sum1 = __shfl_sync(0xffffffffu, pre, 31);
-    float before = __shfl_up_sync(0xffffffffu, pre, 1, 16), after = __shfl_down_sync(0xffffffffu, suf, 1, 16);
-    if ((lane & 15) == 0) before = 0.f;
-    if ((lane & 15) == 15) after = 0.f;
-    const bool low = lane < 16;
+    float before = __shfl_up_sync(0xffffffffu, pre, 1, 8), after = __shfl_down_sync(0xffffffffu, suf, 1, 8);
+    if ((lane & 7) == 0) before = 0.f;
+    if ((lane & 7) == 7) after = 0.f;
+    float base = 0.f, rest = 0.f, all = 0.f;  // of the blocks before the lane's, and after
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float v = __shfl_sync(0xffffffffu, pre, 8 * k + 7);
+      all += v;
+      if (k < lane >> 3) base += v;
+      if (k > lane >> 3) rest += v;
+    }
     Decays& d = decays[chunk_record(first, s, c) * a.H + h];
-    const float base = low ? 0.f : sum0, rest = low ? sum1 : 0.f, S0 = before + e0;
+    const float S0 = before + e0;
     *reinterpret_cast<float2*>(&d.S[2 * lane]) = make_float2(S0, pre);
     *reinterpret_cast<float2*>(&d.D[2 * lane]) = make_float2(d0, d1);
-    const float a0 = after + e1;  // after token 2 lane, in its half
-    if (low) *reinterpret_cast<float2*>(&d.E1[2 * lane]) = make_float2(exp2_sfu(a0) * d0, exp2_sfu(after) * d1);
+    const float a0 = after + e1;  // after token 2 lane, in its block
+    *reinterpret_cast<float2*>(&d.b[2 * lane]) = make_float2(exp2_sfu(a0) * d0, exp2_sfu(after) * d1);
     *reinterpret_cast<float2*>(&d.w[2 * lane]) = make_float2(exp2_sfu(a0 + rest) * d0, exp2_sfu(after + rest) * d1);
     *reinterpret_cast<float2*>(&d.e[2 * lane]) = make_float2(exp2_sfu(base + S0), exp2_sfu(base + pre));
-    if (lane == 0) d.total = exp2_sfu(sum0 + sum1);
+    if (lane == 0) d.total = exp2_sfu(all);
     return;
   }
   const uint32_t sb = smem_u32(sm);
@@ -245,19 +251,22 @@ __global__ void __launch_bounds__(NT, 1)
     const float Dh = a.D[head];
     const unsigned long long D2 = pack2(Dh, Dh);
 
-    // P: row (head ph, token t), the group's 16 tokens s: in the same half of the chunk, in the one before, or none
-    const int ph = w4 >> 1, t = (w4 & 1) * 32 + lane, sh = grp4 >> 1;
-    const bool own_half = (w4 & 1) == sh, has_p = (w4 & 1) >= sh;
-    float4 gq[4];
-    const float4* gp = reinterpret_cast<const float4*>(scores + (chunk_record(first, s, c0) * a.G + 2 * pair / (a.H / a.G)) * (Q * Q)) +
-                       (tg >> 2) * Q + t;
+    // P, in blocks of 16 x 16 tokens: a warp makes half of one on the diagonal (4 entries a thread), and twelve of them one
+    // below it (8 entries a thread); above it there are zeros
+    const int lr = lane & 15, lh = lane >> 4;
+    const int dh = warp >> 3, db = (warp >> 1) & 3, dt = 16 * db + lr, du = 16 * db + 8 * (warp & 1) + 4 * lh;
+    const bool below = warp < 12;
+    const int oh = warp / 6, oj = warp % 6, tb = oj < 3 ? oj + 1 : oj == 3 ? 2 : 3, ub = oj < 3 ? 0 : oj < 5 ? 1 : 2;
+    const int ot = 16 * tb + lr, ou = 16 * ub + 8 * lh;
+    float4 gd, go[2];
+    const float4* gp = reinterpret_cast<const float4*>(scores + (chunk_record(first, s, c0) * a.G + 2 * pair / (a.H / a.G)) * (Q * Q));
     auto fetch = [&]() {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) gq[j] = gp[j * Q];
+      gd = gp[(du >> 2) * Q + dt];
+      if (below) go[0] = gp[(ou >> 2) * Q + ot], go[1] = gp[((ou >> 2) + 1) * Q + ot];
       gp += (long long)a.G * (Q * Q / 4);
     };
-    const uint32_t p_off = (uint32_t)(OFF_P + ph * BLK + t * 128);
-    const uint32_t p_ch[2] = {(uint32_t)(((2 * grp4) ^ (t & 7)) << 4), (uint32_t)(((2 * grp4 + 1) ^ (t & 7)) << 4)};
+    const uint32_t d_off = (uint32_t)(OFF_P + dh * BLK + dt * 128 + (((du >> 3) ^ (dt & 7)) << 4) + (du & 7) * 2);
+    const uint32_t o_off = (uint32_t)(OFF_P + oh * BLK + ot * 128 + (((ou >> 3) ^ (ot & 7)) << 4));
 
     bool ok = true;
     uint32_t cur = 0, nxt = 0, nd = OFF_D, cd = OFF_D, full_par = 0;  // stages (and decays) of chunks i and i + 1
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_wait_st();
         tc_fence_before();
         hand_over(B_XW);
-        if (!STATE_ONLY && has_p) fetch();  // for P below: the loads' time passes during y
+        if (!STATE_ONLY) fetch();  // for P below: the loads' time passes during y
       }
       // ---- y of chunk i ----
       if (!STATE_ONLY && i >= 0) {
@@ -439,35 +448,29 @@ __global__ void __launch_bounds__(NT, 1)
         tc_fence_before();
         hand_over(B_H);
         // ---- P of chunk i + 1 ----
-        if (has_p) {
-          const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[ph];
-          unsigned char* pr = smem + p_off + ((i + 1) & 1) * 2 * BLK;
-          const float St = d.S[t];
-#pragma unroll
-          for (int j8 = 0; j8 < 2; ++j8) {
-            uint32_t v[4];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const float4 g = gq[2 * j8 + m];
-              const int u = tg + 8 * j8 + 4 * m;
-              float w[4];
-              if (own_half) {  // 2^(S_t - S_u) D_u
-                const float4 S = *reinterpret_cast<const float4*>(&d.S[u]), D = *reinterpret_cast<const float4*>(&d.D[u]);
-                w[0] = u <= t ? g.x * (exp2_sfu(St - S.x) * D.x) : 0.f;
-                w[1] = u + 1 <= t ? g.y * (exp2_sfu(St - S.y) * D.y) : 0.f;
-                w[2] = u + 2 <= t ? g.z * (exp2_sfu(St - S.z) * D.z) : 0.f;
-                w[3] = u + 3 <= t ? g.w * (exp2_sfu(St - S.w) * D.w) : 0.f;
-              } else {  // to the end of the first half, and from there
-                const float4 f = *reinterpret_cast<const float4*>(&d.E1[u]);
-                const float E2 = exp2_sfu(St);
-                w[0] = g.x * (f.x * E2), w[1] = g.y * (f.y * E2), w[2] = g.z * (f.z * E2), w[3] = g.w * (f.w * E2);
-              }
-              v[2 * m] = pack_bf16x2(w[0], w[1]), v[2 * m + 1] = pack_bf16x2(w[2], w[3]);
-            }
-            *reinterpret_cast<uint4*>(pr + p_ch[j8]) = make_uint4(v[0], v[1], v[2], v[3]);
-          }
-          fence_async_smem();
+        const uint32_t buf = ((i + 1) & 1) * 2 * BLK;
+        {  // 2^(S_t - S_u) D_u
+          const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[dh];
+          const float St = d.S[dt];
+          const float4 S = *reinterpret_cast<const float4*>(&d.S[du]), D = *reinterpret_cast<const float4*>(&d.D[du]);
+          const float w0 = du <= dt ? gd.x * (exp2_sfu(St - S.x) * D.x) : 0.f;
+          const float w1 = du + 1 <= dt ? gd.y * (exp2_sfu(St - S.y) * D.y) : 0.f;
+          const float w2 = du + 2 <= dt ? gd.z * (exp2_sfu(St - S.z) * D.z) : 0.f;
+          const float w3 = du + 3 <= dt ? gd.w * (exp2_sfu(St - S.w) * D.w) : 0.f;
+          *reinterpret_cast<uint2*>(smem + d_off + buf) = make_uint2(pack_bf16x2(w0, w1), pack_bf16x2(w2, w3));
         }
+        if (below) {  // to the end of u's block, and from there
+          const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[oh];
+          float x = d.S[ot];
+          if (tb - ub > 1) x += d.S[16 * tb - 1];
+          if (tb - ub > 2) x += d.S[16 * tb - 17];
+          const float E = exp2_sfu(x);
+          const float4 f0 = *reinterpret_cast<const float4*>(&d.b[ou]), f1 = *reinterpret_cast<const float4*>(&d.b[ou + 4]);
+          *reinterpret_cast<uint4*>(smem + o_off + buf) = make_uint4(
+              pack_bf16x2(go[0].x * (f0.x * E), go[0].y * (f0.y * E)), pack_bf16x2(go[0].z * (f0.z * E), go[0].w * (f0.w * E)),
+              pack_bf16x2(go[1].x * (f1.x * E), go[1].y * (f1.y * E)), pack_bf16x2(go[1].z * (f1.z * E), go[1].w * (f1.w * E)));
+        }
+        fence_async_smem();
         hand_over(B_P);
       }
       cur = nxt, cd = nd, left -= Q;
