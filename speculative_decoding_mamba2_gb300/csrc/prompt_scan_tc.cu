@@ -72,13 +72,55 @@ __device__ __forceinline__ void scale_split3(uint32_t x, unsigned long long w, u
   lo = pack_bf16x2(c.x, c.y);
 }
 
+// Xw = x w of 32 rows (a head's columns) and 16 tokens, three bf16 parts of 32 columns of tensor memory each.  False where an
+// x is not finite: an infinity is then its own first part, which the careful form sees to.
+template <bool CAREFUL>
+__device__ __forceinline__ bool write_xw(uint32_t x, const uint32_t (&f_off)[2], const float* w, int q4, uint32_t to) {
+  const unsigned long long w0 = *reinterpret_cast<const unsigned long long*>(w + 2 * q4);
+  const unsigned long long w1 = *reinterpret_cast<const unsigned long long*>(w + 8 + 2 * q4);
+  uint32_t chk = 0;  // sum of 0 x, in pairs: NaN once an x is not finite
+#pragma unroll CAREFUL ? 1 : 2
+  for (int rh = 0; rh < 2; ++rh) {  // 16 rows, 16 tokens
+    uint32_t xf[4], hi[4], mid[4], lo[4];
+    ldsm4_t(xf, x + (rh ? f_off[1] : f_off[0]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      scale_split3(xf[j], j < 2 ? w0 : w1, hi[j], mid[j], lo[j]);
+      if (CAREFUL) {
+        if ((hi[j] & 0x7f80u) == 0x7f80u) mid[j] &= 0xffff0000u, lo[j] &= 0xffff0000u;
+        if ((hi[j] & 0x7f800000u) == 0x7f800000u) mid[j] &= 0xffffu, lo[j] &= 0xffffu;
+      } else {
+        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(chk) : "r"(xf[j]), "r"(0u));
+      }
+    }
+    const uint32_t at = to + ((uint32_t)(16 * rh) << 16);
+    tmem_st_frag(at, lo);
+    tmem_st_frag(at + 32, mid);
+    tmem_st_frag(at + 64, hi);
+  }
+  return !__any_sync(0xffffffffu, chk & 0x7fff7fffu);
+}
+
 // Once for all walks: grid z < G: scores C_t . B_s of a chunk and group, [record][s / 4][t][s % 4] fp32; then the decays
 // of a chunk and four heads, a warp each.
 __device__ __forceinline__ long long chunk_record(int first, int s, int chunk) { return (long long)(first / Q) + s + chunk; }
-__global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, Decays* decays) {
+__global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, Decays* decays, int* order) {
   __shared__ __align__(128) unsigned char sm[2 * Q * kN * 2];
   launch_dependents();
   const int c = blockIdx.x, s = blockIdx.y, grp = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (c == 0 && grp == 0) {  // the sequence's place in the order of the walks, longest first
+    __shared__ int longer[4];
+    const unsigned mine = (unsigned)a.q.cu[s + 1] - (unsigned)a.q.cu[s];
+    int before = 0;
+    for (int k = tid; k < a.q.n_seq; k += 128) {
+      const unsigned l = (unsigned)a.q.cu[k + 1] - (unsigned)a.q.cu[k];
+      before += l > mine || (l == mine && k < s);
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) longer[warp] = before;
+    __syncthreads();
+    if (tid == 0) order[longer[0] + longer[1] + longer[2] + longer[3]] = s;
+  }
   int first, len, slot;
   if (!seq_range(a.q, s, first, len, slot) || c * Q >= len) return;
   if (grp >= a.G) {
@@ -159,26 +201,14 @@ __global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, De
     }
 }
 
-template <bool STATE_ONLY>
 __global__ void __launch_bounds__(NT, 1)
     scan_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
                    const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap ty, ScanArgs a,
-                   const float* scores, const Decays* decays) {
+                   const float* scores, const Decays* decays, const int* order) {
   extern __shared__ unsigned char smem_raw[];
   // (shuffles tell the compiler what is the same for a warp: it then keeps it in uniform registers)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int pair = blockIdx.x, nseg = STATE_ONLY ? a.nseg - 1 : a.nseg;
-  const int s = blockIdx.y / nseg, seg = blockIdx.y % nseg;
-  int first, len, slot;
-  const bool there = seq_range(a.q, s, first, len, slot);
-  first = __shfl_sync(0xffffffffu, first, 0), len = __shfl_sync(0xffffffffu, len, 0), slot = __shfl_sync(0xffffffffu, slot, 0);
-  const int nch = (len + Q - 1) / Q, per = (nch + a.nseg - 1) / a.nseg;
-  const int c0 = seg * per, c1 = min(nch, c0 + per), n = max(0, c1 - c0);
-  if (!there || (STATE_ONLY ? c1 >= nch : (n == 0 && seg > 0))) {
-    if (!there && pair == 0 && seg == 0 && tid == 0) flag(a.q.status, SSM_STATUS_SEQ_RANGE);
-    grid_dependency_wait();  // the grid does not end before the one it depends on
-    return;
-  }
+  const int pair = blockIdx.x, seg = blockIdx.y % a.nseg;
   unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // stays a shared-memory pointer to the compiler
   const uint32_t sb = smem_u32(smem);
   Bars* bar = reinterpret_cast<Bars*>(smem + OFF_BAR);
@@ -196,14 +226,24 @@ __global__ void __launch_bounds__(NT, 1)
     bar->stop = 0;
     fence_barrier_init();
   }
-  if (!STATE_ONLY)  // P's entries after their token stay zero for the whole walk
-    for (int i = tid; i < 4 * BLK / 16; i += NT) reinterpret_cast<uint4*>(smem + OFF_P)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < 4 * BLK / 16; i += NT) reinterpret_cast<uint4*>(smem + OFF_P)[i] = make_uint4(0, 0, 0, 0);  // P's entries after their token stay so
   if (warp == WARPS) tmem_alloc_warp(smem_u32(&bar->tmem), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar->tmem, 0);
-  grid_dependency_wait();  // scores, decays, what the segments before add
+  grid_dependency_wait();  // scores, decays, the order, what the segments before add
+  const int s = __shfl_sync(0xffffffffu, order[blockIdx.y / a.nseg], 0);
+  int first, len, slot;
+  const bool there = seq_range(a.q, s, first, len, slot);
+  first = __shfl_sync(0xffffffffu, first, 0), len = __shfl_sync(0xffffffffu, len, 0), slot = __shfl_sync(0xffffffffu, slot, 0);
+  const int nch = (len + Q - 1) / Q, per = (nch + a.nseg - 1) / a.nseg;
+  const int c0 = seg * per, c1 = min(nch, c0 + per), n = max(0, c1 - c0);
+  if (!there || (n == 0 && seg > 0)) {
+    if (!there && pair == 0 && seg == 0 && tid == 0) flag(a.q.status, SSM_STATUS_SEQ_RANGE);
+    if (warp == WARPS) tmem_free_warp(tmem, 512);
+    return;
+  }
 
   if (warp < WARPS) {
     const int w4 = warp & 3, grp4 = warp >> 2;        // rows 32 w4 .. of tensor memory; this group's share
@@ -227,27 +267,25 @@ __global__ void __launch_bounds__(NT, 1)
     float h[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) h[j] = 0.f;
-    if (!STATE_ONLY && a.h_in) {
+    if (a.h_in) {
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
         const float4 v = *reinterpret_cast<const float4*>(a.h_in + at + j);
         h[j] = v.x, h[j + 1] = v.y, h[j + 2] = v.z, h[j + 3] = v.w;
       }
     }
-    if (!STATE_ONLY)
 #pragma unroll 1
-      for (int k = 0; k < seg; ++k) {
-        const float* r = ws + k * wrec;
-        const float dk = r[kP * kN];
-        r += p * kN + n0;
+    for (int k = 0; k < seg; ++k) {
+      const float* r = ws + k * wrec;
+      const float dk = r[kP * kN];
+      r += p * kN + n0;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(r + j);
-          h[j] = fmaf(dk, h[j], v.x), h[j + 1] = fmaf(dk, h[j + 1], v.y);
-          h[j + 2] = fmaf(dk, h[j + 2], v.z), h[j + 3] = fmaf(dk, h[j + 3], v.w);
-        }
+      for (int j = 0; j < 32; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(r + j);
+        h[j] = fmaf(dk, h[j], v.x), h[j + 1] = fmaf(dk, h[j + 1], v.y);
+        h[j + 2] = fmaf(dk, h[j + 2], v.z), h[j + 3] = fmaf(dk, h[j + 3], v.w);
       }
-    float seg_decay = 1.f;
+    }
     const float Dh = a.D[head];
     const unsigned long long D2 = pack2(Dh, Dh);
 
@@ -284,7 +322,6 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_ld16_async(tmem + T_S + lanes + n0 + 16, v1);
         const float f = reinterpret_cast<const Decays*>(smem + cd)[hd].total;
         const unsigned long long f2 = pack2(f, f);
-        if (STATE_ONLY) seg_decay *= f;
         tmem_wait_ld16(v0);
         tmem_wait_ld16(v1);
 #pragma unroll
@@ -306,40 +343,10 @@ __global__ void __launch_bounds__(NT, 1)
           fence_async_smem();
           named_sync(B_ALL, 32 * WARPS);
         }
-        const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[hd];
-        const unsigned long long w0 = *reinterpret_cast<const unsigned long long*>(&d.w[tg + 2 * q4]);
-        const unsigned long long w1 = *reinterpret_cast<const unsigned long long*>(&d.w[tg + 8 + 2 * q4]);
-        uint32_t chk = 0;  // sum of 0 x, in pairs: NaN once an x is not finite
-#pragma unroll
-        for (int rh = 0; rh < 2; ++rh) {  // 16 rows, 16 tokens
-          uint32_t xf[4], hi[4], mid[4], lo[4];
-          ldsm4_t(xf, sb + nxt + OFF_TX + f_off[rh]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            scale_split3(xf[j], j < 2 ? w0 : w1, hi[j], mid[j], lo[j]);
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(chk) : "r"(xf[j]), "r"(0u));
-          }
-          const uint32_t to = tmem + T_XW + lanes + ((uint32_t)(16 * rh) << 16) + (tg >> 1);
-          tmem_st_frag(to, lo);
-          tmem_st_frag(to + 32, mid);
-          tmem_st_frag(to + 64, hi);
-        }
-        if (__any_sync(0xffffffffu, chk & 0x7fff7fffu)) {  // seldom: an infinity is its own first part
-#pragma unroll 1
-          for (int rh = 0; rh < 2; ++rh) {
-            uint32_t xf[4], hi[4], mid[4], lo[4];
-            ldsm4_t(xf, sb + nxt + OFF_TX + (rh ? f_off[1] : f_off[0]));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              scale_split3(xf[j], j < 2 ? w0 : w1, hi[j], mid[j], lo[j]);
-              if ((hi[j] & 0x7f80u) == 0x7f80u) mid[j] &= 0xffff0000u, lo[j] &= 0xffff0000u;
-              if ((hi[j] & 0x7f800000u) == 0x7f800000u) mid[j] &= 0xffffu, lo[j] &= 0xffffu;
-            }
-            const uint32_t to = tmem + T_XW + lanes + ((uint32_t)(16 * rh) << 16) + (tg >> 1);
-            tmem_st_frag(to, lo);
-            tmem_st_frag(to + 32, mid);
-            tmem_st_frag(to + 64, hi);
-          }
+        const float* w = reinterpret_cast<const Decays*>(smem + nd)[hd].w + tg;
+        const uint32_t xw = tmem + T_XW + lanes + (tg >> 1);
+        if (!write_xw<false>(sb + nxt + OFF_TX, f_off, w, q4, xw)) {  // seldom
+          write_xw<true>(sb + nxt + OFF_TX, f_off, w, q4, xw);
           // such values leave the tile (each thread its row's): the product with a zero of P would spread them
           uint32_t odd = 0;
 #pragma unroll 1
@@ -352,14 +359,14 @@ __global__ void __launch_bounds__(NT, 1)
           bar->odd_chunk[(i + 1) & 1] = i + 1;
         }
         // the store of the chunk before this one's y has read its buffer
-        if (!STATE_ONLY && w4 == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+        if (w4 == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
         tmem_wait_st();
         tc_fence_before();
         hand_over(B_XW);
-        if (!STATE_ONLY) fetch();  // for P below: the loads' time passes during y
+        fetch();  // for P below: the loads' time passes during y
       }
       // ---- y of chunk i ----
-      if (!STATE_ONLY && i >= 0) {
+      if (i >= 0) {
         const Decays& d = reinterpret_cast<const Decays*>(smem + cd)[hd];
         const uint32_t yb = OFF_Y + (uint32_t)(i & 1) * 2 * BLK;
         const unsigned long long e0 = *reinterpret_cast<const unsigned long long*>(&d.e[tg + 2 * q4]);
@@ -435,49 +442,47 @@ __global__ void __launch_bounds__(NT, 1)
         }
       }
       if (i + 1 >= n) break;
-      if (!STATE_ONLY) {
-        // ---- the state for the next chunk's y, rounded to bf16 (y2 of this chunk, which read the last, is done) ----
+      // ---- the state for the next chunk's y, rounded to bf16 (y2 of this chunk, which read the last, is done) ----
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t v[8];
+      for (int k = 0; k < 2; ++k) {
+        uint32_t v[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(h[16 * k + 2 * j], h[16 * k + 2 * j + 1]);
-          tmem_st8(tmem + T_H + lanes + (n0 >> 1) + 8 * k, v);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        hand_over(B_H);
-        // ---- P of chunk i + 1 ----
-        const uint32_t buf = ((i + 1) & 1) * 2 * BLK;
-        {  // 2^(S_t - S_u) D_u
-          const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[dh];
-          const float St = d.S[dt];
-          const float4 S = *reinterpret_cast<const float4*>(&d.S[du]), D = *reinterpret_cast<const float4*>(&d.D[du]);
-          const float w0 = du <= dt ? gd.x * (exp2_sfu(St - S.x) * D.x) : 0.f;
-          const float w1 = du + 1 <= dt ? gd.y * (exp2_sfu(St - S.y) * D.y) : 0.f;
-          const float w2 = du + 2 <= dt ? gd.z * (exp2_sfu(St - S.z) * D.z) : 0.f;
-          const float w3 = du + 3 <= dt ? gd.w * (exp2_sfu(St - S.w) * D.w) : 0.f;
-          *reinterpret_cast<uint2*>(smem + d_off + buf) = make_uint2(pack_bf16x2(w0, w1), pack_bf16x2(w2, w3));
-        }
-        if (below) {  // to the end of u's block, and from there
-          const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[oh];
-          float x = d.S[ot];
-          if (tb - ub > 1) x += d.S[16 * tb - 1];
-          if (tb - ub > 2) x += d.S[16 * tb - 17];
-          const float E = exp2_sfu(x);
-          const float4 f0 = *reinterpret_cast<const float4*>(&d.b[ou]), f1 = *reinterpret_cast<const float4*>(&d.b[ou + 4]);
-          *reinterpret_cast<uint4*>(smem + o_off + buf) = make_uint4(
-              pack_bf16x2(go[0].x * (f0.x * E), go[0].y * (f0.y * E)), pack_bf16x2(go[0].z * (f0.z * E), go[0].w * (f0.w * E)),
-              pack_bf16x2(go[1].x * (f1.x * E), go[1].y * (f1.y * E)), pack_bf16x2(go[1].z * (f1.z * E), go[1].w * (f1.w * E)));
-        }
-        fence_async_smem();
-        hand_over(B_P);
+        for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(h[16 * k + 2 * j], h[16 * k + 2 * j + 1]);
+        tmem_st8(tmem + T_H + lanes + (n0 >> 1) + 8 * k, v);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      hand_over(B_H);
+      // ---- P of chunk i + 1 ----
+      const uint32_t buf = ((i + 1) & 1) * 2 * BLK;
+      {  // 2^(S_t - S_u) D_u
+        const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[dh];
+        const float St = d.S[dt];
+        const float4 S = *reinterpret_cast<const float4*>(&d.S[du]), D = *reinterpret_cast<const float4*>(&d.D[du]);
+        const float w0 = du <= dt ? gd.x * (exp2_sfu(St - S.x) * D.x) : 0.f;
+        const float w1 = du + 1 <= dt ? gd.y * (exp2_sfu(St - S.y) * D.y) : 0.f;
+        const float w2 = du + 2 <= dt ? gd.z * (exp2_sfu(St - S.z) * D.z) : 0.f;
+        const float w3 = du + 3 <= dt ? gd.w * (exp2_sfu(St - S.w) * D.w) : 0.f;
+        *reinterpret_cast<uint2*>(smem + d_off + buf) = make_uint2(pack_bf16x2(w0, w1), pack_bf16x2(w2, w3));
+      }
+      if (below) {  // to the end of u's block, and from there
+        const Decays& d = reinterpret_cast<const Decays*>(smem + nd)[oh];
+        float x = d.S[ot];
+        if (tb - ub > 1) x += d.S[16 * tb - 1];
+        if (tb - ub > 2) x += d.S[16 * tb - 17];
+        const float E = exp2_sfu(x);
+        const float4 f0 = *reinterpret_cast<const float4*>(&d.b[ou]), f1 = *reinterpret_cast<const float4*>(&d.b[ou + 4]);
+        *reinterpret_cast<uint4*>(smem + o_off + buf) = make_uint4(
+            pack_bf16x2(go[0].x * (f0.x * E), go[0].y * (f0.y * E)), pack_bf16x2(go[0].z * (f0.z * E), go[0].w * (f0.w * E)),
+            pack_bf16x2(go[1].x * (f1.x * E), go[1].y * (f1.y * E)), pack_bf16x2(go[1].z * (f1.z * E), go[1].w * (f1.w * E)));
+      }
+      fence_async_smem();
+      hand_over(B_P);
       cur = nxt, cd = nd, left -= Q;
       nxt += ST_BYTES, nd += 2 * REC, ++full;
       if (nxt == STAGES * ST_BYTES) nxt = 0, nd = OFF_D, full = bar->full, full_par ^= 1;
     }
-    if (!STATE_ONLY && w4 == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+    if (w4 == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     if (!ok) {  // a warp that gives up still takes part in the barriers that others may be waiting at
       asm volatile("bar.arrive %0, %1;\n" ::"r"(1 + grp4), "n"(128) : "memory");
       asm volatile("bar.arrive %0, %1;\n" ::"n"(B_ALL), "n"(32 * WARPS) : "memory");
@@ -485,11 +490,9 @@ __global__ void __launch_bounds__(NT, 1)
       hand_over(B_H);
       hand_over(B_P);
     }
-    if (ok && (STATE_ONLY || c1 == nch)) {
-      float* out = STATE_ONLY ? ws + seg * wrec + p * kN + n0 : a.h_out + at;
+    if (ok && c1 == nch) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(out + j) = make_float4(h[j], h[j + 1], h[j + 2], h[j + 3]);
-      if (STATE_ONLY && p == 0 && n0 == 0) ws[seg * wrec + kP * kN] = seg_decay;
+      for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(a.h_out + at + j) = make_float4(h[j], h[j + 1], h[j + 2], h[j + 3]);
     }
   } else if (warp == WARPS + 1) {
     // ---- copies ----
@@ -501,16 +504,14 @@ __global__ void __launch_bounds__(NT, 1)
       if (lane == 0) {
         const uint32_t f = smem_u32(&bar->full[st]), d = sb + st * ST_BYTES;
         const int t = first + (c0 + i) * Q, bn = 2 * pair / (a.H / a.G) * kN;
-        mbar_arrive_expect_tx(f, (STATE_ONLY ? 4 * BLK : 6 * BLK) + 2 * REC);
+        mbar_arrive_expect_tx(f, ST_BYTES + 2 * REC);
         tma_load_2d(d + OFF_TX, &tx, 2 * pair * kP, t, f);
         tma_load_2d(d + OFF_TX + BLK, &tx, 2 * pair * kP + 64, t, f);
         bulk_load(sb + OFF_D + st * 2 * REC, decays + chunk_record(first, s, c0 + i) * a.H + 2 * pair, 2 * REC, f);
         tma_load_2d(d + OFF_TB, &tb, bn, t, f);
         tma_load_2d(d + OFF_TB + BLK, &tb, bn + 64, t, f);
-        if (!STATE_ONLY) {
-          tma_load_2d(d, &tcm, bn, t, f);
-          tma_load_2d(d + BLK, &tcm, bn + 64, t, f);
-        }
+        tma_load_2d(d, &tcm, bn, t, f);
+        tma_load_2d(d + BLK, &tcm, bn + 64, t, f);
       }
       issued = i + 1;
     }
@@ -531,7 +532,6 @@ __global__ void __launch_bounds__(NT, 1)
       if (*stop) break;
       tc_fence_after();
       if (leader) {
-        if (STATE_ONLY && i > 0) mbar_arrive(smem_u32(last));
         const uint32_t bd = desc_lo(tile + OFF_TB, BLK);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 16 tokens: two groups of 8 rows
@@ -541,38 +541,209 @@ __global__ void __launch_bounds__(NT, 1)
         mma_commit(smem_u32(&bar->s_full));
       }
       __syncwarp();
-      if (!STATE_ONLY) {
-        named_sync(B_H, HANDED);  // h; y of the last chunk has been read
-        if (*stop) break;
-        tc_fence_after();
-        if (leader) {
-          if (i > 0) mbar_arrive(smem_u32(last));
-          const uint32_t cd = desc_lo(tile, 16);
+      named_sync(B_H, HANDED);  // h; y of the last chunk has been read
+      if (*stop) break;
+      tc_fence_after();
+      if (leader) {
+        if (i > 0) mbar_arrive(smem_u32(last));
+        const uint32_t cd = desc_lo(tile, 16);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts<id_y2>(tmem + T_Y2, tmem + T_H + k * 8, cd + ((k >> 2) * (BLK >> 4) + (k & 3) * 2), k != 0);
-        }
-        __syncwarp();
-        named_sync(B_P, HANDED);
-        if (*stop) break;
-        tc_fence_after();
-        if (leader) {
-          const uint32_t xd = desc_lo(tile + OFF_TX, BLK);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss<id_y1>(tmem + T_Y1 + e * 64, xd + k * (2048 >> 4), pd + e * (BLK >> 4) + k * 2, k != 0);
-          mma_commit(smem_u32(&bar->y_full));
-        }
-        __syncwarp();
+        for (int k = 0; k < 8; ++k)
+          mma_ts<id_y2>(tmem + T_Y2, tmem + T_H + k * 8, cd + ((k >> 2) * (BLK >> 4) + (k & 3) * 2), k != 0);
       }
+      __syncwarp();
+      named_sync(B_P, HANDED);
+      if (*stop) break;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t xd = desc_lo(tile + OFF_TX, BLK);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss<id_y1>(tmem + T_Y1 + e * 64, xd + k * (2048 >> 4), pd + e * (BLK >> 4) + k * 2, k != 0);
+        mma_commit(smem_u32(&bar->y_full));
+      }
+      __syncwarp();
       if (leader) mma_commit(smem_u32(fr));
       __syncwarp();
       last = fr;
       pd ^= desc_lo(sb + OFF_P, 16) ^ desc_lo(sb + OFF_P + 2 * BLK, 16);
       tile += ST_BYTES, ++fr;
       if (fr == bar->free_ + STAGES) fr = bar->free_, tile = sb;
+    }
+    if (leader) {
+      mma_commit(smem_u32(&bar->drain));
+      mbar_poll_ns(smem_u32(&bar->drain), 0, kWaitLimitNs);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *stop) flag(a.q.status, SSM_STATUS_TIMEOUT);
+  if (warp == WARPS) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free_warp(tmem, 512);
+  }
+}
+
+// What a segment adds to the state, and its decay: the walk of scan_tc_kernel without y.  Two chunks are under way, each with
+// its own S and Xw in tensor memory: the S of one is made while the one before it is added up and the next one's Xw written
+// (with one, 43 chunks of 80 pairs and segments took 55 us, each step waiting for the one before).  Segments before a
+// sequence's last have whole chunks only.
+constexpr int S_STAGES = 6, S_BYTES = 4 * BLK;        // stages of B | x
+constexpr int S_OFF_D = S_STAGES * S_BYTES, S_OFF_BAR = S_OFF_D + S_STAGES * 2 * REC;
+constexpr int S_SMEM = S_OFF_BAR + 256 + 1024 /* alignment */, S_NT = 32 * WARPS + 64;
+constexpr int T_S2 = 0, T_XW2 = 256;                  // two of 128 columns, two of 96
+struct StateBars {
+  unsigned long long full[S_STAGES], free_[S_STAGES], s_full[2], drain;
+  uint32_t tmem;
+  int stop;
+};
+static_assert(sizeof(StateBars) <= 256 && S_SMEM <= 227 * 1024, "space");
+
+__global__ void __launch_bounds__(S_NT, 1)
+    scan_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb, ScanArgs a,
+                      const Decays* decays, const int* order) {
+  extern __shared__ unsigned char smem_raw[];
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int pair = blockIdx.x, seg = blockIdx.y % (a.nseg - 1);
+  unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  StateBars* bar = reinterpret_cast<StateBars*>(smem + S_OFF_BAR);
+  volatile int* stop = &bar->stop;
+  if (tid == 0) {
+    for (int i = 0; i < S_STAGES; ++i) {
+      mbar_init(smem_u32(&bar->full[i]), 1);
+      mbar_init(smem_u32(&bar->free_[i]), 1);
+    }
+    mbar_init(smem_u32(&bar->s_full[0]), 1);
+    mbar_init(smem_u32(&bar->s_full[1]), 1);
+    mbar_init(smem_u32(&bar->drain), 1);
+    bar->stop = 0;
+    fence_barrier_init();
+  }
+  if (warp == WARPS) tmem_alloc_warp(smem_u32(&bar->tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar->tmem, 0);
+  grid_dependency_wait();  // decays, the order
+  const int s = __shfl_sync(0xffffffffu, order[blockIdx.y / (a.nseg - 1)], 0);
+  int first, len, slot;
+  const bool there = seq_range(a.q, s, first, len, slot);
+  first = __shfl_sync(0xffffffffu, first, 0), len = __shfl_sync(0xffffffffu, len, 0);
+  const int nch = (len + Q - 1) / Q, per = (nch + a.nseg - 1) / a.nseg;
+  const int c0 = seg * per, c1 = c0 + per, n = per;
+  if (!there || c1 >= nch) {
+    if (warp == WARPS) tmem_free_warp(tmem, 512);
+    return;
+  }
+
+  if (warp < WARPS) {
+    const int w4 = warp & 3, grp4 = warp >> 2;  // as in scan_tc_kernel
+    const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+    const int row = w4 * 32 + lane, hd = row >> 6, p = row & 63, head = 2 * pair + hd;
+    const int q4 = lane & 3, p0 = (w4 & 1) * 32, tg = 16 * grp4, n0 = 32 * grp4;
+    const int fr = tg + (lane & 7) + ((lane >> 4) << 3), fc = (p0 >> 3) + ((lane >> 3) & 1);
+    const uint32_t f_off[2] = {(uint32_t)(hd * BLK) + tile_off(fr, fc, 128), (uint32_t)(hd * BLK) + tile_off(fr, fc + 2, 128)};
+    float h[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) h[j] = 0.f;
+    float seg_decay = 1.f, f0 = 0.f, f1 = 0.f;  // decays of chunks i and i + 1
+    bool ok = true;
+    uint32_t st = 0, full_par = 0;  // stage of chunk i + 2
+#pragma unroll 1
+    for (int i = -2; i < n; ++i) {
+      const uint32_t par = i & 1;
+      if (i >= 0) {
+        ok = wait_bar(&bar->s_full[par], (i >> 1) & 1, stop);
+        if (!ok) break;
+        tc_fence_after();
+        float v0[16], v1[16];
+        tmem_ld16_async(tmem + T_S2 + par * 128 + lanes + n0, v0);
+        tmem_ld16_async(tmem + T_S2 + par * 128 + lanes + n0 + 16, v1);
+        const unsigned long long f2 = pack2(f0, f0);
+        seg_decay *= f0;
+        tmem_wait_ld16(v0);
+        tmem_wait_ld16(v1);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float2 u = unpack2(ffma2(f2, pack2(h[j], h[j + 1]), pack2(v0[j], v0[j + 1])));
+          const float2 z = unpack2(ffma2(f2, pack2(h[16 + j], h[17 + j]), pack2(v1[j], v1[j + 1])));
+          h[j] = u.x, h[j + 1] = u.y, h[16 + j] = z.x, h[17 + j] = z.y;
+        }
+      }
+      f0 = f1;
+      if (i + 2 < n) {  // (the MMAs that read this Xw's place are done)
+        ok = wait_bar(&bar->full[st], full_par, stop);
+        if (!ok) break;
+        const Decays& d = reinterpret_cast<const Decays*>(smem + S_OFF_D + st * 2 * REC)[hd];
+        const uint32_t x = sb + st * S_BYTES + 2 * BLK, xw = tmem + T_XW2 + par * 96 + lanes + (tg >> 1);
+        f1 = d.total;
+        if (!write_xw<false>(x, f_off, d.w + tg, q4, xw)) write_xw<true>(x, f_off, d.w + tg, q4, xw);
+        tmem_wait_st();
+        tc_fence_before();
+        hand_over(B_XW + par);
+        if (++st == S_STAGES) st = 0, full_par ^= 1;
+      }
+    }
+    if (!ok) {  // (as in scan_tc_kernel)
+      hand_over(B_XW);
+      hand_over(B_XW + 1);
+    } else {
+      float* out = a.seg_state + (((long long)s * a.H + head) * (a.nseg - 1) + seg) * (kP * kN + 32) + p * kN + n0;
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(out + j) = make_float4(h[j], h[j + 1], h[j + 2], h[j + 3]);
+      if (p == 0 && n0 == 0) out[kP * kN] = seg_decay;
+    }
+  } else if (warp == WARPS + 1) {
+    // ---- copies ----
+    int issued = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int st = i % S_STAGES;
+      if (i >= S_STAGES && !wait_bar(&bar->free_[st], (i / S_STAGES - 1) & 1, stop)) break;
+      if (lane == 0) {
+        const uint32_t f = smem_u32(&bar->full[st]), d = sb + st * S_BYTES;
+        const int t = first + (c0 + i) * Q, bn = 2 * pair / (a.H / a.G) * kN;
+        mbar_arrive_expect_tx(f, S_BYTES + 2 * REC);
+        tma_load_2d(d + 2 * BLK, &tx, 2 * pair * kP, t, f);
+        tma_load_2d(d + 3 * BLK, &tx, 2 * pair * kP + 64, t, f);
+        bulk_load(sb + S_OFF_D + st * 2 * REC, decays + chunk_record(first, s, c0 + i) * a.H + 2 * pair, 2 * REC, f);
+        tma_load_2d(d, &tb, bn, t, f);
+        tma_load_2d(d + BLK, &tb, bn + 64, t, f);
+      }
+      issued = i + 1;
+    }
+    if (lane == 0 && *stop) {  // copies in flight land before the shared memory is given up
+      for (int i = max(0, issued - S_STAGES); i < issued; ++i)
+        mbar_poll_ns(smem_u32(&bar->full[i % S_STAGES]), (i / S_STAGES) & 1, kWaitLimitNs);
+    }
+  } else {
+    // ---- MMAs ----
+    constexpr uint32_t id_s = idesc_major(128, 128, false, true);
+    const bool leader = elect_one();
+    uint32_t st = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const uint32_t par = i & 1;
+      named_sync(B_XW + par, HANDED);  // Xw of this chunk; S of the last but one has been read
+      if (*stop) break;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t bd = desc_lo(sb + st * S_BYTES, BLK);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // 16 tokens: two groups of 8 rows
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+            mma_ts<id_s>(tmem + T_S2 + par * 128, tmem + T_XW2 + par * 96 + part * 32 + k * 8, bd + k * (2048 >> 4), k + part > 0);
+        mma_commit(smem_u32(&bar->s_full[par]));
+        mma_commit(smem_u32(&bar->free_[st]));
+      }
+      __syncwarp();
+      if (++st == S_STAGES) st = 0;
     }
     if (leader) {
       mma_commit(smem_u32(&bar->drain));
@@ -604,6 +775,7 @@ int plan_segments_tc(int H, int n_seq, int max_len) {
 size_t chunk_count(int n_seq, int n_tok) { return (size_t)(n_tok / Q) + n_seq + 1; }
 size_t score_bytes(int n_seq, int n_tok, int G) { return chunk_count(n_seq, n_tok) * G * Q * Q * sizeof(float); }
 size_t decay_bytes(int n_seq, int n_tok, int H) { return chunk_count(n_seq, n_tok) * H * REC; }
+size_t order_bytes(int n_seq) { return ((size_t)n_seq * sizeof(int) + 255) & ~(size_t)255; }
 
 }  // namespace
 
@@ -615,7 +787,7 @@ bool prompt_scan_tc_fits(int H, int G, int n_seq, int max_len) { return (H / G) 
 
 size_t prompt_scan_tc_workspace_bytes(int H, int G, int n_seq, int n_tok, int max_len) {
   const int nseg = plan_segments_tc(H, n_seq, max_len);
-  return 256 + score_bytes(n_seq, n_tok, G) + decay_bytes(n_seq, n_tok, H) +
+  return 256 + score_bytes(n_seq, n_tok, G) + decay_bytes(n_seq, n_tok, H) + order_bytes(n_seq) +
          (size_t)n_seq * H * (nseg - 1) * (kP * kN + 32) * sizeof(float);
 }
 
@@ -627,25 +799,27 @@ cudaError_t launch_prompt_scan_tc(const ScanArgs& args, void* workspace, cudaStr
   ws += score_bytes(a.q.n_seq, a.q.n_tok, a.G);
   Decays* decays = reinterpret_cast<Decays*>(ws);
   ws += decay_bytes(a.q.n_seq, a.q.n_tok, a.H);
+  int* order = reinterpret_cast<int*>(ws);
+  ws += order_bytes(a.q.n_seq);
   a.seg_state = reinterpret_cast<float*>(ws);
   static bool done[2][64];
-  cudaError_t e = allow_smem(scan_tc_kernel<false>, TC_SMEM, done[0]);
-  if (e == cudaSuccess) e = allow_smem(scan_tc_kernel<true>, TC_SMEM, done[1]);
+  cudaError_t e = allow_smem(scan_tc_kernel, TC_SMEM, done[0]);
+  if (e == cudaSuccess) e = allow_smem(scan_state_kernel, S_SMEM, done[1]);
   if (e != cudaSuccess) return e;
   CUtensorMap tx, tb, tcm, ty;
   if (!encode_tiles(&tx, a.x, a.q.n_tok, (long long)a.H * kP, a.ldx, Q) || !encode_tiles(&tb, a.B, a.q.n_tok, (long long)a.G * kN, a.ldb, Q) ||
       !encode_tiles(&tcm, a.C, a.q.n_tok, (long long)a.G * kN, a.ldc, Q) || !encode_tiles(&ty, a.y, a.q.n_tok, (long long)a.H * kP, a.ldy, 16))
     return cudaErrorInvalidValue;
   prep_kernel<<<dim3((unsigned)((a.q.max_len + Q - 1) / Q), (unsigned)a.q.n_seq, (unsigned)(a.G + (a.H + 3) / 4)), 128, 0, s>>>(
-      a, scores, decays);
+      a, scores, decays, order);
   const dim3 grid((unsigned)(a.H / 2), (unsigned)(a.q.n_seq * a.nseg));
   if (a.nseg > 1) {
-    e = launch_early(scan_tc_kernel<true>, dim3(grid.x, (unsigned)(a.q.n_seq * (a.nseg - 1))), NT, TC_SMEM, s, tx, tb, tcm, ty, a,
-                         (const float*)scores, (const Decays*)decays);
+    e = launch_early(scan_state_kernel, dim3(grid.x, (unsigned)(a.q.n_seq * (a.nseg - 1))), S_NT, S_SMEM, s, tx, tb, a,
+                     (const Decays*)decays, (const int*)order);
     if (e != cudaSuccess) return e;
   }
-  e = launch_early(scan_tc_kernel<false>, grid, NT, TC_SMEM, s, tx, tb, tcm, ty, a, (const float*)scores, (const Decays*)decays);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_early(scan_tc_kernel, grid, NT, TC_SMEM, s, tx, tb, tcm, ty, a, (const float*)scores, (const Decays*)decays,
+                      (const int*)order);
 }
 
 }  // namespace ssmtree
