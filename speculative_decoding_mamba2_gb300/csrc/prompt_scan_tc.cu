@@ -761,12 +761,16 @@ __global__ void __launch_bounds__(S_NT, 1)
   }
 }
 
-// as plan_segments of prompt_scan.cu, for one CTA of a head pair to an SM
+// Segments of a sequence's chunks, for one CTA of a head pair to an SM: where sequences and pairs leave SMs idle, the pass over
+// the segments' states pays for itself.  (us back to back, in one segment | in several: 10 chunks of 16 pairs 28 | 33 in two;
+// 16 chunks of 40 pairs 37 | 39 in two, 36 in three; up to 20 chunks of 24 pairs 43 | 38 in five, 37 in three; up to 81 chunks
+// of 48 pairs 137 | 86 in three.)
 int plan_segments_tc(int H, int n_seq, int max_len) {
   const long long items = (long long)(H / 2) * n_seq;
   const int nch = (max_len + Q - 1) / Q;
+  if (nch < 12) return 1;
   int nseg = (int)(kSMs / (items > 0 ? items : 1));
-  if (nseg > nch / 4) nseg = nch / 4;
+  if (nseg > nch / 5) nseg = nch / 5;
   if (nseg > 16) nseg = 16;
   return nseg < 2 ? 1 : nseg;
 }
