@@ -783,11 +783,15 @@ size_t order_bytes(int n_seq) { return ((size_t)n_seq * sizeof(int) + 255) & ~(s
 
 }  // namespace
 
-// Pairs of heads have to share B and C.  One chunk to a sequence leaves nothing to walk: the kernel of prompt_scan.cu takes
-// it in one launch.  80 heads, event times in us, there | here:
-//   sequences x tokens   1 x 64: 13 | 19    64 x 64: 171 | 199    8 x 65: 46 | 46    64 x 65: 246 | 233    1 x 128: 17 | 21
-//                        1 x 512: 48 | 37   64 x 128: 257 | 234   8 x 512: 134 | 81  64 x 512: 797 | 440
-bool prompt_scan_tc_fits(int H, int G, int n_seq, int max_len) { return (H / G) % 2 == 0 && max_len > 64; }
+// Pairs of heads have to share B and C.  One chunk to a sequence leaves nothing to walk, and two do not cover the walk's start
+// where each SM has three walks at most: the kernel of prompt_scan.cu takes these in one launch.  80 heads, event times in us,
+// there | here, sequences x tokens:
+//   1 x 64: 13 | 20    8 x 64: 33 | 43     64 x 64: 171 | 203
+//   1 x 128: 17 | 21   8 x 128: 48 | 48    64 x 65: 246 | 232    64 x 128: 257 | 238
+//   1 x 192: 21 | 23   8 x 192: 60 | 54    64 x 192: 347 | 274   1 x 256: 25 | 25   1 x 512: 48 | 31   64 x 512: 798 | 417
+bool prompt_scan_tc_fits(int H, int G, int n_seq, int max_len) {
+  return (H / G) % 2 == 0 && max_len > ((long long)n_seq * (H / 2) > 3 * kSMs ? 64 : 128);
+}
 
 size_t prompt_scan_tc_workspace_bytes(int H, int G, int n_seq, int n_tok, int max_len) {
   const int nseg = plan_segments_tc(H, n_seq, max_len);

@@ -292,3 +292,27 @@ def test_kv_commit_bad_device_data():
     np.testing.assert_array_equal(out.cpu().numpy(), [5, 16, 8, -2])
     np.testing.assert_array_equal(host(kp), kp64)
     np.testing.assert_array_equal(host(vp), vp64)
+
+
+@pytest.mark.parametrize("S,n,g,Hkv,top", [(40, 1, 4, 2, 3000), (9, 16, 8, 3, 2500), (80, 2, 1, 8, 400), (33, 5, 3, 1, 900)])
+def test_tree_attention_ragged_batches(S, n, g, Hkv, top):
+    """Caches from nothing to `top` rows, cut into runs of the same length (or not at all: 80 x 8 CTAs are enough), under the
+    longest length as the bound and under a loose one."""
+    rng = np.random.default_rng([S, top])
+    lens = [0, top, 1, 64, 63] + [int(v) for v in np.exp(rng.uniform(0, np.log(top), S - 5))]
+    c = case(8, S, n, g, Hkv, 128, lens, 32)
+    for max_len in (None, 10 ** 6):
+        o, status = run(c, max_len=max_len)
+        assert status == 0
+        for s in range(S):
+            check(c, o, s)
+
+
+def test_tree_attention_bad_lengths_beside_long_caches():
+    """A length below 0 or past its pages counts as an empty cache; the others, cut into runs, are as they were."""
+    from speculative_decoding_mamba2_gb300 import SSM_STATUS_SEQ_RANGE
+    c = case(9, 4, 5, 2, 2, 64, [2000, 300, 1500, 700], 16)
+    o, status = run(c, lens=[2000, -7, 1 << 30, 700], max_len=2000)
+    assert status == SSM_STATUS_SEQ_RANGE
+    for s, length in enumerate([2000, 0, 0, 700]):
+        check(c, o, s, length=length)

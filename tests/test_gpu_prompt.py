@@ -350,3 +350,82 @@ def test_prompt_conv_skips_what_is_out_of_range():
         ssm_prompt_conv(Dims(n_heads=1, ring_cap=4), prm, 0, ints(cu), 12, x, ring, head, out, slots=ints(slots), status=status)
         assert int(status) == SSM_STATUS_SEQ_RANGE
         assert head[0] == 3 and (host(ring)[0] == ring64[0]).all() and (host(out)[:10] == 9.0).all()
+
+
+@pytest.mark.parametrize("H,G,lens", [(4, 1, [63, 64, 65]), (4, 2, [1, 128, 0, 127, 2]), (2, 1, [190, 0, 3]), (6, 3, [64] * 5),
+                                      (24, 1, [1 + (37 * k) % 401 for k in range(40)]), (24, 1, [2000, 30, 700])], ids=str)
+def test_prompt_scan_ragged_batches(H, G, lens):
+    """Short, whole-chunk and empty sequences beside long ones, under the longest length and under a loose bound."""
+    c = scan_case(21, H, G, lens)
+    for max_len in (None, 10 ** 6):
+        y, h, status = run_scan(c, max_len=max_len)
+        assert status == 0
+        check_scan(c, y, h)
+
+
+def test_prompt_scan_extreme_decays_long():
+    """Decays of 1 and of 0 next to each other, over chunks and segments."""
+    c = scan_case(22, 4, 1, [1000, 65, 140])
+    rng = np.random.default_rng(56)
+    dt, dt64 = bf(rng.choice([-100.0, -20.0, 0.0, 5.0, 80.0], (c["T"], c["H"])))
+    c["dt"], c["dt64"] = dt, dt64
+    c["prm"]["A_log"].fill_(np.log(np.float32(16.0)))
+    c["prm64"]["A_log"] = c["prm"]["A_log"].double().cpu().numpy()
+    y, h, status = run_scan(c)
+    assert status == 0 and np.isfinite(y).all() and np.isfinite(h).all()
+    check_scan(c, y, h)
+
+
+@pytest.mark.parametrize("what", ["x", "B", "C", "dt"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("at", [64, 200, 1100])
+def test_prompt_scan_what_comes_later_does_not_matter_long(what, value, at):
+    """As above over many chunks: at a chunk's first token, inside one, and in a later segment."""
+    c = scan_case(23, 4, 1, [1200, 130])
+    y0, h0, _ = run_scan(c)
+    t = c[what] if what == "dt" else c["x"]._base
+    if what == "dt":
+        t[at, 1] = value if value > 0 or value != value else float("nan")  # (softplus of -infinity is 0)
+    else:
+        t[at, dict(x=1 * P + 5, B=c["H"] * P + 9, C=c["H"] * P + N + 9)[what]] = value
+    y, h, status = run_scan(c)
+    assert status == 0
+    np.testing.assert_array_equal(y[:at], y0[:at])
+    np.testing.assert_array_equal(y[1200:], y0[1200:])
+    np.testing.assert_array_equal(h[c["slots"][1]], h0[c["slots"][1]])
+    assert not np.isfinite(y[at, 1]).all()
+    s = c["slots"][0]
+    if what in ("x", "dt"):
+        np.testing.assert_array_equal(y[:, [0, 2, 3]], y0[:, [0, 2, 3]])
+        np.testing.assert_array_equal(h[s, 0][[0, 2, 3]], h0[s, 0][[0, 2, 3]])
+    if what == "x":  # one value of x reaches one row of the state
+        keep = np.arange(P) != 5
+        assert np.isfinite(h[s, 0, 1][keep]).all() and np.isfinite(y[:, 1][:, keep]).all()
+    if what == "C":  # an output alone
+        np.testing.assert_array_equal(h, h0)
+        np.testing.assert_array_equal(y[at + 1:], y0[at + 1:])
+
+
+def test_prompt_scan_skips_what_is_out_of_range_long():
+    from speculative_decoding_mamba2_gb300 import SSM_STATUS_SEQ_RANGE
+    for wrong in ("slot", "first", "long", "order"):
+        c = scan_case(24, 4, 1, [200, 300, 100])
+        slots, cu = c["slots"].copy(), c["cu"].copy()
+        bad = {1}
+        if wrong == "slot":
+            c["slots"][1] = -1
+        elif wrong == "first":
+            c["cu"][0], bad = -3, {0}
+        elif wrong == "order":
+            c["cu"][2], bad = 100, {1, 2}  # sequence 2 then has 500 rows: more than the bound
+        y, h, status = run_scan(c, max_len=250 if wrong == "long" else 300)
+        assert status == SSM_STATUS_SEQ_RANGE
+        c["slots"], c["cu"] = slots, cu
+        for s in range(3):
+            if s in bad:
+                assert (y[cu[s]:cu[s + 1]] == 9.0).all() and (h[slots[s]] == 7.0).all(), (wrong, s)
+                continue
+            ry, rh = reference(c, s)
+            my, mh = reference(c, s, magnitude=True)
+            assert (np.abs(y[cu[s]:cu[s + 1]] - ry) <= U * np.abs(ry) + (U + 2.0 ** -12) * my).all(), (wrong, s)
+            assert (np.abs(h[slots[s], 0] - rh) <= 4e-6 * 6 * mh).all(), (wrong, s)
