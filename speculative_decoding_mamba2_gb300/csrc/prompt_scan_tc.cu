@@ -102,8 +102,9 @@ __device__ __forceinline__ bool write_xw(uint32_t x, const uint32_t (&f_off)[2],
 }
 
 // Once for all walks: grid z < G: scores C_t . B_s of a chunk and group, [record][s / 4][t][s % 4] fp32; then the decays
-// of a chunk and four heads, a warp each.
+// of a chunk, HEADS heads to a warp.
 __device__ __forceinline__ long long chunk_record(int first, int s, int chunk) { return (long long)(first / Q) + s + chunk; }
+constexpr int HEADS = 4;  // of a warp: their chains of shuffles and exponentials fill each other's gaps (1: 239, 2: 236, 4: 235.6 us of a scan)
 __global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, Decays* decays, int* order) {
   __shared__ __align__(128) unsigned char sm[2 * Q * kN * 2];
   launch_dependents();
@@ -124,41 +125,51 @@ __global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, De
   int first, len, slot;
   if (!seq_range(a.q, s, first, len, slot) || c * Q >= len) return;
   if (grp >= a.G) {
-    const int h = (grp - a.G) * 4 + warp;
-    if (h >= a.H) return;
-    const float A2 = neg_exp(a.A_log[h]) * kLog2e, bias = a.dt_bias[h];
+    const int h0 = ((grp - a.G) * 4 + warp) * HEADS;
     const int t = c * Q + 2 * lane;  // tokens 2 lane, 2 lane + 1
-    const uint16_t* q = a.dt + (long long)(first + t) * a.lddt + h;
-    const float d0 = t < len ? softplus_f(bf16f(q[0]) + bias) : 0.f;
-    const float d1 = t + 1 < len ? softplus_f(bf16f(q[a.lddt]) + bias) : 0.f;
-    const float e0 = fmaxf(d0 * A2, kLeast2), e1 = fmaxf(d1 * A2, kLeast2);
-    float pre = e0 + e1, suf = pre;  // sums within the lane's block
+    const uint16_t* q = a.dt + (long long)(first + t) * a.lddt + h0;
+    float dt0[HEADS], dt1[HEADS];
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      const float u = __shfl_up_sync(0xffffffffu, pre, o, 8), v = __shfl_down_sync(0xffffffffu, suf, o, 8);
-      if ((lane & 7) >= o) pre += u;
-      if ((lane & 7) + o < 8) suf += v;
+    for (int j = 0; j < HEADS; ++j) {
+      dt0[j] = h0 + j < a.H && t < len ? bf16f(q[j]) : 0.f;
+      dt1[j] = h0 + j < a.H && t + 1 < len ? bf16f(q[a.lddt + j]) : 0.f;
     }
-    float before = __shfl_up_sync(0xffffffffu, pre, 1, 8), after = __shfl_down_sync(0xffffffffu, suf, 1, 8);
-    if ((lane & 7) == 0) before = 0.f;
-    if ((lane & 7) == 7) after = 0.f;
-    float base = 0.f, rest = 0.f, all = 0.f;  // of the blocks before the lane's, and after
+    Decays* rec = decays + chunk_record(first, s, c) * a.H + h0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float v = __shfl_sync(0xffffffffu, pre, 8 * k + 7);
-      all += v;
-      if (k < lane >> 3) base += v;
-      if (k > lane >> 3) rest += v;
+    for (int j = 0; j < HEADS; ++j) {
+      if (h0 + j >= a.H) return;
+      const float A2 = neg_exp(a.A_log[h0 + j]) * kLog2e, bias = a.dt_bias[h0 + j];
+      const float d0 = t < len ? softplus_f(dt0[j] + bias) : 0.f;
+      const float d1 = t + 1 < len ? softplus_f(dt1[j] + bias) : 0.f;
+      const float e0 = fmaxf(d0 * A2, kLeast2), e1 = fmaxf(d1 * A2, kLeast2);
+      float pre = e0 + e1, suf = pre;  // sums within the lane's block
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        const float u = __shfl_up_sync(0xffffffffu, pre, o, 8), v = __shfl_down_sync(0xffffffffu, suf, o, 8);
+        if ((lane & 7) >= o) pre += u;
+        if ((lane & 7) + o < 8) suf += v;
+      }
+      float before = __shfl_up_sync(0xffffffffu, pre, 1, 8), after = __shfl_down_sync(0xffffffffu, suf, 1, 8);
+      if ((lane & 7) == 0) before = 0.f;
+      if ((lane & 7) == 7) after = 0.f;
+      float base = 0.f, rest = 0.f, all = 0.f;  // of the blocks before the lane's, and after
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float v = __shfl_sync(0xffffffffu, pre, 8 * k + 7);
+        all += v;
+        if (k < lane >> 3) base += v;
+        if (k > lane >> 3) rest += v;
+      }
+      Decays& d = rec[j];
+      const float S0 = before + e0;
+      *reinterpret_cast<float2*>(&d.S[2 * lane]) = make_float2(S0, pre);
+      *reinterpret_cast<float2*>(&d.D[2 * lane]) = make_float2(d0, d1);
+      const float a0 = after + e1;  // after token 2 lane, in its block
+      *reinterpret_cast<float2*>(&d.b[2 * lane]) = make_float2(exp2_sfu(a0) * d0, exp2_sfu(after) * d1);
+      *reinterpret_cast<float2*>(&d.w[2 * lane]) = make_float2(exp2_sfu(a0 + rest) * d0, exp2_sfu(after + rest) * d1);
+      *reinterpret_cast<float2*>(&d.e[2 * lane]) = make_float2(exp2_sfu(base + S0), exp2_sfu(base + pre));
+      if (lane == 0) d.total = exp2_sfu(all);
     }
-    Decays& d = decays[chunk_record(first, s, c) * a.H + h];
-    const float S0 = before + e0;
-    *reinterpret_cast<float2*>(&d.S[2 * lane]) = make_float2(S0, pre);
-    *reinterpret_cast<float2*>(&d.D[2 * lane]) = make_float2(d0, d1);
-    const float a0 = after + e1;  // after token 2 lane, in its block
-    *reinterpret_cast<float2*>(&d.b[2 * lane]) = make_float2(exp2_sfu(a0) * d0, exp2_sfu(after) * d1);
-    *reinterpret_cast<float2*>(&d.w[2 * lane]) = make_float2(exp2_sfu(a0 + rest) * d0, exp2_sfu(after + rest) * d1);
-    *reinterpret_cast<float2*>(&d.e[2 * lane]) = make_float2(exp2_sfu(base + S0), exp2_sfu(base + pre));
-    if (lane == 0) d.total = exp2_sfu(all);
     return;
   }
   const uint32_t sb = smem_u32(sm);
@@ -818,7 +829,7 @@ cudaError_t launch_prompt_scan_tc(const ScanArgs& args, void* workspace, cudaStr
   if (!encode_tiles(&tx, a.x, a.q.n_tok, (long long)a.H * kP, a.ldx, Q) || !encode_tiles(&tb, a.B, a.q.n_tok, (long long)a.G * kN, a.ldb, Q) ||
       !encode_tiles(&tcm, a.C, a.q.n_tok, (long long)a.G * kN, a.ldc, Q) || !encode_tiles(&ty, a.y, a.q.n_tok, (long long)a.H * kP, a.ldy, 16))
     return cudaErrorInvalidValue;
-  prep_kernel<<<dim3((unsigned)((a.q.max_len + Q - 1) / Q), (unsigned)a.q.n_seq, (unsigned)(a.G + (a.H + 3) / 4)), 128, 0, s>>>(
+  prep_kernel<<<dim3((unsigned)((a.q.max_len + Q - 1) / Q), (unsigned)a.q.n_seq, (unsigned)(a.G + (a.H + 4 * HEADS - 1) / (4 * HEADS))), 128, 0, s>>>(
       a, scores, decays, order);
   const dim3 grid((unsigned)(a.H / 2), (unsigned)(a.q.n_seq * a.nseg));
   if (a.nseg > 1) {
