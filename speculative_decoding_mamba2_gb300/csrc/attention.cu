@@ -8,8 +8,6 @@
 // grown by more than 2^8 (P then stays below 2^8, and its rounding to bf16 is relative).  S of the next tile is made while
 // the softmax of this one runs, and two CTAs to an SM overlap the rest (one CTA with two such streams took 15 to 25 % longer
 // on 320 rows: nothing covered its start and its end).  K and V tiles come by TMA from their pages, through a ring.
-// Where there are at most 64 (32) rows they stand in tensor memory twice (four times), each copy for its half (quarter)
-// of a tile's keys, so that all 128 threads have exponentials to do; the copies' sums are joined at the end.
 // One tile more than the cache has holds the tree's own rows; there a row keeps its node's ancestors only, read from a
 // 64-bit word per node.  Few rows share a tile (n g operations for each byte of the cache), so the keys are split over the
 // SMs where the (sequence, head, row tile) triples leave SMs idle; the partial sums are then joined by combine_kernel.
@@ -32,11 +30,9 @@ template <int D>
 struct AttendSmem {
   static constexpr int OFF_KV = (D / 64 - 1) * 2 * BLK;      // after Q's other columns: 128 rows of 64
   static constexpr int TILE = (D / 64) * BLK;                // K or V of a tile
-  static constexpr int OFF_ML = OFF_KV + 5 * TILE;           // at the end, behind the copies' sums: their maxima
   static constexpr int OFF_MISC = OFF_KV + UNITS * TILE;
   static constexpr int BYTES = OFF_MISC + 768;
   static_assert(BYTES <= 228 * 1024 / 2 - 1024, "two to an SM");
-  static_assert(3 * 32 * (D + 4) * 4 <= 5 * TILE && 1024 <= TILE, "space for the copies' sums");
 };
 struct AttendMisc {
   unsigned long long anc[64];  // ancestors and self of each node
@@ -116,12 +112,12 @@ __device__ __forceinline__ bool find_run(int S, const int* tiles, int tps, int r
   return false;
 }
 
-template <int D, int DUP>
+template <int D>
 __global__ void __launch_bounds__(ATHREADS, 2)
     attend_kernel(const __grid_constant__ CUtensorMap tkp, const __grid_constant__ CUtensorMap tvp,
                   const __grid_constant__ CUtensorMap tkt, const __grid_constant__ CUtensorMap tvt, AttendArgs a) {
   using Sh = AttendSmem<D>;
-  constexpr int RG = 128 / DUP, KK = KT / DUP, DB = D / 64;  // rows of a copy, its keys of a tile, 64-column blocks
+  constexpr int DB = D / 64;  // 64-column blocks
   extern __shared__ __align__(1024) unsigned char smem[];  // (there is no room to move it: where it is not aligned, nothing runs)
   const uint32_t sb = smem_u32(smem);
   AttendMisc* ms = reinterpret_cast<AttendMisc*>(smem + Sh::OFF_MISC);
@@ -181,7 +177,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   const bool has_tree = i0 + n == ct + 1;
 
   if (warp < 4) {
-    const int r = tid % RG, dg = tid / RG, row = r0 + r;  // this thread's row, and which copy of it
+    const int row = r0 + tid;  // this thread's
     const int node = row < rows ? row / a.g : 0, qh = row < rows ? row % a.g : 0;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     {  // q (zero beyond the last row): 64 columns in tensor memory, others in shared memory
@@ -201,12 +197,6 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
-    }
-    if (DUP > 1) {  // the other copies' keys have weight 0
-      const uint32_t z[8] = {};
-#pragma unroll
-      for (int c = 0; c < 32; c += 8) tmem_st8(tmem + A_P + lanes + c, z);
-      tmem_wait_st();
     }
     // ancestor words: a node's own bit, then its parent's word, its grandparent's, ... by doubling
     if (has_tree && warp == 0) {
@@ -252,11 +242,11 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       ok = wait_bar(&ms->s_full, i & 1, stop);
       if (!ok) break;
       tc_fence_after();
-      float sv[KK];
+      float sv[KT];
 #pragma unroll
-      for (int c = 0; c < KK; c += 16) tmem_ld16_async(tmem + A_S + lanes + dg * KK + c, reinterpret_cast<float(&)[16]>(sv[c]));
+      for (int c = 0; c < KT; c += 16) tmem_ld16_async(tmem + A_S + lanes + c, reinterpret_cast<float(&)[16]>(sv[c]));
 #pragma unroll
-      for (int c = 0; c < KK; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
+      for (int c = 0; c < KT; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
       const bool no_page = *(volatile int*)&ms->no_page[i & 7];  // (read before s_free: the copies are three tiles on at most)
       tc_fence_before();
       __syncwarp();
@@ -290,14 +280,13 @@ __global__ void __launch_bounds__(ATHREADS, 2)
         fence_async_smem();
         named_sync(1, 128);  // (and: the ancestor words are there)
         if (tree) rowsv &= ms->anc[node];
-        rowsv >>= dg * KK;
 #pragma unroll
-        for (int j = 0; j < KK; ++j)
+        for (int j = 0; j < KT; ++j)
           if (!((j < 32 ? (uint32_t)rowsv : (uint32_t)(rowsv >> 32)) >> (j & 31) & 1)) sv[j] = -INFINITY;
       }
       float mx = fmaxf(sv[0], sv[1]), my = fmaxf(sv[2], sv[3]);
 #pragma unroll
-      for (int j = 4; j < KK; j += 4) mx = max3f(mx, sv[j], sv[j + 1]), my = max3f(my, sv[j + 2], sv[j + 3]);
+      for (int j = 4; j < KT; j += 4) mx = max3f(mx, sv[j], sv[j + 1]), my = max3f(my, sv[j + 2], sv[j + 3]);
       mx = fmaxf(mx, my) * a.scale_log2;
       if (i == 0) {
         m = mx;
@@ -327,9 +316,9 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       const unsigned long long sc2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
       unsigned long long sum2[2] = {0ull, 0ull};
       const unsigned long long one2 = pack2(1.f, 1.f);
-      const uint32_t pt = tmem + A_P + lanes + dg * (KK / 2);
+      const uint32_t pt = tmem + A_P + lanes;
 #pragma unroll
-      for (int c = 0; c < KK; c += 16) {
+      for (int c = 0; c < KT; c += 16) {
         uint32_t u[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -347,59 +336,20 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       if (lane == 0) mbar_arrive(smem_u32(&ms->p_full));
     }
     ok = ok && wait_bar(&ms->o_done, (n - 1) & 1, stop);
-    // a warp that gives up still takes part in the barriers that others may be waiting at
-    if (!ok) asm volatile("bar.arrive 1, 128;\nbar.arrive 2, 128;\nbar.arrive 2, 128;\n" ::: "memory");
+    // a warp that gives up still takes part in the barrier that others may be waiting at
+    if (!ok) asm volatile("bar.arrive 1, 128;\n" ::: "memory");
     tc_fence_after();
-    float f = 1.f;
-    if (DUP > 1 && ok) {  // the copies' maxima and sums joined
-      float2* ml = reinterpret_cast<float2*>(smem + Sh::OFF_ML);  // the tiles' space is free: their MMAs are done
-      ml[tid] = make_float2(m, l);
-      named_sync(2, 128);
-      float to = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < DUP; ++k) to = fmaxf(to, ml[k * RG + r].x);
-      const float ref = to == -INFINITY ? 0.f : to;
-#pragma unroll
-      for (int k = 0; k < DUP; ++k) sum = fmaf(ml[k * RG + r].y, exp2_sfu(ml[k * RG + r].x - ref), sum);
-      f = exp2_sfu(m - ref);
-      m = to, l = sum;
-      if (dg > 0) {
-        float* os = reinterpret_cast<float*>(smem + Sh::OFF_KV) + ((dg - 1) * RG + r) * (D + 4);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tmem_ld16_async(tmem + A_O + lanes + c, o);
-          tmem_wait_ld16(o);
-#pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<float4*>(os + c + j) = make_float4(o[j] * f, o[j + 1] * f, o[j + 2] * f, o[j + 3] * f);
-        }
-      }
-      named_sync(2, 128);
-    }
-    if (ok && dg == 0) {
+    if (ok) {
       const unsigned long long odd = has_tree ? (ms->odd[0] | (unsigned long long)ms->odd[1] << 32) & ms->anc[node] : 0ull;
       const long long tok = (long long)s * a.n + node;
       const int head = kvh * a.g + qh;
       const float inv = 1.f / l;
-      const float* os = reinterpret_cast<const float*>(smem + Sh::OFF_KV) + r * (D + 4);
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         float o[16];
         __syncwarp();
         tmem_ld16_async(tmem + A_O + lanes + c, o);
         tmem_wait_ld16(o);
-        if (DUP > 1) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] *= f;
-#pragma unroll
-          for (int k = 1; k < DUP; ++k)
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 v = *reinterpret_cast<const float4*>(os + (k - 1) * RG * (D + 4) + c + j);
-              o[j] += v.x, o[j + 1] += v.y, o[j + 2] += v.z, o[j + 3] += v.w;
-            }
-        }
 #pragma unroll 1
         for (unsigned long long todo = odd; todo; todo &= todo - 1) {  // not finite whatever its weight
           const uint32_t* v = reinterpret_cast<const uint32_t*>(
@@ -585,15 +535,14 @@ __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a) {
   for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(o + v) = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
 }
 
-// Copies of the rows, row tiles, and the most runs that the sequences are cut into (0: they are not cut, where the CTAs
+// Row tiles, and the most runs that the sequences are cut into (0: they are not cut, where the CTAs
 // fill the SMs twice over or the longest sequence is too short for what joining costs).
 struct AttendPlan {
-  int dup, row_tiles, max_runs;
+  int row_tiles, max_runs;
 };
 AttendPlan plan_attend(int S, int n, int Hq, int Hkv, int max_len) {
   AttendPlan p;
   const int rows = n * (Hq / Hkv);
-  p.dup = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
   p.row_tiles = (rows + 127) / 128;
   const long long per = (long long)Hkv * p.row_tiles, slots = 2 * kSMs;
   p.max_runs = max_len > 5 * KT && S * per < 2 * slots ? S + (int)((slots + per - 1) / per) : 0;
@@ -601,13 +550,13 @@ AttendPlan plan_attend(int S, int n, int Hq, int Hkv, int max_len) {
 }
 static_assert(2 * 2 * kSMs * 4 <= 6 * 64 * 64 * 2, "the lengths stand in the ring's space");
 
-template <int D, int DUP>
+template <int D>
 cudaError_t run_attend(const AttendArgs& a, const AttendPlan& p, const CUtensorMap (&m)[4], cudaStream_t s) {
   using Sh = AttendSmem<D>;
   static bool done[64];
-  cudaError_t e = allow_smem(attend_kernel<D, DUP>, Sh::BYTES, done);
+  cudaError_t e = allow_smem(attend_kernel<D>, Sh::BYTES, done);
   if (e != cudaSuccess) return e;
-  return launch_early(attend_kernel<D, DUP>, dim3((unsigned)((p.max_runs ? p.max_runs : a.S) * p.row_tiles), (unsigned)a.Hkv),
+  return launch_early(attend_kernel<D>, dim3((unsigned)((p.max_runs ? p.max_runs : a.S) * p.row_tiles), (unsigned)a.Hkv),
                       ATHREADS, Sh::BYTES, s, m[0], m[1], m[2], m[3], a);
 }
 template <int D>
@@ -622,7 +571,7 @@ cudaError_t run_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream_t 
       !encode_tiles(&m[2], a.k, (long long)a.S * a.n, cols, a.ldk, KT) ||
       !encode_tiles(&m[3], a.v, (long long)a.S * a.n, cols, a.ldv, KT))
     return cudaErrorInvalidValue;
-  cudaError_t e = p.dup == 4 ? run_attend<D, 4>(a, p, m, s) : p.dup == 2 ? run_attend<D, 2>(a, p, m, s) : run_attend<D, 1>(a, p, m, s);
+  cudaError_t e = run_attend<D>(a, p, m, s);
   if (e != cudaSuccess || p.max_runs == 0) return e;
   const long long out_rows = (long long)a.S * a.n * a.Hq;
   const bool wide = p.max_runs >= 8 * a.S;  // four warps to a row: 37 splits of 32 rows 17.6 -> 4 us
