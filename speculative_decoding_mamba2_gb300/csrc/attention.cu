@@ -5,14 +5,22 @@
 // 128 of them (the rows of tensor memory) and walks tiles of 64 keys once, on tcgen05:
 //     S [128 x 64] = Q . K^T,   P = 2^(S - m),   O [128 x D] += P . V        (P, O in tensor memory, V read MN-major)
 // with the running maximum m and sum of each row's softmax in the row's thread.  O is rescaled only when a maximum has
-// grown by more than 2^8 (P then stays below 2^8, and its rounding to bf16 is relative).  S of the next tile is made while
-// the softmax of this one runs, and two CTAs to an SM overlap the rest (one CTA with two such streams took 15 to 25 % longer
-// on 320 rows: nothing covered its start and its end).  K and V tiles come by TMA from their pages, through a ring.
+// grown by more than 2^8 (P then stays below 2^8, and its rounding to bf16 is relative).  One warp copies, one issues the MMAs
+// of S, one those of P . V, four do the softmax: S of the next tile is made while the softmax of this one runs, and two CTAs
+// to an SM overlap the rest (one CTA with two such streams took 15 to 25 % longer on 320 rows: nothing covered its start and
+// its end).  K and V tiles come by TMA from their pages, through a ring.  With S's operands both in shared memory that is
+// what binds wide trees (a tile: 384 cycles of reads for S, 128 for P . V, 256 of writes, against 512 of products), so half
+// of Q stands in tensor memory, as much as there is room for.
 // One tile more than the cache has holds the tree's own rows; there a row keeps its node's ancestors only, read from a
 // 64-bit word per node.  Few rows share a tile (n g operations for each byte of the cache), so the keys are split over the
-// SMs where the (sequence, head, row tile) triples leave SMs idle; the partial sums are then joined by combine_kernel.
+// SMs where the (sequence, head, row tile) triples do not fill them; the partial sums are then joined by combine_kernel.
+// Rounding: P to bf16 for the tensor cores, once; the row's sum is that of the unrounded P, in fp32.
 // Rows of V that no key of the tile owns, and values of V in tree rows that are not finite, are zeroed in shared memory
 // (a weight of 0 would spread them); the latter are added to the rows that see them at the end.
+// Measured, both kernels, back to back in a graph (32 query heads, D = 128): one token of one sequence over 16411 rows, 8 heads
+// of K and V, 18 us (67 MB: 3.7 TB/s; latency: seven tiles to a CTA); 8 trees of 16 nodes over up to 8117 rows 40 us (163 MB:
+// 4.1 TB/s of HBM); 4 trees of 40 nodes over up to 40009 rows, 4 heads, 87 us (85 GFLOP: 0.98 PFLOP/s, 1.17 with the rows
+// that fill up the third row tile; tensor pipe 52 % of the time, shared memory the rest).
 #include "prompt.cuh"
 #include "umma.cuh"
 
@@ -574,13 +582,15 @@ cudaError_t run_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream_t 
   cudaError_t e = run_attend<D>(a, p, m, s);
   if (e != cudaSuccess || p.max_runs == 0) return e;
   const long long out_rows = (long long)a.S * a.n * a.Hq;
-  const bool wide = p.max_runs >= 8 * a.S;  // four warps to a row: 37 splits of 32 rows 17.6 -> 4 us
+  // four warps to a row where there are many runs: 38 runs 22.3 us a call with one warp, 18.4 with four; 7 runs 87 and 90
+  const bool wide = p.max_runs >= 8 * a.S;
   const dim3 grid((unsigned)(wide ? out_rows : (out_rows + 3) / 4));
   return wide ? launch_early(combine_kernel<D, 4>, grid, 128, 0, s, a) : launch_early(combine_kernel<D, 1>, grid, 128, 0, s, a);
 }
 
 // A cluster of 8 CTAs for each sequence: together they copy its path's rows; its length is written by one of them
-// once all eight have read it, so len_out may be cache_len.
+// once all eight have read it, so len_out may be cache_len.  A few megabytes at most: the chain of loads from the path to the
+// page to the row is what takes its 8 us (9 for 32 paths of 8 layers, 7.3 MB), so all rows are asked for at once.
 constexpr int CCTAS = 8, CTHREADS = 256;
 __global__ void __cluster_dims__(CCTAS, 1, 1) __launch_bounds__(CTHREADS) kv_commit_kernel(KvCommitArgs a) {
   const int s = blockIdx.y, part = blockIdx.x;

@@ -14,6 +14,12 @@
 // specialised by step, tried first, each ran their own code: 4000 cycles a chunk, most of them waiting for instructions.)
 // MMAs run in the order they are issued: S, Y2, Y1.  Every wait is bounded: on a time-out all warps leave, the copies and
 // MMAs in flight are waited for (bounded again) and the tensor memory is freed.
+// Rounding: h, P and y to bf16 once each (h and P as operands, relative to themselves); the state's own chain -- decays, Xw, S,
+// h -- keeps 24 bits.
+// Measured: 24571 tokens of 16 prompts, 80 heads, 236 us back to back (604 MB: 2.6 TB/s; 19 us of it prep_kernel); one prompt of
+// 8191 tokens 115 us (prep 9, states of two segments 34, walks of three 77, less what overlaps).  The walk is bound by its
+// 16 warps' instructions: issue slots 66 % taken, the tensor pipe busy 40 % of the time (57 % in the pass over states).  A
+// warp for each kind of MMA, scalar instead of paired fp32 and two waits in one changed nothing.
 #include "prompt.cuh"
 #include "umma.cuh"
 
@@ -104,7 +110,8 @@ __device__ __forceinline__ bool write_xw(uint32_t x, const uint32_t (&f_off)[2],
 // Once for all walks: grid z < G: scores C_t . B_s of a chunk and group, [record][s / 4][t][s % 4] fp32; then the decays
 // of a chunk, HEADS heads to a warp.
 __device__ __forceinline__ long long chunk_record(int first, int s, int chunk) { return (long long)(first / Q) + s + chunk; }
-constexpr int HEADS = 4;  // of a warp: their chains of shuffles and exponentials fill each other's gaps (1: 239, 2: 236, 4: 235.6 us of a scan)
+// of a warp: their chains of shuffles and exponentials fill each other's gaps (1: 239, 2: 236, 4: 235.6 us of a scan)
+constexpr int HEADS = 4;
 __global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, Decays* decays, int* order) {
   __shared__ __align__(128) unsigned char sm[2 * Q * kN * 2];
   launch_dependents();
@@ -237,7 +244,8 @@ __global__ void __launch_bounds__(NT, 1)
     bar->stop = 0;
     fence_barrier_init();
   }
-  for (int i = tid; i < 4 * BLK / 16; i += NT) reinterpret_cast<uint4*>(smem + OFF_P)[i] = make_uint4(0, 0, 0, 0);  // P's entries after their token stay so
+  // P's entries after their token stay zero
+  for (int i = tid; i < 4 * BLK / 16; i += NT) reinterpret_cast<uint4*>(smem + OFF_P)[i] = make_uint4(0, 0, 0, 0);
   if (warp == WARPS) tmem_alloc_warp(smem_u32(&bar->tmem), 512);
   tc_fence_before();
   __syncthreads();
