@@ -16,9 +16,9 @@
 // MMAs in flight are waited for (bounded again) and the tensor memory is freed.
 // Rounding: h, P and y to bf16 once each (h and P as operands, relative to themselves); the state's own chain -- decays, Xw, S,
 // h -- keeps 24 bits.
-// Measured: 24571 tokens of 16 prompts, 80 heads, 236 us back to back (604 MB: 2.6 TB/s; 19 us of it prep_kernel); one prompt of
-// 8191 tokens 115 us (prep 9, states of two segments 34, walks of three 77, less what overlaps).  The walk is bound by its
-// 16 warps' instructions: issue slots 66 % taken, the tensor pipe busy 40 % of the time (57 % in the pass over states).  A
+// Measured: 24571 tokens of 16 prompts, 80 heads, 232 us back to back (604 MB: 2.6 TB/s; 19 us of it prep_kernel); one prompt of
+// 8191 tokens 109 us.  The walk is bound by its 16 warps' instructions: issue slots 66 % taken, the tensor pipe busy 40 % of
+// the time (57 % in the walks over states).  A
 // warp for each kind of MMA, scalar instead of paired fp32 and two waits in one changed nothing.
 #include "prompt.cuh"
 #include "umma.cuh"
@@ -219,14 +219,20 @@ __global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, De
     }
 }
 
-__global__ void __launch_bounds__(NT, 1)
-    scan_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
-                   const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap ty, ScanArgs a,
-                   const float* scores, const Decays* decays, const int* order) {
+// Segment j of a sequence's nch chunks: chunks c0 .. c1 - 1.  With k = nseg - 1, the first is two fifths as long as the others:
+// its walk, in the first grid, then takes as long as the others' walks over states beside it (1.55 and 0.62 us a chunk).
+__device__ __forceinline__ void segment(int nch, int nseg, int j, int& c0, int& c1) {
+  const int k = nseg - 1, b = (5 * nch + 5 * k + 1) / (5 * k + 2), f = nseg == 1 ? nch : max(0, nch - k * b);
+  c0 = j == 0 ? 0 : f + (j - 1) * b;
+  c1 = min(nch, j == 0 ? f : c0 + b);
+}
+
+__device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& tb, const CUtensorMap& tcm, const CUtensorMap& ty,
+                                     const ScanArgs& a, const float* scores, const Decays* decays, const int* order, int rank, int seg) {
   extern __shared__ unsigned char smem_raw[];
   // (shuffles tell the compiler what is the same for a warp: it then keeps it in uniform registers)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int pair = blockIdx.x, seg = blockIdx.y % a.nseg;
+  const int pair = blockIdx.x;
   unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // stays a shared-memory pointer to the compiler
   const uint32_t sb = smem_u32(smem);
   Bars* bar = reinterpret_cast<Bars*>(smem + OFF_BAR);
@@ -251,13 +257,15 @@ __global__ void __launch_bounds__(NT, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar->tmem, 0);
-  grid_dependency_wait();  // scores, decays, the order, what the segments before add
-  const int s = __shfl_sync(0xffffffffu, order[blockIdx.y / a.nseg], 0);
+  grid_dependency_wait();  // scores, decays, the order, the states of the segments before
+  const int s = __shfl_sync(0xffffffffu, order[rank], 0);
   int first, len, slot;
   const bool there = seq_range(a.q, s, first, len, slot);
   first = __shfl_sync(0xffffffffu, first, 0), len = __shfl_sync(0xffffffffu, len, 0), slot = __shfl_sync(0xffffffffu, slot, 0);
-  const int nch = (len + Q - 1) / Q, per = (nch + a.nseg - 1) / a.nseg;
-  const int c0 = seg * per, c1 = min(nch, c0 + per), n = max(0, c1 - c0);
+  const int nch = (len + Q - 1) / Q;
+  int c0, c1;
+  segment(nch, a.nseg, seg, c0, c1);
+  const int n = max(0, c1 - c0);
   if (!there || (n == 0 && seg > 0)) {
     if (!there && pair == 0 && seg == 0 && tid == 0) flag(a.q.status, SSM_STATUS_SEQ_RANGE);
     if (warp == WARPS) tmem_free_warp(tmem, 512);
@@ -286,15 +294,18 @@ __global__ void __launch_bounds__(NT, 1)
     float h[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) h[j] = 0.f;
-    if (a.h_in) {
+    // from the caller's state, or from that after the first segment and what those between add (the caller's, which may be
+    // written in place, is read by the first segment alone, in an earlier grid than its last write)
+    const float* from = seg == 0 ? (a.h_in ? a.h_in + at : nullptr) : ws + p * kN + n0;
+    if (from) {
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(a.h_in + at + j);
+        const float4 v = *reinterpret_cast<const float4*>(from + j);
         h[j] = v.x, h[j + 1] = v.y, h[j + 2] = v.z, h[j + 3] = v.w;
       }
     }
 #pragma unroll 1
-    for (int k = 0; k < seg; ++k) {
+    for (int k = 1; k < seg; ++k) {
       const float* r = ws + k * wrec;
       const float dk = r[kP * kN];
       r += p * kN + n0;
@@ -305,6 +316,7 @@ __global__ void __launch_bounds__(NT, 1)
         h[j + 2] = fmaf(dk, h[j + 2], v.z), h[j + 3] = fmaf(dk, h[j + 3], v.w);
       }
     }
+    float* out = c1 == nch ? a.h_out + at : seg == 0 ? ws + p * kN + n0 : nullptr;  // for the state at the end
     const float Dh = a.D[head];
     const unsigned long long D2 = pack2(Dh, Dh);
 
@@ -509,9 +521,9 @@ __global__ void __launch_bounds__(NT, 1)
       hand_over(B_H);
       hand_over(B_P);
     }
-    if (ok && c1 == nch) {
+    if (ok && out) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(a.h_out + at + j) = make_float4(h[j], h[j + 1], h[j + 2], h[j + 3]);
+      for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(out + j) = make_float4(h[j], h[j + 1], h[j + 2], h[j + 3]);
     }
   } else if (warp == WARPS + 1) {
     // ---- copies ----
@@ -607,27 +619,26 @@ __global__ void __launch_bounds__(NT, 1)
   }
 }
 
-// What a segment adds to the state, and its decay: the walk of scan_tc_kernel without y.  Two chunks are under way, each with
+// What a segment adds to the state, and its decay: the walk above without y.  Two chunks are under way, each with
 // its own S and Xw in tensor memory: the S of one is made while the one before it is added up and the next one's Xw written
 // (with one, 43 chunks of 80 pairs and segments took 55 us, each step waiting for the one before).  Segments before a
 // sequence's last have whole chunks only.
 constexpr int S_STAGES = 6, S_BYTES = 4 * BLK;        // stages of B | x
 constexpr int S_OFF_D = S_STAGES * S_BYTES, S_OFF_BAR = S_OFF_D + S_STAGES * 2 * REC;
-constexpr int S_SMEM = S_OFF_BAR + 256 + 1024 /* alignment */, S_NT = 32 * WARPS + 64;
+constexpr int S_SMEM = S_OFF_BAR + 256 + 1024 /* alignment */;
 constexpr int T_S2 = 0, T_XW2 = 256;                  // two of 128 columns, two of 96
 struct StateBars {
   unsigned long long full[S_STAGES], free_[S_STAGES], s_full[2], drain;
   uint32_t tmem;
   int stop;
 };
-static_assert(sizeof(StateBars) <= 256 && S_SMEM <= 227 * 1024, "space");
+static_assert(sizeof(StateBars) <= 256 && S_SMEM <= TC_SMEM, "space");
 
-__global__ void __launch_bounds__(S_NT, 1)
-    scan_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb, ScanArgs a,
-                      const Decays* decays, const int* order) {
+__device__ __forceinline__ void state_walk(const CUtensorMap& tx, const CUtensorMap& tb, const ScanArgs& a, const Decays* decays,
+                                           const int* order, int rank, int seg) {
   extern __shared__ unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int pair = blockIdx.x, seg = blockIdx.y % (a.nseg - 1);
+  const int pair = blockIdx.x;
   unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   const uint32_t sb = smem_u32(smem);
   StateBars* bar = reinterpret_cast<StateBars*>(smem + S_OFF_BAR);
@@ -649,19 +660,21 @@ __global__ void __launch_bounds__(S_NT, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar->tmem, 0);
   grid_dependency_wait();  // decays, the order
-  const int s = __shfl_sync(0xffffffffu, order[blockIdx.y / (a.nseg - 1)], 0);
+  const int s = __shfl_sync(0xffffffffu, order[rank], 0);
   int first, len, slot;
   const bool there = seq_range(a.q, s, first, len, slot);
   first = __shfl_sync(0xffffffffu, first, 0), len = __shfl_sync(0xffffffffu, len, 0);
-  const int nch = (len + Q - 1) / Q, per = (nch + a.nseg - 1) / a.nseg;
-  const int c0 = seg * per, c1 = c0 + per, n = per;
-  if (!there || c1 >= nch) {
+  const int nch = (len + Q - 1) / Q;
+  int c0, c1;
+  segment(nch, a.nseg, seg, c0, c1);
+  const int n = c1 - c0;
+  if (!there || c1 >= nch) {  // none behind it
     if (warp == WARPS) tmem_free_warp(tmem, 512);
     return;
   }
 
   if (warp < WARPS) {
-    const int w4 = warp & 3, grp4 = warp >> 2;  // as in scan_tc_kernel
+    const int w4 = warp & 3, grp4 = warp >> 2;  // as in walk
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const int row = w4 * 32 + lane, hd = row >> 6, p = row & 63, head = 2 * pair + hd;
     const int q4 = lane & 3, p0 = (w4 & 1) * 32, tg = 16 * grp4, n0 = 32 * grp4;
@@ -708,7 +721,7 @@ __global__ void __launch_bounds__(S_NT, 1)
         if (++st == S_STAGES) st = 0, full_par ^= 1;
       }
     }
-    if (!ok) {  // (as in scan_tc_kernel)
+    if (!ok) {  // (as in walk)
       hand_over(B_XW);
       hand_over(B_XW + 1);
     } else {
@@ -780,10 +793,31 @@ __global__ void __launch_bounds__(S_NT, 1)
   }
 }
 
+// A sequence in one segment, or its segments from the second on.
+__global__ void __launch_bounds__(NT, 1)
+    scan_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
+                   const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap ty, ScanArgs a,
+                   const float* scores, const Decays* decays, const int* order) {
+  const int per = max(1, a.nseg - 1);
+  walk(tx, tb, tcm, ty, a, scores, decays, order, blockIdx.y / per, a.nseg == 1 ? 0 : blockIdx.y % per + 1);
+}
+// Before it, where there are several: the first segment, and beside it the states of those between the first and the last.  (One
+// kernel for both grids made every walk 10 % longer.)
+__global__ void __launch_bounds__(NT, 1)
+    scan_first_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
+                      const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap ty, ScanArgs a,
+                      const float* scores, const Decays* decays, const int* order) {
+  const int rank = blockIdx.y / (a.nseg - 1), j = blockIdx.y % (a.nseg - 1);
+  if (j == 0)
+    walk(tx, tb, tcm, ty, a, scores, decays, order, rank, 0);
+  else
+    state_walk(tx, tb, a, decays, order, rank, j);
+}
+
 // Segments of a sequence's chunks, for one CTA of a head pair to an SM: where sequences and pairs leave SMs idle, the pass over
 // the segments' states pays for itself.  (us back to back, in one segment | in several: 10 chunks of 16 pairs 28 | 33 in two;
-// 16 chunks of 40 pairs 37 | 39 in two, 36 in three; up to 20 chunks of 24 pairs 43 | 38 in five, 37 in three; up to 81 chunks
-// of 48 pairs 137 | 86 in three.)
+// 16 chunks of 40 pairs 37 | 39 in four; up to 20 chunks of 24 pairs 43 | 38 in five, 37 in four; up to 81 chunks of 48 pairs
+// 137 | 86 in four; 128 chunks of 40 pairs 190 | 109 in four.)
 int plan_segments_tc(int H, int n_seq, int max_len) {
   const long long items = (long long)(H / 2) * n_seq;
   const int nch = (max_len + Q - 1) / Q;
@@ -791,7 +825,7 @@ int plan_segments_tc(int H, int n_seq, int max_len) {
   int nseg = (int)(kSMs / (items > 0 ? items : 1));
   if (nseg > nch / 5) nseg = nch / 5;
   if (nseg > 16) nseg = 16;
-  return nseg < 2 ? 1 : nseg;
+  return nseg < 2 ? 1 : nseg + 1;
 }
 
 // workspace: scores, decays, then what segments add to the state; chunks of all sequences at most n_tok / Q + n_seq
@@ -831,7 +865,7 @@ cudaError_t launch_prompt_scan_tc(const ScanArgs& args, void* workspace, cudaStr
   a.seg_state = reinterpret_cast<float*>(ws);
   static bool done[2][64];
   cudaError_t e = allow_smem(scan_tc_kernel, TC_SMEM, done[0]);
-  if (e == cudaSuccess) e = allow_smem(scan_state_kernel, S_SMEM, done[1]);
+  if (e == cudaSuccess) e = allow_smem(scan_first_kernel, TC_SMEM, done[1]);
   if (e != cudaSuccess) return e;
   CUtensorMap tx, tb, tcm, ty;
   if (!encode_tiles(&tx, a.x, a.q.n_tok, (long long)a.H * kP, a.ldx, Q) || !encode_tiles(&tb, a.B, a.q.n_tok, (long long)a.G * kN, a.ldb, Q) ||
@@ -839,10 +873,10 @@ cudaError_t launch_prompt_scan_tc(const ScanArgs& args, void* workspace, cudaStr
     return cudaErrorInvalidValue;
   prep_kernel<<<dim3((unsigned)((a.q.max_len + Q - 1) / Q), (unsigned)a.q.n_seq, (unsigned)(a.G + (a.H + 4 * HEADS - 1) / (4 * HEADS))), 128, 0, s>>>(
       a, scores, decays, order);
-  const dim3 grid((unsigned)(a.H / 2), (unsigned)(a.q.n_seq * a.nseg));
+  const dim3 grid((unsigned)(a.H / 2), (unsigned)(a.q.n_seq * max(1, a.nseg - 1)));
   if (a.nseg > 1) {
-    e = launch_early(scan_state_kernel, dim3(grid.x, (unsigned)(a.q.n_seq * (a.nseg - 1))), S_NT, S_SMEM, s, tx, tb, a,
-                     (const Decays*)decays, (const int*)order);
+    e = launch_early(scan_first_kernel, grid, NT, TC_SMEM, s, tx, tb, tcm, ty, a, (const float*)scores, (const Decays*)decays,
+                     (const int*)order);
     if (e != cudaSuccess) return e;
   }
   return launch_early(scan_tc_kernel, grid, NT, TC_SMEM, s, tx, tb, tcm, ty, a, (const float*)scores, (const Decays*)decays,
