@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_scan_kernel(ScanArgs a) {
   if (STATE_ONLY ? c1 >= nch : (c0 >= c1 && seg > 0)) return;  // no segment after it; nothing in it
   const long long hbase = (((long long)slot * a.L + a.layer) * a.H + h) * (kP * kN);
   const long long wrec = kP * kN + 32;  // a workspace record: the state, then the decay
-  float* ws = a.seg_state + ((long long)s * a.H + h) * (a.nseg - 1) * wrec;
+  float* ws = a.seg_state + ((long long)s * a.H + h) * a.nseg * wrec;  // the last record: the caller's state
   const uint32_t sb = smem_u32(smem);
   const int grp = h / (a.H / a.G), g = lane >> 2, q4 = lane & 3;
   const float A = neg_exp(a.A_log[h]), bias = a.dt_bias[h], Dh = a.D[h];
@@ -77,14 +77,24 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_scan_kernel(ScanArgs a) {
   if (c0 < c1) load(c0);
 
   // the state: warp w rows 16w + g and + 8, columns 8 nt + 2 q4, + 1 (the accumulator fragments)
+  // (the caller's state may be written in place by a sequence's last segment: where there are several, the first grid copies it)
   float hs[16][4];
+  const float* from = !a.h_in || (STATE_ONLY && seg > 0)  ? nullptr
+                      : STATE_ONLY || (seg == 0 && c1 == nch) ? a.h_in + hbase
+                                                              : ws + (a.nseg - 1) * wrec;
 #pragma unroll
   for (int nt = 0; nt < 16; ++nt) {
     const int n = nt * 8 + 2 * q4;
     float2 lo = make_float2(0.f, 0.f), hi = lo;
-    if (!STATE_ONLY && a.h_in) {
-      lo = *reinterpret_cast<const float2*>(a.h_in + hbase + (16 * warp + g) * kN + n);
-      hi = *reinterpret_cast<const float2*>(a.h_in + hbase + (16 * warp + g + 8) * kN + n);
+    if (from) {
+      lo = *reinterpret_cast<const float2*>(from + (16 * warp + g) * kN + n);
+      hi = *reinterpret_cast<const float2*>(from + (16 * warp + g + 8) * kN + n);
+      if (STATE_ONLY) {
+        float* copy = ws + (a.nseg - 1) * wrec;
+        *reinterpret_cast<float2*>(copy + (16 * warp + g) * kN + n) = lo;
+        *reinterpret_cast<float2*>(copy + (16 * warp + g + 8) * kN + n) = hi;
+        lo = hi = make_float2(0.f, 0.f);
+      }
     }
     if (!STATE_ONLY) {
 #pragma unroll 1
@@ -308,7 +318,7 @@ int plan_segments(int H, int n_seq, int max_len) {
 size_t prompt_scan_workspace_bytes(int H, int G, int n_seq, int n_tok, int max_len) {
   if (prompt_scan_tc_fits(H, G, n_seq, max_len)) return prompt_scan_tc_workspace_bytes(H, G, n_seq, n_tok, max_len);
   const int nseg = plan_segments(H, n_seq, max_len);
-  return 256 + (size_t)n_seq * H * (nseg - 1) * (kP * kN + 32) * sizeof(float);
+  return 256 + (size_t)n_seq * H * (nseg > 1 ? nseg : 0) * (kP * kN + 32) * sizeof(float);
 }
 
 cudaError_t launch_prompt_scan(const ScanArgs& args, void* workspace, cudaStream_t s) {

@@ -429,3 +429,16 @@ def test_prompt_scan_skips_what_is_out_of_range_long():
             my, mh = reference(c, s, magnitude=True)
             assert (np.abs(y[cu[s]:cu[s + 1]] - ry) <= U * np.abs(ry) + (U + 2.0 ** -12) * my).all(), (wrong, s)
             assert (np.abs(h[slots[s], 0] - rh) <= 4e-6 * 6 * mh).all(), (wrong, s)
+
+
+@pytest.mark.parametrize("H,G", [(3, 3), (4, 1)])
+def test_prompt_scan_in_place_over_segments(H, G):
+    """A prompt cut into segments (by either kernel), its state written over the one it starts from: as out of place."""
+    c = scan_case(25, H, G, [3000, 100, 1300])
+    y0, h0, _ = run_scan(c)
+    y, h, status = run_scan(c, in_place=True)
+    assert status == 0
+    np.testing.assert_array_equal(y, y0)
+    check_scan(c, y, h, in_place=True)
+    for s in range(c["S"]):
+        np.testing.assert_array_equal(h[c["slots"][s], 0], h0[c["slots"][s], 0])
