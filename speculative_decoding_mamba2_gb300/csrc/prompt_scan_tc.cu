@@ -17,8 +17,8 @@
 // Rounding: h, P and y to bf16 once each (h and P as operands, relative to themselves); the state's own chain -- decays, Xw, S,
 // h -- keeps 24 bits.
 // Measured: 24571 tokens of 16 prompts, 80 heads, 232 us back to back (604 MB: 2.6 TB/s; 19 us of it prep_kernel); one prompt of
-// 8191 tokens 109 us.  The walk is bound by its 16 warps' instructions: issue slots 66 % taken, the tensor pipe busy 40 % of
-// the time (57 % in the walks over states).  A warp for each kind of MMA, scalar instead of paired fp32 and two waits in one
+// 8191 tokens 109 us.  The walk is bound by its 16 warps' instructions: issue slots 64 % taken, the tensor pipe busy 38 % of
+// the time (46 % with the walks over states).  A warp for each kind of MMA, scalar instead of paired fp32 and two waits in one
 // changed nothing.
 #include "prompt.cuh"
 #include "umma.cuh"
@@ -621,7 +621,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
 
 // What a segment adds to the state, and its decay: the walk above without y.  Two chunks are under way, each with
 // its own S and Xw in tensor memory: the S of one is made while the one before it is added up and the next one's Xw written
-// (with one, 43 chunks of 80 pairs and segments took 55 us, each step waiting for the one before).  Segments before a
+// (with one, 43 chunks took 55 us instead of 34, each step waiting for the one before).  Segments before a
 // sequence's last have whole chunks only.
 constexpr int S_STAGES = 6, S_BYTES = 4 * BLK;        // stages of B | x
 constexpr int S_OFF_D = S_STAGES * S_BYTES, S_OFF_BAR = S_OFF_D + S_STAGES * 2 * REC;
