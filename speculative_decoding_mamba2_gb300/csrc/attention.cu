@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   if (smem_u32(smem) & 1023u) {
     grid_dependency_wait();  // no grid ends before the one that it depends on
     if (tid == 0) flag(a.status, SSM_STATUS_TIMEOUT);
+    if (tid == 0 && run < a.S && a.max_runs > 0) a.runs[run] = make_int2(0, 1);  // nothing to join
     return;
   }
   if (tid == 0) {
