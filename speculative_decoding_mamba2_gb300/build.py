@@ -20,10 +20,10 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["api.cu", "verify.cu", "verify_tc.cu", "commit.cu", "draft.cu", "noalloc.cu", "chain.cu", "gemm.cu", "norm.cu",
-           "layer_api.cu", "draft_tree.cu", "selftest.cu", "prompt.cu", "prompt_scan.cu", "prompt_scan_tc.cu", "attention.cu", "prompt_api.cu",
-           "layout.cpp"]
-HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "draft_tree.cuh", "log_apply.cuh", "tc.cuh", "mma_tiles.cuh", "prompt.cuh",
-                                              "umma.cuh")] + \
+           "layer_api.cu", "draft_tree.cu", "selftest.cu", "prompt.cu", "prompt_scan.cu", "prompt_scan_tc.cu", "attention.cu",
+           "prompt_api.cu", "layout.cpp"]
+HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "draft_tree.cuh", "log_apply.cuh", "tc.cuh", "mma_tiles.cuh",
+                                           "prompt.cuh", "umma.cuh")] + \
     [os.path.join(INCLUDE, h) for h in ("ssm_tree.h", "ssm_layer.h", "ssm_prompt.h", "ssm_attention.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 LIBNAME = "libssmtree.so"

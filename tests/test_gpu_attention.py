@@ -316,3 +316,28 @@ def test_tree_attention_bad_lengths_beside_long_caches():
     assert status == SSM_STATUS_SEQ_RANGE
     for s, length in enumerate([2000, 0, 0, 700]):
         check(c, o, s, length=length)
+
+
+def test_pages_past_32_bit_offsets():
+    """Pages whose bytes and elements lie past 2^32: read by the attention, written by the commit, as in a small pool."""
+    from speculative_decoding_mamba2_gb300 import ssm_kv_commit
+    c = case(10, 2, 4, 2, 2, 128, [300, 64], 128)
+    o0, status = run(c)
+    assert status == 0
+    total = 140000  # pages of 2 x 128 x 128 bf16: 4.6e9 elements
+    far = {k: torch.empty(total, c["Hkv"], c["page"], c["D"], dtype=torch.bfloat16, device="cuda") for k in ("kp", "vp")}
+    base = total - c["pool"]
+    for k, pages in far.items():
+        pages[base:] = c[k]
+    near = {k: c[k].clone() for k in far}
+    big = dict(c, **far, table=c["table"] + base)
+    o, status = run(big)
+    assert status == 0
+    np.testing.assert_array_equal(o, o0)
+    path, pl, out = ints([[0, 1], [0, -1]]), ints([2, 1]), torch.zeros(2, dtype=torch.int32, device="cuda")
+    for kp, vp, table in ((near["kp"], near["vp"], c["table"]), (far["kp"], far["vp"], big["table"])):
+        ssm_kv_commit(2, 4, path, pl, c["k"].contiguous()[None], c["v"].contiguous()[None], kp[None], vp[None], ints(table), ints(c["lens"]), out)
+    torch.cuda.synchronize()
+    assert out.tolist() == [302, 65]
+    for k in far:
+        assert torch.equal(far[k][base:], near[k]) and not torch.equal(near[k], c[k])

@@ -442,3 +442,36 @@ def test_prompt_scan_in_place_over_segments(H, G):
     check_scan(c, y, h, in_place=True)
     for s in range(c["S"]):
         np.testing.assert_array_equal(h[c["slots"][s], 0], h0[c["slots"][s], 0])
+
+
+@pytest.mark.parametrize("H,G", [(2, 1), (1, 1)])
+def test_prompt_scan_and_conv_past_32_bit_offsets(H, G):
+    """Rows 2^25 elements apart (the last one starts past 2^32 elements): as rows side by side, by either scan kernel."""
+    from speculative_decoding_mamba2_gb300 import Dims, ssm_prompt_conv, ssm_prompt_scan, ssm_prompt_scan_workspace_size
+    T, ld = 200, 1 << 25
+    c = scan_case(26, H, G, [T])
+    y0, h0, _ = run_scan(c)
+    d = Dims(n_heads=H)
+    wide = torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")
+    cols, at = {}, 0
+    for k, n in (("x", H * P), ("B", G * N), ("C", G * N), ("dt", H), ("y", H * P), ("pre", d.conv_dim), ("post", d.conv_dim)):
+        cols[k], at = wide[:, at:at + n], at + (n + 7) // 8 * 8
+    for k in ("x", "B", "C", "dt"):
+        cols[k].copy_(c[k])
+    h = torch.empty_like(f32(c["h0"]))
+    ws = torch.empty(ssm_prompt_scan_workspace_size(d, 1, T, T, G), dtype=torch.uint8, device="cuda")
+    ssm_prompt_scan(d, c["prm"], 0, ints(c["cu"]), T, cols["x"], cols["B"], cols["C"], cols["dt"], f32(c["h0"]), h, cols["y"], ws,
+                    slots=ints(c["slots"]))
+    np.testing.assert_array_equal(host(cols["y"]).reshape(T, H, P), y0)
+    np.testing.assert_array_equal(host(h)[c["slots"][0]], h0[c["slots"][0]])
+
+    pre = torch.randn(T, d.conv_dim, device="cuda").bfloat16()
+    prm = dict(conv_w=torch.randn(1, d.conv_dim, 4, device="cuda"), conv_b=torch.randn(1, d.conv_dim, device="cuda"))
+    cols["pre"].copy_(pre)
+    outs = []
+    for x, out in ((pre, torch.empty_like(pre)), (cols["pre"], cols["post"])):
+        ring, head = torch.zeros(1, 1, 20, d.conv_dim, dtype=torch.bfloat16, device="cuda"), torch.full((1, 1), 3, dtype=torch.int32, device="cuda")
+        ssm_prompt_conv(d, prm, 0, ints([0, T]), T, x, ring, head, out)
+        outs.append((out.clone(), ring, head))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
