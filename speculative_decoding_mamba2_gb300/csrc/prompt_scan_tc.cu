@@ -252,6 +252,8 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
   }
   // P's entries after their token stay zero
   for (int i = tid; i < 4 * BLK / 16; i += NT) reinterpret_cast<uint4*>(smem + OFF_P)[i] = make_uint4(0, 0, 0, 0);
+  // a warp writes its tokens' word only where there is something to mark, and all of them are read
+  for (int i = tid; i < 2 * 4 * 128; i += NT) reinterpret_cast<uint32_t*>(smem + OFF_ODD)[i] = 0;
   if (warp == WARPS) tmem_alloc_warp(smem_u32(&bar->tmem), 512);
   tc_fence_before();
   __syncthreads();

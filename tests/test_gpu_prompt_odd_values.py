@@ -1,0 +1,67 @@
+"""Values of x that are not finite, in the prompt scan: what they reach, and that nothing else changes.
+
+A value of x in column p of a head makes that column of y, from its token on, and that row of the state something that is
+not finite.  Every other output is the same products and sums of the same values as without it: equal to the last bit."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_prompt import P, _lib, run_scan, scan_case  # noqa: F401 (the fixture builds the library)
+
+pytestmark = pytest.mark.gpu
+VALUES = [float("inf"), -float("inf"), float("nan")]
+
+
+def put(c, where, rng):
+    """Such values at (token row, head, column): (x as it was, first token of each (sequence, head, column) reached)."""
+    was, reach = c["x"].clone(), {}
+    for row, head, p in where:
+        c["x"][row, head * P + p] = VALUES[int(rng.integers(3))]
+        s = int(np.searchsorted(c["cu"], row, side="right")) - 1
+        reach[s, head, p] = min(row, reach.get((s, head, p), row))
+    return was, reach
+
+
+def check_reach(c, reach, y0, h0, y, h):
+    want_y, want_h = np.zeros(y.shape, bool), np.zeros(h.shape[:1] + h.shape[2:4], bool)
+    for (s, head, p), row in reach.items():
+        want_y[row:c["cu"][s + 1], head, p] = True
+        want_h[c["slots"][s], head, p] = True
+    np.testing.assert_array_equal(~np.isfinite(y), want_y)
+    np.testing.assert_array_equal(y[~want_y], y0[~want_y])
+    np.testing.assert_array_equal(~np.isfinite(h[:, 0]), np.broadcast_to(want_h[..., None], h[:, 0].shape))
+    np.testing.assert_array_equal(h[:, 0][~want_h], h0[:, 0][~want_h])
+
+
+@pytest.mark.parametrize("H,G,lens", [(4, 1, [1200, 130]), (3, 3, [100, 30]), (3, 3, [1200, 130]), (4, 2, [70])], ids=str)
+@pytest.mark.parametrize("at", [0, 17, 64])
+def test_one_value_reaches_one_column(H, G, lens, at):
+    c = scan_case(41, H, G, lens)
+    y0, h0, _ = run_scan(c)
+    _, reach = put(c, [(at, 1, 5)], np.random.default_rng(at))
+    y, h, status = run_scan(c)
+    assert status == 0
+    check_reach(c, reach, y0, h0, y, h)
+
+
+@pytest.mark.parametrize("lens", [[330, 201, 129, 251] * 4, [240] * 9], ids=str)
+def test_values_in_one_chunk_of_many_walks(lens):
+    """Every sequence and pair of heads has a value in its chunk 3 (the last one and a short one among them), each at
+    another token and column.  More walks than SMs: one follows the other in the same shared memory; call after call."""
+    H = 80
+    c = scan_case(42, H, 1, lens)
+    y0, h0, _ = run_scan(c)
+    rng = np.random.default_rng(43)
+    for _ in range(3):
+        where = []
+        for s, n in enumerate(lens):
+            chunk = min(3, (n - 1) // 64)
+            for pair in range(H // 2):
+                if rng.random() < 0.8:
+                    row = int(rng.integers(chunk * 64, min(n, chunk * 64 + 64)))
+                    where.append((int(c["cu"][s]) + row, 2 * pair + int(rng.integers(2)), int(rng.integers(P))))
+        was, reach = put(c, where, rng)
+        y, h, status = run_scan(c)
+        assert status == 0
+        check_reach(c, reach, y0, h0, y, h)
+        c["x"].copy_(was)
