@@ -65,3 +65,20 @@ def test_values_in_one_chunk_of_many_walks(lens):
         assert status == 0
         check_reach(c, reach, y0, h0, y, h)
         c["x"].copy_(was)
+
+
+@pytest.mark.parametrize("H,G,lens", [(80, 1, [700, 640, 333]), (24, 1, [2000, 130]), (3, 3, [330, 65])], ids=str)
+def test_values_in_many_chunks(H, G, lens):
+    """Several in each chunk, or in every second one, at random tokens and columns: what one chunk's outputs still need is
+    not what a later chunk marks."""
+    c = scan_case(44, H, G, lens)
+    y0, h0, _ = run_scan(c)
+    rng = np.random.default_rng(45)
+    for step, each in ((1, 2), (2, 3), (2, 1)):
+        where = [(int(c["cu"][s]) + int(rng.integers(k * 64, min(n, k * 64 + 64))), int(rng.integers(H)), int(rng.integers(P)))
+                 for s, n in enumerate(lens) for k in range(0, -(-n // 64), step) for _ in range(each * H // 2)]
+        was, reach = put(c, where, rng)
+        y, h, status = run_scan(c)
+        assert status == 0
+        check_reach(c, reach, y0, h0, y, h)
+        c["x"].copy_(was)
