@@ -35,11 +35,17 @@ constexpr int BLK = Q * 128;  // a 64 x 64 bf16 block with 128-byte rows
 constexpr int ST_BYTES = 6 * BLK, OFF_TB = 2 * BLK, OFF_TX = 4 * BLK;
 constexpr int OFF_P = STAGES * ST_BYTES;   // [2][head][BLK]
 constexpr int OFF_Y = OFF_P + 4 * BLK;     // [2][64][256]
-constexpr int OFF_D = OFF_Y + 4 * BLK;     // [STAGES]: two decay records, then which x of the chunk are not finite:
-constexpr int REC = 1408;                  // (bytes of a record)
-constexpr int OFF_ODD = 2 * REC;           // a word for each group and row of its 16 tokens, and the last chunk that has such an x
-constexpr int OFF_MARK = OFF_ODD + 4 * 128 * 4, D_BYTES = OFF_MARK + 16;
-constexpr int OFF_BAR = OFF_D + STAGES * D_BYTES;
+constexpr int OFF_D = OFF_Y + 4 * BLK;     // [STAGES][head] decay records
+constexpr int REC = 1408;                  // bytes of one
+constexpr int OFF_ODD = OFF_D + STAGES * 2 * REC;
+// Which x are not finite, of chunk i at [i & 3]: written with Xw, read with y.  Two places would not do: a group may write chunk
+// i + 1's while another is still at y of chunk i - 1 (it needs S of chunk i, which needs nothing of that y), but not i + 2's.
+struct Odd {
+  uint32_t tokens[4][4][128];  // of a group's 16 tokens and a row; only where its warp has such an x
+  int warp[4][WARPS];          // the last chunk in which a warp has
+  int chunk[4];                // in which any has
+};
+constexpr int OFF_BAR = OFF_ODD + sizeof(Odd);
 constexpr int TC_SMEM = OFF_BAR + 256 + 1024 /* alignment */;
 
 // tensor memory columns
@@ -246,10 +252,11 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
     mbar_init(smem_u32(&bar->s_full), 1);
     mbar_init(smem_u32(&bar->y_full), 1);
     mbar_init(smem_u32(&bar->drain), 1);
-    for (int i = 0; i < STAGES; ++i) *reinterpret_cast<int*>(smem + OFF_D + i * D_BYTES + OFF_MARK) = -1;
     bar->stop = 0;
     fence_barrier_init();
   }
+  Odd* marks = reinterpret_cast<Odd*>(smem + OFF_ODD);
+  if (tid < 4 * (WARPS + 1)) (&marks->warp[0][0])[tid] = -1;
   // P's entries after their token stay zero
   for (int i = tid; i < 4 * BLK / 16; i += NT) reinterpret_cast<uint4*>(smem + OFF_P)[i] = make_uint4(0, 0, 0, 0);
   if (warp == WARPS) tmem_alloc_warp(smem_u32(&bar->tmem), 512);
@@ -279,10 +286,6 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
     const int q4 = lane & 3, p0 = (w4 & 1) * 32;      // the warp's first column of its head's x
     const int tg = 16 * grp4;                         // the group's first token of a chunk
     const int n0 = 32 * grp4;                         // its first column of the state
-    // A stage's words are written with its Xw and read with its y.  Three places: a group may write chunk i + 1's while another is
-    // still at y of chunk i - 1 (it needs S of chunk i, which needs nothing of that y), but not chunk i + 2's.
-    auto odd_tokens = [&](uint32_t stage, int group) { return reinterpret_cast<uint32_t*>(smem + stage + OFF_ODD) + group * 128 + row; };
-    auto odd_chunk = [&](uint32_t stage) { return reinterpret_cast<volatile int*>(smem + stage + OFF_MARK); };
     auto x_at = [&](unsigned char* stage, int t) {    // x of token t in column p: chunk (p >> 3) ^ (t & 7) of the tile's row
       return reinterpret_cast<uint16_t*>(stage + OFF_TX + hd * BLK + t * 128 + (((p >> 3) ^ (t & 7)) << 4) + (p & 7) * 2);
     };
@@ -379,19 +382,20 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
         }
         const float* w = reinterpret_cast<const Decays*>(smem + nd)[hd].w + tg;
         const uint32_t xw = tmem + T_XW + lanes + (tg >> 1);
-        uint32_t odd = 0;
         if (!write_xw<false>(sb + nxt + OFF_TX, f_off, w, q4, xw)) {  // seldom
           write_xw<true>(sb + nxt + OFF_TX, f_off, w, q4, xw);
           // such values leave the tile (each thread its row's): the product with a zero of P would spread them
+          uint32_t odd = 0;
 #pragma unroll 1
           for (int u = 0; u < 16; ++u) {
             uint16_t* v = x_at(smem + nxt, tg + u);
             if ((*v & 0x7f80u) == 0x7f80u) odd |= 1u << u, *v = 0;
           }
           fence_async_smem();
-          *odd_chunk(nd) = i + 1;
+          marks->tokens[(i + 1) & 3][grp4][row] = odd;
+          marks->warp[(i + 1) & 3][warp] = i + 1;
+          marks->chunk[(i + 1) & 3] = i + 1;
         }
-        *odd_tokens(nd, grp4) = odd;  // by every warp: all of them are read where one has marked the chunk
         // the store of the chunk before this one's y has read its buffer
         if (w4 == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
         tmem_wait_st();
@@ -431,12 +435,13 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
           }
           stsm4_t(sb + yb + f_off[rh], o);
         }
-        if (*odd_chunk(cd) == i) {  // what those values add is not finite, so it can be added to the rounded y
+        if (marks->chunk[i & 3] == i) {  // what those values add is not finite, so it can be added to the rounded y
           __syncwarp();
           const int c = c0 + i;
           unsigned long long odd = 0;
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) odd |= (unsigned long long)*odd_tokens(cd, k) << (16 * k);
+          for (int k = 0; k < 4; ++k)
+            if (marks->warp[i & 3][4 * k + w4] == i) odd |= (unsigned long long)marks->tokens[i & 3][k][row] << (16 * k);
           const unsigned char* pt = smem + OFF_P + ((i & 1) * 2 + hd) * BLK;
 #pragma unroll 1
           for (int u = 0; u < tg + 16; ++u) {
@@ -510,7 +515,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
       fence_async_smem();
       hand_over(B_P);
       cur = nxt, cd = nd, left -= Q;
-      nxt += ST_BYTES, nd += D_BYTES, ++full;
+      nxt += ST_BYTES, nd += 2 * REC, ++full;
       if (nxt == STAGES * ST_BYTES) nxt = 0, nd = OFF_D, full = bar->full, full_par ^= 1;
     }
     if (w4 == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
@@ -538,7 +543,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
         mbar_arrive_expect_tx(f, ST_BYTES + 2 * REC);
         tma_load_2d(d + OFF_TX, &tx, 2 * pair * kP, t, f);
         tma_load_2d(d + OFF_TX + BLK, &tx, 2 * pair * kP + 64, t, f);
-        bulk_load(sb + OFF_D + st * D_BYTES, decays + chunk_record(first, s, c0 + i) * a.H + 2 * pair, 2 * REC, f);
+        bulk_load(sb + OFF_D + st * 2 * REC, decays + chunk_record(first, s, c0 + i) * a.H + 2 * pair, 2 * REC, f);
         tma_load_2d(d + OFF_TB, &tb, bn, t, f);
         tma_load_2d(d + OFF_TB + BLK, &tb, bn + 64, t, f);
         tma_load_2d(d, &tcm, bn, t, f);
