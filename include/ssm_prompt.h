@@ -61,6 +61,7 @@ int ssm_prompt_conv(const ssm_dims *dims, const ssm_params *prm, int32_t layer, 
  *   h_out      device fp32, same shape, written for this layer and these sequences' slots (a sequence
  *              without tokens: its h_in); it may be h_in
  *   y          device bf16 [n_tok][ldy]: H*P columns, 16-byte aligned, ldy a multiple of 8
+ *              (it may be x, with ldy = ldx; otherwise it must not overlap an input)
  *   workspace  device, 256-byte aligned, >= ssm_prompt_scan_workspace_size() bytes, as
  *              ssm_tree_verify's
  * State and sums are fp32; the products of the state update keep x D w to 24 bits; what y reads

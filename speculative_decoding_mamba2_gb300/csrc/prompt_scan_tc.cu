@@ -41,7 +41,9 @@ constexpr int OFF_ODD = OFF_D + STAGES * 2 * REC;
 // Which x are not finite, of chunk i at [i & 3]: written with Xw, read with y.  Two places would not do: a group may write chunk
 // i + 1's while another is still at y of chunk i - 1 (it needs S of chunk i, which needs nothing of that y), but not i + 2's.
 struct Odd {
-  uint32_t tokens[4][4][128];  // of a group's 16 tokens and a row; only where its warp has such an x
+  // of a group's 16 tokens and a row, only where its warp has such an x: 2 bits a token, finite, +infinity, -infinity, NaN (y may
+  // stand in the place of x when it is needed)
+  uint32_t tokens[4][4][128];
   int warp[4][WARPS];          // the last chunk in which a warp has
   int chunk[4];                // in which any has
 };
@@ -389,7 +391,8 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
 #pragma unroll 1
           for (int u = 0; u < 16; ++u) {
             uint16_t* v = x_at(smem + nxt, tg + u);
-            if ((*v & 0x7f80u) == 0x7f80u) odd |= 1u << u, *v = 0;
+            const uint32_t b = *v;
+            if ((b & 0x7f80u) == 0x7f80u) odd |= (b & 0x7fu ? 3u : b & 0x8000u ? 2u : 1u) << (2 * u), *v = 0;
           }
           fence_async_smem();
           marks->tokens[(i + 1) & 3][grp4][row] = odd;
@@ -437,16 +440,14 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
         }
         if (marks->chunk[i & 3] == i) {  // what those values add is not finite, so it can be added to the rounded y
           __syncwarp();
-          const int c = c0 + i;
-          unsigned long long odd = 0;
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k)
-            if (marks->warp[i & 3][4 * k + w4] == i) odd |= (unsigned long long)marks->tokens[i & 3][k][row] << (16 * k);
           const unsigned char* pt = smem + OFF_P + ((i & 1) * 2 + hd) * BLK;
 #pragma unroll 1
           for (int u = 0; u < tg + 16; ++u) {
-            if (!(odd >> u & 1)) continue;
-            const float xv = bf16f(a.x[(long long)(first + c * Q + u) * a.ldx + head * kP + p]);
+            if (marks->warp[i & 3][(u >> 4) * 4 + w4] != i) continue;
+            const uint32_t what = marks->tokens[i & 3][u >> 4][row] >> (2 * (u & 15)) & 3u;
+            if (what == 0) continue;
+            // (the bits of what: with an infinity's exponent there, its upper one is the sign)
+            const float xv = __uint_as_float(0x7f800000u | what << 30 | (what == 3 ? 1u << 22 : 0u));
 #pragma unroll 1
             for (int r = max(u, tg); r < tg + 16; ++r) {
               uint16_t* y = reinterpret_cast<uint16_t*>(smem + yb + hd * BLK + tile_off(r, p >> 3, 128) + (p & 7) * 2);

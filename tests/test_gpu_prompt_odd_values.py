@@ -82,3 +82,21 @@ def test_values_in_many_chunks(H, G, lens):
         assert status == 0
         check_reach(c, reach, y0, h0, y, h)
         c["x"].copy_(was)
+
+
+@pytest.mark.parametrize("H,G,lens", [(24, 1, [2000, 130, 700]), (3, 3, [330, 65]), (3, 3, [2000])], ids=str)
+@pytest.mark.parametrize("odd", [False, True])
+def test_y_in_the_place_of_x(H, G, lens, odd):
+    """y written over x: as into a tensor of its own, also where x has values that are not finite."""
+    from speculative_decoding_mamba2_gb300 import Dims, ssm_prompt_scan, ssm_prompt_scan_workspace_size
+    c = scan_case(46, H, G, lens)
+    rng = np.random.default_rng(47)
+    if odd:
+        put(c, [(int(rng.integers(c["T"])), int(rng.integers(H)), int(rng.integers(P))) for _ in range(200)], rng)
+    y0, h0, _ = run_scan(c)
+    d, h = Dims(n_heads=H), torch.from_numpy(c["h0"]).cuda()
+    ws = torch.empty(ssm_prompt_scan_workspace_size(d, c["S"], c["T"], max(lens), G), dtype=torch.uint8, device="cuda")
+    ssm_prompt_scan(d, c["prm"], 0, torch.from_numpy(c["cu"]).cuda(), max(lens), c["x"], c["B"], c["C"], c["dt"], h, h, c["x"], ws,
+                    slots=torch.from_numpy(c["slots"]).cuda())
+    np.testing.assert_array_equal(c["x"].double().cpu().numpy().reshape(c["T"], H, P), y0)
+    np.testing.assert_array_equal(h.double().cpu().numpy()[c["slots"]], h0[c["slots"]])
