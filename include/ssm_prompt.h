@@ -17,7 +17,8 @@
  * (h [n_slots][L][H][P][N], ring [n_slots][L][R][conv_dim], ring_head [n_slots][L]:
  * the order of ssm_tree.h's instances).  Sequences are ragged: sequence s has the
  * token rows cu_seqlens[s] .. cu_seqlens[s+1]-1 (it may have none) and the cache
- * slot slots[s] (slots = NULL: s).  Two sequences of a call must not share a slot.
+ * slot slots[s] (slots = NULL: s).  Two sequences of a call must not share a slot
+ * or a row.
  * A sequence whose rows, slot or length are out of range is skipped (its rows and
  * its slot stay as they were) and sets SSM_STATUS_SEQ_RANGE.
  */

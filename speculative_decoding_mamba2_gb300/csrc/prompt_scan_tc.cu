@@ -117,7 +117,11 @@ __device__ __forceinline__ bool write_xw(uint32_t x, const uint32_t (&f_off)[2],
 
 // Once for all walks: grid z < G: scores C_t . B_s of a chunk and group, [record][s / 4][t][s % 4] fp32; then the decays
 // of a chunk, HEADS heads to a warp.
-__device__ __forceinline__ long long chunk_record(int first, int s, int chunk) { return (long long)(first / Q) + s + chunk; }
+// A record for each chunk of sequences that share no row, in whatever order they stand: whole chunks by the one row before a
+// multiple of Q in them, a sequence's shorter last one by the sequence.
+__device__ __forceinline__ long long chunk_record(const SeqArgs& q, int s, int first, int len, int chunk) {
+  return (chunk + 1) * Q <= len ? first / Q + chunk : (long long)(q.n_tok / Q) + s;
+}
 // of a warp: their chains of shuffles and exponentials fill each other's gaps (1: 239, 2: 236, 4: 235.6 us of a scan)
 constexpr int HEADS = 4;
 __global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, Decays* decays, int* order) {
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, De
       dt0[j] = h0 + j < a.H && t < len ? bf16f(q[j]) : 0.f;
       dt1[j] = h0 + j < a.H && t + 1 < len ? bf16f(q[a.lddt + j]) : 0.f;
     }
-    Decays* rec = decays + chunk_record(first, s, c) * a.H + h0;
+    Decays* rec = decays + chunk_record(a.q, s, first, len, c) * a.H + h0;
 #pragma unroll
     for (int j = 0; j < HEADS; ++j) {
       if (h0 + j >= a.H) return;
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(128) prep_kernel(ScanArgs a, float* scores, De
         mma16816(acc[2 * np + 1], cf, b[2], b[3]);
       }
   }
-  float* out = scores + (chunk_record(first, s, c) * a.G + grp) * (Q * Q);
+  float* out = scores + (chunk_record(a.q, s, first, len, c) * a.G + grp) * (Q * Q);
   const int t = 16 * warp + (lane >> 2);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -336,8 +340,9 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
     const int oh = warp / 6, oj = warp % 6, tb = oj < 3 ? oj + 1 : oj == 3 ? 2 : 3, ub = oj < 3 ? 0 : oj < 5 ? 1 : 2;
     const int ot = 16 * tb + lr, ou = 16 * ub + 8 * lh;
     float4 gd, go[2];
-    const float4* gp = reinterpret_cast<const float4*>(scores + (chunk_record(first, s, c0) * a.G + 2 * pair / (a.H / a.G)) * (Q * Q));
-    auto fetch = [&]() {
+    const float4* gp = reinterpret_cast<const float4*>(scores) + ((first / Q + c0) * (long long)a.G + 2 * pair / (a.H / a.G)) * (Q * Q / 4);
+    auto fetch = [&](bool whole) {
+      if (!whole) gp += (a.q.n_tok / Q + s - first / Q - nch + 1) * (long long)a.G * (Q * Q / 4);  // the sequence's last chunk
       gd = gp[(du >> 2) * Q + dt];
       if (below) go[0] = gp[(ou >> 2) * Q + ot], go[1] = gp[((ou >> 2) + 1) * Q + ot];
       gp += (long long)a.G * (Q * Q / 4);
@@ -404,7 +409,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
         tmem_wait_st();
         tc_fence_before();
         hand_over(B_XW);
-        fetch();  // for P below: the loads' time passes during y
+        fetch(left >= Q);  // for P below: the loads' time passes during y
       }
       // ---- y of chunk i ----
       if (i >= 0) {
@@ -544,7 +549,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
         mbar_arrive_expect_tx(f, ST_BYTES + 2 * REC);
         tma_load_2d(d + OFF_TX, &tx, 2 * pair * kP, t, f);
         tma_load_2d(d + OFF_TX + BLK, &tx, 2 * pair * kP + 64, t, f);
-        bulk_load(sb + OFF_D + st * 2 * REC, decays + chunk_record(first, s, c0 + i) * a.H + 2 * pair, 2 * REC, f);
+        bulk_load(sb + OFF_D + st * 2 * REC, decays + chunk_record(a.q, s, first, len, c0 + i) * a.H + 2 * pair, 2 * REC, f);
         tma_load_2d(d + OFF_TB, &tb, bn, t, f);
         tma_load_2d(d + OFF_TB + BLK, &tb, bn + 64, t, f);
         tma_load_2d(d, &tcm, bn, t, f);
@@ -749,7 +754,7 @@ __device__ __forceinline__ void state_walk(const CUtensorMap& tx, const CUtensor
         mbar_arrive_expect_tx(f, S_BYTES + 2 * REC);
         tma_load_2d(d + 2 * BLK, &tx, 2 * pair * kP, t, f);
         tma_load_2d(d + 3 * BLK, &tx, 2 * pair * kP + 64, t, f);
-        bulk_load(sb + S_OFF_D + st * 2 * REC, decays + chunk_record(first, s, c0 + i) * a.H + 2 * pair, 2 * REC, f);
+        bulk_load(sb + S_OFF_D + st * 2 * REC, decays + chunk_record(a.q, s, first, len, c0 + i) * a.H + 2 * pair, 2 * REC, f);
         tma_load_2d(d, &tb, bn, t, f);
         tma_load_2d(d + BLK, &tb, bn + 64, t, f);
       }
@@ -834,7 +839,7 @@ int plan_segments_tc(int H, int n_seq, int max_len) {
   return nseg < 2 ? 1 : nseg + 1;
 }
 
-// workspace: scores, decays, then what segments add to the state; chunks of all sequences at most n_tok / Q + n_seq
+// workspace: scores, decays, then what segments add to the state; records (chunk_record) up to n_tok / Q + n_seq
 size_t chunk_count(int n_seq, int n_tok) { return (size_t)(n_tok / Q) + n_seq + 1; }
 size_t score_bytes(int n_seq, int n_tok, int G) { return chunk_count(n_seq, n_tok) * G * Q * Q * sizeof(float); }
 size_t decay_bytes(int n_seq, int n_tok, int H) { return chunk_count(n_seq, n_tok) * H * REC; }
