@@ -201,14 +201,15 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
 }  // namespace
 
 cudaError_t launch_prompt_conv(const ConvArgs& a, cudaStream_t s) {
-  if (a.q.n_seq == 0 || a.q.n_tok == 0 || a.q.max_len == 0) return cudaSuccess;
+  if (a.q.n_seq == 0) return cudaSuccess;
   // the channels over blocks of equal size, whole warps; a cluster has 8 of them at most
   const int need = (a.conv_dim + CB - 1) / CB, blocks = min(8, need);
   static bool done[64];
   cudaError_t e = allow_smem(prompt_conv_kernel, CONV_SMEM, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((min(a.q.max_len, a.q.n_tok) + TB - 1) / TB), (unsigned)a.q.n_seq, (unsigned)blocks);
+  const int tiles = max(1, (min(a.q.max_len, a.q.n_tok) + TB - 1) / TB);  // (the first one checks the sequence)
+  cfg.gridDim = dim3((unsigned)tiles, (unsigned)a.q.n_seq, (unsigned)blocks);
   cfg.blockDim = dim3((unsigned)(((a.conv_dim + need - 1) / need + 63) / 64 * 32));
   cfg.dynamicSmemBytes = (size_t)(TB + 3) * cfg.blockDim.x * 4;
   cfg.stream = s;

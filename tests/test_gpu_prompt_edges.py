@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_prompt import U, _lib, reference, run_scan, scan_case  # noqa: F401 (the fixture builds the library)
+from tests.test_gpu_prompt import N, P, U, _lib, bf, host, ints, params, reference, run_scan, scan_case  # noqa: F401 (the fixture builds the library)
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +27,20 @@ def test_prompt_scan_sequences_in_any_order(H, G, cu, bad):
         assert (np.abs(y[cu[s]:cu[s + 1]] - ry) <= U * np.abs(ry) + (U + 2.0 ** -12) * my + 1e-30).all(), s
         chunks = -(-(cu[s + 1] - cu[s]) // 64)
         assert (np.abs(h[c["slots"][s], 0] - rh) <= 4e-6 * (1 + chunks) * mh + 1e-30).all(), s
+
+
+@pytest.mark.parametrize("cu,slots,T,max_len,bad", [([0, 9, 9], [0, 1], 9, 0, True), ([0, 0, 0], [0, 5], 0, 7, True), ([0, 4, 4], [0, 1], 0, 7, True),
+                                                    ([0, 0, 0], [1, 0], 0, 0, False), ([3, 3, 3], [1, 0], 9, 0, False)], ids=str)
+def test_prompt_conv_checks_sequences_without_rows_to_write(cu, slots, T, max_len, bad):
+    """No rows, or a bound of 0: sequences that are out of range are still reported; nothing is written."""
+    from speculative_decoding_mamba2_gb300 import SSM_STATUS_SEQ_RANGE, Dims, ssm_prompt_conv
+    rng = np.random.default_rng(52)
+    cd = P + 2 * N
+    prm, _ = params(rng, 1, 1)
+    x, _ = bf(rng.standard_normal((T, cd)))
+    ring, ring64 = bf(rng.standard_normal((2, 4, cd)))
+    head, out = ints([3, 8]), torch.full((T, cd), 9.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ssm_prompt_conv(Dims(n_heads=1, ring_cap=4), prm, 0, ints(cu), max_len, x, ring, head, out, slots=ints(slots), status=status)
+    assert int(status) == (SSM_STATUS_SEQ_RANGE if bad else 0)
+    assert head.tolist() == [3, 8] and (host(ring) == ring64).all() and (host(out) == 9.0).all()
