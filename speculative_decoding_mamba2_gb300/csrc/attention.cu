@@ -160,11 +160,12 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   int s = run, sp = 0, tps = 1 << 30, splits = 1;
   bool any = true;
   if (a.max_runs > 0) {
-    int* tiles = reinterpret_cast<int*>(smem);  // space not in use yet
+    int* tiles = reinterpret_cast<int*>(smem);  // space not in use yet: with D = 64 a place of the ring
     int first;
     tps = choose_split(a, a.Hkv * rt, tiles, ms);
     any = find_run(a.S, tiles, tps, run, s, first, splits);
     sp = any ? run - first : 0;
+    fence_async_smem();  // (before the barrier behind which the copies may write there)
     if (any && sp == 0 && kvh == 0 && r0 == 0 && tid == 0) a.runs[s] = make_int2(first, splits);
   }
   tc_fence_before();
