@@ -155,8 +155,9 @@ __global__ void __launch_bounds__(ATHREADS, 2)
     ms->odd[0] = ms->odd[1] = 0;
     fence_barrier_init();
   }
-  if (warp == 5) tmem_alloc_warp(smem_u32(&ms->tmem), A_COLS);
   grid_dependency_wait();  // what the stream's kernels before this one write
+  // (not before that: a kernel that lets this one's blocks in before it has its own tensor memory would wait for them for ever)
+  if (warp == 5) tmem_alloc_warp(smem_u32(&ms->tmem), A_COLS);
   int s = run, sp = 0, tps = 1 << 30, splits = 1;
   bool any = true;
   if (a.max_runs > 0) {
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  launch_dependents();  // (not before the tensor memory is there: the next grid's blocks take some too, and wait for this one)
+  launch_dependents();  // (not before the tensor memory is there: the next grid's blocks may take some before they wait for this one)
   const uint32_t tmem = __shfl_sync(0xffffffffu, ms->tmem, 0);
   if (!any) {
     if (warp == 5) tmem_free_warp(tmem, A_COLS);
