@@ -273,11 +273,12 @@ __global__ void __launch_bounds__(ATHREADS, 2)
           }
         }
         const int use = 2 * i + 1;
+        // (a warp that gives up here still meets the others below: they may be through this wait, and through the next tile's
+        // before the products that they then wait for fail to come)
         ok = wait_bar(&ms->full[use % UNITS], (use / UNITS) & 1, stop);
-        if (!ok) break;
         unsigned char* vt = smem + Sh::OFF_KV + use % UNITS * Sh::TILE;
 #pragma unroll 1
-        for (int k = tid; k < KT * D / 8; k += 128) {
+        for (int k = ok ? tid : KT * D / 8; k < KT * D / 8; k += 128) {
           const int vr = k / (D / 8), c = k % (D / 8);
           uint4* v = reinterpret_cast<uint4*>(vt + (c >> 3) * BLK + tile_off(vr, c & 7, 128));
           if (!(rowsv >> vr & 1)) {
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
         }
         fence_async_smem();
         named_sync(1, 128);  // (and: the ancestor words are there)
+        if (!ok) break;
         if (tree) rowsv &= ms->anc[node];
 #pragma unroll
         for (int j = 0; j < KT; ++j)
