@@ -427,12 +427,10 @@ __global__ void __launch_bounds__(ATHREADS, 2)
         }
         issued = use + 1;
       }
-      if (!ok) {  // copies in flight land before the shared memory is given up
-        for (int k = max(0, issued - UNITS); k < issued && lane == 0; ++k)
-          mbar_poll_ns(smem_u32(&ms->full[k % UNITS]), (k / UNITS) & 1, kWaitLimitNs);
-        break;
-      }
+      if (!ok) break;
     }
+    // copies land before the shared memory is given up, whoever gives up, and when (else they have, by the time of the last tile)
+    for (int k = max(0, issued - UNITS); k < issued && lane == 0; ++k) mbar_wait(smem_u32(&ms->full[k % UNITS]), (k / UNITS) & 1);
   } else {
     // ---- MMAs: one warp those of S, the other P . V, each behind its own waits ----
     const bool leader = elect_one();

@@ -557,10 +557,8 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
       }
       issued = i + 1;
     }
-    if (lane == 0 && *stop) {  // copies in flight land before the shared memory is given up
-      for (int i = max(0, issued - STAGES); i < issued; ++i)
-        mbar_poll_ns(smem_u32(&bar->full[i % STAGES]), (i / STAGES) & 1, kWaitLimitNs);
-    }
+    // copies land before the shared memory is given up, whoever gives up, and when
+    for (int i = max(0, issued - STAGES); i < issued && lane == 0; ++i) mbar_wait(smem_u32(&bar->full[i % STAGES]), (i / STAGES) & 1);
   } else {
     // ---- MMAs ----
     constexpr uint32_t id_s = idesc_major(128, 128, false, true), id_y2 = idesc_major(128, 64, false, false),
@@ -760,10 +758,8 @@ __device__ __forceinline__ void state_walk(const CUtensorMap& tx, const CUtensor
       }
       issued = i + 1;
     }
-    if (lane == 0 && *stop) {  // copies in flight land before the shared memory is given up
-      for (int i = max(0, issued - S_STAGES); i < issued; ++i)
-        mbar_poll_ns(smem_u32(&bar->full[i % S_STAGES]), (i / S_STAGES) & 1, kWaitLimitNs);
-    }
+    // copies land before the shared memory is given up, whoever gives up, and when
+    for (int i = max(0, issued - S_STAGES); i < issued && lane == 0; ++i) mbar_wait(smem_u32(&bar->full[i % S_STAGES]), (i / S_STAGES) & 1);
   } else {
     // ---- MMAs ----
     constexpr uint32_t id_s = idesc_major(128, 128, false, true);
