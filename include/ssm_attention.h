@@ -64,7 +64,7 @@ size_t ssm_tree_attention_workspace_size(int32_t n_seq, int32_t n_nodes, int32_t
  * row path[s][i] of sequence s's tree becomes cache row cache_len[s] + i, i < path_len[s].
  *   path, path_len  device int32 [S][max_path], [S] (ssm_accept_path).  A path ends before its first entry
  *                   outside [0, n_nodes) (SSM_STATUS_PATH_RANGE) and before a row without a page
- *                   (SSM_STATUS_SEQ_RANGE)
+ *                   or past 2^31 - 2 (SSM_STATUS_SEQ_RANGE)
  *   k, v            device bf16 [n_layers][S*n][Hkv*D], dense
  *   k_pages, v_pages  device bf16 [n_layers][n_pages][Hkv][page_size][D], written
  *   len_out         device int32 [S]: cache_len + the rows committed; it may be cache_len

@@ -603,7 +603,7 @@ __global__ void __cluster_dims__(CCTAS, 1, 1) __launch_bounds__(CTHREADS) kv_com
     const int lane = threadIdx.x;
     int want = a.path_len[s], bits = 0;
     if (want < 0 || want > a.max_path) bits |= SSM_STATUS_PATH_RANGE, want = want < 0 ? 0 : a.max_path;
-    const long long room = ((long long)a.max_pages << a.page_shift) - len;
+    const long long room = min((long long)a.max_pages << a.page_shift, (long long)INT32_MAX) - len;  // (a length is an int32)
     if (len < 0 || room < 0) bits |= SSM_STATUS_SEQ_RANGE, want = 0;
     int n = want;
     for (int i0 = 0; i0 < want; i0 += 32) {
