@@ -520,7 +520,7 @@ _BF16 = torch.bfloat16
 
 
 def _tok_rows(t, name: str, cols: int | None = None):
-    """_rows of a bf16 tensor that may have no rows (whose strides then say nothing)."""
+    """_rows of a bf16 tensor that may have one row or none (whose row stride then says nothing)."""
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _BF16 and t.dim() == 2:
         rows, c = t.shape
         if cols is None or c == cols:
@@ -528,7 +528,7 @@ def _tok_rows(t, name: str, cols: int | None = None):
                 return None, 0, (c + 7) // 8 * 8
             ld, inner = t.stride()
             if inner == 1 or c <= 1:
-                return t.data_ptr(), rows, ld
+                return t.data_ptr(), rows, ld if rows > 1 else (c + 7) // 8 * 8
     return _rows(t, name, _BF16, cols)  # says what is wrong
 
 
@@ -538,8 +538,8 @@ def _opt_slots(slots, n_seq: int):
 
 def ssm_prompt_conv(dims: Dims, params: dict, layer: int, cu_seqlens, max_len: int, xBC, ring, ring_head, out,
                     slots=None, status=None, stream=None):
-    """Causal conv + SiLU of ragged prompts (xBC, out: bf16 [n_tok, conv_dim], any row stride); the ring's rows
-    before each prompt are read, its last three rows and the head written."""
+    """Causal conv + SiLU of ragged prompts (xBC, out: bf16 [n_tok, conv_dim], row strides that are multiples of 8); the
+    ring's rows before each prompt are read, its last three rows and the head written."""
     d = dims
     px, T, ldx = _tok_rows(xBC, "xBC", d.conv_dim)
     po, To, ldo = _tok_rows(out, "out", d.conv_dim)
@@ -593,7 +593,7 @@ def ssm_prompt_scan_workspace_size(dims: Dims, n_seq: int, n_tok: int, max_len: 
 def ssm_prompt_scan(dims: Dims, params: dict, layer: int, cu_seqlens, max_len: int, x, B, C, dt, h_in, h_out, y,
                     workspace, slots=None, status=None, stream=None):
     """Linear attention with a decay for each head over ragged prompts: y (bf16) and the state after each prompt.
-    x, B, C, dt: bf16 [n_tok, .], any row stride (n_groups = columns of B / d_state); h_in: fp32
+    x, B, C, dt: bf16 [n_tok, .], row strides that are multiples of 8 (dt: any; n_groups = columns of B / d_state); h_in: fp32
     [n_slots, L, H, P, N] or None (zero states); h_out may be h_in."""
     T, G, n_slots, t = _scan_tensors(dims, x, B, C, dt, h_in, h_out, y)
     n_seq = cu_seqlens.numel() - 1
@@ -644,7 +644,7 @@ def _table(t, name: str, n_seq: int):
 def ssm_tree_attention(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, layout, q, k, v, k_pages, v_pages, page_table,
                        cache_len, max_cache_len: int, scale: float, o, workspace, status=None, stream=None):
     """Attention of every node of the draft trees over its sequence's paged cache and its ancestors.  q, o: bf16
-    [S * n, Hq * D], k, v: bf16 [S * n, Hkv * D] (any row stride); k_pages, v_pages: bf16
+    [S * n, Hq * D], k, v: bf16 [S * n, Hkv * D] (row strides that are multiples of 8); k_pages, v_pages: bf16
     [n_pages, Hkv, page_size, D]; page_table: int32 [S, max_pages]."""
     S, n = n_seq, n_nodes
     pq, rq, ldq = _tok_rows(q, "q", Hq * D)

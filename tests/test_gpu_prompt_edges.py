@@ -44,3 +44,34 @@ def test_prompt_conv_checks_sequences_without_rows_to_write(cu, slots, T, max_le
     ssm_prompt_conv(Dims(n_heads=1, ring_cap=4), prm, 0, ints(cu), max_len, x, ring, head, out, slots=ints(slots), status=status)
     assert int(status) == (SSM_STATUS_SEQ_RANGE if bad else 0)
     assert head.tolist() == [3, 8] and (host(ring) == ring64).all() and (host(out) == 9.0).all()
+
+
+def test_one_token_of_a_buffer_of_any_width():
+    """The row stride of a single row says nothing: a token in a buffer whose rows are not multiples of 8 long, by every call."""
+    from speculative_decoding_mamba2_gb300 import (Dims, ssm_prompt_conv, ssm_prompt_scan, ssm_prompt_scan_workspace_size,
+                                                   ssm_scan_step)
+    c = scan_case(53, 2, 1, [1])
+    y0, h0, _ = run_scan(c)
+    d, prm = Dims(n_heads=2), c["prm"]
+    row = torch.full((1, c["x"].size(1) + 2 * N + 5), 9.0, dtype=torch.bfloat16, device="cuda")
+    x, B, C = row[:, :2 * P], row[:, 2 * P:2 * P + N], row[:, 2 * P + N:2 * P + 2 * N]
+    for to, k in ((x, "x"), (B, "B"), (C, "C")):
+        to.copy_(c[k])
+    ws = torch.empty(ssm_prompt_scan_workspace_size(d, 1, 1, 1), dtype=torch.uint8, device="cuda")
+    for call in ("scan", "step"):
+        h, y = torch.from_numpy(c["h0"]).cuda(), torch.zeros(1, 2 * P + 3, dtype=torch.bfloat16, device="cuda")
+        if call == "scan":
+            ssm_prompt_scan(d, prm, 0, ints([0, 1]), 1, x, B, C, c["dt"], h, h, y[:, :2 * P], ws, slots=ints(c["slots"]))
+            np.testing.assert_array_equal(host(y[:, :2 * P]).reshape(1, 2, P), y0)
+        else:
+            ssm_scan_step(d, prm, 0, x, B, C, c["dt"], h, h, y[:, :2 * P], slots=ints(c["slots"]))
+            assert (np.abs(host(y[:, :2 * P]).reshape(2, P) - y0[0]) <= 4 * U * reference(c, 0, magnitude=True)[0][0]).all()
+        assert (host(y[:, 2 * P:]) == 0).all()
+    outs = []
+    for wide in (row[:, :d.conv_dim], row[:, :d.conv_dim].contiguous()):
+        ring, head = torch.zeros(1, 20, d.conv_dim, dtype=torch.bfloat16, device="cuda"), ints([3])
+        out = torch.zeros_like(wide)
+        ssm_prompt_conv(d, prm, 0, ints([0, 1]), 1, wide, ring, head, out)
+        outs.append((host(out), host(ring)))
+    for a, b in zip(*outs):
+        np.testing.assert_array_equal(a, b)
