@@ -45,7 +45,8 @@ extern "C" {
  *   o           device bf16 [S*n][ldo]: Hq*D columns
  *   workspace   device, 256-byte aligned, >= ssm_tree_attention_workspace_size() bytes
  * Pointers 16-byte aligned, row strides multiples of 8.  Scores, maxima, sums and o are accumulated in fp32;
- * the weights exp(score - maximum) are rounded to bf16 for their product with v.
+ * the weights exp(score - maximum) are rounded to bf16 for their product with v (relative error of o 0.0017 to
+ * 0.0023, of which its own rounding 0.0017).
  */
 int ssm_tree_attention(int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D, const ssm_node *layout,
                        const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,

@@ -10,7 +10,8 @@
  * D_t = softplus(dt_t + dt_bias) and a_t = exp(-D_t exp(A_log)),
  *     h_t = a_t h_{t-1} + D_t x_t (x) B_t,     y_t = C_t h_t + D x_t.
  * H heads of head_dim P; B and C are shared by H / n_groups consecutive heads
- * (n_groups = 1: by all, as in ssm_tree.h).
+ * (n_groups = 1: by all).  Groups are the scan's and the step's only: rows of
+ * ssm_prompt_conv, like those of ssm_tree.h, have one group, conv_dim = H*P + 2*N.
  *
  * Same conventions as ssm_tree.h.  The calls work on ONE layer: `layer` picks its
  * parameters, and its part of a cache that holds all L layers of n_slots sequences
@@ -42,7 +43,8 @@ extern "C" {
  * sequence: those rows zero).  Afterwards the last min(len, 3) rows stand at ring
  * positions head+len-3 .. head+len-1 (mod R) and ring_head has advanced by len.
  *   n_seq, n_slots, n_tok   sequences, slots of the cache, rows of xBC and out
- *   max_len     bound on a sequence's length (longer ones are skipped)
+ *   max_len     bound on a sequence's length (longer ones are skipped); blocks are launched for
+ *               max_len tokens of every sequence, so a bound far above the lengths costs time
  *   cu_seqlens  device int32 [n_seq + 1]       slots  device int32 [n_seq] or NULL
  *   xBC         device bf16 [n_tok][ldx], conv_dim columns, ldx a multiple of 8, 16-byte aligned
  *   out         device bf16 [n_tok][ldo], same rules; must not overlap xBC
@@ -65,8 +67,9 @@ int ssm_prompt_conv(const ssm_dims *dims, const ssm_params *prm, int32_t layer, 
  *              (it may be x, with ldy = ldx; otherwise it must not overlap an input)
  *   workspace  device, 256-byte aligned, >= ssm_prompt_scan_workspace_size() bytes, as
  *              ssm_tree_verify's
- * State and sums are fp32; the products of the state update keep x D w to 24 bits; what y reads
- * (the chunk's scores and the state) is rounded to bf16, as y itself is.
+ * max_len as above.  State and sums are fp32; the products of the state update keep x D w to 24 bits;
+ * what y reads (the chunk's scores and the state) is rounded to bf16, as y itself is (relative error of
+ * y 0.0018, of which its own rounding 0.0017).  ssm_scan_step keeps 32 bits throughout.
  * Only conv-free members of dims and prm are used (n_heads, head_dim, d_state, n_layers; dt_bias, A_log, D).
  */
 int ssm_prompt_scan(const ssm_dims *dims, const ssm_params *prm, int32_t layer, int32_t n_groups, int32_t n_seq,

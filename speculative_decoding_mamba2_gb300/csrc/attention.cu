@@ -18,9 +18,9 @@
 // Rows of V that no key of the tile owns, and values of V in tree rows that are not finite, are zeroed in shared memory
 // (a weight of 0 would spread them); the latter are added to the rows that see them at the end.
 // Measured, both kernels, back to back in a graph (32 query heads, D = 128): one token of one sequence over 16411 rows, 8 heads
-// of K and V, 18 us (67 MB: 3.7 TB/s; latency: seven tiles to a CTA); 8 trees of 16 nodes over up to 8117 rows 40 us (163 MB:
-// 4.1 TB/s of HBM); 4 trees of 40 nodes over up to 40009 rows, 4 heads, 87 us (85 GFLOP: 0.98 PFLOP/s, 1.17 with the rows
-// that fill up the third row tile; tensor pipe 52 % of the time, shared memory the rest).
+// of K and V, 18 us (67 MB: 3.7 TB/s; latency: seven tiles to a CTA); 8 trees of 16 nodes over up to 8117 rows 41 us (163 MB:
+// 4.0 TB/s of HBM); 4 trees of 40 nodes over up to 40009 rows, 4 heads, 86 us (85 GFLOP: 0.99 PFLOP/s, 1.19 with the rows
+// that fill up the third row tile; tensor pipe 52 % of the time, shared memory the rest).  D = 64, the same rows: 16, 27 and 73 us.
 #include "prompt.cuh"
 #include "umma.cuh"
 
@@ -547,7 +547,9 @@ __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a) {
 }
 
 // Row tiles, and the most runs that the sequences are cut into (0: they are not cut, where the CTAs
-// fill the SMs twice over or the longest sequence is too short for what joining costs).
+// fill the SMs twice over or the longest sequence is too short for what joining costs).  Uncut, one long cache among many
+// short ones is walked by a CTA for each of its heads: 128 single tokens of 8 heads over 1000 rows each take 98 us, with
+// 64000 rows for one of them 698; 72 of them, which are cut, 112.
 struct AttendPlan {
   int row_tiles, max_runs;
 };

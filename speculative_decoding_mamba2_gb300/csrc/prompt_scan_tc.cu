@@ -16,8 +16,8 @@
 // MMAs in flight are waited for (bounded again) and the tensor memory is freed.
 // Rounding: h, P and y to bf16 once each (h and P as operands, relative to themselves); the state's own chain -- decays, Xw, S,
 // h -- keeps 24 bits.
-// Measured: 24571 tokens of 16 prompts, 80 heads, 232 us back to back (604 MB: 2.6 TB/s; 19 us of it prep_kernel); one prompt of
-// 8191 tokens 109 us.  The walk is bound by its 16 warps' instructions: issue slots 64 % taken, the tensor pipe busy 38 % of
+// Measured: 24571 tokens of 16 prompts, 80 heads, 237 us back to back (604 MB: 2.5 TB/s; 19 us of it prep_kernel); one prompt of
+// 8191 tokens 111 us.  The walk is bound by its 16 warps' instructions: issue slots 64 % taken, the tensor pipe busy 38 % of
 // the time (46 % with the walks over states).  A warp for each kind of MMA, scalar instead of paired fp32 and two waits in one
 // changed nothing.
 #include "prompt.cuh"
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(NT, 1)
 // Segments of a sequence's chunks, for one CTA of a head pair to an SM: where sequences and pairs leave SMs idle, the pass over
 // the segments' states pays for itself.  (us back to back, in one segment | in several: 10 chunks of 16 pairs 28 | 33 in two;
 // 16 chunks of 40 pairs 37 | 39 in four; up to 20 chunks of 24 pairs 43 | 38 in five, 37 in four; up to 81 chunks of 48 pairs
-// 137 | 86 in four; 128 chunks of 40 pairs 190 | 109 in four.)
+// 137 | 86 in four; 128 chunks of 40 pairs 190 | 111 in four.)
 int plan_segments_tc(int H, int n_seq, int max_len) {
   const long long items = (long long)(H / 2) * n_seq;
   const int nch = (max_len + Q - 1) / Q;
