@@ -75,3 +75,17 @@ def test_one_token_of_a_buffer_of_any_width():
         outs.append((host(out), host(ring)))
     for a, b in zip(*outs):
         np.testing.assert_array_equal(a, b)
+
+
+@pytest.mark.parametrize("H,G,S", [(24, 1, 5), (6, 3, 130)])
+def test_scan_step_y_in_the_place_of_x(H, G, S):
+    """The single token's y written over x: as into a tensor of its own."""
+    from speculative_decoding_mamba2_gb300 import Dims, ssm_scan_step
+    c = scan_case(54, H, G, [1] * S)
+    outs = []
+    for y in (torch.empty(S, H * P, dtype=torch.bfloat16, device="cuda"), c["x"]):
+        h = torch.from_numpy(c["h0"]).cuda()
+        ssm_scan_step(Dims(n_heads=H), c["prm"], 0, c["x"], c["B"], c["C"], c["dt"], h, h, y, slots=ints(c["slots"]))
+        outs.append((host(y), host(h)))
+    for a, b in zip(*outs):
+        np.testing.assert_array_equal(a, b)
