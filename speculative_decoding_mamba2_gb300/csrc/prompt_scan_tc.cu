@@ -265,6 +265,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& tx, const CUtensorMap& t
   if (tid < 4 * (WARPS + 1)) (&marks->warp[0][0])[tid] = -1;
   // P's entries after their token stay zero
   for (int i = tid; i < 4 * BLK / 16; i += NT) reinterpret_cast<uint4*>(smem + OFF_P)[i] = make_uint4(0, 0, 0, 0);
+  fence_async_smem();  // (each thread its own: the tensor cores read them)
   if (warp == WARPS) tmem_alloc_warp(smem_u32(&bar->tmem), 512);
   tc_fence_before();
   __syncthreads();
