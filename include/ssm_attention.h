@@ -12,6 +12,10 @@
  * max_cache_len or beyond its page table, or one of whose pages is out of range, sets
  * SSM_STATUS_SEQ_RANGE: the rows that cannot be read count as absent (ssm_tree_attention)
  * or are not written (ssm_kv_commit).
+ *
+ * The cache may be held in 8 bits (the calls that end in _fp8): e4m3 values, and for each block
+ * of `block` tokens of a page and head a scale; a row stands for scale * value.  Rotary
+ * positions are given to q and k before any of these calls (ssm_rope, ssm_tree_rope).
  */
 #ifndef SSM_ATTENTION_H_
 #define SSM_ATTENTION_H_
@@ -21,6 +25,8 @@
 
 #include "ssm_prompt.h"
 #include "ssm_tree.h"
+
+#define SSM_STATUS_SCALE 128 /* a scale of an 8-bit cache outside 2^-100 .. 2^120 */
 
 #ifdef __cplusplus
 extern "C" {
@@ -74,6 +80,91 @@ int ssm_kv_commit(int32_t n_layers, int32_t n_seq, int32_t n_nodes, int32_t Hkv,
                   const int32_t *path, const int32_t *path_len, const uint16_t *k, const uint16_t *v,
                   uint16_t *k_pages, uint16_t *v_pages, int32_t n_pages, int32_t page_size, const int32_t *page_table,
                   int32_t max_pages, const int32_t *cache_len, int32_t *len_out, int32_t *dev_status, void *stream);
+
+/*
+ * ssm_tree_attention_fp8 -- ssm_tree_attention over an 8-bit cache; the nodes' own rows are bf16 as there.
+ *   k_pages, v_pages    device e4m3 [n_pages][Hkv][page_size][D]
+ *   k_scales, v_scales  device fp32 [n_pages][Hkv][page_size / block], from 2^-100 to 2^120 (those that ssm_kv_commit_fp8
+ *                       writes are powers of two).  The rows of a block with any other scale count as absent, where a
+ *                       sequence has such rows, and set SSM_STATUS_SCALE
+ *   block               a power of two, 8 .. page_size
+ * q that is not finite, and values of k that are not, make scores that are NaN.  The other arguments, workspace and rounding as
+ * for ssm_tree_attention.
+ */
+int ssm_tree_attention_fp8(int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D, const ssm_node *layout,
+                           const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                           const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scales, const float *v_scales,
+                           int32_t n_pages, int32_t page_size, int32_t block, const int32_t *page_table, int32_t max_pages,
+                           const int32_t *cache_len, int32_t max_cache_len, float scale, uint16_t *o, int64_t ldo,
+                           void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Host-only.  Bytes of device workspace ssm_tree_attention_fp8 needs (at least 256); 0 if the shape is rejected. */
+size_t ssm_tree_attention_fp8_workspace_size(int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D,
+                                             int32_t max_cache_len);
+
+/*
+ * ssm_kv_commit_fp8 -- ssm_kv_commit into an 8-bit cache.
+ *   k_pages, v_pages    device e4m3 [n_layers][n_pages][Hkv][page_size][D], written
+ *   k_scales, v_scales  device fp32 [n_layers][n_pages][Hkv][page_size / block], written
+ *   block               a power of two, 8 .. page_size
+ * A block's scale is the least power of two, from 2^-100 on, under which the largest finite value of its rows is at most 448 of
+ * it.  A block that starts with these rows takes its scale from them; one that holds rows of the sequence already keeps its
+ * own, or takes the larger one that the new rows need, and those older rows are then rounded again (a step down by a
+ * power of two: only values below 2^-6 of the scale lose anything).  Rows behind the committed ones keep their bits.
+ * A value that is not finite becomes NaN.  A scale outside 2^-100 .. 2^120 where such a block has rows sets
+ * SSM_STATUS_SCALE; it is replaced, and the older rows keep their bits.
+ */
+int ssm_kv_commit_fp8(int32_t n_layers, int32_t n_seq, int32_t n_nodes, int32_t Hkv, int32_t D, int32_t max_path,
+                      const int32_t *path, const int32_t *path_len, const uint16_t *k, const uint16_t *v,
+                      uint8_t *k_pages, uint8_t *v_pages, float *k_scales, float *v_scales, int32_t n_pages,
+                      int32_t page_size, int32_t block, const int32_t *page_table, int32_t max_pages,
+                      const int32_t *cache_len, int32_t *len_out, int32_t *dev_status, void *stream);
+
+/*
+ * Rotary positions.  Of each head the first `rot` columns are rot/2 pairs; pair i of a row at position p is turned by
+ * p * f_i and multiplied by `amplitude`:
+ *     a' = amplitude (a cos - b sin),   b' = amplitude (b cos + a sin).
+ * The pairs are columns (i, i + rot/2), or with `interleaved` (2i, 2i + 1).  The other columns are copied.
+ *
+ * ssm_rope_frequencies -- host-only.  f_i in radians a position, base^(-2i/rot), for a context that is to be `factor` times
+ * as long as the `original_len` positions of the training:
+ *   SSM_ROPE_PLAIN     as they are (factor is not read)
+ *   SSM_ROPE_LINEAR    all divided by factor
+ *   SSM_ROPE_BASE      the base multiplied by factor^(rot/(rot-2)): the slowest pair is divided by factor, the fastest kept
+ *   SSM_ROPE_BY_PARTS  pairs that make `low` turns or fewer over original_len divided by factor, those of `high` turns or more
+ *                      kept, those between divided in part (linearly in the turns); 0 <= low < high
+ *
+ * ssm_rope_turns -- host-only.  The kernels' table of any frequencies: f / (2 pi) in units of 2^-64 of a turn, modulo one.  A
+ * position times it, modulo 2^64, is the angle at any position up to 2^31 without a rounding that grows with it.
+ */
+#define SSM_ROPE_PLAIN 0
+#define SSM_ROPE_LINEAR 1
+#define SSM_ROPE_BASE 2
+#define SSM_ROPE_BY_PARTS 3
+int ssm_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original_len, double low,
+                         double high, double *freq);
+int ssm_rope_turns(int32_t n, const double *freq, uint64_t *turns);
+
+/*
+ * ssm_rope -- q and k rows at given positions.
+ *   Hq, Hkv      heads of q and of k (either may be 0: that tensor is then not read)
+ *   D            columns of a head, a multiple of 8, 8 .. 512;  rot even, 2 .. D
+ *   turns        device uint64 [rot / 2] (ssm_rope_turns);  amplitude finite
+ *   positions    device int32 [n_tok]; a negative one turns backwards
+ *   q, k         device bf16 [n_tok][ldq], [n_tok][ldk]: Hq*D and Hkv*D columns
+ *   q_out, k_out device bf16, strides ldqo, ldko; each may be its input (it may not overlap it in part)
+ * Pointers 16-byte aligned, row strides multiples of 8.  Angles to 2^-24 of a turn; products in fp32, rounded once.
+ *
+ * ssm_tree_rope -- the same for row s*n + v at position cache_len[s] + depth of node v.  A depth outside [0, n_nodes) counts as
+ * 0 and sets SSM_STATUS_BAD_LAYOUT, a negative length counts as 0 and sets SSM_STATUS_SEQ_RANGE.
+ */
+int ssm_rope(int32_t n_tok, int32_t Hq, int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, const uint64_t *turns,
+             float amplitude, const int32_t *positions, const uint16_t *q, int64_t ldq, uint16_t *q_out, int64_t ldqo,
+             const uint16_t *k, int64_t ldk, uint16_t *k_out, int64_t ldko, void *stream);
+int ssm_tree_rope(int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved,
+                  const uint64_t *turns, float amplitude, const ssm_node *layout, const int32_t *cache_len,
+                  const uint16_t *q, int64_t ldq, uint16_t *q_out, int64_t ldqo, const uint16_t *k, int64_t ldk,
+                  uint16_t *k_out, int64_t ldko, int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }

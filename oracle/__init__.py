@@ -30,3 +30,11 @@ from .prompt_oracle import (  # noqa: F401
     tree_attention,
     kv_commit,
 )
+from .decode_oracle import (  # noqa: F401
+    e4m3,
+    least_scale,
+    kv_commit_fp8,
+    rope,
+    rope_frequencies,
+    token_scores,
+)

@@ -30,10 +30,13 @@ SSM_STATUS_K_RANGE = 4
 SSM_STATUS_WALK_TRUNCATED = 8
 SSM_STATUS_TIMEOUT = 16
 SSM_STATUS_SEQ_RANGE = 32
+SSM_STATUS_TOKEN_RANGE = 64
+SSM_STATUS_SCALE = 128
 SSM_MAX_NODES = 64
 SSM_MAX_DEPTH = 15
 SSM_MAX_PATH = 256
 SSM_MAX_CHAIN_NODES = 4096
+SSM_MAX_TOP = 32
 SSM_NOALLOC_WORKSPACE_BYTES = 16 << 20
 NODE_WORDS = 8  # int32 words per ssm_node record
 
@@ -677,3 +680,207 @@ def ssm_kv_commit(n_seq: int, n_nodes: int, path, path_len, k, v, k_pages, v_pag
         _dev(k, "k", _BF16, L * S * n * Hkv * D), _dev(v, "v", _BF16, L * S * n * Hkv * D), kp, vp, n_pages, page, table,
         max_pages, _dev(cache_len, "cache_len", torch.int32, S), _dev(len_out, "len_out", torch.int32, S),
         _opt_status(status), _stream(stream, k_pages)))
+
+
+# ---------------------------------------------------------------------------
+# an 8-bit cache and rotary positions (include/ssm_attention.h)
+# ---------------------------------------------------------------------------
+_SIGS.update({
+    "ssm_tree_attention_fp8": (ctypes.c_int, [_I, _I, _I, _I, _I, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _I, _P, _I,
+                                              _P, _I, ctypes.c_float, _P, _L, _P, ctypes.c_size_t, _P, _P]),
+    "ssm_tree_attention_fp8_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
+    "ssm_kv_commit_fp8": (ctypes.c_int, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _I, _P, _P, _P,
+                                         _P]),
+    "ssm_rope_frequencies": (ctypes.c_int, [_I, ctypes.c_double, _I] + [ctypes.c_double] * 4 + [_P]),
+    "ssm_rope_turns": (ctypes.c_int, [_I, _P, _P]),
+    "ssm_rope": (ctypes.c_int, [_I, _I, _I, _I, _I, _I, _P, ctypes.c_float, _P, _P, _L, _P, _L, _P, _L, _P, _L, _P]),
+    "ssm_tree_rope": (ctypes.c_int, [_I, _I, _I, _I, _I, _I, _I, _P, ctypes.c_float, _P, _P, _P, _L, _P, _L, _P, _L, _P, _L, _P,
+                                     _P]),
+    "ssm_token_scores": (ctypes.c_int, [_I, _I, _P, _I, _L, ctypes.c_float, _I, _P, _P, _P, _I, _P, _P, _P, _P]),
+})
+_FP8 = torch.float8_e4m3fn
+
+
+def _call_on(device: int, fn, *args):
+    """The library's call with the tensors' device current (a launch goes to the current device)."""
+    if device == torch._C._cuda_getDevice():
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args))
+
+
+def _same_device(like, **tensors):
+    d = like.get_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"{name}: on another device than the others")
+    return d
+
+
+def _pages_fp8(k_pages, v_pages, k_scales, v_scales, lead: int, Hkv: int, D: int):
+    """(addresses of the pages and scales, n_pages, page_size, block): pages e4m3 [..lead.., n_pages, Hkv, page_size, D], scales
+    fp32 [..lead.., n_pages, Hkv, page_size / block]."""
+    shape = k_pages.shape if isinstance(k_pages, torch.Tensor) else ()
+    if len(shape) != lead + 4 or shape[-3] != Hkv or shape[-1] != D:
+        raise ValueError("k_pages: [" + "n_layers, " * lead + "n_pages, Hkv, page_size, D]")
+    sshape = k_scales.shape if isinstance(k_scales, torch.Tensor) else ()
+    page = shape[-2]
+    if len(sshape) != lead + 3 or sshape[:-1] != shape[:-2] or not 0 < sshape[-1] <= page or page % sshape[-1]:
+        raise ValueError("k_scales: [" + "n_layers, " * lead + "n_pages, Hkv, page_size / block]")
+    return (_dev(k_pages, "k_pages", _FP8), _dev(v_pages, "v_pages", _FP8, k_pages.numel()),
+            _dev(k_scales, "k_scales", torch.float32), _dev(v_scales, "v_scales", torch.float32, k_scales.numel()), shape[-4], page,
+            page // sshape[-1])
+
+
+def ssm_tree_attention_fp8_workspace_size(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, max_cache_len: int) -> int:
+    """Bytes of device workspace ssm_tree_attention_fp8 needs (host call)."""
+    b = lib().ssm_tree_attention_fp8_workspace_size(n_seq, n_nodes, Hq, Hkv, D, max_cache_len)
+    if b == 0:
+        raise SSMError(SSM_ERR_INVALID_ARG, ssm_last_error())
+    return int(b)
+
+
+def ssm_tree_attention_fp8(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, layout, q, k, v, k_pages, v_pages, k_scales,
+                           v_scales, page_table, cache_len, max_cache_len: int, scale: float, o, workspace, status=None,
+                           stream=None):
+    """ssm_tree_attention over an 8-bit cache: k_pages, v_pages float8_e4m3fn [n_pages, Hkv, page_size, D], k_scales, v_scales
+    fp32 [n_pages, Hkv, page_size / block].  The nodes' own k and v rows are bf16."""
+    S, n = n_seq, n_nodes
+    pq, rq, ldq = _tok_rows(q, "q", Hq * D)
+    pk, rk, ldk = _tok_rows(k, "k", Hkv * D)
+    pv, rv, ldv = _tok_rows(v, "v", Hkv * D)
+    po, ro, ldo = _tok_rows(o, "o", Hq * D)
+    if not rq == rk == rv == ro == S * n:
+        raise ValueError("q, k, v and o: n_seq * n_nodes rows each")
+    kp, vp, ks, vs, n_pages, page, block = _pages_fp8(k_pages, v_pages, k_scales, v_scales, 0, Hkv, D)
+    table, max_pages = _table(page_table, "page_table", S)
+    lay, lens = _dev(layout, "layout", torch.int32, S * n * NODE_WORDS), _dev(cache_len, "cache_len", torch.int32, S)
+    ws = _dev(workspace, "workspace", torch.uint8)
+    dev = _same_device(q, k=k, v=v, o=o, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, layout=layout,
+                       page_table=page_table, cache_len=cache_len, workspace=workspace, status=status)
+    _call_on(dev, lib().ssm_tree_attention_fp8, S, n, Hq, Hkv, D, lay, pq, ldq, pk, ldk, pv, ldv, kp, vp, ks, vs, n_pages, page,
+             block, table, max_pages, lens, int(max_cache_len), float(scale), po, ldo, ws, workspace.numel(), _opt_status(status),
+             _stream(stream, q))
+
+
+def ssm_kv_commit_fp8(n_seq: int, n_nodes: int, path, path_len, k, v, k_pages, v_pages, k_scales, v_scales, page_table,
+                      cache_len, len_out, status=None, stream=None):
+    """ssm_kv_commit into an 8-bit cache: pages float8_e4m3fn [L, n_pages, Hkv, page_size, D], scales fp32
+    [L, n_pages, Hkv, page_size / block], both written."""
+    S, n = n_seq, n_nodes
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 5:
+        raise ValueError("k_pages: [n_layers, n_pages, Hkv, page_size, D]")
+    L, Hkv, D = k_pages.size(0), k_pages.size(2), k_pages.size(4)
+    kp, vp, ks, vs, n_pages, page, block = _pages_fp8(k_pages, v_pages, k_scales, v_scales, 1, Hkv, D)
+    paths, max_path = _table(path, "path", S)
+    table, max_pages = _table(page_table, "page_table", S)
+    rows = L * S * n * Hkv * D
+    args = (_dev(path_len, "path_len", torch.int32, S), _dev(k, "k", _BF16, rows), _dev(v, "v", _BF16, rows), kp, vp, ks, vs,
+            n_pages, page, block, table, max_pages, _dev(cache_len, "cache_len", torch.int32, S),
+            _dev(len_out, "len_out", torch.int32, S), _opt_status(status), _stream(stream, k_pages))
+    dev = _same_device(k_pages, k=k, v=v, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, path=path, path_len=path_len,
+                       page_table=page_table, cache_len=cache_len, len_out=len_out, status=status)
+    _call_on(dev, lib().ssm_kv_commit_fp8, L, S, n, Hkv, D, max_path, paths, *args)
+
+
+SSM_ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
+
+
+def ssm_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                         original_len: float = 0.0, low: float = 1.0, high: float = 32.0) -> np.ndarray:
+    """Host call: radians a position of the rot / 2 pairs (float64), for a context scaled as `scaling` says ("plain", "linear",
+    "base" or "by_parts")."""
+    if scaling not in SSM_ROPE_SCALINGS:
+        raise ValueError(f"scaling: one of {', '.join(SSM_ROPE_SCALINGS)}")
+    out = np.zeros(max(int(rot) // 2, 1), np.float64)
+    _check(lib().ssm_rope_frequencies(int(rot), float(base), SSM_ROPE_SCALINGS[scaling], float(factor), float(original_len),
+                                      float(low), float(high), out.ctypes.data_as(_P)))
+    return out
+
+
+def ssm_rope_turns(freq) -> torch.Tensor:
+    """Host call: the rotary kernels' table of frequencies (radians a position), an int64 tensor on the CPU: 2^-64 parts of a turn."""
+    f = np.ascontiguousarray(np.asarray(freq, np.float64).reshape(-1))
+    out = np.zeros(f.shape, np.int64)
+    _check(lib().ssm_rope_turns(f.size, f.ctypes.data_as(_P), out.ctypes.data_as(_P)))
+    return torch.from_numpy(out)
+
+
+def _rope_tensor(x, out, name: str, D: int):
+    """(heads, rows, address and stride of x, of out) of an optional pair of tensors."""
+    if x is None and out is None:
+        return 0, None, (None, 0, None, 0)
+    if x is None or out is None:
+        raise ValueError(f"{name} and {name}_out: both or neither")
+    cols = x.size(1) if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
+    if D < 1 or cols % D:
+        raise ValueError(f"{name}: [rows, heads * D]")
+    p, rows, ld = _tok_rows(x, name, cols)
+    po, ro, ldo = _tok_rows(out, name + "_out", cols)
+    if ro != rows:
+        raise ValueError(f"{name}_out: as many rows as {name}")
+    return cols // D, rows, (p, ld, po, ldo)
+
+
+def _rope_args(D: int, turns, q, q_out, k, k_out):
+    Hq, rq, tq = _rope_tensor(q, q_out, "q", D)
+    Hkv, rk, tk = _rope_tensor(k, k_out, "k", D)
+    if rq is None and rk is None:
+        raise ValueError("q or k: one of them at least")
+    if rq is not None and rk is not None and rq != rk:
+        raise ValueError("q and k: as many rows each")
+    return Hq, Hkv, rk if rq is None else rq, 2 * turns.numel(), _dev(turns, "turns", torch.int64), (*tq, *tk)
+
+
+def ssm_rope(D: int, positions, turns, q, q_out, k=None, k_out=None, interleaved: bool = False, amplitude: float = 1.0,
+             stream=None):
+    """Rotary positions of q and k rows (bf16 [rows, heads * D], row strides that are multiples of 8; outputs may be their inputs; q or
+    k may be None).  positions: int32 [rows]; turns: int64 [rot / 2] on the GPU (ssm_rope_turns): the first rot columns turn."""
+    Hq, Hkv, rows, rot, pt, t = _rope_args(D, turns, q, q_out, k, k_out)
+    like = k if q is None else q
+    dev = _same_device(like, turns=turns, positions=positions, q_out=q_out, k=k, k_out=k_out)
+    _call_on(dev, lib().ssm_rope, rows, Hq, Hkv, D, rot, int(interleaved), pt, float(amplitude),
+             _dev(positions, "positions", torch.int32, rows), *t, _stream(stream, like))
+
+
+def ssm_tree_rope(n_seq: int, n_nodes: int, D: int, layout, cache_len, turns, q, q_out, k=None, k_out=None,
+                  interleaved: bool = False, amplitude: float = 1.0, status=None, stream=None):
+    """ssm_rope of draft trees' rows (row s * n_nodes + v): node v stands at cache_len[s] + its depth."""
+    Hq, Hkv, rows, rot, pt, t = _rope_args(D, turns, q, q_out, k, k_out)
+    if rows != n_seq * n_nodes:
+        raise ValueError("q and k: n_seq * n_nodes rows")
+    like = k if q is None else q
+    dev = _same_device(like, turns=turns, layout=layout, cache_len=cache_len, q_out=q_out, k=k, k_out=k_out, status=status)
+    _call_on(dev, lib().ssm_tree_rope, n_seq, n_nodes, Hq, Hkv, D, rot, int(interleaved), pt, float(amplitude),
+             _dev(layout, "layout", torch.int32, rows * NODE_WORDS), _dev(cache_len, "cache_len", torch.int32, n_seq), *t,
+             _opt_status(status), _stream(stream, like))
+
+
+# ---------------------------------------------------------------------------
+# logits (include/ssm_logits.h)
+# ---------------------------------------------------------------------------
+def ssm_token_scores(logits, tokens, logprob, entropy, top, top_logprob=None, scale: float = 1.0, status=None, stream=None):
+    """Of every row of logits (fp32 or bf16 [T, V], any row stride): the log probabilities of tokens (int32 [T, m] -> logprob fp32
+    [T, m]; -1: none), the entropy (fp32 [T]), and the k largest logits' indices and log probabilities (top int32, top_logprob fp32
+    [T, k], of equal ones the lowest index first).  Any of tokens and logprob, entropy, top and top_logprob may be None.  scale
+    multiplies the logits (1 / temperature)."""
+    f32 = isinstance(logits, torch.Tensor) and logits.dtype == torch.float32
+    px, T, ld = _rows(logits, "logits", torch.float32 if f32 else _BF16)
+    V, m, k = logits.size(1), 0, 0
+    ld = max(ld, V) if T < 2 else ld
+    pt = pl = pi = pe = ps = None
+    if tokens is not None or logprob is not None:
+        pt, m = _table(tokens, "tokens", T)
+        pl = _dev(logprob, "logprob", torch.float32, T * m)
+    if top is not None:
+        pi, k = _table(top, "top", T)
+    if top_logprob is not None:
+        if top is None:
+            raise ValueError("top_logprob: with top")
+        ps = _dev(top_logprob, "top_logprob", torch.float32, T * k)
+    if entropy is not None:
+        pe = _dev(entropy, "entropy", torch.float32, T)
+    dev = _same_device(logits, tokens=tokens, logprob=logprob, entropy=entropy, top=top, top_logprob=top_logprob, status=status)
+    _call_on(dev, lib().ssm_token_scores, T, V, px, int(f32), ld, float(scale), m, pt, pl, pe, k, pi, ps, _opt_status(status),
+             _stream(stream, logits))

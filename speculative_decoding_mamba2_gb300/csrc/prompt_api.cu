@@ -1,10 +1,11 @@
-// C ABI of the prompt and attention calls (ssm_prompt.h, ssm_attention.h): host-side validation, then launches.
+// C ABI of the prompt and attention calls and of token scores (ssm_prompt.h, ssm_attention.h, ssm_logits.h): host-side
+// validation, then launches.
 #include <math.h>
 #include <stdio.h>
 
 #include <string>
 
-#include "prompt.cuh"
+#include "decode.cuh"
 
 namespace ssmtree {
 void set_error(const std::string& msg);
@@ -100,6 +101,101 @@ int page_shift(int32_t page) {  // -1: not a power of two in [8, 1024]
   return -1;
 }
 
+// the checks and arguments that the attention calls share (pages: of either width)
+int check_attend(const char* fn, int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D, const ssm_node* layout,
+                 const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                 const void* k_pages, const void* v_pages, int32_t n_pages, int32_t page_size, const int32_t* page_table,
+                 int32_t max_pages, const int32_t* cache_len, int32_t max_cache_len, float scale, uint16_t* o, int64_t ldo,
+                 const void* workspace, int32_t* dev_status, AttendArgs* out) {
+  if (int rc = check_attend_shape(fn, n_seq, n_nodes, Hq, Hkv, D, max_cache_len)) return rc;
+  const int shift = page_shift(page_size);
+  if (shift < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "page_size must be a power of two in [8, 1024]");
+  if (n_pages < 0 || max_pages < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "n_pages and max_pages must be >= 0");
+  if ((long long)n_pages * Hkv * page_size > INT32_MAX || (long long)n_seq * n_nodes > INT32_MAX)
+    return pfail(SSM_ERR_CAPACITY, fn, "more than 2^31 - 1 rows of pages");
+  if (!(scale > 0.f) || isinf(scale)) return pfail(SSM_ERR_RANGE, fn, "scale must be positive and finite");
+  if (n_seq > 0 && (!layout || !q || !k || !v || !o || !cache_len)) return pfail(SSM_ERR_INVALID_ARG, fn, "a pointer is NULL");
+  if (max_cache_len > 0 && (!k_pages || !v_pages || !page_table))
+    return pfail(SSM_ERR_INVALID_ARG, fn, "k_pages, v_pages or page_table is NULL");
+  if (off16(q) || off16(k) || off16(v) || off16(k_pages) || off16(v_pages) || off16(o))
+    return pfail(SSM_ERR_INVALID_ARG, fn, "q, k, v, the pages and o must be 16-byte aligned");
+  if (ldq < (int64_t)Hq * D || ldo < (int64_t)Hq * D || ldk < (int64_t)Hkv * D || ldv < (int64_t)Hkv * D ||
+      ((ldq | ldo | ldk | ldv) & 7))
+    return pfail(SSM_ERR_INVALID_ARG, fn, "row strides must be at least the row's width and multiples of 8");
+  if (!workspace || ((uintptr_t)workspace & 255)) return pfail(SSM_ERR_INVALID_ARG, fn, "workspace must be 256-byte aligned");
+  AttendArgs a{};
+  a.S = n_seq, a.n = n_nodes, a.Hq = Hq, a.Hkv = Hkv, a.D = D, a.g = Hq / Hkv;
+  a.layout = layout, a.q = q, a.k = k, a.v = v, a.ldq = ldq, a.ldk = ldk, a.ldv = ldv;
+  a.n_pages = n_pages, a.page_shift = shift;
+  a.table = page_table, a.max_pages = max_pages, a.cache_len = cache_len, a.max_len = max_cache_len;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.o = o, a.ldo = ldo, a.status = dev_status;
+  *out = a;
+  return SSM_OK;
+}
+
+int check_commit(const char* fn, int32_t n_layers, int32_t n_seq, int32_t n_nodes, int32_t Hkv, int32_t D, int32_t max_path,
+                 const int32_t* path, const int32_t* path_len, const uint16_t* k, const uint16_t* v, const void* k_pages,
+                 const void* v_pages, int32_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
+                 const int32_t* cache_len, int32_t* len_out, int32_t* dev_status, KvCommitArgs* out) {
+  if (n_seq < 0 || n_seq > 65535) return pfail(SSM_ERR_INVALID_ARG, fn, "n_seq must be in [0, 65535]");
+  if (n_layers < 1 || n_nodes < 1 || Hkv < 1) return pfail(SSM_ERR_INVALID_ARG, fn, "n_layers, n_nodes and Hkv must be >= 1");
+  if (max_path < 1 || max_path > SSM_MAX_PATH) return pfail(SSM_ERR_INVALID_ARG, fn, "max_path must be in [1, SSM_MAX_PATH]");
+  if (D != 64 && D != 128) return pfail(SSM_ERR_INVALID_ARG, fn, "D must be 64 or 128");
+  if ((long long)n_layers * max_path * Hkv * (D / 8) > (1ll << 30))
+    return pfail(SSM_ERR_CAPACITY, fn, "n_layers * max_path * Hkv * D too large");
+  const int shift = page_shift(page_size);
+  if (shift < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "page_size must be a power of two in [8, 1024]");
+  if (n_pages < 0 || max_pages < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "n_pages and max_pages must be >= 0");
+  if (n_seq > 0 && (!path || !path_len || !k || !v || !k_pages || !v_pages || !page_table || !cache_len || !len_out))
+    return pfail(SSM_ERR_INVALID_ARG, fn, "a pointer is NULL");
+  if (off16(k) || off16(v) || off16(k_pages) || off16(v_pages))
+    return pfail(SSM_ERR_INVALID_ARG, fn, "k, v and the pages must be 16-byte aligned");
+  KvCommitArgs a{};
+  a.L = n_layers, a.S = n_seq, a.n = n_nodes, a.Hkv = Hkv, a.D = D, a.max_path = max_path;
+  a.path = path, a.path_len = path_len, a.k = k, a.v = v;
+  a.n_pages = n_pages, a.page_shift = shift, a.table = page_table, a.max_pages = max_pages;
+  a.cache_len = cache_len, a.len_out = len_out, a.status = dev_status;
+  *out = a;
+  return SSM_OK;
+}
+
+// the shift of a block of tokens; -1: not a power of two from 8 to page_size
+int block_shift(int32_t block, int32_t page_size) {
+  const int shift = page_shift(block);
+  return shift < 0 || block > page_size ? -1 : shift;
+}
+
+int check_rope(const char* fn, int32_t Hq, int32_t Hkv, int32_t D, int32_t rot, const uint64_t* turns, float amplitude,
+               long long rows, const uint16_t* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, const uint16_t* k,
+               int64_t ldk, uint16_t* k_out, int64_t ldko, int32_t interleaved, RopeArgs* out) {
+  if (rows > INT32_MAX) return pfail(SSM_ERR_CAPACITY, fn, "more than 2^31 - 1 rows");
+  if (Hq < 0 || Hkv < 0 || Hq > 4096 || Hkv > 4096) return pfail(SSM_ERR_INVALID_ARG, fn, "Hq and Hkv must be in [0, 4096]");
+  if (D < 8 || D > 512 || D % 8) return pfail(SSM_ERR_INVALID_ARG, fn, "D must be a multiple of 8 in [8, 512]");
+  if (rot < 2 || rot > D || rot % 2) return pfail(SSM_ERR_INVALID_ARG, fn, "rot must be even and in [2, D]");
+  if (!isfinite(amplitude)) return pfail(SSM_ERR_RANGE, fn, "amplitude must be finite");
+  RopeArgs a{};
+  a.n_tok = (int)rows, a.heads[0] = Hq, a.heads[1] = Hkv, a.D = D, a.rot = rot, a.interleaved = interleaved != 0;
+  a.turns = reinterpret_cast<const unsigned long long*>(turns), a.amp = amplitude;
+  a.in[0] = q, a.in[1] = k, a.out[0] = q_out, a.out[1] = k_out;
+  a.ldi[0] = ldq, a.ldi[1] = ldk, a.ldo[0] = ldqo, a.ldo[1] = ldko;
+  if (rows > 0 && (Hq || Hkv)) {
+    if (!turns || ((uintptr_t)turns & 7)) return pfail(SSM_ERR_INVALID_ARG, fn, "turns must be there and 8-byte aligned");
+    for (int i = 0; i < 2; ++i) {
+      if (a.heads[i] == 0) continue;
+      if (!a.in[i] || !a.out[i] || off16(a.in[i]) || off16(a.out[i]))
+        return pfail(SSM_ERR_INVALID_ARG, fn, "q, k, q_out and k_out must be there and 16-byte aligned");
+      const int64_t width = (int64_t)a.heads[i] * D;
+      if (a.ldi[i] < width || a.ldo[i] < width || ((a.ldi[i] | a.ldo[i]) & 7))
+        return pfail(SSM_ERR_INVALID_ARG, fn, "row strides must be at least the row's width and multiples of 8");
+      if (a.in[i] == a.out[i] && a.ldi[i] != a.ldo[i] && rows > 1)
+        return pfail(SSM_ERR_INVALID_ARG, fn, "an output in its input's place has its input's row stride");
+    }
+  }
+  *out = a;
+  return SSM_OK;
+}
+
 }  // namespace
 
 extern "C" int ssm_prompt_conv(const ssm_dims* dims, const ssm_params* prm, int32_t layer, int32_t n_seq,
@@ -190,31 +286,13 @@ extern "C" int ssm_tree_attention(int32_t n_seq, int32_t n_nodes, int32_t Hq, in
                                   int32_t max_cache_len, float scale, uint16_t* o, int64_t ldo, void* workspace,
                                   size_t workspace_bytes, int32_t* dev_status, void* stream) {
   const char* fn = "ssm_tree_attention";
-  if (int rc = check_attend_shape(fn, n_seq, n_nodes, Hq, Hkv, D, max_cache_len)) return rc;
-  const int shift = page_shift(page_size);
-  if (shift < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "page_size must be a power of two in [8, 1024]");
-  if (n_pages < 0 || max_pages < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "n_pages and max_pages must be >= 0");
-  if ((long long)n_pages * Hkv * page_size > INT32_MAX || (long long)n_seq * n_nodes > INT32_MAX)
-    return pfail(SSM_ERR_CAPACITY, fn, "more than 2^31 - 1 rows of pages");
-  if (!(scale > 0.f) || isinf(scale)) return pfail(SSM_ERR_RANGE, fn, "scale must be positive and finite");
-  if (n_seq > 0 && (!layout || !q || !k || !v || !o || !cache_len)) return pfail(SSM_ERR_INVALID_ARG, fn, "a pointer is NULL");
-  if (max_cache_len > 0 && (!k_pages || !v_pages || !page_table))
-    return pfail(SSM_ERR_INVALID_ARG, fn, "k_pages, v_pages or page_table is NULL");
-  if (off16(q) || off16(k) || off16(v) || off16(k_pages) || off16(v_pages) || off16(o))
-    return pfail(SSM_ERR_INVALID_ARG, fn, "q, k, v, the pages and o must be 16-byte aligned");
-  if (ldq < (int64_t)Hq * D || ldo < (int64_t)Hq * D || ldk < (int64_t)Hkv * D || ldv < (int64_t)Hkv * D ||
-      ((ldq | ldo | ldk | ldv) & 7))
-    return pfail(SSM_ERR_INVALID_ARG, fn, "row strides must be at least the row's width and multiples of 8");
-  if (!workspace || ((uintptr_t)workspace & 255)) return pfail(SSM_ERR_INVALID_ARG, fn, "workspace must be 256-byte aligned");
+  AttendArgs a;
+  if (int rc = check_attend(fn, n_seq, n_nodes, Hq, Hkv, D, layout, q, ldq, k, ldk, v, ldv, k_pages, v_pages, n_pages, page_size,
+                            page_table, max_pages, cache_len, max_cache_len, scale, o, ldo, workspace, dev_status, &a))
+    return rc;
   if (workspace_bytes < tree_attention_workspace_bytes(n_seq, n_nodes, Hq, Hkv, D, max_cache_len))
     return pfail(SSM_ERR_CAPACITY, fn, "workspace too small (ssm_tree_attention_workspace_size)");
-  AttendArgs a{};
-  a.S = n_seq, a.n = n_nodes, a.Hq = Hq, a.Hkv = Hkv, a.D = D, a.g = Hq / Hkv;
-  a.layout = layout, a.q = q, a.k = k, a.v = v, a.ldq = ldq, a.ldk = ldk, a.ldv = ldv;
-  a.kp = k_pages, a.vp = v_pages, a.n_pages = n_pages, a.page_shift = shift;
-  a.table = page_table, a.max_pages = max_pages, a.cache_len = cache_len, a.max_len = max_cache_len;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.o = o, a.ldo = ldo, a.status = dev_status;
+  a.kp = k_pages, a.vp = v_pages;
   return pfinish(fn, launch_tree_attention(a, workspace, (cudaStream_t)stream));
 }
 
@@ -224,23 +302,147 @@ extern "C" int ssm_kv_commit(int32_t n_layers, int32_t n_seq, int32_t n_nodes, i
                              const int32_t* page_table, int32_t max_pages, const int32_t* cache_len, int32_t* len_out,
                              int32_t* dev_status, void* stream) {
   const char* fn = "ssm_kv_commit";
-  if (n_seq < 0 || n_seq > 65535) return pfail(SSM_ERR_INVALID_ARG, fn, "n_seq must be in [0, 65535]");
-  if (n_layers < 1 || n_nodes < 1 || Hkv < 1) return pfail(SSM_ERR_INVALID_ARG, fn, "n_layers, n_nodes and Hkv must be >= 1");
-  if (max_path < 1 || max_path > SSM_MAX_PATH) return pfail(SSM_ERR_INVALID_ARG, fn, "max_path must be in [1, SSM_MAX_PATH]");
-  if (D != 64 && D != 128) return pfail(SSM_ERR_INVALID_ARG, fn, "D must be 64 or 128");
-  if ((long long)n_layers * max_path * Hkv * (D / 8) > (1ll << 30))
-    return pfail(SSM_ERR_CAPACITY, fn, "n_layers * max_path * Hkv * D too large");
-  const int shift = page_shift(page_size);
-  if (shift < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "page_size must be a power of two in [8, 1024]");
-  if (n_pages < 0 || max_pages < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "n_pages and max_pages must be >= 0");
-  if (n_seq > 0 && (!path || !path_len || !k || !v || !k_pages || !v_pages || !page_table || !cache_len || !len_out))
-    return pfail(SSM_ERR_INVALID_ARG, fn, "a pointer is NULL");
-  if (off16(k) || off16(v) || off16(k_pages) || off16(v_pages))
-    return pfail(SSM_ERR_INVALID_ARG, fn, "k, v and the pages must be 16-byte aligned");
-  KvCommitArgs a{};
-  a.L = n_layers, a.S = n_seq, a.n = n_nodes, a.Hkv = Hkv, a.D = D, a.max_path = max_path;
-  a.path = path, a.path_len = path_len, a.k = k, a.v = v, a.kp = k_pages, a.vp = v_pages;
-  a.n_pages = n_pages, a.page_shift = shift, a.table = page_table, a.max_pages = max_pages;
-  a.cache_len = cache_len, a.len_out = len_out, a.status = dev_status;
+  KvCommitArgs a;
+  if (int rc = check_commit(fn, n_layers, n_seq, n_nodes, Hkv, D, max_path, path, path_len, k, v, k_pages, v_pages, n_pages,
+                            page_size, page_table, max_pages, cache_len, len_out, dev_status, &a))
+    return rc;
+  a.kp = k_pages, a.vp = v_pages;
   return pfinish(fn, launch_kv_commit(a, (cudaStream_t)stream));
+}
+
+extern "C" size_t ssm_tree_attention_fp8_workspace_size(int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D,
+                                                        int32_t max_cache_len) {
+  if (check_attend_shape("ssm_tree_attention_fp8_workspace_size", n_seq, n_nodes, Hq, Hkv, D, max_cache_len)) return 0;
+  set_error("");
+  return tree_attention_fp8_workspace_bytes(n_seq, n_nodes, Hq, Hkv, D, max_cache_len);
+}
+
+extern "C" int ssm_tree_attention_fp8(int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D,
+                                      const ssm_node* layout, const uint16_t* q, int64_t ldq, const uint16_t* k,
+                                      int64_t ldk, const uint16_t* v, int64_t ldv, const uint8_t* k_pages,
+                                      const uint8_t* v_pages, const float* k_scales, const float* v_scales,
+                                      int32_t n_pages, int32_t page_size, int32_t block, const int32_t* page_table,
+                                      int32_t max_pages, const int32_t* cache_len, int32_t max_cache_len, float scale,
+                                      uint16_t* o, int64_t ldo, void* workspace, size_t workspace_bytes,
+                                      int32_t* dev_status, void* stream) {
+  const char* fn = "ssm_tree_attention_fp8";
+  AttendFp8Args f{};
+  if (int rc = check_attend(fn, n_seq, n_nodes, Hq, Hkv, D, layout, q, ldq, k, ldk, v, ldv, k_pages, v_pages, n_pages, page_size,
+                            page_table, max_pages, cache_len, max_cache_len, scale, o, ldo, workspace, dev_status, &f.a))
+    return rc;
+  f.block_shift = block_shift(block, page_size);
+  if (f.block_shift < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "block must be a power of two from 8 to page_size");
+  if (max_cache_len > 0 && (!k_scales || !v_scales)) return pfail(SSM_ERR_INVALID_ARG, fn, "k_scales or v_scales is NULL");
+  if (((uintptr_t)k_scales | (uintptr_t)v_scales) & 3) return pfail(SSM_ERR_INVALID_ARG, fn, "the scales must be 4-byte aligned");
+  if (workspace_bytes < tree_attention_fp8_workspace_bytes(n_seq, n_nodes, Hq, Hkv, D, max_cache_len))
+    return pfail(SSM_ERR_CAPACITY, fn, "workspace too small (ssm_tree_attention_fp8_workspace_size)");
+  f.kp = k_pages, f.vp = v_pages, f.ks = k_scales, f.vs = v_scales;
+  return pfinish(fn, launch_tree_attention_fp8(f, workspace, (cudaStream_t)stream));
+}
+
+extern "C" int ssm_kv_commit_fp8(int32_t n_layers, int32_t n_seq, int32_t n_nodes, int32_t Hkv, int32_t D, int32_t max_path,
+                                 const int32_t* path, const int32_t* path_len, const uint16_t* k, const uint16_t* v,
+                                 uint8_t* k_pages, uint8_t* v_pages, float* k_scales, float* v_scales, int32_t n_pages,
+                                 int32_t page_size, int32_t block, const int32_t* page_table, int32_t max_pages,
+                                 const int32_t* cache_len, int32_t* len_out, int32_t* dev_status, void* stream) {
+  const char* fn = "ssm_kv_commit_fp8";
+  KvCommitFp8Args f{};
+  if (int rc = check_commit(fn, n_layers, n_seq, n_nodes, Hkv, D, max_path, path, path_len, k, v, k_pages, v_pages, n_pages,
+                            page_size, page_table, max_pages, cache_len, len_out, dev_status, &f.a))
+    return rc;
+  f.block_shift = block_shift(block, page_size);
+  if (f.block_shift < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "block must be a power of two from 8 to page_size");
+  if (n_seq > 0 && (!k_scales || !v_scales)) return pfail(SSM_ERR_INVALID_ARG, fn, "k_scales or v_scales is NULL");
+  if (((uintptr_t)k_scales | (uintptr_t)v_scales) & 3) return pfail(SSM_ERR_INVALID_ARG, fn, "the scales must be 4-byte aligned");
+  f.kp = k_pages, f.vp = v_pages, f.ks = k_scales, f.vs = v_scales;
+  return pfinish(fn, launch_kv_commit_fp8(f, (cudaStream_t)stream));
+}
+
+extern "C" int ssm_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original_len,
+                                    double low, double high, double* freq) {
+  const char* fn = "ssm_rope_frequencies";
+  if (rot < 2 || rot % 2 || !freq) return pfail(SSM_ERR_INVALID_ARG, fn, "rot must be even and at least 2, freq not NULL");
+  if (!(base > 0) || !isfinite(base)) return pfail(SSM_ERR_RANGE, fn, "base must be positive and finite");
+  if (scaling < SSM_ROPE_PLAIN || scaling > SSM_ROPE_BY_PARTS) return pfail(SSM_ERR_INVALID_ARG, fn, "no such scaling");
+  if (scaling != SSM_ROPE_PLAIN && (!(factor > 0) || !isfinite(factor)))
+    return pfail(SSM_ERR_RANGE, fn, "factor must be positive and finite");
+  if (scaling == SSM_ROPE_BASE && rot < 4) return pfail(SSM_ERR_RANGE, fn, "one pair has no slower one: rot must be at least 4");
+  if (scaling == SSM_ROPE_BY_PARTS && (!(original_len > 0) || !isfinite(original_len) || !(low >= 0) || !(high > low) || !isfinite(high)))
+    return pfail(SSM_ERR_RANGE, fn, "need original_len > 0 and 0 <= low < high");
+  if (scaling == SSM_ROPE_BASE) base *= pow(factor, rot / (rot - 2.0));
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot);
+    if (scaling == SSM_ROPE_LINEAR) f /= factor;
+    if (scaling == SSM_ROPE_BY_PARTS) {
+      const double keep = fmin(fmax((original_len * f / 6.283185307179586 - low) / (high - low), 0.0), 1.0);
+      f *= keep + (1.0 - keep) / factor;
+    }
+    freq[i] = f;
+  }
+  set_error("");
+  return SSM_OK;
+}
+
+extern "C" int ssm_rope_turns(int32_t n, const double* freq, uint64_t* turns) {
+  const char* fn = "ssm_rope_turns";
+  if (n < 0 || (n > 0 && (!freq || !turns))) return pfail(SSM_ERR_INVALID_ARG, fn, "n must be >= 0, freq and turns not NULL");
+  for (int i = 0; i < n; ++i)
+    if (!isfinite(freq[i])) return pfail(SSM_ERR_RANGE, fn, "a frequency is not finite");
+  for (int i = 0; i < n; ++i) {
+    const double t = freq[i] / 6.283185307179586, part = t - floor(t);
+    // (rounded by the two halves: the whole may be 2^64)
+    const double hi = floor(part * 0x1p32), lo = rint((part * 0x1p32 - hi) * 0x1p32);
+    turns[i] = ((uint64_t)hi << 32) + (uint64_t)lo;
+  }
+  set_error("");
+  return SSM_OK;
+}
+
+extern "C" int ssm_rope(int32_t n_tok, int32_t Hq, int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved,
+                        const uint64_t* turns, float amplitude, const int32_t* positions, const uint16_t* q, int64_t ldq,
+                        uint16_t* q_out, int64_t ldqo, const uint16_t* k, int64_t ldk, uint16_t* k_out, int64_t ldko,
+                        void* stream) {
+  const char* fn = "ssm_rope";
+  if (n_tok < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "n_tok must be >= 0");
+  RopeArgs a;
+  if (int rc = check_rope(fn, Hq, Hkv, D, rot, turns, amplitude, n_tok, q, ldq, q_out, ldqo, k, ldk, k_out, ldko, interleaved, &a)) return rc;
+  if (n_tok > 0 && !positions) return pfail(SSM_ERR_INVALID_ARG, fn, "positions is NULL");
+  a.pos = positions;
+  return pfinish(fn, launch_rope(a, (cudaStream_t)stream));
+}
+
+extern "C" int ssm_tree_rope(int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D, int32_t rot,
+                             int32_t interleaved, const uint64_t* turns, float amplitude, const ssm_node* layout,
+                             const int32_t* cache_len, const uint16_t* q, int64_t ldq, uint16_t* q_out, int64_t ldqo,
+                             const uint16_t* k, int64_t ldk, uint16_t* k_out, int64_t ldko, int32_t* dev_status,
+                             void* stream) {
+  const char* fn = "ssm_tree_rope";
+  if (n_seq < 0 || n_seq > 65535) return pfail(SSM_ERR_INVALID_ARG, fn, "n_seq must be in [0, 65535]");
+  if (n_nodes < 1) return pfail(SSM_ERR_INVALID_ARG, fn, "n_nodes must be >= 1");
+  RopeArgs a;
+  if (int rc = check_rope(fn, Hq, Hkv, D, rot, turns, amplitude, (long long)n_seq * n_nodes, q, ldq, q_out, ldqo, k, ldk, k_out, ldko,
+                          interleaved, &a))
+    return rc;
+  if (n_seq > 0 && (!layout || !cache_len)) return pfail(SSM_ERR_INVALID_ARG, fn, "layout or cache_len is NULL");
+  a.n = n_nodes, a.layout = layout, a.cache_len = cache_len, a.status = dev_status;
+  return pfinish(fn, launch_rope(a, (cudaStream_t)stream));
+}
+
+extern "C" int ssm_token_scores(int32_t n_rows, int32_t n_vocab, const void* logits, int32_t f32, int64_t ld, float scale,
+                                int32_t m, const int32_t* tokens, float* logprob, float* entropy, int32_t k, int32_t* top,
+                                float* top_logprob, int32_t* dev_status, void* stream) {
+  const char* fn = "ssm_token_scores";
+  if (n_rows < 0 || n_rows > (1 << 27)) return pfail(SSM_ERR_INVALID_ARG, fn, "n_rows must be in [0, 2^27]");
+  if (n_vocab < 1 || ld < n_vocab) return pfail(SSM_ERR_INVALID_ARG, fn, "n_vocab must be >= 1, ld at least that");
+  if (!(scale > 0.f) || isinf(scale)) return pfail(SSM_ERR_RANGE, fn, "scale must be positive and finite");
+  if (m < 0 || k < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "m and k must be >= 0");
+  if (k > SSM_MAX_TOP) return pfail(SSM_ERR_CAPACITY, fn, "k above SSM_MAX_TOP");
+  if (k > n_vocab) return pfail(SSM_ERR_INVALID_ARG, fn, "k above n_vocab");
+  if (n_rows > 0 && (!logits || (m > 0 && (!tokens || !logprob)) || (k > 0 && !top)))
+    return pfail(SSM_ERR_INVALID_ARG, fn, "a pointer is NULL");
+  if ((uintptr_t)logits & (f32 ? 3 : 1)) return pfail(SSM_ERR_INVALID_ARG, fn, "logits must be aligned to an element");
+  ScoreArgs a{};
+  a.T = n_rows, a.V = n_vocab, a.m = m, a.k = k, a.x = logits, a.f32 = f32 != 0, a.ld = ld, a.scale = scale;
+  a.tok = tokens, a.logprob = logprob, a.entropy = entropy, a.top = top, a.top_logprob = top_logprob, a.status = dev_status;
+  return pfinish(fn, launch_token_scores(a, (cudaStream_t)stream));
 }
