@@ -23,7 +23,7 @@ SOURCES = ["api.cu", "verify.cu", "verify_tc.cu", "commit.cu", "draft.cu", "noal
            "layer_api.cu", "draft_tree.cu", "selftest.cu", "prompt.cu", "prompt_scan.cu", "prompt_scan_tc.cu", "attention.cu",
            "attention_fp8.cu", "rope.cu", "scores.cu", "prompt_api.cu", "layout.cpp"]
 HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "draft_tree.cuh", "log_apply.cuh", "tc.cuh", "mma_tiles.cuh",
-                                           "prompt.cuh", "umma.cuh", "decode.cuh")] + \
+                                           "prompt.cuh", "umma.cuh", "attend.cuh", "decode.cuh")] + \
     [os.path.join(INCLUDE, h) for h in ("ssm_tree.h", "ssm_layer.h", "ssm_prompt.h", "ssm_attention.h",
                                               "ssm_logits.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

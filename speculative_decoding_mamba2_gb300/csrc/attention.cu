@@ -21,13 +21,11 @@
 // of K and V, 18 us (67 MB: 3.7 TB/s; latency: seven tiles to a CTA); 8 trees of 16 nodes over up to 8117 rows 41 us (163 MB:
 // 4.0 TB/s of HBM); 4 trees of 40 nodes over up to 40009 rows, 4 heads, 86 us (85 GFLOP: 0.99 PFLOP/s, 1.19 with the rows
 // that fill up the third row tile; tensor pipe 52 % of the time, shared memory the rest).  D = 64, the same rows: 16, 27 and 73 us.
-#include "prompt.cuh"
-#include "umma.cuh"
+#include "attend.cuh"
 
 namespace ssmtree {
 namespace {
 
-constexpr int KT = 64;          // keys per tile
 constexpr int ATHREADS = 224;   // 4 softmax warps, one for copies, two for MMAs
 constexpr int UNITS = 6;        // tiles of K and V, by turns, in the ring: what lets two CTAs share an SM's memory
 constexpr int BLK = KT * 128;   // 64 rows x 64 columns of bf16
@@ -39,7 +37,7 @@ struct AttendSmem {
   static constexpr int OFF_KV = (D / 64 - 1) * 2 * BLK;      // after Q's other columns: 128 rows of 64
   static constexpr int TILE = (D / 64) * BLK;                // K or V of a tile
   static constexpr int OFF_MISC = OFF_KV + UNITS * TILE;
-  static constexpr int BYTES = OFF_MISC + 768;
+  static constexpr int BYTES = OFF_MISC + 832;
   static_assert(BYTES <= 228 * 1024 / 2 - 1024, "two to an SM");
 };
 struct AttendMisc {
@@ -49,76 +47,9 @@ struct AttendMisc {
   uint32_t tmem;
   int stop;
   int no_page[8];              // whether a page of tile i (at i % 8) is out of range
-  int most[ATHREADS / 32];     // for the splits, of each warp: tiles of the longest sequence, the least estimate
-  unsigned int least[ATHREADS / 32];
+  SplitScratch split;
 };
-static_assert(sizeof(AttendMisc) <= 768, "space");
-
-__device__ __forceinline__ float max3f(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-
-// a sequence's cached rows; -1: not a length there is room for
-__device__ __forceinline__ int cached_rows(const AttendArgs& a, int s) {
-  const int len = a.cache_len[s];
-  return len < 0 || len > a.max_len || (long long)len > ((long long)a.max_pages << a.page_shift) ? -1 : len;
-}
-
-// Splits.  Every sequence's tiles are cut into runs of the same length, and every CTA works out that length from the lengths
-// in device memory: of 189 from the longest sequence's tiles down to a 64th of them, each tried by a thread, the one whose
-// CTAs take least, where a CTA costs about four tiles beside its own and joining about two.  (Cut by the longest sequence
-// alone, eight ragged caches of up to 8117 rows took 50 us and four of up to 40009 rows, 101 us.)
-constexpr int CANDIDATES = 189;
-__device__ __forceinline__ int choose_split(const AttendArgs& a, int per, int* tiles, AttendMisc* ms) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int most = 0;
-  for (int s = tid; s < a.S; s += ATHREADS) most = max(most, tiles[s] = (max(cached_rows(a, s), 0) + KT - 1) / KT + 1);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) ms->most[warp] = most;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < ATHREADS / 32; ++w) most = max(most, ms->most[w]);
-  unsigned int key = 0xffffffffu;
-  const unsigned int tps = (3u * most + tid + 2) / (tid + 3);
-  if (tid < CANDIDATES) {
-    unsigned int runs = 0;
-    float total = 0.f;
-    for (int s = 0; s < a.S; ++s) runs += (tiles[s] + tps - 1) / tps, total += (float)tiles[s];
-    if (runs <= (unsigned)a.max_runs) {  // (one run to a sequence always is)
-      constexpr float slots = 2 * kSMs;
-      const float ctas = (float)(runs * per), len = tps + 4.f;
-      const float waves = ceilf(ctas / slots) * len, list = (total * per + 4.f * ctas) / slots + len;
-      const float est = fminf(waves, list) + (runs > (unsigned)a.S ? 2.f : 0.f);
-      key = (unsigned int)fminf(est / most * 65536.f, 16777215.f) << 8 | tid;
-    }
-  }
-  key = __reduce_min_sync(0xffffffffu, key);
-  if (lane == 0) ms->least[warp] = key;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < ATHREADS / 32; ++w) key = min(key, ms->least[w]);
-  const unsigned int c = key & 255u;
-  return (int)((3u * most + c + 2) / (c + 3));
-}
-// the sequence of the run-th run, its first run and their number
-__device__ __forceinline__ bool find_run(int S, const int* tiles, int tps, int run, int& s, int& first, int& runs) {
-  const int lane = threadIdx.x & 31;
-  for (int b = 0, before = 0; b < S; b += 32) {
-    const int k = b + lane < S ? (tiles[b + lane] + tps - 1) / tps : 0;
-    int upto = k;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += u;
-    }
-    const unsigned int past = __ballot_sync(0xffffffffu, before + upto > run);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      s = b + l, runs = __shfl_sync(0xffffffffu, k, l), first = before + __shfl_sync(0xffffffffu, upto, l) - runs;
-      return true;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return false;
-}
+static_assert(sizeof(AttendMisc) <= 832, "space");
 
 template <int D>
 __global__ void __launch_bounds__(ATHREADS, 2)
@@ -163,7 +94,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
   if (a.max_runs > 0) {
     int* tiles = reinterpret_cast<int*>(smem);  // space not in use yet: with D = 64 a place of the ring
     int first;
-    tps = choose_split(a, a.Hkv * rt, tiles, ms);
+    tps = choose_split<ATHREADS>(a, a.Hkv * rt, tiles, &ms->split);
     any = find_run(a.S, tiles, tps, run, s, first, splits);
     sp = any ? run - first : 0;
     fence_async_smem();  // (before the barrier behind which the copies may write there)
@@ -209,39 +140,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
     }
-    // ancestor words: a node's own bit, then its parent's word, its grandparent's, ... by doubling
-    if (has_tree && warp == 0) {
-      unsigned long long w[2];
-      int p[2];
-      bool bad = false;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int v = lane + 32 * k;
-        p[k] = -1;
-        if (v > 0 && v < a.n) {
-          p[k] = a.layout[(long long)s * a.n + v].parent;
-          if (p[k] < 0 || p[k] >= v) p[k] = -1, bad = true;
-        }
-        w[k] = 1ull << v;
-      }
-      if (bad && kvh == 0 && r0 == 0) flag(a.status, SSM_STATUS_BAD_LAYOUT);
-#pragma unroll 1
-      for (int hop = 0; hop < 6; ++hop) {
-        unsigned long long up[2];
-        int pp[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {  // the word and the link of node p[k], which lane p[k] % 32 holds
-          const int from = p[k] & 31;
-          const unsigned long long u0 = __shfl_sync(0xffffffffu, w[0], from), u1 = __shfl_sync(0xffffffffu, w[1], from);
-          const int q0 = __shfl_sync(0xffffffffu, p[0], from), q1 = __shfl_sync(0xffffffffu, p[1], from);
-          up[k] = p[k] < 32 ? u0 : u1, pp[k] = p[k] < 32 ? q0 : q1;
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (p[k] >= 0) w[k] |= up[k], p[k] = pp[k];
-      }
-      ms->anc[lane] = w[0], ms->anc[lane + 32] = w[1];
-    }
+    if (has_tree && warp == 0) ancestor_words(a, s, ms->anc, kvh == 0 && r0 == 0);
 
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -546,22 +445,16 @@ __global__ void __launch_bounds__(128) combine_kernel(AttendArgs a) {
   for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(o + v) = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
 }
 
-// Row tiles, and the most runs that the sequences are cut into (0: they are not cut, where the CTAs
-// fill the SMs twice over or the longest sequence is too short for what joining costs).  Uncut, one long cache among many
-// short ones is walked by a CTA for each of its heads: 128 single tokens of 8 heads over 1000 rows each take 98 us, with
-// 64000 rows for one of them 698; 72 of them, which are cut, 112.
-struct AttendPlan {
-  int row_tiles, max_runs;
-};
-AttendPlan plan_attend(int S, int n, int Hq, int Hkv, int max_len) {
-  AttendPlan p;
-  const int rows = n * (Hq / Hkv);
-  p.row_tiles = (rows + 127) / 128;
-  const long long per = (long long)Hkv * p.row_tiles, slots = 2 * kSMs;
-  p.max_runs = max_len > 5 * KT && S * per < 2 * slots ? S + (int)((slots + per - 1) / per) : 0;
-  return p;
-}
 static_assert(2 * 2 * kSMs * 4 <= 6 * 64 * 64 * 2, "the lengths stand in the ring's space");
+
+template <int D>
+cudaError_t join_runs(const AttendArgs& a, cudaStream_t s) {
+  const long long out_rows = (long long)a.S * a.n * a.Hq;
+  // four warps to a row where there are many runs: 38 runs 22.3 us a call with one warp, 18.4 with four; 7 runs 87 and 90
+  const bool wide = a.max_runs >= 8 * a.S;
+  const dim3 grid((unsigned)(wide ? out_rows : (out_rows + 3) / 4));
+  return wide ? launch_early(combine_kernel<D, 4>, grid, 128, 0, s, a) : launch_early(combine_kernel<D, 1>, grid, 128, 0, s, a);
+}
 
 template <int D>
 cudaError_t run_attend(const AttendArgs& a, const AttendPlan& p, const CUtensorMap (&m)[4], cudaStream_t s) {
@@ -586,11 +479,7 @@ cudaError_t run_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream_t 
     return cudaErrorInvalidValue;
   cudaError_t e = run_attend<D>(a, p, m, s);
   if (e != cudaSuccess || p.max_runs == 0) return e;
-  const long long out_rows = (long long)a.S * a.n * a.Hq;
-  // four warps to a row where there are many runs: 38 runs 22.3 us a call with one warp, 18.4 with four; 7 runs 87 and 90
-  const bool wide = p.max_runs >= 8 * a.S;
-  const dim3 grid((unsigned)(wide ? out_rows : (out_rows + 3) / 4));
-  return wide ? launch_early(combine_kernel<D, 4>, grid, 128, 0, s, a) : launch_early(combine_kernel<D, 1>, grid, 128, 0, s, a);
+  return join_runs<D>(a, s);
 }
 
 // A cluster of 8 CTAs for each sequence: together they copy its path's rows; its length is written by one of them
@@ -656,19 +545,18 @@ __global__ void __cluster_dims__(CCTAS, 1, 1) __launch_bounds__(CTHREADS) kv_com
 }  // namespace
 
 size_t tree_attention_workspace_bytes(int S, int n, int Hq, int Hkv, int D, int max_len) {
-  const AttendPlan p = plan_attend(S, n, Hq, Hkv, max_len);
-  return 256 + (p.max_runs ? (size_t)p.max_runs * Hkv * n * (Hq / Hkv) * (D + 2) * sizeof(float) + S * sizeof(int2) : 0);
+  return attend_workspace_bytes(plan_attend(S, n, Hq, Hkv, max_len), S, n, Hq, Hkv, D);
+}
+
+cudaError_t launch_attend_join(const AttendArgs& a, cudaStream_t s) {
+  return a.D == 64 ? join_runs<64>(a, s) : join_runs<128>(a, s);
 }
 
 cudaError_t launch_tree_attention(const AttendArgs& args, void* workspace, cudaStream_t s) {
   if (args.S == 0) return cudaSuccess;
   AttendArgs a = args;
   const AttendPlan p = plan_attend(a.S, a.n, a.Hq, a.Hkv, a.max_len);
-  const size_t parts = (size_t)p.max_runs * a.Hkv * a.n * a.g;
-  a.max_runs = p.max_runs;
-  a.part = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part + parts * a.D);
-  a.runs = reinterpret_cast<int2*>(a.part_ml + parts);
+  lay_workspace(a, p, workspace);
   return a.D == 64 ? run_attend_d<64>(a, p, s) : run_attend_d<128>(a, p, s);
 }
 

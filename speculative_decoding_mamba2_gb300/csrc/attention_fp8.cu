@@ -1,78 +1,69 @@
 // Attention of a draft tree's nodes over an 8-bit paged cache and their ancestors, and the commit of the accepted path into it
 // (ssm_attention.h).
+#include "attend.cuh"
 #include "decode.cuh"
-#include "mma_tiles.cuh"
 
 namespace ssmtree {
 namespace {
 
-// One warp to a query row, D / 32 columns a lane; a row of keys at a time.
+// The plan is that of the 16-bit kernel (attention.cu): up to 128 query rows of a key/value head walk tiles of 64 keys,
+//     S = Q . K^T,   P = 2^(S - m),   O += P . V
+// on tcgen05, softmax statistics in a row's thread, two CTAs to an SM, the caches cut into runs.  What 8 bits change:
+//  * K is multiplied as it is (kind::f8f6f4).  Q goes as two e4m3 terms of a row scale that is a power of two: bf16's 8 bits are
+//    4 + 4, so nothing is lost but what is below 2^-18 of a row's largest.  Twice the products at twice bf16's rate, and half the bytes.
+//  * V is made fp16 (exact) by a warp of its own on the way, since P in e4m3 would not do: P goes as fp16, whose 11 bits are
+//    more than bf16's.  Converting V costs a cvt for two values; splitting P into two terms would cost four for two of as many.
+//  * A block's scale of K multiplies its scores in the softmax's own multiply-add.  Its scale of V is part of the weight: m is the
+//    maximum of S + log2 vs, so the weight w = 2^(S + log2 vs - m) fits fp16 whatever the scales, and the row's sum adds w / vs.  Scales
+//    of V count relative to one of them, so that neither sum leaves fp32.
+// Weights are 2^7 times as large (at most 2^15 with a maximum that lags by 2^8), so that fp16 holds them to 2^-31 of the largest.
+// The tree's own rows are bf16 and the first tile of a sequence's first run: their products are bf16's, with Q as it came in the columns
+// that O will take, and their K and V in the places of the first two fp16 tiles of V.
+constexpr int A8THREADS = 256;  // 4 softmax warps, copies, MMAs of S, MMAs of P . V, V to fp16
+constexpr int BLK = KT * 128;   // 64 rows x 64 columns of 16 bits
+constexpr float kShift = 7.f;
+constexpr int A_S = 0, A_P = 64, A_Q = 96, A_O = 128, A_COLS = 256;  // tensor memory columns: S, P, Q's upper terms, O
+
 template <int D>
-__global__ void __launch_bounds__(128) attend8_kernel(AttendFp8Args f) {
-  constexpr int V = D / 32;
-  const AttendArgs& a = f.a;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= (long long)a.S * a.n * a.Hq) return;
-  const long long tok = row / a.Hq;
-  const int head = (int)(row % a.Hq), s = (int)(tok / a.n), node = (int)(tok % a.n), kvh = head / a.g;
-  int len = a.cache_len[s];
-  if (len < 0 || len > a.max_len || (long long)len > ((long long)a.max_pages << a.page_shift)) {
-    if (lane == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
-    len = 0;
+struct Attend8Smem {
+  static constexpr int UNITS = D == 128 ? 7 : 12;   // tiles of K and V in e4m3, by turns, in the ring
+  static constexpr int TILE8 = KT * D, TILE16 = KT * D * 2;
+  static constexpr int OFF_V16 = 128 * D;            // after Q's lower terms
+  static constexpr int OFF_RING = OFF_V16 + 2 * TILE16;
+  static constexpr int OFF_MISC = OFF_RING + UNITS * TILE8;
+  static constexpr int BYTES = OFF_MISC + 1408;
+  static_assert(BYTES <= 228 * 1024 / 2 - 1024, "two to an SM");
+  static constexpr uint32_t DESC_HI = D == 128 ? kDescHi : (512u >> 4) | 1u << 14 | 4u << 29;  // 128- or 64-byte rows, swizzled
+  // byte offset of 16-byte chunk `chunk` of row `row` of a tile of D-byte rows
+  static __device__ __forceinline__ uint32_t off8(int row, int chunk) {
+    return D == 128 ? tile_off(row, chunk, 128) : (uint32_t)(row * 64 + ((chunk ^ (row >> 1 & 3)) << 4));
   }
-  float q[V], o[V], m = -INFINITY, l = 0.f;
-  for (int v = 0; v < V; ++v) q[v] = bf16f(a.q[tok * a.ldq + head * D + lane * V + v]), o[v] = 0.f;
-  auto add = [&](const float (&k)[V], const float (&val)[V]) {
-    float d = 0.f;
-    for (int v = 0; v < V; ++v) d = fmaf(q[v], k[v], d);
-    const float x = warp_sum(d) * a.scale_log2, to = fmaxf(m, x), ref = to == -INFINITY ? 0.f : to;
-    const float g = exp2_sfu(m - ref), p = exp2_sfu(x - ref);
-    l = l * g + p, m = to;
-    for (int v = 0; v < V; ++v) o[v] = fmaf(p, val[v], o[v] * g);
-  };
-  for (int i = 0; i < len; ++i) {
-    const int pg = a.table[(long long)s * a.max_pages + (i >> a.page_shift)], r = i & ((1 << a.page_shift) - 1);
-    if (pg < 0 || pg >= a.n_pages) {
-      if (lane == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
-      continue;
-    }
-    const long long at = (((long long)pg * a.Hkv + kvh) << a.page_shift) + r, sc = at >> f.block_shift;
-    const float ks = f.ks[sc], vs = f.vs[sc];
-    if (!good_scale(ks) || !good_scale(vs)) {
-      if (lane == 0) flag(a.status, SSM_STATUS_SCALE);
-      continue;
-    }
-    float k[V], v[V];
-    for (int j = 0; j < V; j += 2) {
-      const float2 x = f16x2_f32(e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(f.kp + at * D + lane * V + j)));
-      const float2 y = f16x2_f32(e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(f.vp + at * D + lane * V + j)));
-      k[j] = x.x * ks, k[j + 1] = x.y * ks, v[j] = y.x * vs, v[j + 1] = y.y * vs;
-    }
-    add(k, v);
-  }
-  for (int u = node, hops = 0; u >= 0 && hops < a.n; ++hops) {
-    float k[V], v[V];
-    const long long at = (long long)s * a.n + u;
-    for (int j = 0; j < V; ++j) k[j] = bf16f(a.k[at * a.ldk + kvh * D + lane * V + j]), v[j] = bf16f(a.v[at * a.ldv + kvh * D + lane * V + j]);
-    add(k, v);
-    const int p = u > 0 ? a.layout[(long long)s * a.n + u].parent : -1;
-    if (u > 0 && (p < 0 || p >= u)) {
-      if (lane == 0) flag(a.status, SSM_STATUS_BAD_LAYOUT);
-      break;
-    }
-    u = p;
-  }
-  const float inv = 1.f / l;
-  for (int j = 0; j < V; j += 2)
-    *reinterpret_cast<uint32_t*>(a.o + tok * a.ldo + head * D + lane * V + j) = pack_bf16x2(o[j] * inv, o[j + 1] * inv);
+};
+struct TileInfo {  // of each 8 keys: scale of k, log2 of the scale of v and its inverse, relative to the run's; which keys there are
+  float ks[8], lv[8], rv[8];
+  unsigned long long mask;
+  unsigned long long pad;
+};
+struct Attend8Misc {
+  TileInfo info[4];            // of tile i, at i % 4
+  unsigned long long anc[64];  // ancestors and self of each node
+  unsigned long long full[12], free_[12], v16_full[2], v16_free[2], info_full[4], q_full, s_full, s_free, p_full, o_done, tree_full, drain[2];
+  SplitScratch split;
+  unsigned int odd[2];         // tree rows with a value of v that is not finite
+  uint32_t tmem;
+  int stop;
+  float v0;                    // what the run's scales of v are relative to
+};
+static_assert(sizeof(Attend8Misc) <= 1408, "space");
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {  // fp16 x fp16 -> fp32
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-
-// Commit.  A cluster of 8 CTAs for each sequence, a warp for each block of tokens of a layer, head and K or V: the largest of its new
-// rows gives the scale that they need, the block takes that or its own, rows that it holds are rounded again if it grew.  The
-// sequence's length is written by one of the CTAs once all eight have read it, so len_out may be cache_len.
-constexpr int CCTAS = 8, CTHREADS = 512;
-
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ float least_scale(uint32_t most) {  // of a largest magnitude's bits: 448 is 1.75 * 2^8
   const int e = (int)(most >> 23) - 127 - 8 + ((most & 0x7fffffu) > 0x600000u);
   return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
@@ -84,6 +75,512 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {  // |x|, 0 where it i
 __device__ __forceinline__ float nan_unless_finite(float x) {
   return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x;
 }
+
+template <int D>
+__global__ void __launch_bounds__(A8THREADS, 2)
+    attend8_kernel(const __grid_constant__ CUtensorMap tkp, const __grid_constant__ CUtensorMap tkt,
+                   const __grid_constant__ CUtensorMap tvt, AttendFp8Args f) {
+  using Sh = Attend8Smem<D>;
+  constexpr int DB = D / 64, UNITS = Sh::UNITS;
+  const AttendArgs& a = f.a;
+  extern __shared__ __align__(1024) unsigned char smem[];  // (there is no room to move it: where it is not aligned, nothing runs)
+  const uint32_t sb = smem_u32(smem);
+  Attend8Misc* ms = reinterpret_cast<Attend8Misc*>(smem + Sh::OFF_MISC);
+  volatile int* stop = &ms->stop;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int rows = a.n * a.g, rt = (rows + 127) / 128;
+  const int r0 = (blockIdx.x % rt) * 128, run = blockIdx.x / rt, kvh = blockIdx.y;
+  if (smem_u32(smem) & 1023u) {
+    grid_dependency_wait();  // no grid ends before the one that it depends on
+    if (tid == 0) flag(a.status, SSM_STATUS_TIMEOUT);
+    if (tid == 0 && run < a.S && a.max_runs > 0) a.runs[run] = make_int2(0, 1);  // nothing to join
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < UNITS; ++i) {
+      mbar_init(smem_u32(&ms->full[i]), 1);
+      mbar_init(smem_u32(&ms->free_[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ms->v16_full[i]), 1);
+      mbar_init(smem_u32(&ms->v16_free[i]), 1);
+      mbar_init(smem_u32(&ms->drain[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&ms->info_full[i]), 1);
+    mbar_init(smem_u32(&ms->q_full), 4);
+    mbar_init(smem_u32(&ms->s_full), 1);
+    mbar_init(smem_u32(&ms->s_free), 4);
+    mbar_init(smem_u32(&ms->p_full), 4);
+    mbar_init(smem_u32(&ms->o_done), 1);
+    mbar_init(smem_u32(&ms->tree_full), 1);
+    ms->stop = 0;
+    ms->odd[0] = ms->odd[1] = 0;
+    fence_barrier_init();
+  }
+  grid_dependency_wait();  // what the stream's kernels before this one write
+  // (not before that: a kernel that lets this one's blocks in before it has its own tensor memory would wait for them for ever)
+  if (warp == 5) tmem_alloc_warp(smem_u32(&ms->tmem), A_COLS);
+  int s = run, sp = 0, tps = 1 << 30, splits = 1;
+  bool any = true;
+  if (a.max_runs > 0) {
+    int* tiles = reinterpret_cast<int*>(smem);  // space not in use yet: of Q's lower terms
+    int first;
+    tps = choose_split<A8THREADS>(a, a.Hkv * rt, tiles, &ms->split);
+    any = find_run(a.S, tiles, tps, run, s, first, splits);
+    sp = any ? run - first : 0;
+    if (any && sp == 0 && kvh == 0 && r0 == 0 && tid == 0) a.runs[s] = make_int2(first, splits);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  launch_dependents();  // (not before the tensor memory is there: the next grid's blocks may take some before they wait for this one)
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ms->tmem, 0);
+  if (!any) {
+    if (warp == 5) tmem_free_warp(tmem, A_COLS);
+    return;
+  }
+  int len = __shfl_sync(0xffffffffu, cached_rows(a, s), 0);
+  if (len < 0) {
+    if (sp == 0 && kvh == 0 && r0 == 0 && tid == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
+    len = 0;
+  }
+  const int ct = (len + KT - 1) / KT;  // tiles of the cache; the tree's is before them
+  const int i0 = sp * tps, n = min(ct + 1 - i0, tps), has_tree = sp == 0;
+  // tile i of the run is cache tile i0 + i - 1, at turn 2 (i - has_tree) (K) and the next (V) of the ring, and its V at i % 2 in fp16
+
+  if (warp < 4) {
+    const int row = r0 + tid;  // this thread's
+    const int node = row < rows ? row / a.g : 0, qh = row < rows ? row % a.g : 0;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    float qc;  // this row's scale of Q, times scale log2 e
+    {  // q (zero beyond the last row): upper terms to tensor memory, lower terms to shared memory
+      uint4 x[D / 8];
+      uint32_t most = 0;
+      const uint4* q = reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + node) * a.ldq + (kvh * a.g + qh) * D);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) x[c] = row < rows ? q[c] : make_uint4(0, 0, 0, 0);
+      if (has_tree) {  // and as it is where O will be
+#pragma unroll
+        for (int c = 0; c < D / 8; c += 2) {
+          const uint32_t u[8] = {x[c].x, x[c].y, x[c].z, x[c].w, x[c + 1].x, x[c + 1].y, x[c + 1].z, x[c + 1].w};
+          tmem_st8(tmem + A_O + lanes + 4 * c, u);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = max(most, max(finite_bits(bf16_lo(w[j])), finite_bits(bf16_hi(w[j]))));
+      }
+      const float qs = least_scale(most), inv = 1.f / qs;
+      qc = qs * a.scale_log2;
+#pragma unroll
+      for (int c = 0; c < D / 8; c += 4) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 y = x[c + j / 2];
+          const uint32_t w[2] = {j & 1 ? y.z : y.x, j & 1 ? y.w : y.y};
+          hi[j] = lo[j] = 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float p0 = nan_unless_finite(bf16_lo(w[k])) * inv, p1 = nan_unless_finite(bf16_hi(w[k])) * inv;
+            const uint32_t h = f32_e4m3x2(p0, p1);
+            const float2 back = f16x2_f32(e4m3x2_f16x2(h));
+            hi[j] |= h << 16 * k, lo[j] |= f32_e4m3x2(p0 - back.x, p1 - back.y) << 16 * k;
+          }
+        }
+        tmem_st8(tmem + A_Q + lanes + 2 * c, hi);
+        *reinterpret_cast<uint4*>(smem + Sh::off8(tid, c / 2)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(smem + Sh::off8(tid, c / 2 + 1)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
+    }
+    if (has_tree && warp == 0) ancestor_words(a, s, ms->anc, kvh == 0 && r0 == 0);
+
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const bool tree = has_tree && i == 0;
+      ok = wait_bar(&ms->info_full[i & 3], (i >> 2) & 1, stop) && wait_bar(&ms->s_full, i & 1, stop);
+      if (!ok) break;
+      tc_fence_after();
+      float sv[KT];
+#pragma unroll
+      for (int c = 0; c < KT; c += 16) tmem_ld16_async(tmem + A_S + lanes + c, reinterpret_cast<float(&)[16]>(sv[c]));
+#pragma unroll
+      for (int c = 0; c < KT; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->s_free));
+      const TileInfo* in = &ms->info[i & 3];
+      unsigned long long there = in->mask;
+      if (tree) {  // rows of V that are not to be multiplied, and values that are not finite, become zeros
+        ok = wait_bar(&ms->tree_full, 0, stop);
+        unsigned char* vt = smem + Sh::OFF_V16;
+        // (a warp that gives up here still meets the others below)
+#pragma unroll 1
+        for (int k = ok ? tid : KT * D / 8; k < KT * D / 8; k += 128) {
+          const int vr = k / (D / 8), c = k % (D / 8);
+          uint4* v = reinterpret_cast<uint4*>(vt + (c >> 3) * BLK + tile_off(vr, c & 7, 128));
+          if (!(there >> vr & 1)) {
+            *v = make_uint4(0, 0, 0, 0);
+          } else {
+            const uint4 x = *v;
+            const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+            if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *v = y, atomicOr(&ms->odd[vr >> 5], 1u << (vr & 31));
+          }
+        }
+        fence_async_smem();
+        named_sync(1, 128);  // (and: the ancestor words are there)
+        if (!ok) break;
+        there &= ms->anc[node];
+      }
+      if (there != ~0ull) {
+#pragma unroll
+        for (int j = 0; j < KT; ++j)
+          if (!((j < 32 ? (uint32_t)there : (uint32_t)(there >> 32)) >> (j & 31) & 1)) sv[j] = -INFINITY;
+      }
+      const float by = tree ? a.scale_log2 : qc;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float* v = sv + 8 * g;
+        const float top = fmaxf(max3f(max3f(v[0], v[1], v[2]), v[3], v[4]), max3f(v[5], v[6], v[7]));
+        mx = fmaxf(mx, fmaf(top, fmaxf(in->ks[g] * by, 1e-37f), in->lv[g]));
+      }
+      if (i == 0) {
+        m = mx;
+      } else {  // P . V of the last tile has read its P
+        ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (i > 0 && __any_sync(0xffffffffu, mx > m + 8.f)) {
+        const float to = fmaxf(m, mx), g = to == m ? 1.f : exp2_sfu(m - to);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          uint32_t u[8];
+          tmem_ld16_async(tmem + A_O + lanes + c, o);
+          tmem_wait_ld16(o);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(o[8 * half + j] * g);
+            tmem_st8(tmem + A_O + lanes + c + 8 * half, u);
+          }
+        }
+        l *= g, m = to;
+      }
+      const float ref = (m == -INFINITY ? 0.f : m) - kShift;  // minus infinity: a row none of whose keys so far counts
+      const unsigned long long one2 = pack2(1.f, 1.f);
+      unsigned long long l2 = pack2(l, 0.f);
+      const uint32_t pt = tmem + A_P + lanes;
+#pragma unroll
+      for (int c = 0; c < KT; c += 16) {
+        uint32_t u[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int g = c / 8 + h;
+          const float sc = fmaxf(in->ks[g] * by, 1e-37f), off = in->lv[g] - ref;
+          const unsigned long long sc2 = pack2(sc, sc), off2 = pack2(off, off);
+          unsigned long long sum2 = 0ull;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 e = unpack2(ffma2(pack2(sv[8 * g + 2 * j], sv[8 * g + 2 * j + 1]), sc2, off2));
+            const float p0 = exp2_sfu(e.x), p1 = exp2_sfu(e.y);
+            sum2 = ffma2(one2, pack2(p0, p1), sum2);
+            u[4 * h + j] = tree ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+          }
+          l2 = ffma2(sum2, pack2(in->rv[g], in->rv[g]), l2);
+        }
+        tmem_st8(pt + c / 2, u);
+      }
+      l = pair_sum(l2);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->p_full));
+    }
+    ok = ok && wait_bar(&ms->o_done, (n - 1) & 1, stop);
+    // a warp that gives up still takes part in the barrier that others may be waiting at
+    if (!ok) asm volatile("bar.arrive 1, 128;\n" ::: "memory");
+    tc_fence_after();
+    if (ok) {
+      const unsigned long long odd = has_tree ? (ms->odd[0] | (unsigned long long)ms->odd[1] << 32) & ms->anc[node] : 0ull;
+      const long long tok = (long long)s * a.n + node;
+      const int head = kvh * a.g + qh;
+      const float inv = 1.f / l, v0 = ms->v0;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float o[16];
+        __syncwarp();
+        tmem_ld16_async(tmem + A_O + lanes + c, o);
+        tmem_wait_ld16(o);
+#pragma unroll 1
+        for (unsigned long long todo = odd; todo; todo &= todo - 1) {  // not finite whatever its weight
+          const uint32_t* v = reinterpret_cast<const uint32_t*>(
+              a.v + ((long long)s * a.n + __ffsll((long long)todo) - 1) * a.ldv + kvh * D + c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t x = v[j], out = x ^ finite_or_zero(x);
+            if (out & 0xffffu) o[2 * j] += bf16_lo(x);
+            if (out & 0xffff0000u) o[2 * j + 1] += bf16_hi(x);
+          }
+        }
+        if (row >= rows) {
+        } else if (splits == 1) {  // (the run has the tree: v0 is 1)
+          uint32_t u[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+          uint4* p = reinterpret_cast<uint4*>(a.o + tok * a.ldo + head * D + c);
+          p[0] = make_uint4(u[0], u[1], u[2], u[3]), p[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        } else {
+          float4* p = reinterpret_cast<float4*>(a.part + (((long long)run * a.Hkv + kvh) * rows + row) * D + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = make_float4(o[4 * j] * v0, o[4 * j + 1] * v0, o[4 * j + 2] * v0, o[4 * j + 3] * v0);
+        }
+      }
+      if (row < rows && splits > 1) a.part_ml[((long long)run * a.Hkv + kvh) * rows + row] = make_float2(m, l);
+    }
+  } else if (warp == 4) {
+    // ---- copies: lane b the b-th page piece of a tile ----
+    const int32_t* table = a.table + (long long)s * a.max_pages;
+    const int shift = min(a.page_shift, 6), box = 1 << shift, pieces = KT >> shift, pmask = (1 << a.page_shift) - 1;
+    auto lookup = [&](int ti) {  // the piece's page; -1: no such row; -2: out of range
+      const int at = ti * KT + lane * box;
+      if (lane >= pieces || ti >= ct || at >= len) return -1;
+      const int pg = table[at >> a.page_shift];
+      return pg < 0 || pg >= a.n_pages ? -2 : pg;
+    };
+    int issued = 0, pg = lookup(i0 + has_tree - 1);
+    if (has_tree) {  // the tree's V and K, in the places of the first two fp16 tiles
+      const uint32_t full = smem_u32(&ms->tree_full);
+      if (lane == 0) mbar_arrive_expect_tx(full, 2 * Sh::TILE16);
+      __syncwarp();
+      if (lane < 2 * DB)
+        tma_load_2d(sb + Sh::OFF_V16 + lane * BLK, lane < DB ? &tvt : &tkt, kvh * D + lane % DB * 64, s * a.n, full);
+    }
+#pragma unroll 1
+    for (int i = has_tree; i < n; ++i) {
+      const int ti = i0 + i - 1, mine = pg;
+      pg = lookup(ti + 1);
+      if (__any_sync(0xffffffffu, mine == -2) && lane == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine >= 0)) * box * D;
+      const int crd = ((mine * a.Hkv + kvh) << a.page_shift) + ((ti * KT + lane * box) & pmask);
+      bool ok = true;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int use = 2 * (i - has_tree) + kv, unit = use % UNITS;
+        const uint32_t full = smem_u32(&ms->full[unit]), dst = sb + Sh::OFF_RING + unit * Sh::TILE8 + lane * box * D;
+        if (use >= UNITS) ok = ok && wait_bar(&ms->free_[unit], (use / UNITS - 1) & 1, stop);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        __syncwarp();
+        if (mine >= 0) {
+          if (kv == 0)
+            tma_load_2d(dst, &tkp, 0, crd, full);
+          else
+            bulk_load(dst, f.vp + (long long)crd * D, box * D, full);
+        }
+        issued = use + 1;
+      }
+      if (!ok) break;
+    }
+    // copies land before the shared memory is given up, whoever gives up, and when (else they have, by the time of the last tile)
+    if (lane == 0) {
+      if (has_tree) mbar_wait(smem_u32(&ms->tree_full), 0);
+      for (int k = max(0, issued - UNITS); k < issued; ++k) mbar_wait(smem_u32(&ms->full[k % UNITS]), (k / UNITS) & 1);
+    }
+  } else if (warp == 7) {
+    // ---- what a tile's keys are (lanes 0 .. 7 of K, 8 .. 15 of V, each of 8 keys), and its V to fp16 ----
+    const int32_t* table = a.table + (long long)s * a.max_pages;
+    const int grp = lane & 7, is_v = lane >> 3 & 1, pmask = (1 << a.page_shift) - 1;
+    auto page_of = [&](int ti) {  // -1: no such rows, or their page is out of range
+      const int at = ti * KT + grp * 8;
+      if (lane >= 16 || ti >= ct || at >= len) return -1;
+      const int pg = table[at >> a.page_shift];
+      return pg < 0 || pg >= a.n_pages ? -1 : pg;
+    };
+    auto scale_of = [&](int ti, int pg) {
+      if (pg < 0) return 1.f;
+      const long long at = (((long long)pg * a.Hkv + kvh) << a.page_shift) + ((ti * KT + grp * 8) & pmask);
+      return (is_v ? f.vs : f.ks)[at >> f.block_shift];
+    };
+    const int t0 = i0 + has_tree - 1;  // the run's first tile of the cache
+    int pg = page_of(t0);
+    float sc = scale_of(t0, pg), v0 = 1.f;
+    int pg1 = page_of(t0 + 1);
+    if (has_tree) {
+      TileInfo* in = &ms->info[0];
+      if (lane < 8) in->ks[lane] = 1.f, in->lv[lane] = 0.f, in->rv[lane] = 1.f;
+      if (lane == 0) in->mask = a.n < 64 ? (1ull << a.n) - 1 : ~0ull, ms->v0 = 1.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->info_full[0]));
+    }
+#pragma unroll 1
+    for (int i = has_tree; i < n; ++i) {
+      const int ti = i0 + i - 1;
+      const bool good = good_scale(sc);
+      if (__any_sync(0xffffffffu, pg >= 0 && !good) && lane == 0) flag(a.status, SSM_STATUS_SCALE);
+      const unsigned int fine = __ballot_sync(0xffffffffu, pg >= 0 && good);
+      const unsigned int groups = fine & fine >> 8 & 255u;
+      if (!good) sc = 1.f;
+      if (i == 0) {  // what scales of v are relative to: the largest of the first tile, as a power of two
+        const unsigned int top = __reduce_max_sync(0xffffffffu, lane >= 8 && lane < 16 && groups >> grp & 1 ? __float_as_uint(sc) & 0x7f800000u : 0u);
+        v0 = top ? __uint_as_float(top) : 1.f;
+        if (lane == 0) ms->v0 = v0;
+      }
+      const int left = min(max(len - ti * KT - 8 * grp, 0), 8);
+      const unsigned long long keys = lane < 8 && groups >> grp & 1 ? (unsigned long long)((1u << left) - 1) << 8 * grp : 0ull;
+      const unsigned long long mask = (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(keys >> 32)) << 32 |
+                                      __reduce_or_sync(0xffffffffu, (uint32_t)keys);
+      TileInfo* in = &ms->info[i & 3];
+      if (lane < 8) {
+        in->ks[grp] = sc;
+      } else if (lane < 16) {
+        const float rel = fminf(fmaxf(sc / v0, 0x1p-120f), 0x1p120f);
+        in->lv[grp] = log2f(rel), in->rv[grp] = 1.f / rel;
+      }
+      if (lane == 0) in->mask = mask;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->info_full[i & 3]));
+      pg = pg1, sc = scale_of(ti + 1, pg), pg1 = page_of(ti + 2);
+
+      const int use = 2 * (i - has_tree) + 1, unit = use % UNITS, at = i & 1, k = i >> 1;
+      const bool first = k == 0 && !(at && has_tree);  // nobody has had this place (of the tree's, S has read K, P . V V)
+      bool ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop);
+      ok = ok && (first || wait_bar(&ms->v16_free[at], (at && has_tree ? k : k - 1) & 1, stop));
+      if (!ok) break;
+      const unsigned char* src = smem + Sh::OFF_RING + unit * Sh::TILE8;
+      unsigned char* dst = smem + Sh::OFF_V16 + at * Sh::TILE16;
+      constexpr int PER = D / 8, STEP = 32 / PER;  // pieces of 8 values in a row, rows at a time
+      const int piece = lane % PER;
+#pragma unroll 8
+      for (int r = lane / PER; r < KT; r += STEP) {
+        uint2 x = *reinterpret_cast<const uint2*>(src + r * D + piece * 8);
+        if (!(mask >> r & 1)) x = make_uint2(0, 0);
+        *reinterpret_cast<uint4*>(dst + (piece >> 3) * BLK + tile_off(r, piece & 7, 128)) =
+            make_uint4(e4m3x2_f16x2(x.x & 0xffffu), e4m3x2_f16x2(x.x >> 16), e4m3x2_f16x2(x.y & 0xffffu), e4m3x2_f16x2(x.y >> 16));
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&ms->free_[unit]));
+        mbar_arrive(smem_u32(&ms->v16_full[at]));
+      }
+    }
+  } else {
+    // ---- MMAs: one warp those of S, the other P . V, each behind its own waits ----
+    const bool leader = elect_one();
+    bool ok = true;
+    if (warp == 5) {
+      constexpr uint32_t id8 = (1u << 4) | (uint32_t)(KT >> 3) << 17 | (128u >> 4) << 24;  // e4m3 x e4m3 -> fp32
+      constexpr uint32_t id_t = idesc_major(128, KT, false, false);
+      ok = wait_bar(&ms->q_full, 0, stop);
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const bool tree = has_tree && i == 0;
+        const int use = 2 * (i - has_tree), unit = use % UNITS;
+        ok = tree ? wait_bar(&ms->tree_full, 0, stop) : wait_bar(&ms->full[unit], (use / UNITS) & 1, stop);
+        ok = ok && (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          if (tree) {
+            const uint32_t kd = desc_lo(sb + Sh::OFF_V16 + Sh::TILE16, 16);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ts<id_t>(tmem + A_S, tmem + A_O + k * 8, kd + (((k >> 2) * BLK + (k & 3) * 32) >> 4), k > 0);
+            mma_commit(smem_u32(&ms->s_full));
+            mma_commit(smem_u32(&ms->v16_free[1]));
+          } else {
+            const uint32_t qd = desc_lo(sb, 16), kd = desc_lo(sb + Sh::OFF_RING + unit * Sh::TILE8, 16);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              mma8_ts<id8, Sh::DESC_HI>(tmem + A_S, tmem + A_Q + k * 8, kd + k * 2, k > 0);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) mma8_ss<id8, Sh::DESC_HI>(tmem + A_S, qd + k * 2, kd + k * 2, true);
+            mma_commit(smem_u32(&ms->s_full));
+            mma_commit(smem_u32(&ms->free_[unit]));
+          }
+        }
+        __syncwarp();
+      }
+    } else {
+      constexpr uint32_t id_o = idesc_f16(128, D, true), id_t = idesc_major(128, D, false, true);
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const bool tree = has_tree && i == 0;
+        const int at = i & 1;
+        ok = tree ? wait_bar(&ms->tree_full, 0, stop)
+                  : wait_bar(&ms->v16_full[at], ((i >> 1) - (at == 0 ? has_tree : 0)) & 1, stop);
+        ok = ok && wait_bar(&ms->p_full, i & 1, stop);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t vd = desc_lo(sb + Sh::OFF_V16 + at * Sh::TILE16, BLK);
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k) {  // 16 keys: two groups of 8 rows
+            if (tree)
+              mma_ts<id_t>(tmem + A_O, tmem + A_P + k * 8, vd + k * (2048 >> 4), k > 0);
+            else
+              mma_ts<id_o>(tmem + A_O, tmem + A_P + k * 8, vd + k * (2048 >> 4), i + k > 0);
+          }
+          mma_commit(smem_u32(&ms->o_done));
+          mma_commit(smem_u32(&ms->v16_free[at]));
+        }
+        __syncwarp();
+      }
+    }
+    if (leader) {
+      mma_commit(smem_u32(&ms->drain[warp - 5]));
+      mbar_poll_ns(smem_u32(&ms->drain[warp - 5]), 0, kWaitLimitNs);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *stop) flag(a.status, SSM_STATUS_TIMEOUT);
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free_warp(tmem, A_COLS);
+  }
+}
+
+template <int D>
+cudaError_t run_attend8(const AttendFp8Args& f, const AttendPlan& p, cudaStream_t s) {
+  using Sh = Attend8Smem<D>;
+  const AttendArgs& a = f.a;
+  CUtensorMap m[3];
+  const long long page_rows = ((long long)a.n_pages * a.Hkv) << a.page_shift, cols = (long long)a.Hkv * D;
+  const int box = a.page_shift < 6 ? 1 << a.page_shift : KT;
+  // a call without cached rows reads no page: any matrix will do
+  const bool none = a.max_len == 0 || page_rows == 0;
+  if (!encode_byte_tiles(&m[0], none ? static_cast<const void*>(a.k) : f.kp, none ? 1 : page_rows, D, box) ||
+      !encode_tiles(&m[1], a.k, (long long)a.S * a.n, cols, a.ldk, KT) ||
+      !encode_tiles(&m[2], a.v, (long long)a.S * a.n, cols, a.ldv, KT))
+    return cudaErrorInvalidValue;
+  static bool done[64];
+  cudaError_t e = allow_smem(attend8_kernel<D>, Sh::BYTES, done);
+  if (e != cudaSuccess) return e;
+  e = launch_early(attend8_kernel<D>, dim3((unsigned)((p.max_runs ? p.max_runs : a.S) * p.row_tiles), (unsigned)a.Hkv), A8THREADS,
+                   Sh::BYTES, s, m[0], m[1], m[2], f);
+  return e != cudaSuccess || p.max_runs == 0 ? e : launch_attend_join(a, s);
+}
+static_assert(2 * 2 * kSMs * 4 <= 128 * 64, "the lengths stand in the space of Q's lower terms");
+
+// Commit.  A cluster of 8 CTAs for each sequence, a warp for each block of tokens of a layer, head and K or V: the largest of its new
+// rows gives the scale that they need, the block takes that or its own, rows that it holds are rounded again if it grew.  The
+// sequence's length is written by one of the CTAs once all eight have read it, so len_out may be cache_len.
+constexpr int CCTAS = 8, CTHREADS = 512;
 
 template <int D>
 __global__ void __cluster_dims__(CCTAS, 1, 1) __launch_bounds__(CTHREADS) kv_commit8_kernel(KvCommitFp8Args f) {
@@ -209,17 +706,16 @@ __global__ void __cluster_dims__(CCTAS, 1, 1) __launch_bounds__(CTHREADS) kv_com
 
 }  // namespace
 
-size_t tree_attention_fp8_workspace_bytes(int S, int n, int Hq, int Hkv, int D, int max_len) { return 256; }
+size_t tree_attention_fp8_workspace_bytes(int S, int n, int Hq, int Hkv, int D, int max_len) {
+  return attend_workspace_bytes(plan_attend(S, n, Hq, Hkv, max_len), S, n, Hq, Hkv, D);
+}
 
-cudaError_t launch_tree_attention_fp8(const AttendFp8Args& f, void* workspace, cudaStream_t s) {
-  if (f.a.S == 0) return cudaSuccess;
-  const long long rows = (long long)f.a.S * f.a.n * f.a.Hq;
-  const unsigned grid = (unsigned)((rows + 3) / 4);
-  if (f.a.D == 64)
-    attend8_kernel<64><<<grid, 128, 0, s>>>(f);
-  else
-    attend8_kernel<128><<<grid, 128, 0, s>>>(f);
-  return cudaGetLastError();
+cudaError_t launch_tree_attention_fp8(const AttendFp8Args& args, void* workspace, cudaStream_t s) {
+  if (args.a.S == 0) return cudaSuccess;
+  AttendFp8Args f = args;
+  const AttendPlan p = plan_attend(f.a.S, f.a.n, f.a.Hq, f.a.Hkv, f.a.max_len);
+  lay_workspace(f.a, p, workspace);
+  return f.a.D == 64 ? run_attend8<64>(f, p, s) : run_attend8<128>(f, p, s);
 }
 
 cudaError_t launch_kv_commit_fp8(const KvCommitFp8Args& f, cudaStream_t s) {
