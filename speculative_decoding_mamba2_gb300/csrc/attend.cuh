@@ -23,12 +23,12 @@ __device__ __forceinline__ int cached_rows(const AttendArgs& a, int s) {
 // alone, eight ragged caches of up to 8117 rows took 50 us and four of up to 40009 rows, 101 us.)
 constexpr int CANDIDATES = 189;
 struct SplitScratch {        // of each warp: tiles of the longest sequence, the least estimate
-  int most[8];
-  unsigned int least[8];
+  int most[12];
+  unsigned int least[12];
 };
 template <int THREADS>
 __device__ __forceinline__ int choose_split(const AttendArgs& a, int per, int* tiles, SplitScratch* ms) {
-  static_assert(THREADS >= CANDIDATES && THREADS <= 256, "a thread to each");
+  static_assert(THREADS >= CANDIDATES && THREADS <= 384, "a thread to each");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int most = 0;
   for (int s = tid; s < a.S; s += THREADS) most = max(most, tiles[s] = (max(cached_rows(a, s), 0) + KT - 1) / KT + 1);

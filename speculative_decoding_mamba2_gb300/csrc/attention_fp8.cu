@@ -1,5 +1,7 @@
 // Attention of a draft tree's nodes over an 8-bit paged cache and their ancestors, and the commit of the accepted path into it
 // (ssm_attention.h).
+#include <type_traits>
+
 #include "attend.cuh"
 #include "decode.cuh"
 
@@ -19,19 +21,22 @@ namespace {
 // Weights are 2^7 times as large (at most 2^15 with a maximum that lags by 2^8), so that fp16 holds them to 2^-31 of the largest.
 // The tree's own rows are bf16 and the first tile of a sequence's first run: their products are bf16's, with Q as it came in the columns
 // that O will take, and their K and V in the places of the first two fp16 tiles of V.
-constexpr int A8THREADS = 256;  // 4 softmax warps, copies, MMAs of S, MMAs of P . V, V to fp16
+constexpr int A8THREADS = 384;  // 4 softmax warps; copies, MMAs of S, MMAs of P . V, what keys a tile has; 4 warps that make V fp16
+// registers of the three groups of four warps: the block has 384 x 80
+constexpr int R_SOFTMAX = 136, R_MMA = 48, R_CONVERT = 56;
+static_assert(R_SOFTMAX + R_MMA + R_CONVERT == 3 * 80, "what the block is launched with");
 constexpr int BLK = KT * 128;   // 64 rows x 64 columns of 16 bits
 constexpr float kShift = 7.f;
 constexpr int A_S = 0, A_P = 64, A_Q = 96, A_O = 128, A_COLS = 256;  // tensor memory columns: S, P, Q's upper terms, O
 
 template <int D>
 struct Attend8Smem {
-  static constexpr int UNITS = D == 128 ? 7 : 12;   // tiles of K and V in e4m3, by turns, in the ring
+  static constexpr int KU = D == 128 ? 4 : 6, VU = D == 128 ? 3 : 6;  // tiles of K and of V in e4m3, in rings
   static constexpr int TILE8 = KT * D, TILE16 = KT * D * 2;
   static constexpr int OFF_V16 = 128 * D;            // after Q's lower terms
-  static constexpr int OFF_RING = OFF_V16 + 2 * TILE16;
-  static constexpr int OFF_MISC = OFF_RING + UNITS * TILE8;
-  static constexpr int BYTES = OFF_MISC + 1408;
+  static constexpr int OFF_K = OFF_V16 + 2 * TILE16, OFF_V = OFF_K + KU * TILE8;
+  static constexpr int OFF_MISC = OFF_V + VU * TILE8;
+  static constexpr int BYTES = OFF_MISC + 2048;
   static_assert(BYTES <= 228 * 1024 / 2 - 1024, "two to an SM");
   static constexpr uint32_t DESC_HI = D == 128 ? kDescHi : (512u >> 4) | 1u << 14 | 4u << 29;  // 128- or 64-byte rows, swizzled
   // byte offset of 16-byte chunk `chunk` of row `row` of a tile of D-byte rows
@@ -39,22 +44,24 @@ struct Attend8Smem {
     return D == 128 ? tile_off(row, chunk, 128) : (uint32_t)(row * 64 + ((chunk ^ (row >> 1 & 3)) << 4));
   }
 };
+constexpr int INFOS = 8;  // a tile of V is copied once five tiles before are done with
 struct TileInfo {  // of each 8 keys: scale of k, log2 of the scale of v and its inverse, relative to the run's; which keys there are
   float ks[8], lv[8], rv[8];
   unsigned long long mask;
   unsigned long long pad;
 };
 struct Attend8Misc {
-  TileInfo info[4];            // of tile i, at i % 4
+  TileInfo info[INFOS];        // of tile i, at i % INFOS
   unsigned long long anc[64];  // ancestors and self of each node
-  unsigned long long full[12], free_[12], v16_full[2], v16_free[2], info_full[4], q_full, s_full, s_free, p_full, o_done, tree_full, drain[2];
+  unsigned long long k_full[6], k_free[6], v_full[6], v_free[6], v16_full[2], v16_free[2], info_full[INFOS], q_full, s_full, s_free, p_full, o_done, tree_full, drain[2];
   SplitScratch split;
   unsigned int odd[2];         // tree rows with a value of v that is not finite
   uint32_t tmem;
   int stop;
   float v0;                    // what the run's scales of v are relative to
 };
-static_assert(sizeof(Attend8Misc) <= 1408, "space");
+static_assert(sizeof(Attend8Misc) <= 2048, "space");
+static_assert(Attend8Smem<64>::VU + 2 <= INFOS && Attend8Smem<128>::VU + 2 <= INFOS, "a place is free when its next tile is there");
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {  // fp16 x fp16 -> fp32
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -81,7 +88,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     attend8_kernel(const __grid_constant__ CUtensorMap tkp, const __grid_constant__ CUtensorMap tkt,
                    const __grid_constant__ CUtensorMap tvt, AttendFp8Args f) {
   using Sh = Attend8Smem<D>;
-  constexpr int DB = D / 64, UNITS = Sh::UNITS;
+  constexpr int DB = D / 64, KU = Sh::KU, VU = Sh::VU;
   const AttendArgs& a = f.a;
   extern __shared__ __align__(1024) unsigned char smem[];  // (there is no room to move it: where it is not aligned, nothing runs)
   const uint32_t sb = smem_u32(smem);
@@ -97,16 +104,18 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < UNITS; ++i) {
-      mbar_init(smem_u32(&ms->full[i]), 1);
-      mbar_init(smem_u32(&ms->free_[i]), 1);
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(smem_u32(&ms->k_full[i]), 1);
+      mbar_init(smem_u32(&ms->k_free[i]), 1);
+      mbar_init(smem_u32(&ms->v_full[i]), 1);
+      mbar_init(smem_u32(&ms->v_free[i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ms->v16_full[i]), 1);
+      mbar_init(smem_u32(&ms->v16_full[i]), 4);
       mbar_init(smem_u32(&ms->v16_free[i]), 1);
       mbar_init(smem_u32(&ms->drain[i]), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&ms->info_full[i]), 1);
+    for (int i = 0; i < INFOS; ++i) mbar_init(smem_u32(&ms->info_full[i]), 1);
     mbar_init(smem_u32(&ms->q_full), 4);
     mbar_init(smem_u32(&ms->s_full), 1);
     mbar_init(smem_u32(&ms->s_free), 4);
@@ -146,53 +155,50 @@ __global__ void __launch_bounds__(A8THREADS, 2)
   }
   const int ct = (len + KT - 1) / KT;  // tiles of the cache; the tree's is before them
   const int i0 = sp * tps, n = min(ct + 1 - i0, tps), has_tree = sp == 0;
-  // tile i of the run is cache tile i0 + i - 1, at turn 2 (i - has_tree) (K) and the next (V) of the ring, and its V at i % 2 in fp16
+  // tile i of the run is cache tile i0 + i - 1, the (i - has_tree)-th of the rings; its V is at i % 2 in fp16
 
   if (warp < 4) {
+    take_registers<R_SOFTMAX>();
     const int row = r0 + tid;  // this thread's
     const int node = row < rows ? row / a.g : 0, qh = row < rows ? row % a.g : 0;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     float qc;  // this row's scale of Q, times scale log2 e
-    {  // q (zero beyond the last row): upper terms to tensor memory, lower terms to shared memory
-      uint4 x[D / 8];
+    {  // q (zero beyond the last row): upper terms to tensor memory, lower terms to shared memory; rolled up, since code that runs
+      // once is fetched from afar (unrolled, this took 4 us)
       uint32_t most = 0;
       const uint4* q = reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + node) * a.ldq + (kvh * a.g + qh) * D);
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) x[c] = row < rows ? q[c] : make_uint4(0, 0, 0, 0);
-      if (has_tree) {  // and as it is where O will be
-#pragma unroll
-        for (int c = 0; c < D / 8; c += 2) {
-          const uint32_t u[8] = {x[c].x, x[c].y, x[c].z, x[c].w, x[c + 1].x, x[c + 1].y, x[c + 1].z, x[c + 1].w};
-          tmem_st8(tmem + A_O + lanes + 4 * c, u);
-        }
-      }
-#pragma unroll
+      const bool some = row < rows;
+#pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
-        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        const uint4 x = some ? q[c] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) most = max(most, max(finite_bits(bf16_lo(w[j])), finite_bits(bf16_hi(w[j]))));
       }
       const float qs = least_scale(most), inv = 1.f / qs;
-      qc = qs * a.scale_log2;
-#pragma unroll
+      qc = fmaxf(qs * a.scale_log2, 0x1p-60f);  // (with ks at least 2^-66: their product is a normal number)
+#pragma unroll 1
       for (int c = 0; c < D / 8; c += 4) {
         uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 y = x[c + j / 2];
-          const uint32_t w[2] = {j & 1 ? y.z : y.x, j & 1 ? y.w : y.y};
-          hi[j] = lo[j] = 0;
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x = some ? q[c + 2 * h] : make_uint4(0, 0, 0, 0), y = some ? q[c + 2 * h + 1] : make_uint4(0, 0, 0, 0);
+          const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          if (has_tree) tmem_st8(tmem + A_O + lanes + 4 * (c + 2 * h), w);  // as it is where O will be
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float p0 = nan_unless_finite(bf16_lo(w[k])) * inv, p1 = nan_unless_finite(bf16_hi(w[k])) * inv;
-            const uint32_t h = f32_e4m3x2(p0, p1);
-            const float2 back = f16x2_f32(e4m3x2_f16x2(h));
-            hi[j] |= h << 16 * k, lo[j] |= f32_e4m3x2(p0 - back.x, p1 - back.y) << 16 * k;
+          for (int j = 0; j < 4; ++j) {
+            hi[4 * h + j] = lo[4 * h + j] = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float p0 = nan_unless_finite(bf16_lo(w[2 * j + k])) * inv, p1 = nan_unless_finite(bf16_hi(w[2 * j + k])) * inv;
+              const uint32_t top = f32_e4m3x2(p0, p1);
+              const float2 back = f16x2_f32(e4m3x2_f16x2(top));
+              hi[4 * h + j] |= top << 16 * k, lo[4 * h + j] |= f32_e4m3x2(p0 - back.x, p1 - back.y) << 16 * k;
+            }
           }
+          *reinterpret_cast<uint4*>(smem + Sh::off8(tid, c / 2 + h)) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
         }
         tmem_st8(tmem + A_Q + lanes + 2 * c, hi);
-        *reinterpret_cast<uint4*>(smem + Sh::off8(tid, c / 2)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4*>(smem + Sh::off8(tid, c / 2 + 1)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -202,12 +208,14 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     }
     if (has_tree && warp == 0) ancestor_words(a, s, ms->anc, kvh == 0 && r0 == 0);
 
+    // (a barrier that is past costs some 100 cycles to look at: it is looked at ahead, and awaited where it was not past yet)
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
+    bool ok = true, s_there = false, info_there = false;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const bool tree = has_tree && i == 0;
-      ok = wait_bar(&ms->info_full[i & 3], (i >> 2) & 1, stop) && wait_bar(&ms->s_full, i & 1, stop);
+      ok = __all_sync(0xffffffffu, s_there) || wait_bar(&ms->s_full, i & 1, stop);
+      ok = ok && (__all_sync(0xffffffffu, info_there) || wait_bar(&ms->info_full[i % INFOS], (i / INFOS) & 1, stop));
       if (!ok) break;
       tc_fence_after();
       float sv[KT];
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->s_free));
-      const TileInfo* in = &ms->info[i & 3];
+      const TileInfo* in = &ms->info[i % INFOS];
       unsigned long long there = in->mask;
       if (tree) {  // rows of V that are not to be multiplied, and values that are not finite, become zeros
         ok = wait_bar(&ms->tree_full, 0, stop);
@@ -247,21 +255,24 @@ __global__ void __launch_bounds__(A8THREADS, 2)
           if (!((j < 32 ? (uint32_t)there : (uint32_t)(there >> 32)) >> (j & 31) & 1)) sv[j] = -INFINITY;
       }
       const float by = tree ? a.scale_log2 : qc;
-      float mx = -INFINITY;
+      float sc[8], mx = -INFINITY;
+      {
+        const float4 x = *reinterpret_cast<const float4*>(in->ks), y = *reinterpret_cast<const float4*>(in->ks + 4);
+        sc[0] = x.x * by, sc[1] = x.y * by, sc[2] = x.z * by, sc[3] = x.w * by;
+        sc[4] = y.x * by, sc[5] = y.y * by, sc[6] = y.z * by, sc[7] = y.w * by;
+      }
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         const float* v = sv + 8 * g;
         const float top = fmaxf(max3f(max3f(v[0], v[1], v[2]), v[3], v[4]), max3f(v[5], v[6], v[7]));
-        mx = fmaxf(mx, fmaf(top, fmaxf(in->ks[g] * by, 1e-37f), in->lv[g]));
+        mx = fmaxf(mx, fmaf(top, sc[g], in->lv[g]));
       }
-      if (i == 0) {
-        m = mx;
-      } else {  // P . V of the last tile has read its P
+      if (i == 0) m = mx;
+      const bool grows = i > 0 && __any_sync(0xffffffffu, mx > m + 8.f);
+      if (grows) {  // O is made relative to the new maximum, once the products so far are in it
         ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
         if (!ok) break;
         tc_fence_after();
-      }
-      if (i > 0 && __any_sync(0xffffffffu, mx > m + 8.f)) {
         const float to = fmaxf(m, mx), g = to == m ? 1.f : exp2_sfu(m - to);
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
@@ -279,30 +290,35 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         l *= g, m = to;
       }
       const float ref = (m == -INFINITY ? 0.f : m) - kShift;  // minus infinity: a row none of whose keys so far counts
-      const unsigned long long one2 = pack2(1.f, 1.f);
-      unsigned long long l2 = pack2(l, 0.f);
-      const uint32_t pt = tmem + A_P + lanes;
+      const bool o_there = i == 0 || grows || mbar_past(smem_u32(&ms->o_done), (i - 1) & 1);
+      unsigned long long l2[2] = {pack2(l, 0.f), 0ull};
+      uint32_t u[KT / 2];
+      auto weigh = [&](auto bf16) {  // P, and what it adds to the row's sum
 #pragma unroll
-      for (int c = 0; c < KT; c += 16) {
-        uint32_t u[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int g = c / 8 + h;
-          const float sc = fmaxf(in->ks[g] * by, 1e-37f), off = in->lv[g] - ref;
-          const unsigned long long sc2 = pack2(sc, sc), off2 = pack2(off, off);
-          unsigned long long sum2 = 0ull;
+        for (int g = 0; g < 8; ++g) {
+          const float off = in->lv[g] - ref, r = in->rv[g];
+          const unsigned long long sc2 = pack2(sc[g], sc[g]), off2 = pack2(off, off), r2 = pack2(r, r);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 e = unpack2(ffma2(pack2(sv[8 * g + 2 * j], sv[8 * g + 2 * j + 1]), sc2, off2));
             const float p0 = exp2_sfu(e.x), p1 = exp2_sfu(e.y);
-            sum2 = ffma2(one2, pack2(p0, p1), sum2);
-            u[4 * h + j] = tree ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+            l2[j & 1] = ffma2(pack2(p0, p1), r2, l2[j & 1]);
+            u[4 * g + j] = decltype(bf16)::value ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
           }
-          l2 = ffma2(sum2, pack2(in->rv[g], in->rv[g]), l2);
         }
-        tmem_st8(pt + c / 2, u);
-      }
-      l = pair_sum(l2);
+      };
+      if (tree)
+        weigh(std::true_type{});
+      else
+        weigh(std::false_type{});
+      l = pair_sum(l2[0]) + pair_sum(l2[1]);
+      ok = __all_sync(0xffffffffu, o_there) || wait_bar(&ms->o_done, (i - 1) & 1, stop);  // P . V of the last tile has read its P
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < KT / 2; c += 8) tmem_st8(tmem + A_P + lanes + c, reinterpret_cast<const uint32_t(&)[8]>(u[c]));
+      s_there = i + 1 < n && mbar_past(smem_u32(&ms->s_full), (i + 1) & 1);
+      info_there = i + 1 < n && mbar_past(smem_u32(&ms->info_full[(i + 1) % INFOS]), ((i + 1) / INFOS) & 1);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -349,201 +365,216 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       }
       if (row < rows && splits > 1) a.part_ml[((long long)run * a.Hkv + kvh) * rows + row] = make_float2(m, l);
     }
-  } else if (warp == 4) {
-    // ---- copies: lane b the b-th page piece of a tile ----
-    const int32_t* table = a.table + (long long)s * a.max_pages;
-    const int shift = min(a.page_shift, 6), box = 1 << shift, pieces = KT >> shift, pmask = (1 << a.page_shift) - 1;
-    auto lookup = [&](int ti) {  // the piece's page; -1: no such row; -2: out of range
-      const int at = ti * KT + lane * box;
-      if (lane >= pieces || ti >= ct || at >= len) return -1;
-      const int pg = table[at >> a.page_shift];
-      return pg < 0 || pg >= a.n_pages ? -2 : pg;
-    };
-    int issued = 0, pg = lookup(i0 + has_tree - 1);
-    if (has_tree) {  // the tree's V and K, in the places of the first two fp16 tiles
-      const uint32_t full = smem_u32(&ms->tree_full);
-      if (lane == 0) mbar_arrive_expect_tx(full, 2 * Sh::TILE16);
-      __syncwarp();
-      if (lane < 2 * DB)
-        tma_load_2d(sb + Sh::OFF_V16 + lane * BLK, lane < DB ? &tvt : &tkt, kvh * D + lane % DB * 64, s * a.n, full);
-    }
+  } else if (warp >= 8) {
+    give_registers<R_CONVERT>();
+    // ---- V to fp16: 16 rows of a tile to each of four warps ----
+    constexpr int PER = D / 8, STEP = 32 / PER, BATCH = 16 / STEP;  // pieces of 8 values in a row, rows at a time, rows of a lane
+    const int piece = lane % PER, r0_ = (warp - 8) * 16 + lane / PER;
 #pragma unroll 1
     for (int i = has_tree; i < n; ++i) {
-      const int ti = i0 + i - 1, mine = pg;
-      pg = lookup(ti + 1);
-      if (__any_sync(0xffffffffu, mine == -2) && lane == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine >= 0)) * box * D;
-      const int crd = ((mine * a.Hkv + kvh) << a.page_shift) + ((ti * KT + lane * box) & pmask);
-      bool ok = true;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int use = 2 * (i - has_tree) + kv, unit = use % UNITS;
-        const uint32_t full = smem_u32(&ms->full[unit]), dst = sb + Sh::OFF_RING + unit * Sh::TILE8 + lane * box * D;
-        if (use >= UNITS) ok = ok && wait_bar(&ms->free_[unit], (use / UNITS - 1) & 1, stop);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-        __syncwarp();
-        if (mine >= 0) {
-          if (kv == 0)
-            tma_load_2d(dst, &tkp, 0, crd, full);
-          else
-            bulk_load(dst, f.vp + (long long)crd * D, box * D, full);
-        }
-        issued = use + 1;
-      }
-      if (!ok) break;
-    }
-    // copies land before the shared memory is given up, whoever gives up, and when (else they have, by the time of the last tile)
-    if (lane == 0) {
-      if (has_tree) mbar_wait(smem_u32(&ms->tree_full), 0);
-      for (int k = max(0, issued - UNITS); k < issued; ++k) mbar_wait(smem_u32(&ms->full[k % UNITS]), (k / UNITS) & 1);
-    }
-  } else if (warp == 7) {
-    // ---- what a tile's keys are (lanes 0 .. 7 of K, 8 .. 15 of V, each of 8 keys), and its V to fp16 ----
-    const int32_t* table = a.table + (long long)s * a.max_pages;
-    const int grp = lane & 7, is_v = lane >> 3 & 1, pmask = (1 << a.page_shift) - 1;
-    auto page_of = [&](int ti) {  // -1: no such rows, or their page is out of range
-      const int at = ti * KT + grp * 8;
-      if (lane >= 16 || ti >= ct || at >= len) return -1;
-      const int pg = table[at >> a.page_shift];
-      return pg < 0 || pg >= a.n_pages ? -1 : pg;
-    };
-    auto scale_of = [&](int ti, int pg) {
-      if (pg < 0) return 1.f;
-      const long long at = (((long long)pg * a.Hkv + kvh) << a.page_shift) + ((ti * KT + grp * 8) & pmask);
-      return (is_v ? f.vs : f.ks)[at >> f.block_shift];
-    };
-    const int t0 = i0 + has_tree - 1;  // the run's first tile of the cache
-    int pg = page_of(t0);
-    float sc = scale_of(t0, pg), v0 = 1.f;
-    int pg1 = page_of(t0 + 1);
-    if (has_tree) {
-      TileInfo* in = &ms->info[0];
-      if (lane < 8) in->ks[lane] = 1.f, in->lv[lane] = 0.f, in->rv[lane] = 1.f;
-      if (lane == 0) in->mask = a.n < 64 ? (1ull << a.n) - 1 : ~0ull, ms->v0 = 1.f;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ms->info_full[0]));
-    }
-#pragma unroll 1
-    for (int i = has_tree; i < n; ++i) {
-      const int ti = i0 + i - 1;
-      const bool good = good_scale(sc);
-      if (__any_sync(0xffffffffu, pg >= 0 && !good) && lane == 0) flag(a.status, SSM_STATUS_SCALE);
-      const unsigned int fine = __ballot_sync(0xffffffffu, pg >= 0 && good);
-      const unsigned int groups = fine & fine >> 8 & 255u;
-      if (!good) sc = 1.f;
-      if (i == 0) {  // what scales of v are relative to: the largest of the first tile, as a power of two
-        const unsigned int top = __reduce_max_sync(0xffffffffu, lane >= 8 && lane < 16 && groups >> grp & 1 ? __float_as_uint(sc) & 0x7f800000u : 0u);
-        v0 = top ? __uint_as_float(top) : 1.f;
-        if (lane == 0) ms->v0 = v0;
-      }
-      const int left = min(max(len - ti * KT - 8 * grp, 0), 8);
-      const unsigned long long keys = lane < 8 && groups >> grp & 1 ? (unsigned long long)((1u << left) - 1) << 8 * grp : 0ull;
-      const unsigned long long mask = (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(keys >> 32)) << 32 |
-                                      __reduce_or_sync(0xffffffffu, (uint32_t)keys);
-      TileInfo* in = &ms->info[i & 3];
-      if (lane < 8) {
-        in->ks[grp] = sc;
-      } else if (lane < 16) {
-        const float rel = fminf(fmaxf(sc / v0, 0x1p-120f), 0x1p120f);
-        in->lv[grp] = log2f(rel), in->rv[grp] = 1.f / rel;
-      }
-      if (lane == 0) in->mask = mask;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ms->info_full[i & 3]));
-      pg = pg1, sc = scale_of(ti + 1, pg), pg1 = page_of(ti + 2);
-
-      const int use = 2 * (i - has_tree) + 1, unit = use % UNITS, at = i & 1, k = i >> 1;
+      const int use = i - has_tree, unit = use % VU, at = i & 1, k = i >> 1;
       const bool first = k == 0 && !(at && has_tree);  // nobody has had this place (of the tree's, S has read K, P . V V)
-      bool ok = wait_bar(&ms->full[unit], (use / UNITS) & 1, stop);
+      bool ok = wait_bar(&ms->info_full[i % INFOS], (i / INFOS) & 1, stop) && wait_bar(&ms->v_full[unit], (use / VU) & 1, stop);
       ok = ok && (first || wait_bar(&ms->v16_free[at], (at && has_tree ? k : k - 1) & 1, stop));
       if (!ok) break;
-      const unsigned char* src = smem + Sh::OFF_RING + unit * Sh::TILE8;
-      unsigned char* dst = smem + Sh::OFF_V16 + at * Sh::TILE16;
-      constexpr int PER = D / 8, STEP = 32 / PER;  // pieces of 8 values in a row, rows at a time
-      const int piece = lane % PER;
-#pragma unroll 8
-      for (int r = lane / PER; r < KT; r += STEP) {
-        uint2 x = *reinterpret_cast<const uint2*>(src + r * D + piece * 8);
-        if (!(mask >> r & 1)) x = make_uint2(0, 0);
-        *reinterpret_cast<uint4*>(dst + (piece >> 3) * BLK + tile_off(r, piece & 7, 128)) =
-            make_uint4(e4m3x2_f16x2(x.x & 0xffffu), e4m3x2_f16x2(x.x >> 16), e4m3x2_f16x2(x.y & 0xffffu), e4m3x2_f16x2(x.y >> 16));
+      const unsigned long long mask = ms->info[i % INFOS].mask;
+      const unsigned char* src = smem + Sh::OFF_V + unit * Sh::TILE8 + r0_ * D + piece * 8;
+      unsigned char* dst = smem + Sh::OFF_V16 + at * Sh::TILE16 + (piece >> 3) * BLK;
+      uint2 x[BATCH];
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) x[b] = *reinterpret_cast<const uint2*>(src + b * STEP * D);
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const int row = r0_ + b * STEP;
+        if (!(mask >> row & 1)) x[b] = make_uint2(0, 0);  // (whatever stands there)
+        *reinterpret_cast<uint4*>(dst + tile_off(row, piece & 7, 128)) = make_uint4(
+            e4m3x2_f16x2(x[b].x & 0xffffu), e4m3x2_f16x2(x[b].x >> 16), e4m3x2_f16x2(x[b].y & 0xffffu), e4m3x2_f16x2(x[b].y >> 16));
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_u32(&ms->free_[unit]));
+        mbar_arrive(smem_u32(&ms->v_free[unit]));
         mbar_arrive(smem_u32(&ms->v16_full[at]));
       }
     }
   } else {
-    // ---- MMAs: one warp those of S, the other P . V, each behind its own waits ----
-    const bool leader = elect_one();
-    bool ok = true;
-    if (warp == 5) {
-      constexpr uint32_t id8 = (1u << 4) | (uint32_t)(KT >> 3) << 17 | (128u >> 4) << 24;  // e4m3 x e4m3 -> fp32
-      constexpr uint32_t id_t = idesc_major(128, KT, false, false);
-      ok = wait_bar(&ms->q_full, 0, stop);
-#pragma unroll 1
-      for (int i = 0; i < n && ok; ++i) {
-        const bool tree = has_tree && i == 0;
-        const int use = 2 * (i - has_tree), unit = use % UNITS;
-        ok = tree ? wait_bar(&ms->tree_full, 0, stop) : wait_bar(&ms->full[unit], (use / UNITS) & 1, stop);
-        ok = ok && (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          if (tree) {
-            const uint32_t kd = desc_lo(sb + Sh::OFF_V16 + Sh::TILE16, 16);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ts<id_t>(tmem + A_S, tmem + A_O + k * 8, kd + (((k >> 2) * BLK + (k & 3) * 32) >> 4), k > 0);
-            mma_commit(smem_u32(&ms->s_full));
-            mma_commit(smem_u32(&ms->v16_free[1]));
-          } else {
-            const uint32_t qd = desc_lo(sb, 16), kd = desc_lo(sb + Sh::OFF_RING + unit * Sh::TILE8, 16);
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              mma8_ts<id8, Sh::DESC_HI>(tmem + A_S, tmem + A_Q + k * 8, kd + k * 2, k > 0);
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) mma8_ss<id8, Sh::DESC_HI>(tmem + A_S, qd + k * 2, kd + k * 2, true);
-            mma_commit(smem_u32(&ms->s_full));
-            mma_commit(smem_u32(&ms->free_[unit]));
-          }
-        }
+    give_registers<R_MMA>();
+    if (warp == 4) {
+      // ---- copies: lane b the b-th page piece of a tile ----
+      const int32_t* table = a.table + (long long)s * a.max_pages;
+      const int shift = min(a.page_shift, 6), box = 1 << shift, pieces = KT >> shift, pmask = (1 << a.page_shift) - 1;
+      auto lookup = [&](int ti) {  // the piece's page; -1: no such row; -2: out of range
+        const int at = ti * KT + lane * box;
+        if (lane >= pieces || ti >= ct || at >= len) return -1;
+        const int pg = table[at >> a.page_shift];
+        return pg < 0 || pg >= a.n_pages ? -2 : pg;
+      };
+      int k_issued = 0, v_issued = 0, pg = lookup(i0 + has_tree - 1);
+      if (has_tree) {  // the tree's V and K, in the places of the first two fp16 tiles
+        const uint32_t full = smem_u32(&ms->tree_full);
+        if (lane == 0) mbar_arrive_expect_tx(full, 2 * Sh::TILE16);
         __syncwarp();
+        if (lane < 2 * DB)
+          tma_load_2d(sb + Sh::OFF_V16 + lane * BLK, lane < DB ? &tvt : &tkt, kvh * D + lane % DB * 64, s * a.n, full);
+      }
+#pragma unroll 1
+      for (int i = has_tree; i < n; ++i) {
+        const int ti = i0 + i - 1, use = i - has_tree, mine = pg;
+        pg = lookup(ti + 1);
+        if (__any_sync(0xffffffffu, mine == -2) && lane == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine >= 0)) * box * D;
+        const int crd = ((mine * a.Hkv + kvh) << a.page_shift) + ((ti * KT + lane * box) & pmask);
+        if (use >= KU && !wait_bar(&ms->k_free[use % KU], (use / KU - 1) & 1, stop)) break;
+        uint32_t full = smem_u32(&ms->k_full[use % KU]);
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        __syncwarp();
+        if (mine >= 0) tma_load_2d(sb + Sh::OFF_K + use % KU * Sh::TILE8 + lane * box * D, &tkp, 0, crd, full);
+        k_issued = use + 1;
+        if (use >= VU && !wait_bar(&ms->v_free[use % VU], (use / VU - 1) & 1, stop)) break;
+        full = smem_u32(&ms->v_full[use % VU]);
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        __syncwarp();
+        if (mine >= 0)
+          bulk_load(sb + Sh::OFF_V + use % VU * Sh::TILE8 + lane * box * D, f.vp + (long long)crd * D, box * D, full);
+        v_issued = use + 1;
+      }
+      // copies land before the shared memory is given up, whoever gives up, and when (else they have, by the time of the last tile)
+      if (lane == 0) {
+        if (has_tree) mbar_wait(smem_u32(&ms->tree_full), 0);
+        for (int k = max(0, k_issued - KU); k < k_issued; ++k) mbar_wait(smem_u32(&ms->k_full[k % KU]), (k / KU) & 1);
+        for (int k = max(0, v_issued - VU); k < v_issued; ++k) mbar_wait(smem_u32(&ms->v_full[k % VU]), (k / VU) & 1);
+      }
+    } else if (warp == 7) {
+      // ---- what a tile's keys are.  Lane 8 j + g has the scales of the g-th 8 keys of tile j of four: they are asked for four tiles
+      // ahead, their pages eight (a load that misses the caches takes longer than a tile) ----
+      const int32_t* table = a.table + (long long)s * a.max_pages;
+      const int grp = lane & 7, t0 = i0 + has_tree - 1, count = n - has_tree, pmask = (1 << a.page_shift) - 1;
+      auto page_of = [&](int c) {  // of the lane's keys in the c-th four tiles; -1: no such rows, or their page is out of range
+        const int ti = t0 + 4 * c + (lane >> 3), at = ti * KT + grp * 8;
+        if (4 * c + (lane >> 3) >= count || at >= len) return -1;
+        const int pg = table[at >> a.page_shift];
+        return pg < 0 || pg >= a.n_pages ? -1 : pg;
+      };
+      auto scales_of = [&](int c, int pg) {
+        if (pg < 0) return make_float2(1.f, 1.f);
+        const int ti = t0 + 4 * c + (lane >> 3);
+        const long long at = ((((long long)pg * a.Hkv + kvh) << a.page_shift) + ((ti * KT + grp * 8) & pmask)) >> f.block_shift;
+        return make_float2(f.ks[at], f.vs[at]);
+      };
+      int pg = page_of(0);
+      int pg1 = page_of(1);
+      float2 sc = scales_of(0, pg);
+      float v0 = 1.f;
+      if (has_tree) {
+        TileInfo* in = &ms->info[0];
+        if (lane < 8) in->ks[lane] = 1.f, in->lv[lane] = 0.f, in->rv[lane] = 1.f;
+        if (lane == 0) in->mask = a.n < 64 ? (1ull << a.n) - 1 : ~0ull, ms->v0 = 1.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->info_full[0]));
+      }
+      bool ok = true;
+#pragma unroll 1
+      for (int c = 0; 4 * c < count && ok; ++c) {
+        const float2 next = scales_of(c + 1, pg1);
+        const int pg2 = page_of(c + 2);
+        const bool good = good_scale(sc.x) && good_scale(sc.y);
+        if (__any_sync(0xffffffffu, pg >= 0 && !good) && lane == 0) flag(a.status, SSM_STATUS_SCALE);
+        const bool there = pg >= 0 && good;
+        if (!there) sc = make_float2(1.f, 1.f);
+        if (c == 0 && !has_tree) {  // what scales of v are relative to: the largest of the first tile, as a power of two
+          const unsigned int top = __reduce_max_sync(0xffffffffu, lane < 8 && there ? __float_as_uint(sc.y) & 0x7f800000u : 0u);
+          v0 = top ? __uint_as_float(top) : 1.f;
+          if (lane == 0) ms->v0 = v0;
+        }
+        const int left = min(max(len - (t0 + 4 * c + (lane >> 3)) * KT - 8 * grp, 0), 8);
+        const unsigned long long keys = there ? (unsigned long long)((1u << left) - 1) << 8 * grp : 0ull;
+        const float rel = fminf(fmaxf(sc.y / v0, 0x1p-120f), 0x1p120f), lv = log2f(rel), rv = 1.f / rel;
+#pragma unroll 1
+        for (int j = 0; j < 4 && 4 * c + j < count; ++j) {
+          const int use = 4 * c + j, i = use + has_tree;
+          const bool mine = lane >> 3 == j;
+          const unsigned long long mask = (unsigned long long)__reduce_or_sync(0xffffffffu, mine ? (uint32_t)(keys >> 32) : 0u) << 32 |
+                                          __reduce_or_sync(0xffffffffu, mine ? (uint32_t)keys : 0u);
+          // (a place among the infos is free by the time that the tile's V is there)
+          ok = wait_bar(&ms->v_full[use % VU], (use / VU) & 1, stop);
+          if (!ok) break;
+          TileInfo* in = &ms->info[i % INFOS];
+          if (mine) in->ks[grp] = fmaxf(sc.x, 0x1p-66f), in->lv[grp] = lv, in->rv[grp] = rv;
+          if (lane == 0) in->mask = mask;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ms->info_full[i % INFOS]));
+        }
+        pg = pg1, pg1 = pg2, sc = next;
       }
     } else {
-      constexpr uint32_t id_o = idesc_f16(128, D, true), id_t = idesc_major(128, D, false, true);
+      // ---- MMAs: one warp those of S, the other P . V, each behind its own waits ----
+      const bool leader = elect_one();
+      bool ok = true;
+      if (warp == 5) {
+        constexpr uint32_t id8 = (1u << 4) | (uint32_t)(KT >> 3) << 17 | (128u >> 4) << 24;  // e4m3 x e4m3 -> fp32
+        constexpr uint32_t id_t = idesc_major(128, KT, false, false);
+        ok = wait_bar(&ms->q_full, 0, stop);
 #pragma unroll 1
-      for (int i = 0; i < n && ok; ++i) {
-        const bool tree = has_tree && i == 0;
-        const int at = i & 1;
-        ok = tree ? wait_bar(&ms->tree_full, 0, stop)
-                  : wait_bar(&ms->v16_full[at], ((i >> 1) - (at == 0 ? has_tree : 0)) & 1, stop);
-        ok = ok && wait_bar(&ms->p_full, i & 1, stop);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint32_t vd = desc_lo(sb + Sh::OFF_V16 + at * Sh::TILE16, BLK);
+        for (int i = 0; i < n && ok; ++i) {
+          const bool tree = has_tree && i == 0;
+          const int use = i - has_tree, unit = use % KU;
+          ok = tree ? wait_bar(&ms->tree_full, 0, stop) : wait_bar(&ms->k_full[unit], (use / KU) & 1, stop);
+          ok = ok && (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            if (tree) {
+              const uint32_t kd = desc_lo(sb + Sh::OFF_V16 + Sh::TILE16, 16);
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k) {  // 16 keys: two groups of 8 rows
-            if (tree)
-              mma_ts<id_t>(tmem + A_O, tmem + A_P + k * 8, vd + k * (2048 >> 4), k > 0);
-            else
-              mma_ts<id_o>(tmem + A_O, tmem + A_P + k * 8, vd + k * (2048 >> 4), i + k > 0);
+              for (int k = 0; k < D / 16; ++k)
+                mma_ts<id_t>(tmem + A_S, tmem + A_O + k * 8, kd + (((k >> 2) * BLK + (k & 3) * 32) >> 4), k > 0);
+              mma_commit(smem_u32(&ms->s_full));
+              mma_commit(smem_u32(&ms->v16_free[1]));
+            } else {
+              const uint32_t qd = desc_lo(sb, 16), kd = desc_lo(sb + Sh::OFF_K + unit * Sh::TILE8, 16);
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                mma8_ts<id8, Sh::DESC_HI>(tmem + A_S, tmem + A_Q + k * 8, kd + k * 2, k > 0);
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) mma8_ss<id8, Sh::DESC_HI>(tmem + A_S, qd + k * 2, kd + k * 2, true);
+              mma_commit(smem_u32(&ms->s_full));
+              mma_commit(smem_u32(&ms->k_free[unit]));
+            }
           }
-          mma_commit(smem_u32(&ms->o_done));
-          mma_commit(smem_u32(&ms->v16_free[at]));
+          __syncwarp();
         }
-        __syncwarp();
+      } else {
+        constexpr uint32_t id_o = idesc_f16(128, D, true), id_t = idesc_major(128, D, false, true);
+#pragma unroll 1
+        for (int i = 0; i < n && ok; ++i) {
+          const bool tree = has_tree && i == 0;
+          const int at = i & 1;
+          ok = tree ? wait_bar(&ms->tree_full, 0, stop)
+                    : wait_bar(&ms->v16_full[at], ((i >> 1) - (at == 0 ? has_tree : 0)) & 1, stop);
+          ok = ok && wait_bar(&ms->p_full, i & 1, stop);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint32_t vd = desc_lo(sb + Sh::OFF_V16 + at * Sh::TILE16, BLK);
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k) {  // 16 keys: two groups of 8 rows
+              if (tree)
+                mma_ts<id_t>(tmem + A_O, tmem + A_P + k * 8, vd + k * (2048 >> 4), k > 0);
+              else
+                mma_ts<id_o>(tmem + A_O, tmem + A_P + k * 8, vd + k * (2048 >> 4), i + k > 0);
+            }
+            mma_commit(smem_u32(&ms->o_done));
+            mma_commit(smem_u32(&ms->v16_free[at]));
+          }
+          __syncwarp();
+        }
       }
+      if (leader) {
+        mma_commit(smem_u32(&ms->drain[warp - 5]));
+        mbar_poll_ns(smem_u32(&ms->drain[warp - 5]), 0, kWaitLimitNs);
+      }
+      __syncwarp();
     }
-    if (leader) {
-      mma_commit(smem_u32(&ms->drain[warp - 5]));
-      mbar_poll_ns(smem_u32(&ms->drain[warp - 5]), 0, kWaitLimitNs);
-    }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();

@@ -117,6 +117,17 @@ __device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
                : "memory");
 }
 
+// registers a thread of this warpgroup from here on: given back, or taken from what others gave back (the groups' shares add up to
+// what the block was launched with)
+template <int REGS>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS));
+}
+
 // The warp waits together, and all its lanes get the same answer: false once a second has passed or another warp has given
 // up.  (A waiter has to see every phase of a barrier: the parity of one that it skipped would let it through early.)
 __device__ __forceinline__ bool wait_bar(unsigned long long* bar, uint32_t parity, volatile int* stop) {
@@ -130,6 +141,15 @@ __device__ __forceinline__ bool wait_bar(unsigned long long* bar, uint32_t parit
   }
   *stop = 1;
   return false;
+}
+// whether a phase of an mbarrier is past, at once (where it is, what its arrivals wrote can be read)
+__device__ __forceinline__ bool mbar_past(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
 }
 // ---- host ----
 // a grid whose blocks may be placed while the stream's kernel before it ends; they call grid_dependency_wait before they
