@@ -1,7 +1,5 @@
 // Attention of a draft tree's nodes over an 8-bit paged cache and their ancestors, and the commit of the accepted path into it
 // (ssm_attention.h).
-#include <type_traits>
-
 #include "attend.cuh"
 #include "decode.cuh"
 
@@ -214,21 +212,14 @@ __global__ void __launch_bounds__(A8THREADS, 2)
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const bool tree = has_tree && i == 0;
-      ok = __all_sync(0xffffffffu, s_there) || wait_bar(&ms->s_full, i & 1, stop);
-      ok = ok && (__all_sync(0xffffffffu, info_there) || wait_bar(&ms->info_full[i % INFOS], (i / INFOS) & 1, stop));
-      if (!ok) break;
+      if (__builtin_expect(!__all_sync(0xffffffffu, s_there && info_there), 0)) {
+        ok = wait_bar(&ms->s_full, i & 1, stop) && wait_bar(&ms->info_full[i % INFOS], (i / INFOS) & 1, stop);
+        if (!ok) break;
+      }
       tc_fence_after();
-      float sv[KT];
-#pragma unroll
-      for (int c = 0; c < KT; c += 16) tmem_ld16_async(tmem + A_S + lanes + c, reinterpret_cast<float(&)[16]>(sv[c]));
-#pragma unroll
-      for (int c = 0; c < KT; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ms->s_free));
       const TileInfo* in = &ms->info[i % INFOS];
       unsigned long long there = in->mask;
-      if (tree) {  // rows of V that are not to be multiplied, and values that are not finite, become zeros
+      if (__builtin_expect(tree, 0)) {  // rows of V that are not to be multiplied, and values that are not finite, become zeros
         ok = wait_bar(&ms->tree_full, 0, stop);
         unsigned char* vt = smem + Sh::OFF_V16;
         // (a warp that gives up here still meets the others below)
@@ -249,11 +240,34 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         if (!ok) break;
         there &= ms->anc[node];
       }
-      if (there != ~0ull) {
+      // The loop is as long as it need not be for the tiles that most are: what few need is rolled up, and goes over tensor memory
+      // (scores that do not count, the tree's weights as bf16): with it unrolled in registers wide trees took 136 us, the
+      // instructions of one tile no longer staying near.
+      if (__builtin_expect(__any_sync(0xffffffffu, there != ~0ull), 0)) {
+#pragma unroll 1
+        for (int c = 0; c < KT; c += 16) {
+          float x[16];
+          uint32_t y[8];
+          tmem_ld16_async(tmem + A_S + lanes + c, x);
+          tmem_wait_ld16(x);
+          const uint32_t bits = (uint32_t)(there >> c);
 #pragma unroll
-        for (int j = 0; j < KT; ++j)
-          if (!((j < 32 ? (uint32_t)there : (uint32_t)(there >> 32)) >> (j & 31) & 1)) sv[j] = -INFINITY;
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = bits >> (8 * h + j) & 1 ? __float_as_uint(x[8 * h + j]) : 0xff800000u;
+            tmem_st8(tmem + A_S + lanes + c + 8 * h, y);
+          }
+        }
+        tmem_wait_st();
       }
+      float sv[KT];
+#pragma unroll
+      for (int c = 0; c < KT; c += 16) tmem_ld16_async(tmem + A_S + lanes + c, reinterpret_cast<float(&)[16]>(sv[c]));
+#pragma unroll
+      for (int c = 0; c < KT; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->s_free));
       const float by = tree ? a.scale_log2 : qc;
       float sc[8], mx = -INFINITY;
       {
@@ -269,7 +283,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       }
       if (i == 0) m = mx;
       const bool grows = i > 0 && __any_sync(0xffffffffu, mx > m + 8.f);
-      if (grows) {  // O is made relative to the new maximum, once the products so far are in it
+      if (__builtin_expect(grows, 0)) {  // O is made relative to the new maximum, once the products so far are in it
         ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
         if (!ok) break;
         tc_fence_after();
@@ -293,30 +307,45 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       const bool o_there = i == 0 || grows || mbar_past(smem_u32(&ms->o_done), (i - 1) & 1);
       unsigned long long l2[2] = {pack2(l, 0.f), 0ull};
       uint32_t u[KT / 2];
-      auto weigh = [&](auto bf16) {  // P, and what it adds to the row's sum
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float off = in->lv[g] - ref, r = in->rv[g];
-          const unsigned long long sc2 = pack2(sc[g], sc[g]), off2 = pack2(off, off), r2 = pack2(r, r);
+      for (int g = 0; g < 8; ++g) {  // P, and what it adds to the row's sum
+        const float off = in->lv[g] - ref, r = in->rv[g];
+        const unsigned long long sc2 = pack2(sc[g], sc[g]), off2 = pack2(off, off), r2 = pack2(r, r);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 e = unpack2(ffma2(pack2(sv[8 * g + 2 * j], sv[8 * g + 2 * j + 1]), sc2, off2));
-            const float p0 = exp2_sfu(e.x), p1 = exp2_sfu(e.y);
-            l2[j & 1] = ffma2(pack2(p0, p1), r2, l2[j & 1]);
-            u[4 * g + j] = decltype(bf16)::value ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
-          }
+        for (int j = 0; j < 4; ++j) {
+          const float2 e = unpack2(ffma2(pack2(sv[8 * g + 2 * j], sv[8 * g + 2 * j + 1]), sc2, off2));
+          const float p0 = exp2_sfu(e.x), p1 = exp2_sfu(e.y);
+          l2[j & 1] = ffma2(pack2(p0, p1), r2, l2[j & 1]);
+          u[4 * g + j] = pack_f16x2(p0, p1);
         }
-      };
-      if (tree)
-        weigh(std::true_type{});
-      else
-        weigh(std::false_type{});
+      }
       l = pair_sum(l2[0]) + pair_sum(l2[1]);
-      ok = __all_sync(0xffffffffu, o_there) || wait_bar(&ms->o_done, (i - 1) & 1, stop);  // P . V of the last tile has read its P
-      if (!ok) break;
+      if (__builtin_expect(!__all_sync(0xffffffffu, o_there), 0)) {  // P . V of the last tile has not read its P yet
+        ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
+        if (!ok) break;
+      }
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < KT / 2; c += 8) tmem_st8(tmem + A_P + lanes + c, reinterpret_cast<const uint32_t(&)[8]>(u[c]));
+      if (__builtin_expect(tree, 0)) {
+        tmem_wait_st();
+#pragma unroll 1
+        for (int c = 0; c < KT / 2; c += 16) {
+          float x[16];
+          uint32_t y[8];
+          tmem_ld16_async(tmem + A_P + lanes + c, x);
+          tmem_wait_ld16(x);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float2 w = f16x2_f32(__float_as_uint(x[8 * h + j]));
+              y[j] = pack_bf16x2(w.x, w.y);
+            }
+            tmem_st8(tmem + A_P + lanes + c + 8 * h, y);
+          }
+        }
+      }
       s_there = i + 1 < n && mbar_past(smem_u32(&ms->s_full), (i + 1) & 1);
       info_there = i + 1 < n && mbar_past(smem_u32(&ms->info_full[(i + 1) % INFOS]), ((i + 1) / INFOS) & 1);
       tmem_wait_st();
