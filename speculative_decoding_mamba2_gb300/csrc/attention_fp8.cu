@@ -25,13 +25,15 @@ constexpr int R_SOFTMAX = 136, R_MMA = 48, R_CONVERT = 56;
 static_assert(R_SOFTMAX + R_MMA + R_CONVERT == 3 * 80, "what the block is launched with");
 constexpr int BLK = KT * 128;   // 64 rows x 64 columns of 16 bits
 constexpr float kShift = 7.f;
-constexpr int A_S = 0, A_P = 64, A_Q = 96, A_O = 128, A_COLS = 256;  // tensor memory columns: S, P, Q's upper terms, O
+// tensor memory columns: S of even and of odd tiles, each then overwritten by its P; O; where there is room Q's two terms
+constexpr int A_S = 0, A_O = 128, A_Q = 192, A_COLS = 256;
 
 template <int D>
 struct Attend8Smem {
-  static constexpr int KU = D == 128 ? 4 : 6, VU = D == 128 ? 3 : 6;  // tiles of K and of V in e4m3, in rings
+  static constexpr bool Q_TMEM = D == 64;            // Q's two terms stand in tensor memory (else in shared memory)
+  static constexpr int KU = D == 128 ? 3 : 6, VU = D == 128 ? 2 : 6;  // tiles of K and of V in e4m3, in rings
   static constexpr int TILE8 = KT * D, TILE16 = KT * D * 2;
-  static constexpr int OFF_V16 = 128 * D;            // after Q's lower terms
+  static constexpr int OFF_V16 = Q_TMEM ? 0 : 2 * 128 * D;  // after Q's terms
   static constexpr int OFF_K = OFF_V16 + 2 * TILE16, OFF_V = OFF_K + KU * TILE8;
   static constexpr int OFF_MISC = OFF_V + VU * TILE8;
   static constexpr int BYTES = OFF_MISC + 2048;
@@ -51,7 +53,7 @@ struct TileInfo {  // of each 8 keys: scale of k, log2 of the scale of v and its
 struct Attend8Misc {
   TileInfo info[INFOS];        // of tile i, at i % INFOS
   unsigned long long anc[64];  // ancestors and self of each node
-  unsigned long long k_full[6], k_free[6], v_full[6], v_free[6], v16_full[2], v16_free[2], info_full[INFOS], q_full, s_full, s_free, p_full, o_done, tree_full, drain[2];
+  unsigned long long k_full[6], k_free[6], v_full[6], v_free[6], v16_full[2], v16_free[2], info_full[INFOS], q_full, s_full[2], p_full[2], o_done[2], all_done, tree_full, drain[2];
   SplitScratch split;
   unsigned int odd[2];         // tree rows with a value of v that is not finite
   uint32_t tmem;
@@ -111,14 +113,14 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms->v16_full[i]), 4);
       mbar_init(smem_u32(&ms->v16_free[i]), 1);
+      mbar_init(smem_u32(&ms->s_full[i]), 1);
+      mbar_init(smem_u32(&ms->p_full[i]), 4);
+      mbar_init(smem_u32(&ms->o_done[i]), 1);
       mbar_init(smem_u32(&ms->drain[i]), 1);
     }
     for (int i = 0; i < INFOS; ++i) mbar_init(smem_u32(&ms->info_full[i]), 1);
     mbar_init(smem_u32(&ms->q_full), 4);
-    mbar_init(smem_u32(&ms->s_full), 1);
-    mbar_init(smem_u32(&ms->s_free), 4);
-    mbar_init(smem_u32(&ms->p_full), 4);
-    mbar_init(smem_u32(&ms->o_done), 1);
+    mbar_init(smem_u32(&ms->all_done), 1);
     mbar_init(smem_u32(&ms->tree_full), 1);
     ms->stop = 0;
     ms->odd[0] = ms->odd[1] = 0;
@@ -130,11 +132,12 @@ __global__ void __launch_bounds__(A8THREADS, 2)
   int s = run, sp = 0, tps = 1 << 30, splits = 1;
   bool any = true;
   if (a.max_runs > 0) {
-    int* tiles = reinterpret_cast<int*>(smem);  // space not in use yet: of Q's lower terms
+    int* tiles = reinterpret_cast<int*>(smem);  // space not in use yet
     int first;
     tps = choose_split<A8THREADS>(a, a.Hkv * rt, tiles, &ms->split);
     any = find_run(a.S, tiles, tps, run, s, first, splits);
     sp = any ? run - first : 0;
+    fence_async_smem();  // (before the barrier behind which the copies may write there)
     if (any && sp == 0 && kvh == 0 && r0 == 0 && tid == 0) a.runs[s] = make_int2(first, splits);
   }
   tc_fence_before();
@@ -153,7 +156,8 @@ __global__ void __launch_bounds__(A8THREADS, 2)
   }
   const int ct = (len + KT - 1) / KT;  // tiles of the cache; the tree's is before them
   const int i0 = sp * tps, n = min(ct + 1 - i0, tps), has_tree = sp == 0;
-  // tile i of the run is cache tile i0 + i - 1, the (i - has_tree)-th of the rings; its V is at i % 2 in fp16
+  // tile i of the run is cache tile i0 + i - 1, the (i - has_tree)-th of the rings; its S, P and fp16 V are at i % 2, and every
+  // barrier of those is one of two: who waits could otherwise find it two phases on, and take that for none
 
   if (warp < 4) {
     take_registers<R_SOFTMAX>();
@@ -161,8 +165,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     const int node = row < rows ? row / a.g : 0, qh = row < rows ? row % a.g : 0;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     float qc;  // this row's scale of Q, times scale log2 e
-    {  // q (zero beyond the last row): upper terms to tensor memory, lower terms to shared memory; rolled up, since code that runs
-      // once is fetched from afar (unrolled, this took 4 us)
+    {  // q's two terms (zero beyond the last row); rolled up, since code that runs once is fetched from afar (unrolled: 4 us)
       uint32_t most = 0;
       const uint4* q = reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + node) * a.ldq + (kvh * a.g + qh) * D);
       const bool some = row < rows;
@@ -194,9 +197,13 @@ __global__ void __launch_bounds__(A8THREADS, 2)
               hi[4 * h + j] |= top << 16 * k, lo[4 * h + j] |= f32_e4m3x2(p0 - back.x, p1 - back.y) << 16 * k;
             }
           }
-          *reinterpret_cast<uint4*>(smem + Sh::off8(tid, c / 2 + h)) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+          if constexpr (!Sh::Q_TMEM) {
+            const uint32_t at = Sh::off8(tid, c / 2 + h);
+            *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
+            *reinterpret_cast<uint4*>(smem + 128 * D + at) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+          }
         }
-        tmem_st8(tmem + A_Q + lanes + 2 * c, hi);
+        if constexpr (Sh::Q_TMEM) tmem_st8(tmem + A_Q + lanes + 2 * c, hi), tmem_st8(tmem + A_Q + D / 4 + lanes + 2 * c, lo);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -206,16 +213,15 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     }
     if (has_tree && warp == 0) ancestor_words(a, s, ms->anc, kvh == 0 && r0 == 0);
 
-    // (a barrier that is past costs some 100 cycles to look at: it is looked at ahead, and awaited where it was not past yet)
     float m = -INFINITY, l = 0.f;
-    bool ok = true, s_there = false, info_there = false;
+    bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const bool tree = has_tree && i == 0;
-      if (__builtin_expect(!__all_sync(0xffffffffu, s_there && info_there), 0)) {
-        ok = wait_bar(&ms->s_full, i & 1, stop) && wait_bar(&ms->info_full[i % INFOS], (i / INFOS) & 1, stop);
-        if (!ok) break;
-      }
+      const uint32_t st = tmem + A_S + (i & 1) * KT + lanes;
+      // (S was made once what the tile's keys are was known)
+      ok = wait_bar(&ms->s_full[i & 1], (i >> 1) & 1, stop) && wait_bar(&ms->info_full[i % INFOS], (i / INFOS) & 1, stop);
+      if (!ok) break;
       tc_fence_after();
       const TileInfo* in = &ms->info[i % INFOS];
       unsigned long long there = in->mask;
@@ -248,26 +254,23 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         for (int c = 0; c < KT; c += 16) {
           float x[16];
           uint32_t y[8];
-          tmem_ld16_async(tmem + A_S + lanes + c, x);
+          tmem_ld16_async(st + c, x);
           tmem_wait_ld16(x);
           const uint32_t bits = (uint32_t)(there >> c);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] = bits >> (8 * h + j) & 1 ? __float_as_uint(x[8 * h + j]) : 0xff800000u;
-            tmem_st8(tmem + A_S + lanes + c + 8 * h, y);
+            tmem_st8(st + c + 8 * h, y);
           }
         }
         tmem_wait_st();
       }
       float sv[KT];
 #pragma unroll
-      for (int c = 0; c < KT; c += 16) tmem_ld16_async(tmem + A_S + lanes + c, reinterpret_cast<float(&)[16]>(sv[c]));
+      for (int c = 0; c < KT; c += 16) tmem_ld16_async(st + c, reinterpret_cast<float(&)[16]>(sv[c]));
 #pragma unroll
       for (int c = 0; c < KT; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ms->s_free));
       const float by = tree ? a.scale_log2 : qc;
       float sc[8], mx = -INFINITY;
       {
@@ -284,7 +287,8 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       if (i == 0) m = mx;
       const bool grows = i > 0 && __any_sync(0xffffffffu, mx > m + 8.f);
       if (__builtin_expect(grows, 0)) {  // O is made relative to the new maximum, once the products so far are in it
-        ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
+        // (those of the tile before the last are, since S of this one has taken its P's place)
+        ok = wait_bar(&ms->o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, stop);
         if (!ok) break;
         tc_fence_after();
         const float to = fmaxf(m, mx), g = to == m ? 1.f : exp2_sfu(m - to);
@@ -304,7 +308,6 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         l *= g, m = to;
       }
       const float ref = (m == -INFINITY ? 0.f : m) - kShift;  // minus infinity: a row none of whose keys so far counts
-      const bool o_there = i == 0 || grows || mbar_past(smem_u32(&ms->o_done), (i - 1) & 1);
       unsigned long long l2[2] = {pack2(l, 0.f), 0ull};
       uint32_t u[KT / 2];
 #pragma unroll
@@ -320,20 +323,15 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         }
       }
       l = pair_sum(l2[0]) + pair_sum(l2[1]);
-      if (__builtin_expect(!__all_sync(0xffffffffu, o_there), 0)) {  // P . V of the last tile has not read its P yet
-        ok = wait_bar(&ms->o_done, (i - 1) & 1, stop);
-        if (!ok) break;
-      }
-      tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < KT / 2; c += 8) tmem_st8(tmem + A_P + lanes + c, reinterpret_cast<const uint32_t(&)[8]>(u[c]));
+      for (int c = 0; c < KT / 2; c += 8) tmem_st8(st + c, reinterpret_cast<const uint32_t(&)[8]>(u[c]));
       if (__builtin_expect(tree, 0)) {
         tmem_wait_st();
 #pragma unroll 1
         for (int c = 0; c < KT / 2; c += 16) {
           float x[16];
           uint32_t y[8];
-          tmem_ld16_async(tmem + A_P + lanes + c, x);
+          tmem_ld16_async(st + c, x);
           tmem_wait_ld16(x);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -342,18 +340,16 @@ __global__ void __launch_bounds__(A8THREADS, 2)
               const float2 w = f16x2_f32(__float_as_uint(x[8 * h + j]));
               y[j] = pack_bf16x2(w.x, w.y);
             }
-            tmem_st8(tmem + A_P + lanes + c + 8 * h, y);
+            tmem_st8(st + c + 8 * h, y);
           }
         }
       }
-      s_there = i + 1 < n && mbar_past(smem_u32(&ms->s_full), (i + 1) & 1);
-      info_there = i + 1 < n && mbar_past(smem_u32(&ms->info_full[(i + 1) % INFOS]), ((i + 1) / INFOS) & 1);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ms->p_full));
+      if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[i & 1]));
     }
-    ok = ok && wait_bar(&ms->o_done, (n - 1) & 1, stop);
+    ok = ok && wait_bar(&ms->all_done, 0, stop);
     // a warp that gives up still takes part in the barrier that others may be waiting at
     if (!ok) asm volatile("bar.arrive 1, 128;\n" ::: "memory");
     tc_fence_after();
@@ -398,27 +394,34 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     give_registers<R_CONVERT>();
     // ---- V to fp16: 16 rows of a tile to each of four warps ----
     constexpr int PER = D / 8, STEP = 32 / PER, BATCH = 16 / STEP;  // pieces of 8 values in a row, rows at a time, rows of a lane
-    const int piece = lane % PER, r0_ = (warp - 8) * 16 + lane / PER;
+    const int piece = lane % PER, first = (warp - 8) * 16 + lane / PER;
+    // where a row's piece goes: rows 8 on have the same place in their group of 8
+    constexpr int SAME = 8 / STEP;
+    uint32_t to[SAME];
+#pragma unroll
+    for (int b = 0; b < SAME; ++b) to[b] = Sh::OFF_V16 + (piece >> 3) * BLK + tile_off(first + b * STEP, piece & 7, 128);
 #pragma unroll 1
     for (int i = has_tree; i < n; ++i) {
       const int use = i - has_tree, unit = use % VU, at = i & 1, k = i >> 1;
-      const bool first = k == 0 && !(at && has_tree);  // nobody has had this place (of the tree's, S has read K, P . V V)
+      const bool fresh = k == 0 && !(at && has_tree);  // nobody has had this place (of the tree's, S has read K, P . V V)
       bool ok = wait_bar(&ms->info_full[i % INFOS], (i / INFOS) & 1, stop) && wait_bar(&ms->v_full[unit], (use / VU) & 1, stop);
-      ok = ok && (first || wait_bar(&ms->v16_free[at], (at && has_tree ? k : k - 1) & 1, stop));
+      ok = ok && (fresh || wait_bar(&ms->v16_free[at], (at && has_tree ? k : k - 1) & 1, stop));
       if (!ok) break;
       const unsigned long long mask = ms->info[i % INFOS].mask;
-      const unsigned char* src = smem + Sh::OFF_V + unit * Sh::TILE8 + r0_ * D + piece * 8;
-      unsigned char* dst = smem + Sh::OFF_V16 + at * Sh::TILE16 + (piece >> 3) * BLK;
+      const unsigned char* src = smem + Sh::OFF_V + unit * Sh::TILE8 + first * D + piece * 8;
+      unsigned char* dst = smem + at * Sh::TILE16;
       uint2 x[BATCH];
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) x[b] = *reinterpret_cast<const uint2*>(src + b * STEP * D);
+      if (__builtin_expect(mask != ~0ull, 0)) {  // (whatever stands where no key is)
 #pragma unroll
-      for (int b = 0; b < BATCH; ++b) {
-        const int row = r0_ + b * STEP;
-        if (!(mask >> row & 1)) x[b] = make_uint2(0, 0);  // (whatever stands there)
-        *reinterpret_cast<uint4*>(dst + tile_off(row, piece & 7, 128)) = make_uint4(
-            e4m3x2_f16x2(x[b].x & 0xffffu), e4m3x2_f16x2(x[b].x >> 16), e4m3x2_f16x2(x[b].y & 0xffffu), e4m3x2_f16x2(x[b].y >> 16));
+        for (int b = 0; b < BATCH; ++b)
+          if (!(mask >> (first + b * STEP) & 1)) x[b] = make_uint2(0, 0);
       }
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b)
+        *reinterpret_cast<uint4*>(dst + to[b % SAME] + b / SAME * 1024) = make_uint4(
+            e4m3x2_f16x2(x[b].x), e4m3x2_f16x2(x[b].x >> 16), e4m3x2_f16x2(x[b].y), e4m3x2_f16x2(x[b].y >> 16));
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -547,8 +550,9 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         for (int i = 0; i < n && ok; ++i) {
           const bool tree = has_tree && i == 0;
           const int use = i - has_tree, unit = use % KU;
+          const uint32_t st = tmem + A_S + (i & 1) * KT;
           ok = tree ? wait_bar(&ms->tree_full, 0, stop) : wait_bar(&ms->k_full[unit], (use / KU) & 1, stop);
-          ok = ok && (i == 0 || wait_bar(&ms->s_free, (i - 1) & 1, stop));
+          ok = ok && (i < 2 || wait_bar(&ms->o_done[i & 1], ((i >> 1) - 1) & 1, stop));  // P . V has read the P that stands there
           if (!ok) break;
           tc_fence_after();
           if (leader) {
@@ -556,17 +560,21 @@ __global__ void __launch_bounds__(A8THREADS, 2)
               const uint32_t kd = desc_lo(sb + Sh::OFF_V16 + Sh::TILE16, 16);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
-                mma_ts<id_t>(tmem + A_S, tmem + A_O + k * 8, kd + (((k >> 2) * BLK + (k & 3) * 32) >> 4), k > 0);
-              mma_commit(smem_u32(&ms->s_full));
+                mma_ts<id_t>(st, tmem + A_O + k * 8, kd + (((k >> 2) * BLK + (k & 3) * 32) >> 4), k > 0);
+              mma_commit(smem_u32(&ms->s_full[i & 1]));
               mma_commit(smem_u32(&ms->v16_free[1]));
             } else {
               const uint32_t qd = desc_lo(sb, 16), kd = desc_lo(sb + Sh::OFF_K + unit * Sh::TILE8, 16);
 #pragma unroll
-              for (int k = 0; k < D / 32; ++k)
-                mma8_ts<id8, Sh::DESC_HI>(tmem + A_S, tmem + A_Q + k * 8, kd + k * 2, k > 0);
+              for (int t = 0; t < 2; ++t)  // Q's upper terms, its lower terms
 #pragma unroll
-              for (int k = 0; k < D / 32; ++k) mma8_ss<id8, Sh::DESC_HI>(tmem + A_S, qd + k * 2, kd + k * 2, true);
-              mma_commit(smem_u32(&ms->s_full));
+                for (int k = 0; k < D / 32; ++k) {
+                  if constexpr (Sh::Q_TMEM)
+                    mma8_ts<id8, Sh::DESC_HI>(st, tmem + A_Q + t * (D / 4) + k * 8, kd + k * 2, t + k > 0);
+                  else
+                    mma8_ss<id8, Sh::DESC_HI>(st, qd + t * (128 * D >> 4) + k * 2, kd + k * 2, t + k > 0);
+                }
+              mma_commit(smem_u32(&ms->s_full[i & 1]));
               mma_commit(smem_u32(&ms->k_free[unit]));
             }
           }
@@ -578,9 +586,10 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         for (int i = 0; i < n && ok; ++i) {
           const bool tree = has_tree && i == 0;
           const int at = i & 1;
+          const uint32_t st = tmem + A_S + at * KT;
           ok = tree ? wait_bar(&ms->tree_full, 0, stop)
                     : wait_bar(&ms->v16_full[at], ((i >> 1) - (at == 0 ? has_tree : 0)) & 1, stop);
-          ok = ok && wait_bar(&ms->p_full, i & 1, stop);
+          ok = ok && wait_bar(&ms->p_full[at], (i >> 1) & 1, stop);
           if (!ok) break;
           tc_fence_after();
           if (leader) {
@@ -588,12 +597,13 @@ __global__ void __launch_bounds__(A8THREADS, 2)
 #pragma unroll
             for (int k = 0; k < KT / 16; ++k) {  // 16 keys: two groups of 8 rows
               if (tree)
-                mma_ts<id_t>(tmem + A_O, tmem + A_P + k * 8, vd + k * (2048 >> 4), k > 0);
+                mma_ts<id_t>(tmem + A_O, st + k * 8, vd + k * (2048 >> 4), k > 0);
               else
-                mma_ts<id_o>(tmem + A_O, tmem + A_P + k * 8, vd + k * (2048 >> 4), i + k > 0);
+                mma_ts<id_o>(tmem + A_O, st + k * 8, vd + k * (2048 >> 4), i + k > 0);
             }
-            mma_commit(smem_u32(&ms->o_done));
+            mma_commit(smem_u32(&ms->o_done[at]));
             mma_commit(smem_u32(&ms->v16_free[at]));
+            if (i + 1 == n) mma_commit(smem_u32(&ms->all_done));
           }
           __syncwarp();
         }
@@ -635,7 +645,7 @@ cudaError_t run_attend8(const AttendFp8Args& f, const AttendPlan& p, cudaStream_
                    Sh::BYTES, s, m[0], m[1], m[2], f);
   return e != cudaSuccess || p.max_runs == 0 ? e : launch_attend_join(a, s);
 }
-static_assert(2 * 2 * kSMs * 4 <= 128 * 64, "the lengths stand in the space of Q's lower terms");
+static_assert(2 * 2 * kSMs * 4 <= 2 * Attend8Smem<64>::TILE16, "the lengths stand in the space of V");
 
 // Commit.  A cluster of 8 CTAs for each sequence, a warp for each block of tokens of a layer, head and K or V: the largest of its new
 // rows gives the scale that they need, the block takes that or its own, rows that it holds are rounded again if it grew.  The

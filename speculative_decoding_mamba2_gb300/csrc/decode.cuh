@@ -56,10 +56,10 @@ struct ScoreArgs {
 };
 cudaError_t launch_token_scores(const ScoreArgs& a, cudaStream_t s);
 
-// two e4m3 values as two of fp16 (exact)
+// two e4m3 values (the lower half of v) as two of fp16 (exact)
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   uint32_t r;
-  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(v));
+  asm("{\n .reg .b16 h, g;\n mov.b32 {h, g}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(v));
   return r;
 }
 __device__ __forceinline__ float2 f16x2_f32(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
