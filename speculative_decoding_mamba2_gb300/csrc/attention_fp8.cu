@@ -25,18 +25,17 @@ constexpr int R_SOFTMAX = 136, R_MMA = 48, R_CONVERT = 56;
 static_assert(R_SOFTMAX + R_MMA + R_CONVERT == 3 * 80, "what the block is launched with");
 constexpr int BLK = KT * 128;   // 64 rows x 64 columns of 16 bits
 constexpr float kShift = 7.f;
-// tensor memory columns: S of even and of odd tiles, each then overwritten by its P; O; where there is room Q's two terms
-constexpr int A_S = 0, A_O = 128, A_Q = 192, A_COLS = 256;
+// tensor memory columns: S of even and of odd tiles, each then overwritten by its P; O
+constexpr int A_S = 0, A_O = 128, A_COLS = 256;
 
 template <int D>
 struct Attend8Smem {
-  static constexpr bool Q_TMEM = D == 64;            // Q's two terms stand in tensor memory (else in shared memory)
   static constexpr int KU = D == 128 ? 3 : 6, VU = D == 128 ? 2 : 6;  // tiles of K and of V in e4m3, in rings
   static constexpr int TILE8 = KT * D, TILE16 = KT * D * 2;
-  static constexpr int OFF_V16 = Q_TMEM ? 0 : 2 * 128 * D;  // after Q's terms
+  static constexpr int OFF_V16 = 2 * 128 * D;        // after Q's two terms
   static constexpr int OFF_K = OFF_V16 + 2 * TILE16, OFF_V = OFF_K + KU * TILE8;
   static constexpr int OFF_MISC = OFF_V + VU * TILE8;
-  static constexpr int BYTES = OFF_MISC + 2048;
+  static constexpr int BYTES = OFF_MISC + 2688;
   static_assert(BYTES <= 228 * 1024 / 2 - 1024, "two to an SM");
   static constexpr uint32_t DESC_HI = D == 128 ? kDescHi : (512u >> 4) | 1u << 14 | 4u << 29;  // 128- or 64-byte rows, swizzled
   // byte offset of 16-byte chunk `chunk` of row `row` of a tile of D-byte rows
@@ -56,11 +55,12 @@ struct Attend8Misc {
   unsigned long long k_full[6], k_free[6], v_full[6], v_free[6], v16_full[2], v16_free[2], info_full[INFOS], q_full, s_full[2], p_full[2], o_done[2], all_done, tree_full, drain[2];
   SplitScratch split;
   unsigned int odd[2];         // tree rows with a value of v that is not finite
+  float qs[128];               // a row's scale of Q
   uint32_t tmem;
   int stop;
   float v0;                    // what the run's scales of v are relative to
 };
-static_assert(sizeof(Attend8Misc) <= 2048, "space");
+static_assert(sizeof(Attend8Misc) <= 2688, "space");
 static_assert(Attend8Smem<64>::VU + 2 <= INFOS && Attend8Smem<128>::VU + 2 <= INFOS, "a place is free when its next tile is there");
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {  // fp16 x fp16 -> fp32
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms->v16_full[i]), 4);
       mbar_init(smem_u32(&ms->v16_free[i]), 1);
-      mbar_init(smem_u32(&ms->s_full[i]), 1);
+      mbar_init(smem_u32(&ms->s_full[i]), 2);
       mbar_init(smem_u32(&ms->p_full[i]), 4);
       mbar_init(smem_u32(&ms->o_done[i]), 1);
       mbar_init(smem_u32(&ms->drain[i]), 1);
@@ -164,53 +164,86 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     const int row = r0 + tid;  // this thread's
     const int node = row < rows ? row / a.g : 0, qh = row < rows ? row % a.g : 0;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    float qc;  // this row's scale of Q, times scale log2 e
-    {  // q's two terms (zero beyond the last row); rolled up, since code that runs once is fetched from afar (unrolled: 4 us)
-      uint32_t most = 0;
-      const uint4* q = reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + node) * a.ldq + (kvh * a.g + qh) * D);
-      const bool some = row < rows;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = some ? q[c] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    {  // q as it is, where O will be: for the tree's tile
+      uint4 x[D / 8];
+      if (has_tree) {
+        const uint4* q = reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + node) * a.ldq + (kvh * a.g + qh) * D);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) most = max(most, max(finite_bits(bf16_lo(w[j])), finite_bits(bf16_hi(w[j]))));
+        for (int c = 0; c < D / 8; ++c) x[c] = row < rows ? q[c] : make_uint4(0, 0, 0, 0);
       }
-      const float qs = least_scale(most), inv = 1.f / qs;
-      qc = fmaxf(qs * a.scale_log2, 0x1p-60f);  // (with ks at least 2^-66: their product is a normal number)
+      // its two terms: eight columns a thread, a row's columns side by side, two rows at a time.  (Beyond the last row stands
+      // anything: it stays in its own row of S and O, whose maximum is not looked at.)
+      constexpr int PIECES = D / 8, RI = 128 / PIECES, BATCH = 2;
+      const int piece = tid % PIECES, last = min(rows - r0, 128);
+      int r = tid / PIECES;
+      const uint16_t* q = a.q + (long long)s * a.n * a.ldq + kvh * a.g * D + piece * 8;
 #pragma unroll 1
-      for (int c = 0; c < D / 8; c += 4) {
-        uint32_t hi[8], lo[8];
+      for (int r1 = 0; r1 < last; r1 += BATCH * RI) {
+        uint32_t w[BATCH][4], most[BATCH];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 x = some ? q[c + 2 * h] : make_uint4(0, 0, 0, 0), y = some ? q[c + 2 * h + 1] : make_uint4(0, 0, 0, 0);
-          const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          if (has_tree) tmem_st8(tmem + A_O + lanes + 4 * (c + 2 * h), w);  // as it is where O will be
+        for (int b = 0; b < BATCH; ++b) {
+          const int at = r + b * RI;
+          const unsigned int u = (unsigned)(r0 + at) / (unsigned)a.g;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (at < last) v = *reinterpret_cast<const uint4*>(q + u * a.ldq + (r0 + at - u * a.g) * D);
+          w[b][0] = v.x, w[b][1] = v.y, w[b][2] = v.z, w[b][3] = v.w;
+        }
+        bool odd = false;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            hi[4 * h + j] = lo[4 * h + j] = 0;
+        for (int b = 0; b < BATCH; ++b) {  // the largest magnitude's bits
+          const uint32_t two = __vmaxu2(__vmaxu2(w[b][0] & 0x7fff7fffu, w[b][1] & 0x7fff7fffu), __vmaxu2(w[b][2] & 0x7fff7fffu, w[b][3] & 0x7fff7fffu));
+          most[b] = max(two & 0xffffu, two >> 16);
+          odd = odd || most[b] >= 0x7f80u;
+        }
+        if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {  // what is not finite becomes NaN, and does not count
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float p0 = nan_unless_finite(bf16_lo(w[2 * j + k])) * inv, p1 = nan_unless_finite(bf16_hi(w[2 * j + k])) * inv;
-              const uint32_t top = f32_e4m3x2(p0, p1);
-              const float2 back = f16x2_f32(e4m3x2_f16x2(top));
-              hi[4 * h + j] |= top << 16 * k, lo[4 * h + j] |= f32_e4m3x2(p0 - back.x, p1 - back.y) << 16 * k;
+          for (int b = 0; b < BATCH; ++b) {
+            most[b] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t lo = w[b][j] & 0x7fffu, hi = w[b][j] >> 16 & 0x7fffu;
+              most[b] = max(most[b], max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+              w[b][j] |= (lo < 0x7f80u ? 0u : 0x7fffu) | (hi < 0x7f80u ? 0u : 0x7fff0000u);
             }
           }
-          if constexpr (!Sh::Q_TMEM) {
-            const uint32_t at = Sh::off8(tid, c / 2 + h);
-            *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
-            *reinterpret_cast<uint4*>(smem + 128 * D + at) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
-          }
         }
-        if constexpr (Sh::Q_TMEM) tmem_st8(tmem + A_Q + lanes + 2 * c, hi), tmem_st8(tmem + A_Q + D / 4 + lanes + 2 * c, lo);
+#pragma unroll
+        for (int o = PIECES / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int b = 0; b < BATCH; ++b) most[b] = max(most[b], __shfl_xor_sync(0xffffffffu, most[b], o));
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          const float qs = least_scale(most[b] << 16);
+          const uint32_t inv = (0x7f000000u - __float_as_uint(qs)) >> 16, inv2 = inv | inv << 16;  // 1 / 2^e
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t x = bf16x2_mul(w[b][j], inv2), p = pack_f16x2(bf16_lo(x), bf16_hi(x));  // (exact: 8 of 11 bits)
+            const uint32_t top = f16x2_e4m3x2(p), rest = f16x2_e4m3x2(f16x2_sub(p, e4m3x2_f16x2(top)));
+            hi[j / 2] = j & 1 ? hi[j / 2] | top << 16 : top, lo[j / 2] = j & 1 ? lo[j / 2] | rest << 16 : rest;
+          }
+          const uint32_t to = Sh::off8(r + b * RI, piece / 2) + piece % 2 * 8;
+          *reinterpret_cast<uint2*>(smem + to) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(smem + 128 * D + to) = make_uint2(lo[0], lo[1]);
+          if (piece == 0) ms->qs[r + b * RI] = qs;
+        }
+        r += BATCH * RI;
       }
-      tmem_wait_st();
+      if (has_tree) {
+#pragma unroll
+        for (int c = 0; c < D / 8; c += 2) {
+          const uint32_t u[8] = {x[c].x, x[c].y, x[c].z, x[c].w, x[c + 1].x, x[c + 1].y, x[c + 1].z, x[c + 1].w};
+          tmem_st8(tmem + A_O + lanes + 4 * c, u);
+        }
+        tmem_wait_st();
+      }
       tc_fence_before();
       fence_async_smem();
-      __syncwarp();
+      named_sync(2, 128);
       if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
     }
+    // this row's scale of Q, times scale log2 e (with ks at least 2^-66: their product is a normal number)
+    const float qc = fmaxf(ms->qs[tid] * a.scale_log2, 0x1p-60f);
     if (has_tree && warp == 0) ancestor_words(a, s, ms->anc, kvh == 0 && r0 == 0);
 
     float m = -INFINITY, l = 0.f;
@@ -219,12 +252,18 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     for (int i = 0; i < n; ++i) {
       const bool tree = has_tree && i == 0;
       const uint32_t st = tmem + A_S + (i & 1) * KT + lanes;
-      // (S was made once what the tile's keys are was known)
-      ok = wait_bar(&ms->s_full[i & 1], (i >> 1) & 1, stop) && wait_bar(&ms->info_full[i % INFOS], (i / INFOS) & 1, stop);
+      ok = wait_bar(&ms->s_full[i & 1], (i >> 1) & 1, stop);  // (and what the tile's keys are)
       if (!ok) break;
       tc_fence_after();
       const TileInfo* in = &ms->info[i % INFOS];
+      float sv[KT];
+#pragma unroll
+      for (int c = 0; c < KT; c += 16) tmem_ld16_async(st + c, reinterpret_cast<float(&)[16]>(sv[c]));
       unsigned long long there = in->mask;
+      const float4 ks0 = *reinterpret_cast<const float4*>(in->ks), ks1 = *reinterpret_cast<const float4*>(in->ks + 4);
+      const float4 lv0 = *reinterpret_cast<const float4*>(in->lv), lv1 = *reinterpret_cast<const float4*>(in->lv + 4);
+#pragma unroll
+      for (int c = 0; c < KT; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
       if (__builtin_expect(tree, 0)) {  // rows of V that are not to be multiplied, and values that are not finite, become zeros
         ok = wait_bar(&ms->tree_full, 0, stop);
         unsigned char* vt = smem + Sh::OFF_V16;
@@ -249,7 +288,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       // The loop is as long as it need not be for the tiles that most are: what few need is rolled up, and goes over tensor memory
       // (scores that do not count, the tree's weights as bf16): with it unrolled in registers wide trees took 136 us, the
       // instructions of one tile no longer staying near.
-      if (__builtin_expect(__any_sync(0xffffffffu, there != ~0ull), 0)) {
+      if (__builtin_expect(tree || there != ~0ull, 0)) {
 #pragma unroll 1
         for (int c = 0; c < KT; c += 16) {
           float x[16];
@@ -265,25 +304,22 @@ __global__ void __launch_bounds__(A8THREADS, 2)
           }
         }
         tmem_wait_st();
+#pragma unroll
+        for (int c = 0; c < KT; c += 16) tmem_ld16_async(st + c, reinterpret_cast<float(&)[16]>(sv[c]));
+#pragma unroll
+        for (int c = 0; c < KT; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
       }
-      float sv[KT];
-#pragma unroll
-      for (int c = 0; c < KT; c += 16) tmem_ld16_async(st + c, reinterpret_cast<float(&)[16]>(sv[c]));
-#pragma unroll
-      for (int c = 0; c < KT; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
       const float by = tree ? a.scale_log2 : qc;
-      float sc[8], mx = -INFINITY;
-      {
-        const float4 x = *reinterpret_cast<const float4*>(in->ks), y = *reinterpret_cast<const float4*>(in->ks + 4);
-        sc[0] = x.x * by, sc[1] = x.y * by, sc[2] = x.z * by, sc[3] = x.w * by;
-        sc[4] = y.x * by, sc[5] = y.y * by, sc[6] = y.z * by, sc[7] = y.w * by;
-      }
+      const float sc[8] = {ks0.x * by, ks0.y * by, ks0.z * by, ks0.w * by, ks1.x * by, ks1.y * by, ks1.z * by, ks1.w * by};
+      const float off[8] = {lv0.x, lv0.y, lv0.z, lv0.w, lv1.x, lv1.y, lv1.z, lv1.w};
+      float mx = -INFINITY;
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         const float* v = sv + 8 * g;
         const float top = fmaxf(max3f(max3f(v[0], v[1], v[2]), v[3], v[4]), max3f(v[5], v[6], v[7]));
-        mx = fmaxf(mx, fmaf(top, sc[g], in->lv[g]));
+        mx = fmaxf(mx, fmaf(top, sc[g], off[g]));
       }
+      if (row >= rows) mx = -INFINITY;
       if (i == 0) m = mx;
       const bool grows = i > 0 && __any_sync(0xffffffffu, mx > m + 8.f);
       if (__builtin_expect(grows, 0)) {  // O is made relative to the new maximum, once the products so far are in it
@@ -307,13 +343,15 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         }
         l *= g, m = to;
       }
+      const float4 rv0 = *reinterpret_cast<const float4*>(in->rv), rv1 = *reinterpret_cast<const float4*>(in->rv + 4);
+      const float rv[8] = {rv0.x, rv0.y, rv0.z, rv0.w, rv1.x, rv1.y, rv1.z, rv1.w};
       const float ref = (m == -INFINITY ? 0.f : m) - kShift;  // minus infinity: a row none of whose keys so far counts
       unsigned long long l2[2] = {pack2(l, 0.f), 0ull};
       uint32_t u[KT / 2];
 #pragma unroll
       for (int g = 0; g < 8; ++g) {  // P, and what it adds to the row's sum
-        const float off = in->lv[g] - ref, r = in->rv[g];
-        const unsigned long long sc2 = pack2(sc[g], sc[g]), off2 = pack2(off, off), r2 = pack2(r, r);
+        const float b = off[g] - ref, r = rv[g];
+        const unsigned long long sc2 = pack2(sc[g], sc[g]), off2 = pack2(b, b), r2 = pack2(r, r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 e = unpack2(ffma2(pack2(sv[8 * g + 2 * j], sv[8 * g + 2 * j + 1]), sc2, off2));
@@ -552,10 +590,12 @@ __global__ void __launch_bounds__(A8THREADS, 2)
           const int use = i - has_tree, unit = use % KU;
           const uint32_t st = tmem + A_S + (i & 1) * KT;
           ok = tree ? wait_bar(&ms->tree_full, 0, stop) : wait_bar(&ms->k_full[unit], (use / KU) & 1, stop);
+          ok = ok && wait_bar(&ms->info_full[i % INFOS], (i / INFOS) & 1, stop);
           ok = ok && (i < 2 || wait_bar(&ms->o_done[i & 1], ((i >> 1) - 1) & 1, stop));  // P . V has read the P that stands there
           if (!ok) break;
           tc_fence_after();
           if (leader) {
+            mbar_arrive(smem_u32(&ms->s_full[i & 1]));  // (who sees S then sees the tile's info too)
             if (tree) {
               const uint32_t kd = desc_lo(sb + Sh::OFF_V16 + Sh::TILE16, 16);
 #pragma unroll
@@ -568,12 +608,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
 #pragma unroll
               for (int t = 0; t < 2; ++t)  // Q's upper terms, its lower terms
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                  if constexpr (Sh::Q_TMEM)
-                    mma8_ts<id8, Sh::DESC_HI>(st, tmem + A_Q + t * (D / 4) + k * 8, kd + k * 2, t + k > 0);
-                  else
-                    mma8_ss<id8, Sh::DESC_HI>(st, qd + t * (128 * D >> 4) + k * 2, kd + k * 2, t + k > 0);
-                }
+                for (int k = 0; k < D / 32; ++k) mma8_ss<id8, Sh::DESC_HI>(st, qd + t * (128 * D >> 4) + k * 2, kd + k * 2, t + k > 0);
               mma_commit(smem_u32(&ms->s_full[i & 1]));
               mma_commit(smem_u32(&ms->k_free[unit]));
             }

@@ -69,6 +69,22 @@ __device__ __forceinline__ uint32_t f32_e4m3x2(float lo, float hi) {
   asm("{\n .reg .b16 h;\n cvt.rn.satfinite.e4m3x2.f32 h, %2, %1;\n cvt.u32.u16 %0, h;\n}\n" : "=r"(r) : "f"(lo), "f"(hi));
   return r;
 }
+// the same of two fp16 values; x * y and x - y of two bf16, two fp16 values
+__device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t v) {
+  uint32_t r;
+  asm("{\n .reg .b16 h;\n cvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n cvt.u32.u16 %0, h;\n}\n" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 __device__ __forceinline__ bool good_scale(float s) { return s >= 0x1p-100f && s <= 0x1p120f; }
 
 }  // namespace ssmtree
