@@ -710,11 +710,12 @@ def _call_on(device: int, fn, *args):
             _check(fn(*args))
 
 
-def _same_device(like, **tensors):
+def _same_device(like, *tensors):
+    """The device that all of them (None: not given) are on."""
     d = like.get_device()
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.get_device() != d:
-            raise ValueError(f"{name}: on another device than the others")
+            raise ValueError("the tensors are on different devices")
     return d
 
 
@@ -757,8 +758,7 @@ def ssm_tree_attention_fp8(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, 
     table, max_pages = _table(page_table, "page_table", S)
     lay, lens = _dev(layout, "layout", torch.int32, S * n * NODE_WORDS), _dev(cache_len, "cache_len", torch.int32, S)
     ws = _dev(workspace, "workspace", torch.uint8)
-    dev = _same_device(q, k=k, v=v, o=o, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, layout=layout,
-                       page_table=page_table, cache_len=cache_len, workspace=workspace, status=status)
+    dev = _same_device(q, k, v, o, k_pages, v_pages, k_scales, v_scales, layout, page_table, cache_len, workspace, status)
     _call_on(dev, lib().ssm_tree_attention_fp8, S, n, Hq, Hkv, D, lay, pq, ldq, pk, ldk, pv, ldv, kp, vp, ks, vs, n_pages, page,
              block, table, max_pages, lens, int(max_cache_len), float(scale), po, ldo, ws, workspace.numel(), _opt_status(status),
              _stream(stream, q))
@@ -779,8 +779,7 @@ def ssm_kv_commit_fp8(n_seq: int, n_nodes: int, path, path_len, k, v, k_pages, v
     args = (_dev(path_len, "path_len", torch.int32, S), _dev(k, "k", _BF16, rows), _dev(v, "v", _BF16, rows), kp, vp, ks, vs,
             n_pages, page, block, table, max_pages, _dev(cache_len, "cache_len", torch.int32, S),
             _dev(len_out, "len_out", torch.int32, S), _opt_status(status), _stream(stream, k_pages))
-    dev = _same_device(k_pages, k=k, v=v, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, path=path, path_len=path_len,
-                       page_table=page_table, cache_len=cache_len, len_out=len_out, status=status)
+    dev = _same_device(k_pages, k, v, v_pages, k_scales, v_scales, path, path_len, page_table, cache_len, len_out, status)
     _call_on(dev, lib().ssm_kv_commit_fp8, L, S, n, Hkv, D, max_path, paths, *args)
 
 
@@ -838,10 +837,9 @@ def ssm_rope(D: int, positions, turns, q, q_out, k=None, k_out=None, interleaved
     """Rotary positions of q and k rows (bf16 [rows, heads * D], row strides that are multiples of 8; outputs may be their inputs; q or
     k may be None).  positions: int32 [rows]; turns: int64 [rot / 2] on the GPU (ssm_rope_turns): the first rot columns turn."""
     Hq, Hkv, rows, rot, pt, t = _rope_args(D, turns, q, q_out, k, k_out)
-    like = k if q is None else q
-    dev = _same_device(like, turns=turns, positions=positions, q_out=q_out, k=k, k_out=k_out)
-    _call_on(dev, lib().ssm_rope, rows, Hq, Hkv, D, rot, int(interleaved), pt, float(amplitude),
-             _dev(positions, "positions", torch.int32, rows), *t, _stream(stream, like))
+    like, pp = k if q is None else q, _dev(positions, "positions", torch.int32, rows)
+    dev = _same_device(like, turns, positions, q_out, k, k_out)
+    _call_on(dev, lib().ssm_rope, rows, Hq, Hkv, D, rot, int(interleaved), pt, float(amplitude), pp, *t, _stream(stream, like))
 
 
 def ssm_tree_rope(n_seq: int, n_nodes: int, D: int, layout, cache_len, turns, q, q_out, k=None, k_out=None,
@@ -851,10 +849,10 @@ def ssm_tree_rope(n_seq: int, n_nodes: int, D: int, layout, cache_len, turns, q,
     if rows != n_seq * n_nodes:
         raise ValueError("q and k: n_seq * n_nodes rows")
     like = k if q is None else q
-    dev = _same_device(like, turns=turns, layout=layout, cache_len=cache_len, q_out=q_out, k=k, k_out=k_out, status=status)
-    _call_on(dev, lib().ssm_tree_rope, n_seq, n_nodes, Hq, Hkv, D, rot, int(interleaved), pt, float(amplitude),
-             _dev(layout, "layout", torch.int32, rows * NODE_WORDS), _dev(cache_len, "cache_len", torch.int32, n_seq), *t,
-             _opt_status(status), _stream(stream, like))
+    lay, lens = _dev(layout, "layout", torch.int32, rows * NODE_WORDS), _dev(cache_len, "cache_len", torch.int32, n_seq)
+    dev, st = _same_device(like, turns, layout, cache_len, q_out, k, k_out, status), _opt_status(status)
+    _call_on(dev, lib().ssm_tree_rope, n_seq, n_nodes, Hq, Hkv, D, rot, int(interleaved), pt, float(amplitude), lay, lens, *t, st,
+             _stream(stream, like))
 
 
 # ---------------------------------------------------------------------------
@@ -881,6 +879,6 @@ def ssm_token_scores(logits, tokens, logprob, entropy, top, top_logprob=None, sc
         ps = _dev(top_logprob, "top_logprob", torch.float32, T * k)
     if entropy is not None:
         pe = _dev(entropy, "entropy", torch.float32, T)
-    dev = _same_device(logits, tokens=tokens, logprob=logprob, entropy=entropy, top=top, top_logprob=top_logprob, status=status)
+    dev = _same_device(logits, tokens, logprob, entropy, top, top_logprob, status)
     _call_on(dev, lib().ssm_token_scores, T, V, px, int(f32), ld, float(scale), m, pt, pl, pe, k, pi, ps, _opt_status(status),
              _stream(stream, logits))
