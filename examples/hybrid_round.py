@@ -5,7 +5,13 @@
 A prompt goes through the Mamba2 layers by ``ssm_prompt_conv`` and ``ssm_prompt_scan`` and through the attention layers as
 chains of up to 64 nodes (``ssm_tree_attention``, ``ssm_kv_commit``).  A single token takes ``ssm_scan_step`` and a tree of
 one node.  A speculative round drafts a tree, verifies it with ``ssm_tree_verify`` and ``ssm_tree_attention``, walks the
-accepted path and commits it to the states (``ssm_commit``) and to the paged cache (``ssm_kv_commit``).
+accepted path and commits it to the states (``ssm_commit``) and to the paged cache (``ssm_kv_commit``).  The target's tokens are the
+first of ``ssm_token_scores``' alternatives.
+
+    python examples/hybrid_round.py rope fp8
+
+gives the attention layers rotary positions (``ssm_tree_rope``) and a cache of 8 bits (``ssm_tree_attention_fp8``,
+``ssm_kv_commit_fp8``).
 """
 import os
 import sys
@@ -15,18 +21,22 @@ import torch
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), ".."))
 from speculative_decoding_mamba2_gb300 import (Dims, ssm_accept_path, ssm_commit, ssm_gated_rmsnorm, ssm_kv_commit,  # noqa: E402
-                                               ssm_linear, ssm_prompt_conv, ssm_prompt_scan, ssm_prompt_scan_workspace_size,
-                                               ssm_rmsnorm, ssm_scan_step, ssm_tree_attention,
-                                               ssm_tree_attention_workspace_size, ssm_tree_layout_build, ssm_tree_verify,
+                                               ssm_kv_commit_fp8, ssm_linear, ssm_prompt_conv, ssm_prompt_scan,
+                                               ssm_prompt_scan_workspace_size, ssm_rmsnorm, ssm_rope_frequencies, ssm_rope_turns,
+                                               ssm_scan_step, ssm_token_scores, ssm_tree_attention, ssm_tree_attention_fp8,
+                                               ssm_tree_attention_fp8_workspace_size, ssm_tree_attention_workspace_size,
+                                               ssm_tree_layout_build, ssm_tree_rope, ssm_tree_verify,
                                                ssm_tree_verify_workspace_size)
 
 EPS, PIECE = 1e-5, 64
 
 
 class Hybrid:
-    """``pairs`` Mamba2 layers, each followed by an attention layer, for S sequences of up to ``room`` tokens."""
+    """``pairs`` Mamba2 layers, each followed by an attention layer, for S sequences of up to ``room`` tokens.  rope: rotary
+    positions; fp8: a cache of 8 bits, with a scale for each 16 tokens (or page, where that is shorter) of a head."""
 
-    def __init__(self, S=3, pairs=2, H=8, Hq=8, Hkv=2, D=64, vocab=512, room=1024, page=32, seed=0, dev="cuda"):
+    def __init__(self, S=3, pairs=2, H=8, Hq=8, Hkv=2, D=64, vocab=512, room=1024, page=32, seed=0, dev="cuda", rope=False,
+                 fp8=False):
         self.S, self.L, self.H, self.Hq, self.Hkv, self.D, self.room, self.vocab = S, pairs, H, Hq, Hkv, D, room, vocab
         self.dims = Dims(n_heads=H, n_layers=1, ring_cap=20)  # a layer's state and ring are its own tensors
         self.d_inner, self.conv_dim, self.d_model = self.dims.d_inner, self.dims.conv_dim, Hq * D
@@ -52,7 +62,10 @@ class Hybrid:
         self.ring = [torch.zeros(S, 20, self.conv_dim, dtype=torch.bfloat16, device=dev) for _ in range(pairs)]
         self.ring_head = [torch.full((S,), 3, dtype=torch.int32, device=dev) for _ in range(pairs)]
         per = -(-room // page)
-        self.kp, self.vp = (torch.zeros(pairs, S * per, Hkv, page, D, dtype=torch.bfloat16, device=dev) for _ in range(2))
+        self.turns = ssm_rope_turns(ssm_rope_frequencies(D)).to(dev) if rope else None
+        self.fp8, held = fp8, torch.float8_e4m3fn if fp8 else torch.bfloat16
+        self.kp, self.vp = (torch.zeros(pairs, S * per, Hkv, page, D, dtype=torch.bfloat16, device=dev).to(held) for _ in range(2))
+        self.ks, self.vs = (torch.ones(pairs, S * per, Hkv, max(1, page // 16), device=dev) for _ in range(2))
         self.table = torch.randperm(S * per, device=dev, generator=gen).to(torch.int32).view(S, per)
         self.len = torch.zeros(S, dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -102,9 +115,17 @@ class Hybrid:
             ssm_rmsnorm(x, self.norm, EPS, u)
             q = bf(T, self.Hq * D)
             ssm_linear(u, self.W_qkv[i], [(0, q), (self.Hq * D, k[i]), ((self.Hq + self.Hkv) * D, v[i])], status=self.status)
-            ws = torch.empty(ssm_tree_attention_workspace_size(S, n, self.Hq, self.Hkv, D, self.room), dtype=torch.uint8, device=dev)
-            ssm_tree_attention(S, n, self.Hq, self.Hkv, D, layout, q, k[i], v[i], self.kp[i], self.vp[i], self.table, self.len,
-                               self.room, D ** -0.5, o, ws, status=self.status)
+            if self.turns is not None:
+                ssm_tree_rope(S, n, D, layout, self.len, self.turns, q, q, k[i], k[i], status=self.status)
+            shape = (S, n, self.Hq, self.Hkv, D)
+            if self.fp8:
+                ws = torch.empty(ssm_tree_attention_fp8_workspace_size(*shape, self.room), dtype=torch.uint8, device=dev)
+                ssm_tree_attention_fp8(*shape, layout, q, k[i], v[i], self.kp[i], self.vp[i], self.ks[i], self.vs[i], self.table,
+                                       self.len, self.room, D ** -0.5, o, ws, status=self.status)
+            else:
+                ws = torch.empty(ssm_tree_attention_workspace_size(*shape, self.room), dtype=torch.uint8, device=dev)
+                ssm_tree_attention(*shape, layout, q, k[i], v[i], self.kp[i], self.vp[i], self.table, self.len, self.room, D ** -0.5,
+                                   o, ws, status=self.status)
             ssm_linear(o, self.W_o[i], [(0, x)], residual=x, status=self.status)
         logits = torch.empty(T, self.vocab, device=dev)
         ssm_rmsnorm(x, self.norm, EPS, u)
@@ -113,8 +134,10 @@ class Hybrid:
 
     def keep(self, n, path, path_len):
         """The K and V rows of the accepted path into the pages, all layers."""
-        ssm_kv_commit(self.S, n, path, path_len, self.k, self.v, self.kp, self.vp, self.table, self.len, self.len,
-                      status=self.status)
+        scales = (self.ks, self.vs) if self.fp8 else ()
+        commit = ssm_kv_commit_fp8 if self.fp8 else ssm_kv_commit
+        commit(self.S, n, path, path_len, self.k, self.v, self.kp, self.vp, *scales, self.table, self.len, self.len,
+               status=self.status)
 
     def chain(self, tokens, mode):
         """The next n <= 64 tokens of each sequence: logits [S, n, vocab]."""
@@ -142,7 +165,8 @@ class Hybrid:
         logits = self.forward(tokens, layout, depth, "tree")
         path = torch.empty(S, depth + 1, dtype=torch.int32, device=self.dev)
         path_len, bonus = (torch.empty(S, dtype=torch.int32, device=self.dev) for _ in range(2))
-        target = logits.argmax(-1).to(torch.int32)
+        target = torch.empty(S * n, 1, dtype=torch.int32, device=self.dev)
+        ssm_token_scores(logits, None, None, None, target, status=self.status)
         ssm_accept_path(S, n, depth + 1, layout, tokens, target, path, path_len, bonus, status=self.status)
         for i in range(self.L):
             ssm_commit(self.dims, self.prm[i], S, n, layout, depth + 1, path, path_len, self.xBC[i], self.dt[i], self.h[i],
@@ -197,5 +221,5 @@ def run(S=3, prompt_len=150, tokens=40, nodes=12, seed=0, **model):
 
 
 if __name__ == "__main__":
-    per_round, worst = run()
+    per_round, worst = run(rope="rope" in sys.argv[1:], fp8="fp8" in sys.argv[1:])
     print(f"{per_round:.2f} tokens a round; logits within {worst:.3f} standard deviations of single steps")

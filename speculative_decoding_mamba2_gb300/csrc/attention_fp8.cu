@@ -1,5 +1,7 @@
 // Attention of a draft tree's nodes over an 8-bit paged cache and their ancestors, and the commit of the accepted path into it
 // (ssm_attention.h).
+#include <type_traits>
+
 #include "attend.cuh"
 #include "decode.cuh"
 
@@ -772,15 +774,23 @@ __global__ void __cluster_dims__(CCTAS, 1, 1) __launch_bounds__(CTHREADS) kv_com
           scale = old;
         } else {  // the block grows: what it holds, in units of the new scale
           const float by = old / scale;
-          for (int r = 0; r < held; ++r) {
-            uint8_t* p = page + r * D;
-            if constexpr (W == 2) {
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-              const float2 y = f16x2_f32(e4m3x2_f16x2(v & 0xffffu)), z = f16x2_f32(e4m3x2_f16x2(v >> 16));
-              *reinterpret_cast<uint32_t*>(p) = f32_e4m3x2(y.x * by, y.y * by) | f32_e4m3x2(z.x * by, z.y * by) << 16;
-            } else {
-              const float2 y = f16x2_f32(e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(p)));
-              *reinterpret_cast<uint16_t*>(p) = (uint16_t)f32_e4m3x2(y.x * by, y.y * by);
+          using Held = typename std::conditional<W == 2, uint32_t, uint16_t>::type;
+#pragma unroll 1
+          for (int r0 = 0; r0 < held; r0 += 8) {  // (eight rows under way: a block may hold a thousand)
+            Held y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (r0 + i < held) y[i] = *reinterpret_cast<const Held*>(page + (r0 + i) * D);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (r0 + i >= held) break;
+              const float2 lo = f16x2_f32(e4m3x2_f16x2(y[i]));
+              uint32_t to = f32_e4m3x2(lo.x * by, lo.y * by);
+              if constexpr (W == 2) {
+                const float2 hi = f16x2_f32(e4m3x2_f16x2(y[i] >> 16));
+                to |= f32_e4m3x2(hi.x * by, hi.y * by) << 16;
+              }
+              *reinterpret_cast<Held*>(page + (r0 + i) * D) = (Held)to;
             }
           }
         }

@@ -4,7 +4,8 @@
 // a 64-bit fraction: p times the table's f / (2 pi) 2^64 modulo 2^64 is exact, so a position of 2^30 costs no precision, and its upper
 // 32 bits are the angle of a sine and cosine in half turns.
 // One thread has eight columns (and their eight partners, half a rotated part on) of a row, makes their sines once and turns
-// a run of heads with them; where there are few rows a run is one head, so that all heads are under way at once.
+// a run of eight heads with them; where there are few rows a run is one head, so that all heads are under way at once.  Bound by
+// HBM where there are many rows: 8191 rows of 40 heads of 128 in 31 us (168 MB: 5.3 TB/s; runs of 4 or 20 heads 33 and 32).
 #include <type_traits>
 
 #include "decode.cuh"
@@ -103,7 +104,9 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   const bool vec = a.rot % (a.interleaved ? 8 : 16) == 0;
   const int v = vec ? 8 : 1, slots = (a.interleaved && vec ? a.rot / 8 : a.rot / 2 / v) + (a.D - a.rot) / v;
   const long long all = (long long)a.n_tok * slots * heads;
-  const int run = all > 4ll * kSMs * RTHREADS * 8 ? (heads < 8 ? heads : 8) : 1;
+  // (the sines of many rows cost more than their heads one after the other: 640 rows, half of each head, 7.7 us with runs of one,
+  // 4.8 with runs of eight; 300 whole ones 4.2 and 5.3)
+  const int run = all > 8ll * kSMs * RTHREADS ? (heads < 8 ? heads : 8) : 1;
   const int runs = (heads + run - 1) / run, per = slots * runs;
   const int rows = per >= RTHREADS ? 1 : RTHREADS / per;
   const unsigned grid = (unsigned)((a.n_tok + rows - 1) / rows);
