@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       mbar_init(smem_u32(&ms->drain[i]), 1);
     }
     for (int i = 0; i < INFOS; ++i) mbar_init(smem_u32(&ms->info_full[i]), 1);
-    mbar_init(smem_u32(&ms->q_full), 4);
+    mbar_init(smem_u32(&ms->q_full), 8);
     mbar_init(smem_u32(&ms->all_done), 1);
     mbar_init(smem_u32(&ms->tree_full), 1);
     ms->stop = 0;
@@ -161,6 +161,67 @@ __global__ void __launch_bounds__(A8THREADS, 2)
   // tile i of the run is cache tile i0 + i - 1, the (i - has_tree)-th of the rings; its S, P and fp16 V are at i % 2, and every
   // barrier of those is one of two: who waits could otherwise find it two phases on, and take that for none
 
+  // Q's two terms: eight columns a thread, a row's columns side by side, two rows at a time, by eight warps.  (Beyond the last row
+  // stands anything: it stays in its own row of S and O, whose maximum is not looked at.)
+  auto split_q = [&](int t) {
+    constexpr int PIECES = D / 8, RI = 256 / PIECES, BATCH = 2;
+    const int piece = t % PIECES, last = min(rows - r0, 128);
+    int r = t / PIECES;
+    const uint16_t* q = a.q + (long long)s * a.n * a.ldq + kvh * a.g * D + piece * 8;
+#pragma unroll 1
+    for (int r1 = 0; r1 < last; r1 += BATCH * RI) {
+      uint32_t w[BATCH][4], most[BATCH];
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const int at = r + b * RI;
+        const unsigned int u = (unsigned)(r0 + at) / (unsigned)a.g;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (at < last) v = *reinterpret_cast<const uint4*>(q + u * a.ldq + (r0 + at - u * a.g) * D);
+        w[b][0] = v.x, w[b][1] = v.y, w[b][2] = v.z, w[b][3] = v.w;
+      }
+      bool odd = false;
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {  // the largest magnitude's bits
+        const uint32_t two = __vmaxu2(__vmaxu2(w[b][0] & 0x7fff7fffu, w[b][1] & 0x7fff7fffu), __vmaxu2(w[b][2] & 0x7fff7fffu, w[b][3] & 0x7fff7fffu));
+        most[b] = max(two & 0xffffu, two >> 16);
+        odd = odd || most[b] >= 0x7f80u;
+      }
+      if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {  // what is not finite becomes NaN, and does not count
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          most[b] = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = w[b][j] & 0x7fffu, hi = w[b][j] >> 16 & 0x7fffu;
+            most[b] = max(most[b], max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+            w[b][j] |= (lo < 0x7f80u ? 0u : 0x7fffu) | (hi < 0x7f80u ? 0u : 0x7fff0000u);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = PIECES / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) most[b] = max(most[b], __shfl_xor_sync(0xffffffffu, most[b], o));
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const float qs = least_scale(most[b] << 16);
+        const uint32_t inv = (0x7f000000u - __float_as_uint(qs)) >> 16, inv2 = inv | inv << 16;  // 1 / 2^e
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = bf16x2_mul(w[b][j], inv2), p = pack_f16x2(bf16_lo(x), bf16_hi(x));  // (exact: 8 of 11 bits)
+          const uint32_t top = f16x2_e4m3x2(p), rest = f16x2_e4m3x2(f16x2_sub(p, e4m3x2_f16x2(top)));
+          hi[j / 2] = j & 1 ? hi[j / 2] | top << 16 : top, lo[j / 2] = j & 1 ? lo[j / 2] | rest << 16 : rest;
+        }
+        const uint32_t to = Sh::off8(r + b * RI, piece / 2) + piece % 2 * 8;
+        *reinterpret_cast<uint2*>(smem + to) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(smem + 128 * D + to) = make_uint2(lo[0], lo[1]);
+        if (piece == 0) ms->qs[r + b * RI] = qs;
+      }
+      r += BATCH * RI;
+    }
+  };
+
   if (warp < 4) {
     take_registers<R_SOFTMAX>();
     const int row = r0 + tid;  // this thread's
@@ -173,64 +234,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) x[c] = row < rows ? q[c] : make_uint4(0, 0, 0, 0);
       }
-      // its two terms: eight columns a thread, a row's columns side by side, two rows at a time.  (Beyond the last row stands
-      // anything: it stays in its own row of S and O, whose maximum is not looked at.)
-      constexpr int PIECES = D / 8, RI = 128 / PIECES, BATCH = 2;
-      const int piece = tid % PIECES, last = min(rows - r0, 128);
-      int r = tid / PIECES;
-      const uint16_t* q = a.q + (long long)s * a.n * a.ldq + kvh * a.g * D + piece * 8;
-#pragma unroll 1
-      for (int r1 = 0; r1 < last; r1 += BATCH * RI) {
-        uint32_t w[BATCH][4], most[BATCH];
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-          const int at = r + b * RI;
-          const unsigned int u = (unsigned)(r0 + at) / (unsigned)a.g;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (at < last) v = *reinterpret_cast<const uint4*>(q + u * a.ldq + (r0 + at - u * a.g) * D);
-          w[b][0] = v.x, w[b][1] = v.y, w[b][2] = v.z, w[b][3] = v.w;
-        }
-        bool odd = false;
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {  // the largest magnitude's bits
-          const uint32_t two = __vmaxu2(__vmaxu2(w[b][0] & 0x7fff7fffu, w[b][1] & 0x7fff7fffu), __vmaxu2(w[b][2] & 0x7fff7fffu, w[b][3] & 0x7fff7fffu));
-          most[b] = max(two & 0xffffu, two >> 16);
-          odd = odd || most[b] >= 0x7f80u;
-        }
-        if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {  // what is not finite becomes NaN, and does not count
-#pragma unroll
-          for (int b = 0; b < BATCH; ++b) {
-            most[b] = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t lo = w[b][j] & 0x7fffu, hi = w[b][j] >> 16 & 0x7fffu;
-              most[b] = max(most[b], max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-              w[b][j] |= (lo < 0x7f80u ? 0u : 0x7fffu) | (hi < 0x7f80u ? 0u : 0x7fff0000u);
-            }
-          }
-        }
-#pragma unroll
-        for (int o = PIECES / 2; o > 0; o >>= 1)
-#pragma unroll
-          for (int b = 0; b < BATCH; ++b) most[b] = max(most[b], __shfl_xor_sync(0xffffffffu, most[b], o));
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-          const float qs = least_scale(most[b] << 16);
-          const uint32_t inv = (0x7f000000u - __float_as_uint(qs)) >> 16, inv2 = inv | inv << 16;  // 1 / 2^e
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t x = bf16x2_mul(w[b][j], inv2), p = pack_f16x2(bf16_lo(x), bf16_hi(x));  // (exact: 8 of 11 bits)
-            const uint32_t top = f16x2_e4m3x2(p), rest = f16x2_e4m3x2(f16x2_sub(p, e4m3x2_f16x2(top)));
-            hi[j / 2] = j & 1 ? hi[j / 2] | top << 16 : top, lo[j / 2] = j & 1 ? lo[j / 2] | rest << 16 : rest;
-          }
-          const uint32_t to = Sh::off8(r + b * RI, piece / 2) + piece % 2 * 8;
-          *reinterpret_cast<uint2*>(smem + to) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(smem + 128 * D + to) = make_uint2(lo[0], lo[1]);
-          if (piece == 0) ms->qs[r + b * RI] = qs;
-        }
-        r += BATCH * RI;
-      }
+      split_q(tid);
       if (has_tree) {
 #pragma unroll
         for (int c = 0; c < D / 8; c += 2) {
@@ -241,17 +245,17 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       }
       tc_fence_before();
       fence_async_smem();
-      named_sync(2, 128);
+      __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
     }
-    // this row's scale of Q, times scale log2 e (with ks at least 2^-66: their product is a normal number)
-    const float qc = fmaxf(ms->qs[tid] * a.scale_log2, 0x1p-60f);
     if (has_tree && warp == 0) ancestor_words(a, s, ms->anc, kvh == 0 && r0 == 0);
 
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
+    bool ok = wait_bar(&ms->q_full, 0, stop);
+    // this row's scale of Q, times scale log2 e (with ks at least 2^-66: their product is a normal number)
+    const float qc = fmaxf(ms->qs[tid] * a.scale_log2, 0x1p-60f);
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < n && ok; ++i) {
       const bool tree = has_tree && i == 0;
       const uint32_t st = tmem + A_S + (i & 1) * KT + lanes;
       ok = wait_bar(&ms->s_full[i & 1], (i >> 1) & 1, stop);  // (and what the tile's keys are)
@@ -431,6 +435,10 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       if (row < rows && splits > 1) a.part_ml[((long long)run * a.Hkv + kvh) * rows + row] = make_float2(m, l);
     }
   } else if (warp >= 8) {
+    split_q(tid - 128);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
     give_registers<R_CONVERT>();
     // ---- V to fp16: 16 rows of a tile to each of four warps ----
     constexpr int PER = D / 8, STEP = 32 / PER, BATCH = 16 / STEP;  // pieces of 8 values in a row, rows at a time, rows of a lane
