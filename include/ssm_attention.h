@@ -88,8 +88,11 @@ int ssm_kv_commit(int32_t n_layers, int32_t n_seq, int32_t n_nodes, int32_t Hkv,
  *                       writes are powers of two).  The rows of a block with any other scale count as absent, where a
  *                       sequence has such rows, and set SSM_STATUS_SCALE
  *   block               a power of two, 8 .. page_size
- * q that is not finite, and values of k that are not, make scores that are NaN.  The other arguments, workspace and rounding as
- * for ssm_tree_attention.
+ * q that is not finite, and values of k that are not, make scores that are NaN.  scale from 2^-40 to 2^40.  The other arguments,
+ * workspace and rounding as for ssm_tree_attention: q loses what is below 2^-18 of its row's largest magnitude, weights are held
+ * in fp16 to 2^-11 of themselves and 2^-31 of a row's largest.
+ * A row of q * scale whose largest magnitude is below 2^-52, and a block of k below 2^-58, may count as that large.  Scales of v
+ * are to lie within 2^100 of each other, and values of v below 2^100: the sums before the division are fp32.
  */
 int ssm_tree_attention_fp8(int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D, const ssm_node *layout,
                            const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
@@ -112,7 +115,8 @@ size_t ssm_tree_attention_fp8_workspace_size(int32_t n_seq, int32_t n_nodes, int
  * own, or takes the larger one that the new rows need, and those older rows are then rounded again (a step down by a
  * power of two: only values below 2^-6 of the scale lose anything).  Rows behind the committed ones keep their bits.
  * A value that is not finite becomes NaN.  A scale outside 2^-100 .. 2^120 where such a block has rows sets
- * SSM_STATUS_SCALE; it is replaced, and the older rows keep their bits.
+ * SSM_STATUS_SCALE; it is replaced, and the older rows keep their bits.  A block is one sequence's: two that share a page have
+ * shared rows in whole blocks only, since a block that grows is rounded again.
  */
 int ssm_kv_commit_fp8(int32_t n_layers, int32_t n_seq, int32_t n_nodes, int32_t Hkv, int32_t D, int32_t max_path,
                       const int32_t *path, const int32_t *path_len, const uint16_t *k, const uint16_t *v,

@@ -28,7 +28,7 @@ extern "C" {
  * in one pass over the logits.
  *   n_rows, n_vocab  rows and columns; n_vocab >= 1
  *   logits           device fp32 (f32 = 1) or bf16 (f32 = 0) [n_rows][ld], ld >= n_vocab, rows of any alignment
- *   scale            positive and finite (1 / temperature)
+ *   scale            1 / temperature, from 2^-100 to 2^100
  *   m, tokens        tokens device int32 [n_rows][m]; -1: none, its logprob is 0; others outside [0, n_vocab): NaN and
  *                    SSM_STATUS_TOKEN_RANGE.  logprob device fp32 [n_rows][m].  m = 0: neither is read or written
  *   entropy          device fp32 [n_rows], or NULL

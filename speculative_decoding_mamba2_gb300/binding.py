@@ -829,7 +829,8 @@ def _rope_args(D: int, turns, q, q_out, k, k_out):
         raise ValueError("q or k: one of them at least")
     if rq is not None and rk is not None and rq != rk:
         raise ValueError("q and k: as many rows each")
-    return Hq, Hkv, rk if rq is None else rq, 2 * turns.numel(), _dev(turns, "turns", torch.int64), (*tq, *tk)
+    pt = _dev(turns, "turns", torch.int64)
+    return Hq, Hkv, rk if rq is None else rq, 2 * turns.numel(), pt, (*tq, *tk)
 
 
 def ssm_rope(D: int, positions, turns, q, q_out, k=None, k_out=None, interleaved: bool = False, amplitude: float = 1.0,

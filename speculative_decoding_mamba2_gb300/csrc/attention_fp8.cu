@@ -12,15 +12,23 @@ namespace {
 //     S = Q . K^T,   P = 2^(S - m),   O += P . V
 // on tcgen05, softmax statistics in a row's thread, two CTAs to an SM, the caches cut into runs.  What 8 bits change:
 //  * K is multiplied as it is (kind::f8f6f4).  Q goes as two e4m3 terms of a row scale that is a power of two: bf16's 8 bits are
-//    4 + 4, so nothing is lost but what is below 2^-18 of a row's largest.  Twice the products at twice bf16's rate, and half the bytes.
-//  * V is made fp16 (exact) by a warp of its own on the way, since P in e4m3 would not do: P goes as fp16, whose 11 bits are
-//    more than bf16's.  Converting V costs a cvt for two values; splitting P into two terms would cost four for two of as many.
+//    4 + 4, so nothing is lost but what is below 2^-18 of a row's largest.  Twice the products at twice bf16's rate, and half the
+//    bytes.  Eight warps make the terms, a row's columns side by side (a thread to a row, in registers, spilled: 10 % of all).
+//  * V is made fp16 (exact) by four warps on the way, since P in e4m3 would not do: P goes as fp16, whose 11 bits are more than
+//    bf16's.  Converting V costs a cvt for two values; splitting P into two terms would cost four for two of as many.  (The
+//    softmax's own warps converting it: one token 24 us, 8 trees 50, wide trees 149; see below for the three.)
 //  * A block's scale of K multiplies its scores in the softmax's own multiply-add.  Its scale of V is part of the weight: m is the
 //    maximum of S + log2 vs, so the weight w = 2^(S + log2 vs - m) fits fp16 whatever the scales, and the row's sum adds w / vs.  Scales
 //    of V count relative to one of them, so that neither sum leaves fp32.
 // Weights are 2^7 times as large (at most 2^15 with a maximum that lags by 2^8), so that fp16 holds them to 2^-31 of the largest.
 // The tree's own rows are bf16 and the first tile of a sequence's first run: their products are bf16's, with Q as it came in the columns
 // that O will take, and their K and V in the places of the first two fp16 tiles of V.
+//
+// In a CUDA graph, 32 query and 8 (wide trees: 4) key/value heads of 128: one token over 16411 rows 21.3 us (34 MB of cache at 1.6 TB/s:
+// a few tiles' round trips to a run, the launch and the join), 8 trees of 16 nodes over up to 8117 rows 40 us, 4 of 40 over up to
+// 40009 rows 113 us (750 TFLOP/s with Q's terms counted once); with heads of 64 19.5, 36 and 96.  Wide trees are bound by the round
+// trips of the two tiles under way (P to P . V to S to the softmax) on top of the products: without copies, conversion or Q's lower
+// terms they take as long; with an idle softmax 15 % less, with that and no products a third less.
 constexpr int A8THREADS = 384;  // 4 softmax warps; copies, MMAs of S, MMAs of P . V, what keys a tile has; 4 warps that make V fp16
 // registers of the three groups of four warps: the block has 384 x 80
 constexpr int R_SOFTMAX = 136, R_MMA = 48, R_CONVERT = 56;
@@ -291,9 +299,8 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         if (!ok) break;
         there &= ms->anc[node];
       }
-      // The loop is as long as it need not be for the tiles that most are: what few need is rolled up, and goes over tensor memory
-      // (scores that do not count, the tree's weights as bf16): with it unrolled in registers wide trees took 136 us, the
-      // instructions of one tile no longer staying near.
+      // What few tiles need (scores that do not count, the tree's weights as bf16) is rolled up and goes over tensor memory: with it
+      // unrolled in registers, the instructions of a tile no longer staying near, wide trees took 136 us and not 125.
       if (__builtin_expect(tree || there != ~0ull, 0)) {
 #pragma unroll 1
         for (int c = 0; c < KT; c += 16) {
@@ -694,7 +701,8 @@ static_assert(2 * 2 * kSMs * 4 <= 2 * Attend8Smem<64>::TILE16, "the lengths stan
 
 // Commit.  A cluster of 8 CTAs for each sequence, a warp for each block of tokens of a layer, head and K or V: the largest of its new
 // rows gives the scale that they need, the block takes that or its own, rows that it holds are rounded again if it grew.  The
-// sequence's length is written by one of the CTAs once all eight have read it, so len_out may be cache_len.
+// sequence's length is written by one of the CTAs once all eight have read it, so len_out may be cache_len.  Bound by latency:
+// 4.2 us for one sequence's path of 5 in 4 layers of 8 heads of 128 (in a CUDA graph; its bytes 0.02), 7.7 for 32 sequences' in 8 layers.
 constexpr int CCTAS = 8, CTHREADS = 512;
 
 template <int D>

@@ -330,6 +330,7 @@ extern "C" int ssm_tree_attention_fp8(int32_t n_seq, int32_t n_nodes, int32_t Hq
   if (int rc = check_attend(fn, n_seq, n_nodes, Hq, Hkv, D, layout, q, ldq, k, ldk, v, ldv, k_pages, v_pages, n_pages, page_size,
                             page_table, max_pages, cache_len, max_cache_len, scale, o, ldo, workspace, dev_status, &f.a))
     return rc;
+  if (!(scale >= 0x1p-40f && scale <= 0x1p40f)) return pfail(SSM_ERR_RANGE, fn, "scale must be in [2^-40, 2^40]");
   f.block_shift = block_shift(block, page_size);
   if (f.block_shift < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "block must be a power of two from 8 to page_size");
   if (max_cache_len > 0 && (!k_scales || !v_scales)) return pfail(SSM_ERR_INVALID_ARG, fn, "k_scales or v_scales is NULL");
@@ -434,13 +435,15 @@ extern "C" int ssm_token_scores(int32_t n_rows, int32_t n_vocab, const void* log
   const char* fn = "ssm_token_scores";
   if (n_rows < 0 || n_rows > (1 << 27)) return pfail(SSM_ERR_INVALID_ARG, fn, "n_rows must be in [0, 2^27]");
   if (n_vocab < 1 || ld < n_vocab) return pfail(SSM_ERR_INVALID_ARG, fn, "n_vocab must be >= 1, ld at least that");
-  if (!(scale > 0.f) || isinf(scale)) return pfail(SSM_ERR_RANGE, fn, "scale must be positive and finite");
+  if (!(scale >= 0x1p-100f && scale <= 0x1p100f)) return pfail(SSM_ERR_RANGE, fn, "scale must be in [2^-100, 2^100]");
   if (m < 0 || k < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "m and k must be >= 0");
   if (k > SSM_MAX_TOP) return pfail(SSM_ERR_CAPACITY, fn, "k above SSM_MAX_TOP");
   if (k > n_vocab) return pfail(SSM_ERR_INVALID_ARG, fn, "k above n_vocab");
   if (n_rows > 0 && (!logits || (m > 0 && (!tokens || !logprob)) || (k > 0 && !top)))
     return pfail(SSM_ERR_INVALID_ARG, fn, "a pointer is NULL");
   if ((uintptr_t)logits & (f32 ? 3 : 1)) return pfail(SSM_ERR_INVALID_ARG, fn, "logits must be aligned to an element");
+  if (((uintptr_t)tokens | (uintptr_t)logprob | (uintptr_t)entropy | (uintptr_t)top | (uintptr_t)top_logprob) & 3)
+    return pfail(SSM_ERR_INVALID_ARG, fn, "tokens and the results must be 4-byte aligned");
   ScoreArgs a{};
   a.T = n_rows, a.V = n_vocab, a.m = m, a.k = k, a.x = logits, a.f32 = f32 != 0, a.ld = ld, a.scale = scale;
   a.tok = tokens, a.logprob = logprob, a.entropy = entropy, a.top = top, a.top_logprob = top_logprob, a.status = dev_status;

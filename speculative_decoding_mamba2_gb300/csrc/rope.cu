@@ -109,7 +109,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   const int run = all > 8ll * kSMs * RTHREADS ? (heads < 8 ? heads : 8) : 1;
   const int runs = (heads + run - 1) / run, per = slots * runs;
   const int rows = per >= RTHREADS ? 1 : RTHREADS / per;
-  const unsigned grid = (unsigned)((a.n_tok + rows - 1) / rows);
+  const unsigned grid = ((unsigned)a.n_tok + rows - 1) / rows;
   if (vec && a.interleaved)
     rope_kernel<8, true><<<grid, RTHREADS, 0, s>>>(a, run, runs, rows);
   else if (vec)

@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(STHREADS, sblocks(sizeof(T) == 4)) scores_kern
   const Row<T> row(reinterpret_cast<const T*>(a.x) + (long long)t * a.ld, a.V);
   const int per = (row.vecs + parts - 1) / parts, j0 = min(part * per, row.vecs), j1 = min(j0 + per, row.vecs);
   const float c = a.scale * 1.4426950408889634f;
-  // Nothing below this has a weight, and (x - m) c stays finite from it on, which 0 times minus infinity would not be.
+  // Nothing below this has a weight, and (x - m) c stays finite from it on, which 0 times minus infinity would not be.  (With m
+  // itself as far from 0 on either side logits are taken one by one.)
   const float low = __uint_as_float(__float_as_uint(-1e38f / fmaxf(c, 1.f)) & 0xffff0000u);
   const uint32_t low2 = __float_as_uint(low) >> 16 | __float_as_uint(low);
   if (parts > 1) cluster.barrier_arrive();  // (awaited before another block's shared memory is written)
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(STHREADS, sblocks(sizeof(T) == 4)) scores_kern
     l += p, s = fmaf(p, fmaxf(d, -200.f), s);
   };
   auto add = [&](const Vec& u, float ref) {  // a vector's logits
-    if (__builtin_expect(ref < low, 0)) {  // they are all below it
+    if (__builtin_expect(fabsf(ref) > -low, 0)) {
       float v[E];
       values(u, v);
 #pragma unroll 1
@@ -411,14 +412,14 @@ __global__ void __launch_bounds__(STHREADS, sblocks(sizeof(T) == 4)) scores_kern
       __syncthreads();
     }
   }
-  const float log_l = logf(l);
+  const float log_l = logf(l), twice = 2.f * a.scale;
   if (tid == 0 && a.entropy) a.entropy[t] = log_l - 0.6931471805599453f * (s / l);
   for (int i = tid; i < a.m; i += STHREADS) {
     if (i >= STHREADS) {
       tok = a.tok[(long long)t * a.m + i];
       if (tok >= 0 && tok < a.V) given = row.one(tok);
     }
-    float r = fmaf(given - m, a.scale, -log_l);
+    float r = fmaf(0.5f * given - 0.5f * m, twice, -log_l);  // (halves: the difference itself may be beyond fp32)
     if (tok == -1) {
       r = 0.f;
     } else if (tok < 0 || tok >= a.V) {
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(STHREADS, sblocks(sizeof(T) == 4)) scores_kern
   if (TOP && tid < a.k) {
     const u64 key = sm.sorted[tid];
     a.top[(long long)t * a.k + tid] = (int)(0xffffffffu - (unsigned int)key);
-    if (a.top_logprob) a.top_logprob[(long long)t * a.k + tid] = fmaf(value_of((unsigned int)(key >> 32)) - m, a.scale, -log_l);
+    if (a.top_logprob) a.top_logprob[(long long)t * a.k + tid] = fmaf(0.5f * value_of((unsigned int)(key >> 32)) - 0.5f * m, twice, -log_l);
   }
 }
 static_assert(RUNS * STHREADS <= 65536 && 2 * 31 < STHREADS, "a run's number in 16 bits, a thread to each logit of the edge");

@@ -44,15 +44,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
       : "memory");
 }
 // the same of 8-bit operands (kind::f8f6f4; both e4m3 where the descriptor's type fields are 0), 32 of them along K; HI: the upper
-// word of B's (and A's) shared-memory descriptor
-template <uint32_t IDESC, uint32_t HI>
-__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint32_t b_lo, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b_lo), "n"(IDESC), "r"((uint32_t)acc), "n"(HI)
-      : "memory");
-}
+// word of both shared-memory descriptors
 template <uint32_t IDESC, uint32_t HI>
 __device__ __forceinline__ void mma8_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, bool acc) {
   asm volatile(
@@ -141,15 +133,6 @@ __device__ __forceinline__ bool wait_bar(unsigned long long* bar, uint32_t parit
   }
   *stop = 1;
   return false;
-}
-// whether a phase of an mbarrier is past, at once (where it is, what its arrivals wrote can be read)
-__device__ __forceinline__ bool mbar_past(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(ok)
-               : "r"(bar), "r"(parity)
-               : "memory");
-  return ok != 0;
 }
 // ---- host ----
 // a grid whose blocks may be placed while the stream's kernel before it ends; they call grid_dependency_wait before they

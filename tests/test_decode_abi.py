@@ -59,6 +59,10 @@ BAD += [("ssm_token_scores", SCORES, kw, code) for kw, code in [
     (dict(scale=float("inf")), RANGE), (dict(scale=float("nan")), RANGE), (dict(m=-1), INV), (dict(k=-1), INV), (dict(k=33), CAP),
     (dict(V=3, k=4), INV), (dict(x=None), INV), (dict(x=ODD), INV), (dict(tok=None), INV), (dict(lp=None), INV), (dict(top=None), INV),
     (dict(f32=0, x=ctypes.c_void_p(4097)), INV)]]
+BAD += [("ssm_tree_attention_fp8", ATTEND, dict(scale=v), RANGE) for v in (2.0 ** -41, 2.0 ** 41, float("inf"))]
+BAD += [("ssm_token_scores", SCORES, kw, code) for kw, code in [
+    (dict(scale=2.0 ** -101), RANGE), (dict(scale=2.0 ** 101), RANGE), (dict(tok=ODD), INV), (dict(lp=ODD), INV), (dict(h=ODD), INV),
+    (dict(top=ODD), INV), (dict(tlp=ODD), INV)]]
 
 
 @pytest.mark.parametrize("fn,base,kw,code", BAD, ids=lambda v: str(v)[:60] if not isinstance(v, dict) or len(v) < 3 else "")

@@ -417,3 +417,52 @@ def test_fp8_pages_past_32_bit_offsets():
     for x in far:
         a, b, was = (t.view(torch.uint8) for t in (far[x][base:].contiguous(), near_[x], c[x]))
         assert torch.equal(a, b) and not torch.equal(b, was)
+
+
+def test_tree_attention_fp8_a_cache_of_zeros():
+    """Keys and values that are all 0, in blocks of the least scale, as a commit of zeros leaves them."""
+    c = case(20, 2, 9, 2, 2, 128, [3000, 65], 32, 8)
+    for x in "kv":
+        c[x + "p"] = torch.zeros_like(c[x + "p"])
+        c[x + "s"] = torch.full_like(c[x + "s"], 2.0 ** -100)
+        c[x + "p64"] = np.zeros_like(c[x + "p64"])
+    o, status = run(c)
+    assert status == 0
+    for s in range(2):
+        check(c, o, s)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_tree_attention_fp8_graphs_that_share_a_workspace(D):
+    """Two captured calls over one workspace, replayed in turn after the lengths and q have changed: as called one by one."""
+    from speculative_decoding_mamba2_gb300 import (ssm_tree_attention_fp8, ssm_tree_attention_fp8_workspace_size,
+                                                   ssm_tree_layout_build)
+    cases = [case(21, 1, 16, 4, 2, D, [4000], 64, 16), case(22, 5, 1, 8, 2, D, [700, 0, 64, 1500, 3], 32, 32)]
+    sizes = [ssm_tree_attention_fp8_workspace_size(c["S"], c["n"], c["Hq"], c["Hkv"], D, max(c["lens"])) for c in cases]
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device="cuda")
+    calls = []
+    for c in cases:
+        lay, table, lens = torch.from_numpy(ssm_tree_layout_build(c["par"])[0]).cuda(), ints(c["table"]), ints(c["lens"])
+        o, status = torch.empty(c["S"] * c["n"], c["Hq"] * D, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+        def call(c=c, lay=lay, table=table, lens=lens, o=o, status=status):
+            ssm_tree_attention_fp8(c["S"], c["n"], c["Hq"], c["Hkv"], D, lay, c["q"], c["k"], c["v"], c["kp"], c["vp"], c["ks"], c["vs"],
+                                   table, lens, max(c["lens"]), c["scale"], o, ws, status=status)
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        calls.append((c, graph, lens, o, status, call))  # (the call holds the layout and the table)
+    for turn in range(3):
+        for c, graph, lens, o, status, _ in calls:
+            less = [max(l - 13 * turn, 0) for l in c["lens"]]
+            lens.copy_(ints(less))
+            c["q"].mul_(-1.0)
+            c["q64"] = -c["q64"]
+            o.fill_(9.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert int(status) == 0
+            for s in range(c["S"]):
+                check(c, host(o).reshape(c["S"], c["n"], c["Hq"], D), s, less[s])

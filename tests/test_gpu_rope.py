@@ -134,3 +134,20 @@ def test_tree_rope_bad_device_data():
     L.ssm_tree_rope(2, 9, 64, torch.from_numpy(lay).cuda(), ints([-3, 50]), L.ssm_rope_turns(freq).cuda(), q, out, status=status)
     assert int(status) == L.SSM_STATUS_BAD_LAYOUT | L.SSM_STATUS_SEQ_RANGE
     near(out, qv, pos, freq, False, 1.0, 64)
+
+
+def test_rope_of_as_many_rows_as_an_int32_counts():
+    """2^31 - 1 rows of one head of 8: the first and the last ones turned, and those between as they were where the position is 0."""
+    import speculative_decoding_mamba2_gb300 as L
+    T = 2 ** 31 - 1
+    freq = L.ssm_rope_frequencies(8)
+    x = torch.zeros(T, 8, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    some = torch.tensor([0, 1, 2 ** 30, 2 ** 30 + 1, T - 258, T - 2, T - 1], device="cuda")
+    put, v = bf(np.random.default_rng(4).standard_normal((7, 8)))
+    x[some] = put
+    at = [3, 0, 70, 0, 12, 5, 9]
+    pos[some] = ints(at)
+    L.ssm_rope(8, pos, L.ssm_rope_turns(freq).cuda(), x, x)
+    near(x[some], v.reshape(7, 1, 8), np.array(at, float), freq, False, 1.0, 8)
+    np.testing.assert_array_equal(host(x[some[[1, 3]]]), v[[1, 3]])

@@ -140,6 +140,28 @@ def test_token_scores_far_from_zero():
     check(x, rng.integers(0, 30011, (2, 3)), 5)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("scale", [2.0 ** -100, 1.0, 2.0 ** 100])
+def test_token_scores_as_far_from_zero_as_there_are(scale, dtype):
+    """The largest and the lowest values of fp32 side by side, at any temperature: nothing that is not a number; what a log
+    probability is below fp32 becomes minus infinity."""
+    rng = np.random.default_rng([12, int(np.log2(scale)) + 200])
+    x = torch.from_numpy(rng.choice([-3e38, -1e38, -1.0, 0.0, 2.0, 1e38], (4, 9001))).to(dtype).cuda()
+    x[0, ::1000], x[1] = 3e38, -3e38
+    x[1, 5], x[2, 7], x[3] = -1e38, 2e38, 1e30
+    x[3, 9:] = -1e30
+    tok = rng.integers(0, 9001, (4, 3))
+    tok[:, 0] = 5
+    lp, h, top, tlp, status = run(x, tok, 6, scale)
+    want = oracle.token_scores(x.double().cpu().numpy(), tok, 6, scale)
+    low = lambda v: np.where(v < -float(np.finfo(np.float32).max), -np.inf, v)  # noqa: E731
+    E = (9001 / 512 + 64) * 2.0 ** -24 + (np.log(9001) + 32) * 2.0 ** -22 + 2.0 ** -20
+    assert status == 0
+    np.testing.assert_array_equal(top, want[2])
+    for got, ref, e in ((lp, low(want[0]), E), (tlp, low(want[3]), E), (h, want[1], E * (1 + np.log(9001)))):
+        np.testing.assert_allclose(got, ref, rtol=2.0 ** -22, atol=e)
+
+
 def test_token_scores_bad_tokens():
     from speculative_decoding_mamba2_gb300 import SSM_STATUS_TOKEN_RANGE
     rng = np.random.default_rng(8)
