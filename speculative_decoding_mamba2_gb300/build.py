@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["api.cu", "verify.cu", "verify_tc.cu", "commit.cu", "draft.cu", "noalloc.cu", "chain.cu", "gemm.cu", "norm.cu",
            "layer_api.cu", "draft_tree.cu", "selftest.cu", "prompt.cu", "prompt_scan.cu", "prompt_scan_tc.cu", "attention.cu",
-           "attention_fp8.cu", "rope.cu", "scores.cu", "prompt_api.cu", "layout.cpp"]
+           "attention_fp8.cu", "attention_fp8_few.cu", "rope.cu", "scores.cu", "prompt_api.cu", "layout.cpp"]
 HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "draft_tree.cuh", "log_apply.cuh", "tc.cuh", "mma_tiles.cuh",
                                            "prompt.cuh", "umma.cuh", "attend.cuh", "decode.cuh")] + \
     [os.path.join(INCLUDE, h) for h in ("ssm_tree.h", "ssm_layer.h", "ssm_prompt.h", "ssm_attention.h",

@@ -846,6 +846,7 @@ cudaError_t launch_tree_attention_fp8(const AttendFp8Args& args, void* workspace
   AttendFp8Args f = args;
   const AttendPlan p = plan_attend(f.a.S, f.a.n, f.a.Hq, f.a.Hkv, f.a.max_len);
   lay_workspace(f.a, p, workspace);
+  if (f.a.n * f.a.g <= kFewRows) return launch_few_attention_fp8(f, p.max_runs, s);
   return f.a.D == 64 ? run_attend8<64>(f, p, s) : run_attend8<128>(f, p, s);
 }
 

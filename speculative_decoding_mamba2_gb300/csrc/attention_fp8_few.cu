@@ -1,0 +1,423 @@
+// Tree attention over an 8-bit paged cache for up to 16 query rows of a key/value head (ssm_attention.h): single tokens, small trees.
+//
+// The plan of attention_fp8.cu has 128 rows and tiles of 64 keys that pass from warp to warp; a few rows want the cache read as
+// fast as memory gives it instead.  Here each warp takes 16 keys at a time by itself, straight from global memory into the fragments
+// of warp-level products (a few rows use little of any tensor core), with no barrier before the end:
+//     S^T = K . Q^T,   P^T = 2^(S^T + log2 vs - m),   O^T += V^T . P^T
+// with K and V made fp16 (exact) in registers, Q fp16 under a row scale that is a power of two (exact down to 2^-38 of a row's
+// largest).  The columns of K's rows may stand in any order along a product's inner axis, and those of V's rows in any order along
+// its outer one: a lane takes 16 bytes in a row of both, four lanes 64 bytes of a row of K, eight a row of V; two keys' bytes of V are
+// put side by side by byte permutes before they are converted.  P^T goes from accumulators to operands by transposing 8 x 8 of fp16.
+// Scales, weights and sums are those of attention_fp8.cu; the warps' sums are joined in shared memory, runs of a cache as there.
+#include "attend.cuh"
+#include "decode.cuh"
+
+namespace ssmtree {
+namespace {
+
+constexpr float kShift = 7.f;  // weights are 2^7 times as large, so that fp16 holds them to 2^-31 of the largest
+
+template <int D, int NT>  // NT: eights of rows
+struct Few {
+  static constexpr int WARPS = NT == 1 ? 8 : 6, THREADS = WARPS * 32, ROWS = 8 * NT, LD = D + 4;
+  static constexpr int BYTES = WARPS * ROWS * LD * 4;
+};
+template <int D, int NT>
+struct FewMisc {
+  using Sh = Few<D, NT>;
+  unsigned long long anc[64];
+  SplitScratch split;
+  float m[Sh::WARPS][Sh::ROWS], l[Sh::WARPS][Sh::ROWS];
+  unsigned int odd;  // tree rows with a value of v that is not finite
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float nan_unless_finite(float x) {
+  return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x;
+}
+// a lane's bytes of a row (read once: they need no place in L1)
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t (&x)[WORDS], const void* p, bool there) {
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) x[i] = 0;
+  if (!there) return;
+  if constexpr (WORDS == 4)
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "l"(p) : "memory");
+  else
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "l"(p) : "memory");
+}
+
+// a warp's rows so far: of each eight, this lane's are 2 (lane % 4) and the one behind
+template <int D, int NT>
+struct FewState {
+  float o[D / 16][NT][4];  // columns (lane / 4) D/8 + 2 j, of the two rows, and the column behind
+  float m[NT][2], l[NT][2];
+
+  // scores in powers of two (of keys lane/4 of two eights; minus infinity: does not count) to weights; r: what they count in the sum
+  __device__ __forceinline__ void weigh(float (&x)[NT][4], float ra, float rb) {
+    bool grows = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) grows = grows || fmaxf(x[t][0], x[t][2]) > m[t][0] + 8.f || fmaxf(x[t][1], x[t][3]) > m[t][1] + 8.f;
+    if (__any_sync(0xffffffffu, grows)) {  // what there is so far of such rows is made relative to the new maximum
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float by[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(x[t][e], x[t][2 + e]);
+#pragma unroll
+          for (int s = 4; s < 32; s *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+          if (!(mx > m[t][e] + 8.f)) mx = m[t][e];  // (a row's weights do not depend on the other rows)
+          by[e] = mx == m[t][e] ? 1.f : exp2_sfu(m[t][e] - mx);
+          m[t][e] = mx, l[t][e] *= by[e];
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) o[j][t][0] *= by[0], o[j][t][1] *= by[1], o[j][t][2] *= by[0], o[j][t][3] *= by[1];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = (m[t][e] == -INFINITY ? 0.f : m[t][e]) - kShift;
+        x[t][e] = exp2_sfu(x[t][e] - ref), x[t][2 + e] = exp2_sfu(x[t][2 + e] - ref);
+        l[t][e] = fmaf(x[t][e], ra, fmaf(x[t][2 + e], rb, l[t][e]));
+      }
+  }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(AttendFp8Args f) {
+  using Sh = Few<D, NT>;
+  constexpr int W = Sh::WARPS, KI = D / 64, VW = D / 32;  // 64-column parts of a row; words of V's row in a lane
+  const AttendArgs& a = f.a;
+  extern __shared__ __align__(16) float o_s[];
+  __shared__ FewMisc<D, NT> ms;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int rows = a.n * a.g, run = blockIdx.x, kvh = blockIdx.y;
+  if (tid == 0) ms.odd = 0;
+  grid_dependency_wait();  // what the stream's kernels before this one write
+  launch_dependents();
+  int s = run, sp = 0, tps = 1 << 25, splits = 1;
+  if (a.max_runs > 0) {
+    int* tiles = reinterpret_cast<int*>(o_s);  // space not in use yet
+    int first;
+    tps = choose_split<Sh::THREADS>(a, a.Hkv, tiles, &ms.split);
+    if (!find_run(a.S, tiles, tps, run, s, first, splits)) return;
+    sp = run - first;
+    if (sp == 0 && kvh == 0 && tid == 0) a.runs[s] = make_int2(first, splits);
+  }
+  int len = __shfl_sync(0xffffffffu, cached_rows(a, s), 0);
+  if (len < 0) {
+    if (sp == 0 && kvh == 0 && tid == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
+    len = 0;
+  }
+  // the run's keys of the cache, k0 .. end - 1, in steps of 16: those of this warp are warp + i W, i < mine
+  const bool has_tree = sp == 0;
+  const int t0 = sp * tps + has_tree - 1, t1 = min(sp * tps + tps - 1, (len + KT - 1) / KT), k0 = t0 * KT, end = min(t1 * KT, len);
+  const int steps = max(end - k0 + 15, 0) / 16, mine = (steps - warp + W - 1) / W;
+  const int32_t* table = a.table + (long long)s * a.max_pages;
+
+  // Of 16 steps of the warp a lane knows the eight keys lane & 1 of the lane / 2-th: their first row among the pages' (-1: no such
+  // rows, or their page is out of range), the scales, how many there are.  Pages are asked for 16 steps ahead.
+  auto row_of = [&](int b) {
+    const int i = 16 * b + (lane >> 1), at = k0 + (warp + i * W) * 16 + (lane & 1) * 8;
+    if (i >= mine || at >= end) return -1;
+    const int pg = table[at >> a.page_shift];
+    if (pg < 0 || pg >= a.n_pages) {
+      flag(a.status, SSM_STATUS_SEQ_RANGE);
+      return -1;
+    }
+    return ((pg * a.Hkv + kvh) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+  };
+  int at_row = row_of(0), next_row = -1, there = 0;
+  float ks = 1.f, lv = 0.f, rv = 1.f, v0 = 1.f;
+
+  uint32_t kx[KI][2][4], vx[2][2][VW];
+  auto load_k = [&](int ra, int rb) {
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      load_words(kx[i][0], f.kp + ((long long)ra + g) * D + i * 64 + c * 16, ra >= 0);
+      load_words(kx[i][1], f.kp + ((long long)rb + g) * D + i * 64 + c * 16, rb >= 0);
+    }
+  };
+  auto load_v = [&](int ra, int rb) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      load_words(vx[0][e], f.vp + ((long long)ra + 2 * c + e) * D + g * (D / 8), ra >= 0);
+      load_words(vx[1][e], f.vp + ((long long)rb + 2 * c + e) * D + g * (D / 8), rb >= 0);
+    }
+  };
+  auto row_at = [&](int i, int h) {  // of step i (the 16 of now or the first of the next ones)
+    return __shfl_sync(0xffffffffu, i & 15 ? at_row : next_row, (2 * i & 31) + h);
+  };
+  int ra = __shfl_sync(0xffffffffu, at_row, 0), rb = __shfl_sync(0xffffffffu, at_row, 1);
+  load_k(ra, rb);
+  load_v(ra, rb);
+
+  FewState<D, NT> st;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    st.m[t][0] = st.m[t][1] = -INFINITY, st.l[t][0] = st.l[t][1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.o[j][t][e] = 0.f;
+  }
+
+  // Q: of row g of each eight the columns that a lane has of K's rows, as fp16 of a power of two
+  uint32_t qx[NT][KI][4][2];
+  float qc[NT][2];
+  auto q_row = [&](int t) {
+    const int row = min(8 * t + g, rows - 1);
+    return reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + row / a.g) * a.ldq + (kvh * a.g + row % a.g) * D + c * 16);
+  };
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    uint32_t most = 0;
+    const uint4* q = q_row(t);
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const uint4 x = q[i * 8], y = q[i * 8 + 1];
+      const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        qx[t][i][j / 2][j & 1] = w[j];
+        const uint32_t lo = w[j] << 16 & 0x7fffffffu, hi = w[j] & 0x7fff0000u;
+        most = max(most, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
+      }
+    }
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    const int e = min(14 - ((int)(most >> 23) - 127), 100);  // the largest to 2^14 .. 2^15
+    const float by = __uint_as_float((uint32_t)(127 + e) << 23), back = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < KI; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t& w = qx[t][i][j / 2][j & 1];
+        w = pack_f16x2(nan_unless_finite(bf16_lo(w)) * by, nan_unless_finite(bf16_hi(w)) * by);
+      }
+    qc[t][0] = __shfl_sync(0xffffffffu, back, 8 * c), qc[t][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+  }
+
+  if (has_tree && warp == 0) {  // the tree's own rows, up to 16, in bf16
+    ancestor_words(a, s, ms.anc, kvh == 0);
+    __syncwarp();
+    const long long row0 = (long long)s * a.n;
+    float x[NT][4] = {};
+#pragma unroll 1
+    for (int i = 0; i < KI; ++i) {
+      uint32_t w[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4* p = reinterpret_cast<const uint4*>(a.k + (row0 + g + 8 * h) * a.ldk + kvh * D + i * 64 + c * 16);
+        uint4 y[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (g + 8 * h < a.n) y[0] = p[0], y[1] = p[1];
+        w[h][0] = y[0].x, w[h][1] = y[0].y, w[h][2] = y[0].z, w[h][3] = y[0].w;
+        w[h][4] = y[1].x, w[h][5] = y[1].y, w[h][6] = y[1].z, w[h][7] = y[1].w;
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint4 y0 = q_row(t)[i * 8], y1 = q_row(t)[i * 8 + 1];
+        const uint32_t q[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const uint32_t ka[4] = {w[0][j], w[1][j], w[0][j + 1], w[1][j + 1]}, qb[2] = {q[j], q[j + 1]};
+          mma_bf16(x[t], ka, qb);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int node = min(8 * t + 2 * c + (e & 1), rows - 1) / a.g;
+        x[t][e] = ms.anc[node] >> (g + (e >> 1) * 8) & 1 ? x[t][e] * a.scale_log2 : -INFINITY;
+      }
+    st.weigh(x, 1.f, 1.f);
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) p[t][0] = transposed(pack_bf16x2(x[t][0], x[t][1])), p[t][1] = transposed(pack_bf16x2(x[t][2], x[t][3]));
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {  // eight of a lane's columns
+      uint32_t w[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int key = 2 * c + (k & 1) + (k >> 1) * 8;
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (key < a.n) y = *reinterpret_cast<const uint4*>(a.v + (row0 + key) * a.ldv + kvh * D + g * (D / 8) + h * 8);
+        w[k][0] = finite_or_zero(y.x), w[k][1] = finite_or_zero(y.y), w[k][2] = finite_or_zero(y.z), w[k][3] = finite_or_zero(y.w);
+        if (w[k][0] != y.x || w[k][1] != y.y || w[k][2] != y.z || w[k][3] != y.w) atomicOr(&ms.odd, 1u << key);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t va[4] = {__byte_perm(w[0][j], w[1][j], 0x5410), __byte_perm(w[0][j], w[1][j], 0x7632),
+                                __byte_perm(w[2][j], w[3][j], 0x5410), __byte_perm(w[2][j], w[3][j], 0x7632)};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_bf16(st.o[4 * h + j][t], va, p[t]);
+      }
+    }
+  }
+
+#pragma unroll 1
+  for (int i = 0; i < mine; ++i) {
+    if ((i & 15) == 0) {  // what the next 16 steps' keys are
+      if (i > 0) at_row = next_row;
+      float2 sc = make_float2(1.f, 1.f);
+      if (at_row >= 0) sc = make_float2(f.ks[at_row >> f.block_shift], f.vs[at_row >> f.block_shift]);
+      next_row = row_of(i / 16 + 1);
+      const bool good = good_scale(sc.x) && good_scale(sc.y);
+      if (!good) {
+        flag(a.status, SSM_STATUS_SCALE);
+        sc = make_float2(1.f, 1.f);
+      }
+      there = at_row >= 0 && good ? min(end - (k0 + (warp + (i + (lane >> 1)) * W) * 16 + (lane & 1) * 8), 8) : 0;
+      if (i == 0 && !(has_tree && warp == 0)) {  // what this warp's scales of v are relative to: one of them, as a power of two
+        const unsigned int top = __reduce_max_sync(0xffffffffu, there > 0 ? __float_as_uint(sc.y) & 0x7f800000u : 0u);
+        v0 = top ? __uint_as_float(top) : 1.f;
+      }
+      const float rel = fminf(fmaxf(sc.y / v0, 0x1p-120f), 0x1p120f);
+      ks = sc.x, lv = log2f(rel), rv = 1.f / rel;
+    }
+    const int from = 2 * i & 31;
+    const int ta = __shfl_sync(0xffffffffu, there, from), tb = __shfl_sync(0xffffffffu, there, from + 1);
+    const float ka = __shfl_sync(0xffffffffu, ks, from), kb = __shfl_sync(0xffffffffu, ks, from + 1);
+    const float la = __shfl_sync(0xffffffffu, lv, from), lb = __shfl_sync(0xffffffffu, lv, from + 1);
+    const float ia = __shfl_sync(0xffffffffu, rv, from), ib = __shfl_sync(0xffffffffu, rv, from + 1);
+    ra = row_at(i + 1, 0), rb = row_at(i + 1, 1);
+    float x[NT][4] = {};
+#pragma unroll
+    for (int h = 0; h < KI; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t ak[4] = {e4m3x2_f16x2(kx[h][0][j]), e4m3x2_f16x2(kx[h][1][j]), e4m3x2_f16x2(kx[h][0][j] >> 16),
+                                e4m3x2_f16x2(kx[h][1][j] >> 16)};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_f16(x[t], ak, qx[t][h][j][0], qx[t][h][j][1]);
+      }
+    if (i + 1 < mine) load_k(ra, rb);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float y = fmaf(x[t][e], qc[t][e & 1] * (e < 2 ? ka : kb), e < 2 ? la : lb);
+        x[t][e] = g < (e < 2 ? ta : tb) ? y : -INFINITY;
+      }
+    st.weigh(x, ia, ib);
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) p[t][0] = transposed(pack_f16x2(x[t][0], x[t][1])), p[t][1] = transposed(pack_f16x2(x[t][2], x[t][3]));
+    if (ta + tb < 16) {  // (whatever stands where no key is)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int w = 0; w < VW; ++w) vx[0][e][w] = 2 * c + e < ta ? vx[0][e][w] : 0u, vx[1][e][w] = 2 * c + e < tb ? vx[1][e][w] : 0u;
+    }
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      const uint32_t a01 = __byte_perm(vx[0][0][w], vx[0][1][w], 0x5140), a23 = __byte_perm(vx[0][0][w], vx[0][1][w], 0x7362);
+      const uint32_t b01 = __byte_perm(vx[1][0][w], vx[1][1][w], 0x5140), b23 = __byte_perm(vx[1][0][w], vx[1][1][w], 0x7362);
+      const uint32_t v01[4] = {e4m3x2_f16x2(a01), e4m3x2_f16x2(a01 >> 16), e4m3x2_f16x2(b01), e4m3x2_f16x2(b01 >> 16)};
+      const uint32_t v23[4] = {e4m3x2_f16x2(a23), e4m3x2_f16x2(a23 >> 16), e4m3x2_f16x2(b23), e4m3x2_f16x2(b23 >> 16)};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma_f16(st.o[2 * w][t], v01, p[t][0], p[t][1]), mma_f16(st.o[2 * w + 1][t], v23, p[t][0], p[t][1]);
+    }
+    if (i + 1 < mine) load_v(ra, rb);
+  }
+
+  // the warps' sums as one
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = st.l[t][e];
+#pragma unroll
+      for (int k = 4; k < 32; k *= 2) l += __shfl_xor_sync(0xffffffffu, l, k);
+      if (g == 0) ms.m[warp][8 * t + 2 * c + e] = st.m[t][e], ms.l[warp][8 * t + 2 * c + e] = l;
+    }
+  __syncthreads();  // (the tile counts are not read any more either)
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = 8 * t + 2 * c + e;
+      float top = ms.m[0][row];
+#pragma unroll
+      for (int w = 1; w < W; ++w) top = fmaxf(top, ms.m[w][row]);
+      const float by = st.m[t][e] == -INFINITY ? 0.f : exp2_sfu(st.m[t][e] - top) * v0;
+      float* to = o_s + (warp * Sh::ROWS + row) * Sh::LD + g * (D / 8);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) *reinterpret_cast<float2*>(to + 2 * j) = make_float2(st.o[j][t][e] * by, st.o[j][t][2 + e] * by);
+    }
+  __syncthreads();
+  for (int u = tid; u < rows * (D / 4); u += Sh::THREADS) {
+    const int row = u / (D / 4), col = u % (D / 4) * 4, node = row / a.g, head = kvh * a.g + row % a.g;
+    float top = ms.m[0][row], l = 0.f;
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = fmaxf(top, ms.m[w][row]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(o_s + (w * Sh::ROWS + row) * Sh::LD + col);
+      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+      l = fmaf(ms.l[w][row], ms.m[w][row] == -INFINITY ? 0.f : exp2_sfu(ms.m[w][row] - top), l);
+    }
+    const long long tok = (long long)s * a.n + node;
+    if (has_tree) {
+#pragma unroll 1
+      for (unsigned int odd = ms.odd & (unsigned int)ms.anc[node]; odd; odd &= odd - 1) {  // not finite whatever its weight
+        const uint2 x = *reinterpret_cast<const uint2*>(a.v + ((long long)s * a.n + __ffs((int)odd) - 1) * a.ldv + kvh * D + col);
+        const uint2 out = make_uint2(x.x ^ finite_or_zero(x.x), x.y ^ finite_or_zero(x.y));
+        if (out.x & 0xffffu) o.x += bf16_lo(x.x);
+        if (out.x & 0xffff0000u) o.y += bf16_hi(x.x);
+        if (out.y & 0xffffu) o.z += bf16_lo(x.y);
+        if (out.y & 0xffff0000u) o.w += bf16_hi(x.y);
+      }
+    }
+    if (splits == 1) {
+      const float inv = 1.f / l;
+      *reinterpret_cast<uint2*>(a.o + tok * a.ldo + head * D + col) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    } else {
+      const long long at = ((long long)run * a.Hkv + kvh) * rows + row;
+      *reinterpret_cast<float4*>(a.part + at * D + col) = o;
+      if (col == 0) a.part_ml[at] = make_float2(top, l);
+    }
+  }
+}
+
+template <int D, int NT>
+cudaError_t run_few(const AttendFp8Args& f, int max_runs, cudaStream_t s) {
+  using Sh = Few<D, NT>;
+  static_assert(2 * 2 * kSMs * 4 <= Sh::BYTES, "the tile counts stand in the space of the warps' sums");
+  static bool done[64];
+  cudaError_t e = allow_smem(attend8_few_kernel<D, NT>, Sh::BYTES, done);
+  if (e != cudaSuccess) return e;
+  e = launch_early(attend8_few_kernel<D, NT>, dim3((unsigned)(max_runs ? max_runs : f.a.S), (unsigned)f.a.Hkv), Sh::THREADS, Sh::BYTES, s, f);
+  return e != cudaSuccess || max_runs == 0 ? e : launch_attend_join(f.a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_few_attention_fp8(const AttendFp8Args& f, int max_runs, cudaStream_t s) {
+  const bool one = f.a.n * f.a.g <= 8;
+  if (f.a.D == 64) return one ? run_few<64, 1>(f, max_runs, s) : run_few<64, 2>(f, max_runs, s);
+  return one ? run_few<128, 1>(f, max_runs, s) : run_few<128, 2>(f, max_runs, s);
+}
+
+}  // namespace ssmtree

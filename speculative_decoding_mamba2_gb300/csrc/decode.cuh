@@ -17,6 +17,8 @@ struct AttendFp8Args {
 };
 size_t tree_attention_fp8_workspace_bytes(int S, int n, int Hq, int Hkv, int D, int max_len);
 cudaError_t launch_tree_attention_fp8(const AttendFp8Args& a, void* workspace, cudaStream_t s);
+constexpr int kFewRows = 16;  // up to so many query rows of a key/value head:
+cudaError_t launch_few_attention_fp8(const AttendFp8Args& a, int max_runs, cudaStream_t s);
 
 struct KvCommitFp8Args {
   KvCommitArgs a;  // (kp and vp are not read)

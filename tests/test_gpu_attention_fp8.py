@@ -466,3 +466,83 @@ def test_tree_attention_fp8_graphs_that_share_a_workspace(D):
             assert int(status) == 0
             for s in range(c["S"]):
                 check(c, host(o).reshape(c["S"], c["n"], c["Hq"], D), s, less[s])
+
+
+FEW = [  # S, n, g, Hkv, lens, page, block: up to 16 query rows of a key/value head
+    (1, 1, 8, 1, [0], 8, 8), (2, 8, 1, 2, [7, 8], 8, 8), (1, 2, 4, 3, [1], 64, 64), (3, 1, 1, 2, [15, 16, 17], 16, 8), (2, 9, 1, 2, [333, 0], 32, 16),
+    (1, 16, 1, 2, [5000], 64, 32), (2, 1, 16, 1, [4097, 70], 128, 128), (1, 3, 5, 2, [2047], 8, 8), (4, 2, 8, 2, [129, 127, 1, 900], 1024, 512),
+    (80, 1, 4, 8, [40 + 3 * i for i in range(80)], 32, 32), (1, 1, 3, 1, [70000], 256, 64)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", FEW, ids=lambda s: str(s)[:40])
+def test_tree_attention_fp8_few_rows(shape, D):
+    S, n, g, Hkv, lens, page, block = shape
+    c = case(23, S, n, g, Hkv, D, lens, page, block, fused=n % 2 == 1)
+    o, status = run(c)
+    assert status == 0
+    for s in range(S):
+        check(c, o, s)
+
+
+@pytest.mark.parametrize("n,g", [(1, 8), (6, 2)])
+def test_tree_attention_fp8_few_rows_of_large_scores_and_scales_far_apart(n, g):
+    c = case(24, 2, n, g, 2, 128, [1700, 90], 16, 8, qscale=60.0)
+    o, status = run(c)
+    assert status == 0
+    for s in range(2):  # products of a score add up to 60 times the ones of the tolerance
+        near(c, o, s, *cache(c, s, c["lens"][s]), scores=60)
+    c = case(25, 2, n, g, 2, 128, [1700, 90], 16, 8)
+    by = np.exp2(np.random.default_rng([25, n]).integers(-60, 40, c["vs"].shape))
+    held = c["vp64"] / np.repeat(c["vs"].double().cpu().numpy(), c["block"], -1)[..., None]
+    c["vs"] = torch.from_numpy(by).float().cuda()
+    c["vp64"] = held * np.repeat(by, c["block"], -1)[..., None]
+    o, status = run(c)
+    assert status == 0
+    for s in range(2):
+        check(c, o, s)
+
+
+@pytest.mark.parametrize("n,g,D", [(1, 4, 128), (4, 2, 64), (12, 1, 128)])
+def test_tree_attention_fp8_few_rows_bad_device_data(n, g, D):
+    """Lengths, pages and scales that are out of range; a NaN of v in the cache and an infinity in a node's row: their columns alone."""
+    from speculative_decoding_mamba2_gb300 import SSM_STATUS_SCALE, SSM_STATUS_SEQ_RANGE
+    c = case(26, 2, n, g, 2, D, [100, 600], 16, 8)
+    o, status = run(c, lens=[-5, 600])
+    assert status == SSM_STATUS_SEQ_RANGE
+    check(c, o, 0, length=0)
+    check(c, o, 1)
+    t = c["table"].copy()
+    t[0, 1], t[1, 0] = -1, c["pool"]
+    o, status = run(c, table=t)
+    assert status == SSM_STATUS_SEQ_RANGE
+    for s, gone in ((0, range(16, 32)), (1, range(16))):
+        kc, vc = cache(c, s, c["lens"][s])
+        keep = [i for i in range(c["lens"][s]) if i not in gone]
+        near(c, o, s, kc[keep], vc[keep])
+    clean, _ = run(c)
+    col = np.arange(D) != 11
+    c["vp"].view(torch.uint8)[c["table"][1, 30], 1, 5, 11] = 0x7F
+    c["v"][0, 2 * D - 3] = float("inf")  # node 0 of one, its second head
+    o, status = run(c)
+    assert status == 0
+    np.testing.assert_array_equal(o[1][:, :g], clean[1][:, :g])
+    np.testing.assert_array_equal(o[1][:, g:][:, :, col], clean[1][:, g:][:, :, col])
+    assert np.isnan(o[1][:, g:, 11]).all()
+    seen = [v for v in range(n) if 0 in _chain(c["par"][0], v)]
+    assert np.isposinf(o[0][seen][:, g:, D - 3]).all()
+    rest = [v for v in range(n) if v not in seen]
+    np.testing.assert_array_equal(o[0][rest], clean[0][rest])
+    c["ks"][c["table"][0, 0], :, 1] = 0.0
+    c["vs"][c["table"][1, 3], :, 1] = float("inf")
+    c["vp"].view(torch.uint8)[c["table"][1, 3], :, 8:] = 0x7F  # not multiplied
+    c["vp"].view(torch.uint8)[c["table"][1, 30], 1, 5, 11] = 0
+    c["vp64"][c["table"][1, 30], 1, 5, 11] = 0
+    c["v"][0, 2 * D - 3] = 0.0
+    c["v64"][0, 0, 1, D - 3] = 0.0
+    o, status = run(c)
+    assert status == SSM_STATUS_SCALE
+    for s, gone in ((0, range(8, 16)), (1, range(56, 64))):
+        kc, vc = cache(c, s, c["lens"][s])
+        keep = [i for i in range(c["lens"][s]) if i not in gone]
+        near(c, o, s, kc[keep], vc[keep])
