@@ -99,7 +99,7 @@ __device__ __forceinline__ void ancestor_words(const AttendArgs& a, int s, unsig
   }
   if (bad && report) flag(a.status, SSM_STATUS_BAD_LAYOUT);
 #pragma unroll 1
-  for (int hop = 0; hop < 6; ++hop) {
+  for (int far = 1; far < a.n; far *= 2) {
     unsigned long long up[2];
     int pp[2];
 #pragma unroll

@@ -110,7 +110,6 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
   __shared__ FewMisc<D, NT> ms;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int rows = a.n * a.g, run = blockIdx.x, kvh = blockIdx.y;
-  if (tid == 0) ms.odd = 0;
   grid_dependency_wait();  // what the stream's kernels before this one write
   launch_dependents();
   int s = run, sp = 0, tps = 1 << 25, splits = 1;
@@ -122,30 +121,51 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
     sp = run - first;
     if (sp == 0 && kvh == 0 && tid == 0) a.runs[s] = make_int2(first, splits);
   }
+  // Q: of row g of each eight the columns that a lane has of K's rows, as fp16 of a power of two
+  uint32_t qx[NT][KI][4][2];
+  float qc[NT][2];
+  auto q_row = [&](int t) {
+    const int row = min(8 * t + g, rows - 1);
+    return reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + row / a.g) * a.ldq + (kvh * a.g + row % a.g) * D + c * 16);
+  };
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const uint4 x = q_row(t)[i * 8], y = q_row(t)[i * 8 + 1];
+      qx[t][i][0][0] = x.x, qx[t][i][0][1] = x.y, qx[t][i][1][0] = x.z, qx[t][i][1][1] = x.w;
+      qx[t][i][2][0] = y.x, qx[t][i][2][1] = y.y, qx[t][i][3][0] = y.z, qx[t][i][3][1] = y.w;
+    }
+  // The run's keys of the cache, k0 .. end - 1, in steps of 16: those of this warp are warp + i W, i < mine.  Of 16 steps of the warp a
+  // lane knows the eight keys lane & 1 of the lane / 2-th: their first row among the pages' (-1: no such rows, or their page is out
+  // of range), the scales, how many there are.  Pages are asked for 16 steps ahead, and before the length is known.
+  const bool has_tree = sp == 0;
+  const int t0 = sp * tps + has_tree - 1, k0 = t0 * KT;
+  const int32_t* table = a.table + (long long)s * a.max_pages;
+  auto key_of = [&](int b) { return (unsigned int)k0 + (unsigned int)(warp + (16 * b + (lane >> 1)) * W) * 16 + (lane & 1) * 8; };
+  auto page_of = [&](int b) {
+    const unsigned int at = key_of(b) >> a.page_shift;
+    return at < (unsigned int)a.max_pages ? table[at] : -1;
+  };
+  int next_page = page_of(0);
   int len = __shfl_sync(0xffffffffu, cached_rows(a, s), 0);
   if (len < 0) {
     if (sp == 0 && kvh == 0 && tid == 0) flag(a.status, SSM_STATUS_SEQ_RANGE);
     len = 0;
   }
-  // the run's keys of the cache, k0 .. end - 1, in steps of 16: those of this warp are warp + i W, i < mine
-  const bool has_tree = sp == 0;
-  const int t0 = sp * tps + has_tree - 1, t1 = min(sp * tps + tps - 1, (len + KT - 1) / KT), k0 = t0 * KT, end = min(t1 * KT, len);
+  const int t1 = min(sp * tps + tps - 1, (len + KT - 1) / KT), end = min(t1 * KT, len);
   const int steps = max(end - k0 + 15, 0) / 16, mine = (steps - warp + W - 1) / W;
-  const int32_t* table = a.table + (long long)s * a.max_pages;
-
-  // Of 16 steps of the warp a lane knows the eight keys lane & 1 of the lane / 2-th: their first row among the pages' (-1: no such
-  // rows, or their page is out of range), the scales, how many there are.  Pages are asked for 16 steps ahead.
-  auto row_of = [&](int b) {
-    const int i = 16 * b + (lane >> 1), at = k0 + (warp + i * W) * 16 + (lane & 1) * 8;
-    if (i >= mine || at >= end) return -1;
-    const int pg = table[at >> a.page_shift];
+  auto row_of = [&](int b, int pg) {
+    const unsigned int at = key_of(b);
+    if (16 * b + (lane >> 1) >= mine || at >= (unsigned int)max(end, 0)) return -1;
     if (pg < 0 || pg >= a.n_pages) {
       flag(a.status, SSM_STATUS_SEQ_RANGE);
       return -1;
     }
-    return ((pg * a.Hkv + kvh) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+    return ((pg * a.Hkv + kvh) << a.page_shift) + (int)(at & ((1u << a.page_shift) - 1));
   };
-  int at_row = row_of(0), next_row = -1, there = 0;
+  int at_row = row_of(0, next_page), next_row = -1, there = 0;
+  next_page = page_of(1);
   float ks = 1.f, lv = 0.f, rv = 1.f, v0 = 1.f;
 
   uint32_t kx[KI][2][4], vx[2][2][VW];
@@ -167,8 +187,14 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
     return __shfl_sync(0xffffffffu, i & 15 ? at_row : next_row, (2 * i & 31) + h);
   };
   int ra = __shfl_sync(0xffffffffu, at_row, 0), rb = __shfl_sync(0xffffffffu, at_row, 1);
-  load_k(ra, rb);
-  load_v(ra, rb);
+  const bool tree = has_tree && warp == W - 1;  // this warp has the tree's rows as well (and the fewest steps)
+  if (!tree) load_k(ra, rb), load_v(ra, rb);
+  float2 sc = make_float2(1.f, 1.f);
+  auto load_scales = [&](int r) {
+    sc = make_float2(1.f, 1.f);
+    if (r >= 0) sc = make_float2(f.ks[r >> f.block_shift], f.vs[r >> f.block_shift]);
+  };
+  load_scales(at_row);
 
   FewState<D, NT> st;
 #pragma unroll
@@ -180,28 +206,16 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
       for (int e = 0; e < 4; ++e) st.o[j][t][e] = 0.f;
   }
 
-  // Q: of row g of each eight the columns that a lane has of K's rows, as fp16 of a power of two
-  uint32_t qx[NT][KI][4][2];
-  float qc[NT][2];
-  auto q_row = [&](int t) {
-    const int row = min(8 * t + g, rows - 1);
-    return reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + row / a.g) * a.ldq + (kvh * a.g + row % a.g) * D + c * 16);
-  };
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     uint32_t most = 0;
-    const uint4* q = q_row(t);
 #pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const uint4 x = q[i * 8], y = q[i * 8 + 1];
-      const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    for (int i = 0; i < KI; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        qx[t][i][j / 2][j & 1] = w[j];
-        const uint32_t lo = w[j] << 16 & 0x7fffffffu, hi = w[j] & 0x7fff0000u;
+        const uint32_t w = qx[t][i][j / 2][j & 1], lo = w << 16 & 0x7fffffffu, hi = w & 0x7fff0000u;
         most = max(most, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
       }
-    }
     most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
     most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
     const int e = min(14 - ((int)(most >> 23) - 127), 100);  // the largest to 2^14 .. 2^15
@@ -216,21 +230,37 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
     qc[t][0] = __shfl_sync(0xffffffffu, back, 8 * c), qc[t][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
   }
 
-  if (has_tree && warp == 0) {  // the tree's own rows, up to 16, in bf16
+  if (tree) {  // the tree's own rows, up to 16, in bf16
+    const long long row0 = (long long)s * a.n;
+    uint4 kt[KI][2][2], vt[KI][4];  // all asked for at once
+#pragma unroll
+    for (int i = 0; i < KI; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4* p = reinterpret_cast<const uint4*>(a.k + (row0 + g + 8 * h) * a.ldk + kvh * D + i * 64 + c * 16);
+        kt[i][h][0] = kt[i][h][1] = make_uint4(0, 0, 0, 0);
+        if (g + 8 * h < a.n) kt[i][h][0] = p[0], kt[i][h][1] = p[1];
+      }
+#pragma unroll
+    for (int h = 0; h < KI; ++h)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int key = 2 * c + (k & 1) + (k >> 1) * 8;
+        vt[h][k] = make_uint4(0, 0, 0, 0);
+        if (key < a.n) vt[h][k] = *reinterpret_cast<const uint4*>(a.v + (row0 + key) * a.ldv + kvh * D + g * (D / 8) + h * 8);
+      }
+    if (lane == 0) ms.odd = 0;
     ancestor_words(a, s, ms.anc, kvh == 0);
     __syncwarp();
-    const long long row0 = (long long)s * a.n;
     float x[NT][4] = {};
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < KI; ++i) {
       uint32_t w[2][8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4* p = reinterpret_cast<const uint4*>(a.k + (row0 + g + 8 * h) * a.ldk + kvh * D + i * 64 + c * 16);
-        uint4 y[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (g + 8 * h < a.n) y[0] = p[0], y[1] = p[1];
-        w[h][0] = y[0].x, w[h][1] = y[0].y, w[h][2] = y[0].z, w[h][3] = y[0].w;
-        w[h][4] = y[1].x, w[h][5] = y[1].y, w[h][6] = y[1].z, w[h][7] = y[1].w;
+        const uint4 y0 = kt[i][h][0], y1 = kt[i][h][1];
+        w[h][0] = y0.x, w[h][1] = y0.y, w[h][2] = y0.z, w[h][3] = y0.w;
+        w[h][4] = y1.x, w[h][5] = y1.y, w[h][6] = y1.z, w[h][7] = y1.w;
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -255,13 +285,12 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
 #pragma unroll
     for (int t = 0; t < NT; ++t) p[t][0] = transposed(pack_bf16x2(x[t][0], x[t][1])), p[t][1] = transposed(pack_bf16x2(x[t][2], x[t][3]));
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h) {  // eight of a lane's columns
+    for (int h = 0; h < KI; ++h) {  // eight of a lane's columns
       uint32_t w[4][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int key = 2 * c + (k & 1) + (k >> 1) * 8;
-        uint4 y = make_uint4(0, 0, 0, 0);
-        if (key < a.n) y = *reinterpret_cast<const uint4*>(a.v + (row0 + key) * a.ldv + kvh * D + g * (D / 8) + h * 8);
+        const uint4 y = vt[h][k];
         w[k][0] = finite_or_zero(y.x), w[k][1] = finite_or_zero(y.y), w[k][2] = finite_or_zero(y.z), w[k][3] = finite_or_zero(y.w);
         if (w[k][0] != y.x || w[k][1] != y.y || w[k][2] != y.z || w[k][3] != y.w) atomicOr(&ms.odd, 1u << key);
       }
@@ -273,28 +302,28 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
         for (int t = 0; t < NT; ++t) mma_bf16(st.o[4 * h + j][t], va, p[t]);
       }
     }
+    load_k(ra, rb), load_v(ra, rb);
   }
 
 #pragma unroll 1
   for (int i = 0; i < mine; ++i) {
     if ((i & 15) == 0) {  // what the next 16 steps' keys are
       if (i > 0) at_row = next_row;
-      float2 sc = make_float2(1.f, 1.f);
-      if (at_row >= 0) sc = make_float2(f.ks[at_row >> f.block_shift], f.vs[at_row >> f.block_shift]);
-      next_row = row_of(i / 16 + 1);
+      next_row = row_of(i / 16 + 1, next_page), next_page = page_of(i / 16 + 2);
       const bool good = good_scale(sc.x) && good_scale(sc.y);
       if (!good) {
         flag(a.status, SSM_STATUS_SCALE);
         sc = make_float2(1.f, 1.f);
       }
-      there = at_row >= 0 && good ? min(end - (k0 + (warp + (i + (lane >> 1)) * W) * 16 + (lane & 1) * 8), 8) : 0;
-      if (i == 0 && !(has_tree && warp == 0)) {  // what this warp's scales of v are relative to: one of them, as a power of two
+      there = at_row >= 0 && good ? min(end - (int)key_of(i / 16), 8) : 0;
+      if (i == 0 && !tree) {  // what this warp's scales of v are relative to: one of them, as a power of two
         const unsigned int top = __reduce_max_sync(0xffffffffu, there > 0 ? __float_as_uint(sc.y) & 0x7f800000u : 0u);
         v0 = top ? __uint_as_float(top) : 1.f;
       }
       const float rel = fminf(fmaxf(sc.y / v0, 0x1p-120f), 0x1p120f);
       ks = sc.x, lv = log2f(rel), rv = 1.f / rel;
     }
+    if ((i & 15) == 8) load_scales(next_row);
     const int from = 2 * i & 31;
     const int ta = __shfl_sync(0xffffffffu, there, from), tb = __shfl_sync(0xffffffffu, there, from + 1);
     const float ka = __shfl_sync(0xffffffffu, ks, from), kb = __shfl_sync(0xffffffffu, ks, from + 1);
