@@ -20,16 +20,27 @@ constexpr float kShift = 7.f;  // weights are 2^7 times as large, so that fp16 h
 template <int D, int NT>  // NT: eights of rows
 struct Few {
   static constexpr int WARPS = NT == 1 ? 8 : 6, THREADS = WARPS * 32, ROWS = 8 * NT, LD = D + 4;
-  static constexpr int BYTES = WARPS * ROWS * LD * 4;
+  // a step in a warp's ring: 16 rows of K, 16 of V, as many steps under way as two blocks of an SM have room for
+  static constexpr int KB = 16 * D, STEP = 2 * KB, STAGES = (NT == 1 ? 3 : 4) * (128 / D);
+  static constexpr int OFF_MISC = WARPS * STAGES * STEP;
+  static_assert(WARPS * ROWS * LD * 4 <= OFF_MISC, "the warps' sums stand there at the end");
 };
 template <int D, int NT>
 struct FewMisc {
   using Sh = Few<D, NT>;
   unsigned long long anc[64];
+  unsigned long long full[Sh::WARPS][Sh::STAGES];
   SplitScratch split;
   float m[Sh::WARPS][Sh::ROWS], l[Sh::WARPS][Sh::ROWS];
   unsigned int odd;  // tree rows with a value of v that is not finite
+  int stop;
 };
+template <int D, int NT>
+constexpr int few_bytes() {
+  constexpr int bytes = Few<D, NT>::OFF_MISC + (int)sizeof(FewMisc<D, NT>);
+  static_assert(bytes <= 228 * 1024 / 2 - 1024, "two to an SM");
+  return bytes;
+}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -50,16 +61,15 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float nan_unless_finite(float x) {
   return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x;
 }
-// a lane's bytes of a row (read once: they need no place in L1)
 template <int WORDS>
-__device__ __forceinline__ void load_words(uint32_t (&x)[WORDS], const void* p, bool there) {
-#pragma unroll
-  for (int i = 0; i < WORDS; ++i) x[i] = 0;
-  if (!there) return;
-  if constexpr (WORDS == 4)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "l"(p) : "memory");
-  else
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "l"(p) : "memory");
+__device__ __forceinline__ void load_words(uint32_t (&x)[WORDS], const unsigned char* p) {
+  if constexpr (WORDS == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    x[0] = v.x, x[1] = v.y;
+  }
 }
 
 // a warp's rows so far: of each eight, this lane's are 2 (lane % 4) and the one behind
@@ -102,14 +112,26 @@ struct FewState {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(AttendFp8Args f) {
+__global__ void __launch_bounds__(Few<D, NT>::THREADS, 2)
+    attend8_few_kernel(const __grid_constant__ CUtensorMap tkp, const __grid_constant__ CUtensorMap tvp, AttendFp8Args f) {
   using Sh = Few<D, NT>;
   constexpr int W = Sh::WARPS, KI = D / 64, VW = D / 32;  // 64-column parts of a row; words of V's row in a lane
   const AttendArgs& a = f.a;
-  extern __shared__ __align__(16) float o_s[];
-  __shared__ FewMisc<D, NT> ms;
+  extern __shared__ __align__(1024) unsigned char smem[];  // (there is no room to move it: where it is not aligned, nothing runs)
+  float* o_s = reinterpret_cast<float*>(smem);
+  FewMisc<D, NT>& ms = *reinterpret_cast<FewMisc<D, NT>*>(smem + Sh::OFF_MISC);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int rows = a.n * a.g, run = blockIdx.x, kvh = blockIdx.y;
+  if (smem_u32(smem) & 1023u) {
+    grid_dependency_wait();  // no grid ends before the one that it depends on
+    if (tid == 0) flag(a.status, SSM_STATUS_TIMEOUT);
+    if (tid == 0 && run < a.S && a.max_runs > 0) a.runs[run] = make_int2(0, 1);  // nothing to join
+    return;
+  }
+  if (tid < W * Sh::STAGES) mbar_init(smem_u32(&ms.full[0][0] + tid), 1);
+  if (tid == 0) ms.stop = 0;
+  fence_barrier_init();
+  __syncthreads();
   grid_dependency_wait();  // what the stream's kernels before this one write
   launch_dependents();
   int s = run, sp = 0, tps = 1 << 25, splits = 1;
@@ -118,6 +140,8 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
     int first;
     tps = choose_split<Sh::THREADS>(a, a.Hkv, tiles, &ms.split);
     if (!find_run(a.S, tiles, tps, run, s, first, splits)) return;
+    fence_async_smem();
+    __syncthreads();  // (behind it the copies may write there)
     sp = run - first;
     if (sp == 0 && kvh == 0 && tid == 0) a.runs[s] = make_int2(first, splits);
   }
@@ -126,13 +150,13 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
   float qc[NT][2];
   auto q_row = [&](int t) {
     const int row = min(8 * t + g, rows - 1);
-    return reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + row / a.g) * a.ldq + (kvh * a.g + row % a.g) * D + c * 16);
+    return reinterpret_cast<const uint4*>(a.q + ((long long)s * a.n + row / a.g) * a.ldq + (kvh * a.g + row % a.g) * D + KI * c * 16);
   };
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
-      const uint4 x = q_row(t)[i * 8], y = q_row(t)[i * 8 + 1];
+      const uint4 x = q_row(t)[i * 2], y = q_row(t)[i * 2 + 1];
       qx[t][i][0][0] = x.x, qx[t][i][0][1] = x.y, qx[t][i][1][0] = x.z, qx[t][i][1][1] = x.w;
       qx[t][i][2][0] = y.x, qx[t][i][2][1] = y.y, qx[t][i][3][0] = y.z, qx[t][i][3][1] = y.w;
     }
@@ -168,27 +192,23 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
   next_page = page_of(1);
   float ks = 1.f, lv = 0.f, rv = 1.f, v0 = 1.f;
 
-  uint32_t kx[KI][2][4], vx[2][2][VW];
-  auto load_k = [&](int ra, int rb) {
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      load_words(kx[i][0], f.kp + ((long long)ra + g) * D + i * 64 + c * 16, ra >= 0);
-      load_words(kx[i][1], f.kp + ((long long)rb + g) * D + i * 64 + c * 16, rb >= 0);
+  // One lane asks for a step's rows (box of them at a time, all in one page); swizzled, as they land, a warp's reads have no bank conflicts.
+  unsigned char* ring = smem + warp * Sh::STAGES * Sh::STEP;
+  const int box = min(1 << a.page_shift, 16);
+  auto ask = [&](int i, int stage, int rows_at) {  // step i of the sixteen whose rows these are
+    const int ra = __shfl_sync(0xffffffffu, rows_at, 2 * i & 31), rb = __shfl_sync(0xffffffffu, rows_at, (2 * i & 31) + 1);
+    if (lane == 0) {
+      const uint32_t bar = smem_u32(&ms.full[warp][stage]), to = smem_u32(ring) + stage * Sh::STEP;
+      const bool second = box == 8 && rb >= 0;
+      mbar_arrive_expect_tx(bar, ((ra >= 0 ? box : 0) + (second ? 8 : 0)) * 2 * D);
+      if (ra >= 0) tma_load_2d(to, &tkp, 0, ra, bar), tma_load_2d(to + Sh::KB, &tvp, 0, ra, bar);
+      if (second) tma_load_2d(to + 8 * D, &tkp, 0, rb, bar), tma_load_2d(to + Sh::KB + 8 * D, &tvp, 0, rb, bar);
     }
+    __syncwarp();
   };
-  auto load_v = [&](int ra, int rb) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      load_words(vx[0][e], f.vp + ((long long)ra + 2 * c + e) * D + g * (D / 8), ra >= 0);
-      load_words(vx[1][e], f.vp + ((long long)rb + 2 * c + e) * D + g * (D / 8), rb >= 0);
-    }
-  };
-  auto row_at = [&](int i, int h) {  // of step i (the 16 of now or the first of the next ones)
-    return __shfl_sync(0xffffffffu, i & 15 ? at_row : next_row, (2 * i & 31) + h);
-  };
-  int ra = __shfl_sync(0xffffffffu, at_row, 0), rb = __shfl_sync(0xffffffffu, at_row, 1);
+#pragma unroll 1
+  for (int i = 0; i < Sh::STAGES && i < mine; ++i) ask(i, i, at_row);
   const bool tree = has_tree && warp == W - 1;  // this warp has the tree's rows as well (and the fewest steps)
-  if (!tree) load_k(ra, rb), load_v(ra, rb);
   float2 sc = make_float2(1.f, 1.f);
   auto load_scales = [&](int r) {
     sc = make_float2(1.f, 1.f);
@@ -237,7 +257,7 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
     for (int i = 0; i < KI; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4* p = reinterpret_cast<const uint4*>(a.k + (row0 + g + 8 * h) * a.ldk + kvh * D + i * 64 + c * 16);
+        const uint4* p = reinterpret_cast<const uint4*>(a.k + (row0 + g + 8 * h) * a.ldk + kvh * D + (KI * c + i) * 16);
         kt[i][h][0] = kt[i][h][1] = make_uint4(0, 0, 0, 0);
         if (g + 8 * h < a.n) kt[i][h][0] = p[0], kt[i][h][1] = p[1];
       }
@@ -264,7 +284,7 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const uint4 y0 = q_row(t)[i * 8], y1 = q_row(t)[i * 8 + 1];
+        const uint4 y0 = q_row(t)[i * 2], y1 = q_row(t)[i * 2 + 1];
         const uint32_t q[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -302,11 +322,17 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
         for (int t = 0; t < NT; ++t) mma_bf16(st.o[4 * h + j][t], va, p[t]);
       }
     }
-    load_k(ra, rb), load_v(ra, rb);
   }
 
+  // where a lane's bytes of a step are: 16 bytes of 64 columns of K's rows g and 8 + g, its columns of V's rows 2 c + e and 8 + 2 c + e
+  auto k_at = [&](int h, int e) { return (g + 8 * e) * D + ((KI == 2 ? (2 * c + h) ^ g : c ^ (g >> 1)) << 4); };
+  auto v_at = [&](int e, int b) {
+    return Sh::KB + (2 * c + e + 8 * b) * D + (KI == 2 ? (g ^ (2 * c + e)) << 4 : (((g >> 1) ^ c) << 4) + (g & 1) * 8);
+  };
+  bool ok = true;
+  int i = 0, stage = 0, phase = 0;
 #pragma unroll 1
-  for (int i = 0; i < mine; ++i) {
+  for (; i < mine; ++i) {
     if ((i & 15) == 0) {  // what the next 16 steps' keys are
       if (i > 0) at_row = next_row;
       next_row = row_of(i / 16 + 1, next_page), next_page = page_of(i / 16 + 2);
@@ -329,18 +355,30 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
     const float ka = __shfl_sync(0xffffffffu, ks, from), kb = __shfl_sync(0xffffffffu, ks, from + 1);
     const float la = __shfl_sync(0xffffffffu, lv, from), lb = __shfl_sync(0xffffffffu, lv, from + 1);
     const float ia = __shfl_sync(0xffffffffu, rv, from), ib = __shfl_sync(0xffffffffu, rv, from + 1);
-    ra = row_at(i + 1, 0), rb = row_at(i + 1, 1);
+    ok = wait_bar(&ms.full[warp][stage], phase, &ms.stop);
+    if (!ok) break;
+    const unsigned char* step = ring + stage * Sh::STEP;
     float x[NT][4] = {};
 #pragma unroll
-    for (int h = 0; h < KI; ++h)
+    for (int h = 0; h < KI; ++h) {
+      uint32_t kx[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) load_words(kx[e], step + k_at(h, e));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t ak[4] = {e4m3x2_f16x2(kx[h][0][j]), e4m3x2_f16x2(kx[h][1][j]), e4m3x2_f16x2(kx[h][0][j] >> 16),
-                                e4m3x2_f16x2(kx[h][1][j] >> 16)};
+        const uint32_t ak[4] = {e4m3x2_f16x2(kx[0][j]), e4m3x2_f16x2(kx[1][j]), e4m3x2_f16x2(kx[0][j] >> 16),
+                                e4m3x2_f16x2(kx[1][j] >> 16)};
 #pragma unroll
         for (int t = 0; t < NT; ++t) mma_f16(x[t], ak, qx[t][h][j][0], qx[t][h][j][1]);
       }
-    if (i + 1 < mine) load_k(ra, rb);
+    }
+    uint32_t vx[2][2][VW];  // (read before the weights are made)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) load_words(vx[0][e], step + v_at(e, 0)), load_words(vx[1][e], step + v_at(e, 1));
+    __syncwarp();
+    const int then = i + Sh::STAGES;
+    if (then < mine) ask(then, stage, (then ^ i) & ~15 ? next_row : at_row);
+    if (++stage == Sh::STAGES) stage = 0, phase ^= 1;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -367,7 +405,16 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
 #pragma unroll
       for (int t = 0; t < NT; ++t) mma_f16(st.o[2 * w][t], v01, p[t][0], p[t][1]), mma_f16(st.o[2 * w + 1][t], v23, p[t][0], p[t][1]);
     }
-    if (i + 1 < mine) load_v(ra, rb);
+  }
+  if (!ok) {  // copies land before the shared memory is given up
+    if (lane == 0) {
+      flag(a.status, SSM_STATUS_TIMEOUT);
+      for (int k = i; k < min(i + Sh::STAGES, mine); ++k) {
+        mbar_wait(smem_u32(&ms.full[warp][stage]), phase);
+        if (++stage == Sh::STAGES) stage = 0, phase ^= 1;
+      }
+    }
+    __syncwarp();
   }
 
   // the warps' sums as one
@@ -433,11 +480,21 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2) attend8_few_kernel(Att
 template <int D, int NT>
 cudaError_t run_few(const AttendFp8Args& f, int max_runs, cudaStream_t s) {
   using Sh = Few<D, NT>;
-  static_assert(2 * 2 * kSMs * 4 <= Sh::BYTES, "the tile counts stand in the space of the warps' sums");
+  constexpr int bytes = few_bytes<D, NT>();
+  static_assert(2 * 2 * kSMs * 4 <= Sh::OFF_MISC, "the tile counts stand in the space of the ring");
+  const AttendArgs& a = f.a;
+  CUtensorMap m[2];
+  const long long page_rows = ((long long)a.n_pages * a.Hkv) << a.page_shift;
+  const int box = a.page_shift < 4 ? 8 : 16;
+  // a call without cached rows reads no page: any matrix will do
+  const bool none = a.max_len == 0 || page_rows == 0;
+  if (!encode_byte_tiles(&m[0], none ? static_cast<const void*>(a.k) : f.kp, none ? 1 : page_rows, D, box) ||
+      !encode_byte_tiles(&m[1], none ? static_cast<const void*>(a.v) : f.vp, none ? 1 : page_rows, D, box))
+    return cudaErrorInvalidValue;
   static bool done[64];
-  cudaError_t e = allow_smem(attend8_few_kernel<D, NT>, Sh::BYTES, done);
+  cudaError_t e = allow_smem(attend8_few_kernel<D, NT>, bytes, done);
   if (e != cudaSuccess) return e;
-  e = launch_early(attend8_few_kernel<D, NT>, dim3((unsigned)(max_runs ? max_runs : f.a.S), (unsigned)f.a.Hkv), Sh::THREADS, Sh::BYTES, s, f);
+  e = launch_early(attend8_few_kernel<D, NT>, dim3((unsigned)(max_runs ? max_runs : a.S), (unsigned)a.Hkv), Sh::THREADS, bytes, s, m[0], m[1], f);
   return e != cudaSuccess || max_runs == 0 ? e : launch_attend_join(f.a, s);
 }
 
