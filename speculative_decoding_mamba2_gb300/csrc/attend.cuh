@@ -28,7 +28,7 @@ struct SplitScratch {        // of each warp: tiles of the longest sequence, the
 };
 template <int THREADS>
 __device__ __forceinline__ int choose_split(const AttendArgs& a, int per, int* tiles, SplitScratch* ms) {
-  static_assert(THREADS >= CANDIDATES && THREADS <= 384, "a thread to each");
+  static_assert(THREADS <= 384, "a place for each warp");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int most = 0;
   for (int s = tid; s < a.S; s += THREADS) most = max(most, tiles[s] = (max(cached_rows(a, s), 0) + KT - 1) / KT + 1);
@@ -38,8 +38,8 @@ __device__ __forceinline__ int choose_split(const AttendArgs& a, int per, int* t
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) most = max(most, ms->most[w]);
   unsigned int key = 0xffffffffu;
-  const unsigned int tps = (3u * most + tid + 2) / (tid + 3);
-  if (tid < CANDIDATES) {
+  for (int c = tid; c < CANDIDATES; c += THREADS) {
+    const unsigned int tps = (3u * most + c + 2) / (c + 3);
     unsigned int runs = 0;
     float total = 0.f;
     for (int s = 0; s < a.S; ++s) runs += (tiles[s] + tps - 1) / tps, total += (float)tiles[s];
@@ -48,7 +48,7 @@ __device__ __forceinline__ int choose_split(const AttendArgs& a, int per, int* t
       const float ctas = (float)(runs * per), len = tps + 4.f;
       const float waves = ceilf(ctas / slots) * len, list = (total * per + 4.f * ctas) / slots + len;
       const float est = fminf(waves, list) + (runs > (unsigned)a.S ? 2.f : 0.f);
-      key = (unsigned int)fminf(est / most * 65536.f, 16777215.f) << 8 | tid;
+      key = min(key, (unsigned int)fminf(est / most * 65536.f, 16777215.f) << 8 | (unsigned int)c);
     }
   }
   key = __reduce_min_sync(0xffffffffu, key);

@@ -17,17 +17,17 @@ namespace {
 
 constexpr float kShift = 7.f;  // weights are 2^7 times as large, so that fp16 holds them to 2^-31 of the largest
 
-template <int D, int NT>  // NT: eights of rows
+template <int D, int NT, bool CUT, int BLOCKS>  // NT: eights of rows; BLOCKS: blocks on an SM, which share 16 or 12 warps
 struct Few {
-  static constexpr int WARPS = NT == 1 ? 8 : 6, THREADS = WARPS * 32, ROWS = 8 * NT, LD = D + 4;
+  static constexpr int WARPS = (NT == 1 ? 16 : 12) / BLOCKS, THREADS = WARPS * 32, ROWS = 8 * NT, LD = D + 4;
   // a step in a warp's ring: 16 rows of K, 16 of V, as many steps under way as two blocks of an SM have room for
   static constexpr int KB = 16 * D, STEP = 2 * KB, STAGES = (NT == 1 ? 3 : 4) * (128 / D);
   static constexpr int OFF_MISC = WARPS * STAGES * STEP;
   static_assert(WARPS * ROWS * LD * 4 <= OFF_MISC, "the warps' sums stand there at the end");
 };
-template <int D, int NT>
+template <int D, int NT, bool CUT, int BLOCKS>
 struct FewMisc {
-  using Sh = Few<D, NT>;
+  using Sh = Few<D, NT, CUT, BLOCKS>;
   unsigned long long anc[64];
   unsigned long long full[Sh::WARPS][Sh::STAGES];
   SplitScratch split;
@@ -35,10 +35,10 @@ struct FewMisc {
   unsigned int odd;  // tree rows with a value of v that is not finite
   int stop;
 };
-template <int D, int NT>
+template <int D, int NT, bool CUT, int BLOCKS>
 constexpr int few_bytes() {
-  constexpr int bytes = Few<D, NT>::OFF_MISC + (int)sizeof(FewMisc<D, NT>);
-  static_assert(bytes <= 228 * 1024 / 2 - 1024, "two to an SM");
+  constexpr int bytes = Few<D, NT, CUT, BLOCKS>::OFF_MISC + (int)sizeof(FewMisc<D, NT, CUT, BLOCKS>);
+  static_assert(bytes <= 228 * 1024 / BLOCKS - 1024, "so many to an SM");
   return bytes;
 }
 
@@ -111,21 +111,21 @@ struct FewState {
   }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Few<D, NT>::THREADS, 2)
+template <int D, int NT, bool CUT, int BLOCKS>
+__global__ void __launch_bounds__(Few<D, NT, CUT, BLOCKS>::THREADS, BLOCKS)
     attend8_few_kernel(const __grid_constant__ CUtensorMap tkp, const __grid_constant__ CUtensorMap tvp, AttendFp8Args f) {
-  using Sh = Few<D, NT>;
+  using Sh = Few<D, NT, CUT, BLOCKS>;
   constexpr int W = Sh::WARPS, KI = D / 64, VW = D / 32;  // 64-column parts of a row; words of V's row in a lane
   const AttendArgs& a = f.a;
   extern __shared__ __align__(1024) unsigned char smem[];  // (there is no room to move it: where it is not aligned, nothing runs)
   float* o_s = reinterpret_cast<float*>(smem);
-  FewMisc<D, NT>& ms = *reinterpret_cast<FewMisc<D, NT>*>(smem + Sh::OFF_MISC);
+  FewMisc<D, NT, CUT, BLOCKS>& ms = *reinterpret_cast<FewMisc<D, NT, CUT, BLOCKS>*>(smem + Sh::OFF_MISC);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int rows = a.n * a.g, run = blockIdx.x, kvh = blockIdx.y;
   if (smem_u32(smem) & 1023u) {
     grid_dependency_wait();  // no grid ends before the one that it depends on
     if (tid == 0) flag(a.status, SSM_STATUS_TIMEOUT);
-    if (tid == 0 && run < a.S && a.max_runs > 0) a.runs[run] = make_int2(0, 1);  // nothing to join
+    if (CUT && tid == 0 && run < a.S) a.runs[run] = make_int2(0, 1);  // nothing to join
     return;
   }
   if (tid < W * Sh::STAGES) mbar_init(smem_u32(&ms.full[0][0] + tid), 1);
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2)
   grid_dependency_wait();  // what the stream's kernels before this one write
   launch_dependents();
   int s = run, sp = 0, tps = 1 << 25, splits = 1;
-  if (a.max_runs > 0) {
+  if constexpr (CUT) if (a.max_runs > 0) {  // (it is: said once more, nothing spills)
     int* tiles = reinterpret_cast<int*>(o_s);  // space not in use yet
     int first;
     tps = choose_split<Sh::THREADS>(a, a.Hkv, tiles, &ms.split);
@@ -477,11 +477,11 @@ __global__ void __launch_bounds__(Few<D, NT>::THREADS, 2)
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool CUT, int BLOCKS>
 cudaError_t run_few(const AttendFp8Args& f, int max_runs, cudaStream_t s) {
-  using Sh = Few<D, NT>;
-  constexpr int bytes = few_bytes<D, NT>();
-  static_assert(2 * 2 * kSMs * 4 <= Sh::OFF_MISC, "the tile counts stand in the space of the ring");
+  using Sh = Few<D, NT, CUT, BLOCKS>;
+  constexpr int bytes = few_bytes<D, NT, CUT, BLOCKS>();
+  static_assert(!CUT || 2 * 2 * kSMs * 4 <= Sh::OFF_MISC, "the tile counts stand in the space of the ring");
   const AttendArgs& a = f.a;
   CUtensorMap m[2];
   const long long page_rows = ((long long)a.n_pages * a.Hkv) << a.page_shift;
@@ -492,18 +492,27 @@ cudaError_t run_few(const AttendFp8Args& f, int max_runs, cudaStream_t s) {
       !encode_byte_tiles(&m[1], none ? static_cast<const void*>(a.v) : f.vp, none ? 1 : page_rows, D, box))
     return cudaErrorInvalidValue;
   static bool done[64];
-  cudaError_t e = allow_smem(attend8_few_kernel<D, NT>, bytes, done);
+  cudaError_t e = allow_smem(attend8_few_kernel<D, NT, CUT, BLOCKS>, bytes, done);
   if (e != cudaSuccess) return e;
-  e = launch_early(attend8_few_kernel<D, NT>, dim3((unsigned)(max_runs ? max_runs : a.S), (unsigned)a.Hkv), Sh::THREADS, bytes, s, m[0], m[1], f);
-  return e != cudaSuccess || max_runs == 0 ? e : launch_attend_join(f.a, s);
+  e = launch_early(attend8_few_kernel<D, NT, CUT, BLOCKS>, dim3((unsigned)(CUT ? max_runs : a.S), (unsigned)a.Hkv), Sh::THREADS, bytes, s, m[0], m[1], f);
+  return e != cudaSuccess || !CUT ? e : launch_attend_join(a, s);
+}
+
+template <int D>
+cudaError_t run_few(const AttendFp8Args& f, int max_runs, cudaStream_t s) {
+  const bool many = f.a.S * f.a.Hkv >= 2 * kSMs;
+  if (f.a.n * f.a.g <= 8) {
+    if (max_runs == 0) return run_few<D, 1, false, 4>(f, max_runs, s);
+    return many ? run_few<D, 1, true, 4>(f, max_runs, s) : run_few<D, 1, true, 2>(f, max_runs, s);
+  }
+  if (max_runs == 0) return run_few<D, 2, false, 4>(f, max_runs, s);
+  return many ? run_few<D, 2, true, 4>(f, max_runs, s) : run_few<D, 2, true, 2>(f, max_runs, s);
 }
 
 }  // namespace
 
 cudaError_t launch_few_attention_fp8(const AttendFp8Args& f, int max_runs, cudaStream_t s) {
-  const bool one = f.a.n * f.a.g <= 8;
-  if (f.a.D == 64) return one ? run_few<64, 1>(f, max_runs, s) : run_few<64, 2>(f, max_runs, s);
-  return one ? run_few<128, 1>(f, max_runs, s) : run_few<128, 2>(f, max_runs, s);
+  return f.a.D == 64 ? run_few<64>(f, max_runs, s) : run_few<128>(f, max_runs, s);
 }
 
 }  // namespace ssmtree
