@@ -16,7 +16,7 @@ namespace {
 //    bytes.  Eight warps make the terms, a row's columns side by side (a thread to a row, in registers, spilled: 10 % of all).
 //  * V is made fp16 (exact) by four warps on the way, since P in e4m3 would not do: P goes as fp16, whose 11 bits are more than
 //    bf16's.  Converting V costs a cvt for two values; splitting P into two terms would cost four for two of as many.  (The
-//    softmax's own warps converting it: one token 24 us, 8 trees 50, wide trees 149; see below for the three.)
+//    softmax's own warps converting it: 8 trees 50 us and not 40, wide trees 149 and not 113.)
 //  * A block's scale of K multiplies its scores in the softmax's own multiply-add.  Its scale of V is part of the weight: m is the
 //    maximum of S + log2 vs, so the weight w = 2^(S + log2 vs - m) fits fp16 whatever the scales, and the row's sum adds w / vs.  Scales
 //    of V count relative to one of them, so that neither sum leaves fp32.
@@ -24,11 +24,11 @@ namespace {
 // The tree's own rows are bf16 and the first tile of a sequence's first run: their products are bf16's, with Q as it came in the columns
 // that O will take, and their K and V in the places of the first two fp16 tiles of V.
 //
-// In a CUDA graph, 32 query and 8 (wide trees: 4) key/value heads of 128: one token over 16411 rows 21.3 us (34 MB of cache at 1.6 TB/s:
-// a few tiles' round trips to a run, the launch and the join), 8 trees of 16 nodes over up to 8117 rows 40 us, 4 of 40 over up to
-// 40009 rows 113 us (750 TFLOP/s with Q's terms counted once); with heads of 64 19.5, 36 and 96.  Wide trees are bound by the round
-// trips of the two tiles under way (P to P . V to S to the softmax) on top of the products: without copies, conversion or Q's lower
-// terms they take as long; with an idle softmax 15 % less, with that and no products a third less.
+// In a CUDA graph, 32 query and 8 (wide trees: 4) key/value heads of 128: 8 trees of 16 nodes over up to 8117 rows 40 us (84 MB of
+// cache at 2.1 TB/s), 4 of 40 over up to 40009 rows 113 us (750 TFLOP/s with Q's terms counted once); with heads of 64 36 and 96.
+// (Up to 16 query rows of a key/value head are attention_fp8_few.cu's.)  Wide trees are bound by the round trips of the two tiles under
+// way (P to P . V to S to the softmax) on top of the products: without copies, conversion or Q's lower terms they take as long; with
+// an idle softmax 15 % less, with that and no products a third less.
 constexpr int A8THREADS = 384;  // 4 softmax warps; copies, MMAs of S, MMAs of P . V, what keys a tile has; 4 warps that make V fp16
 // registers of the three groups of four warps: the block has 384 x 80
 constexpr int R_SOFTMAX = 136, R_MMA = 48, R_CONVERT = 56;
@@ -835,16 +835,25 @@ __global__ void __cluster_dims__(CCTAS, 1, 1) __launch_bounds__(CTHREADS) kv_com
   if (part == 0 && threadIdx.x == 0) a.len_out[s] = len + n;
 }
 
+// The plan of the 16-bit kernel; but few rows, whose blocks are half as large, are not cut either where their blocks fill half of the
+// SMs' places and no cache is so long that one block's walk of it takes more than cutting: 64 tokens of 8 heads over up to 1000 rows
+// 20.6 us, cut 32.3, over up to 400 rows 11 and 21.
+AttendPlan plan_attend_fp8(int S, int n, int Hq, int Hkv, int max_len) {
+  AttendPlan p = plan_attend(S, n, Hq, Hkv, max_len);
+  if (n * (Hq / Hkv) <= kFewRows && S * Hkv >= 2 * kSMs && max_len <= 2048) p.max_runs = 0;
+  return p;
+}
+
 }  // namespace
 
 size_t tree_attention_fp8_workspace_bytes(int S, int n, int Hq, int Hkv, int D, int max_len) {
-  return attend_workspace_bytes(plan_attend(S, n, Hq, Hkv, max_len), S, n, Hq, Hkv, D);
+  return attend_workspace_bytes(plan_attend_fp8(S, n, Hq, Hkv, max_len), S, n, Hq, Hkv, D);
 }
 
 cudaError_t launch_tree_attention_fp8(const AttendFp8Args& args, void* workspace, cudaStream_t s) {
   if (args.a.S == 0) return cudaSuccess;
   AttendFp8Args f = args;
-  const AttendPlan p = plan_attend(f.a.S, f.a.n, f.a.Hq, f.a.Hkv, f.a.max_len);
+  const AttendPlan p = plan_attend_fp8(f.a.S, f.a.n, f.a.Hq, f.a.Hkv, f.a.max_len);
   lay_workspace(f.a, p, workspace);
   if (f.a.n * f.a.g <= kFewRows) return launch_few_attention_fp8(f, p.max_runs, s);
   return f.a.D == 64 ? run_attend8<64>(f, p, s) : run_attend8<128>(f, p, s);
