@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(Few<D, NT, CUT, BLOCKS>::THREADS, BLOCKS)
   auto key_of = [&](int b) { return (unsigned int)k0 + (unsigned int)(warp + (16 * b + (lane >> 1)) * W) * 16 + (lane & 1) * 8; };
   auto page_of = [&](int b) {
     const unsigned int at = key_of(b) >> a.page_shift;
-    return at < (unsigned int)a.max_pages ? table[at] : -1;
+    return at < (a.max_len > 0 ? (unsigned int)a.max_pages : 0u) ? table[at] : -1;  // (without cached rows there may be no table)
   };
   int next_page = page_of(0);
   int len = __shfl_sync(0xffffffffu, cached_rows(a, s), 0);

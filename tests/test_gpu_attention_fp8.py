@@ -546,3 +546,23 @@ def test_tree_attention_fp8_few_rows_bad_device_data(n, g, D):
         kc, vc = cache(c, s, c["lens"][s])
         keep = [i for i in range(c["lens"][s]) if i not in gone]
         near(c, o, s, kc[keep], vc[keep])
+
+
+@pytest.mark.parametrize("n,g,D", [(1, 4, 128), (1, 4, 64), (4, 4, 128), (9, 4, 64)])
+def test_tree_attention_fp8_without_a_cache(n, g, D):
+    """No cached rows: pages, scales and the table, whatever its width, may be NULL."""
+    from speculative_decoding_mamba2_gb300 import binding as B
+    from speculative_decoding_mamba2_gb300 import ssm_tree_attention_fp8_workspace_size, ssm_tree_layout_build
+    c = case(27, 3, n, g, 2, D, [0, 0, 0], 16, 8)
+    Hq = c["Hq"]
+    lay = torch.from_numpy(ssm_tree_layout_build(c["par"])[0]).cuda()
+    ws = torch.empty(ssm_tree_attention_fp8_workspace_size(3, n, Hq, 2, D, 0), dtype=torch.uint8, device="cuda")
+    o = torch.empty(3 * n, Hq * D, dtype=torch.bfloat16, device="cuda")
+    lens, status = ints([0, 0, 0]), ints([0])
+    rc = B.lib().ssm_tree_attention_fp8(3, n, Hq, 2, D, lay.data_ptr(), c["q"].data_ptr(), Hq * D, c["k"].data_ptr(), 2 * D, c["v"].data_ptr(),
+                                        2 * D, None, None, None, None, 5, 16, 8, None, 7, lens.data_ptr(), 0, c["scale"], o.data_ptr(), Hq * D,
+                                        ws.data_ptr(), ws.numel(), status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == B.SSM_OK and int(status) == 0
+    for s in range(3):
+        check(c, host(o).reshape(3, n, Hq, D), s, length=0)
