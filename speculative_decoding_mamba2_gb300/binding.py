@@ -154,7 +154,7 @@ def _check(rc: int):
 # ---------------------------------------------------------------------------
 def _dev(t: torch.Tensor, name: str, dtype, numel: int | None = None):
     """The address of a contiguous CUDA tensor of this dtype (and element count)."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous() and numel in (None, t.numel()):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and (numel is None or t.numel() == numel):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
@@ -524,8 +524,8 @@ _BF16 = torch.bfloat16
 
 def _tok_rows(t, name: str, cols: int | None = None):
     """_rows of a bf16 tensor that may have one row or none (whose row stride then says nothing)."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _BF16 and t.dim() == 2:
-        rows, c = t.shape
+    if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.is_cuda and len(shape := t.shape) == 2:
+        rows, c = shape
         if cols is None or c == cols:
             if rows == 0:
                 return None, 0, (c + 7) // 8 * 8
@@ -639,9 +639,9 @@ def _pages(k_pages, v_pages, lead: int, Hkv: int, D: int):
 
 def _table(t, name: str, n_seq: int):
     """(address, columns) of an int32 tensor with a row for each sequence."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.size(0) != n_seq:
+    if not isinstance(t, torch.Tensor) or len(shape := t.shape) != 2 or shape[0] != n_seq:
         raise ValueError(f"{name}: a row for each sequence")
-    return _dev(t, name, torch.int32), t.size(1)
+    return _dev(t, name, torch.int32), shape[1]
 
 
 def ssm_tree_attention(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, layout, q, k, v, k_pages, v_pages, page_table,
@@ -698,12 +698,23 @@ _SIGS.update({
                                      _P]),
     "ssm_token_scores": (ctypes.c_int, [_I, _I, _P, _I, _L, ctypes.c_float, _I, _P, _P, _P, _I, _P, _P, _P, _P]),
 })
-_FP8 = torch.float8_e4m3fn
+_FP8, _F32 = torch.float8_e4m3fn, torch.float32
+
+
+_ONE_GPU = None
+
+
+def _one_gpu() -> bool:
+    """Whether the process sees one GPU: all tensors are then on it, and it is current."""
+    global _ONE_GPU
+    if _ONE_GPU is None:
+        _ONE_GPU = torch.cuda.device_count() == 1
+    return _ONE_GPU
 
 
 def _call_on(device: int, fn, *args):
     """The library's call with the tensors' device current (a launch goes to the current device)."""
-    if device == torch._C._cuda_getDevice():
+    if _ONE_GPU or device == torch._C._cuda_getDevice():
         _check(fn(*args))
     else:
         with torch.cuda.device(device):
@@ -713,6 +724,8 @@ def _call_on(device: int, fn, *args):
 def _same_device(like, *tensors):
     """The device that all of them (None: not given) are on."""
     d = like.get_device()
+    if _ONE_GPU or _one_gpu():
+        return d
     for t in tensors:
         if t is not None and t.get_device() != d:
             raise ValueError("the tensors are on different devices")
@@ -725,13 +738,12 @@ def _pages_fp8(k_pages, v_pages, k_scales, v_scales, lead: int, Hkv: int, D: int
     shape = k_pages.shape if isinstance(k_pages, torch.Tensor) else ()
     if len(shape) != lead + 4 or shape[-3] != Hkv or shape[-1] != D:
         raise ValueError("k_pages: [" + "n_layers, " * lead + "n_pages, Hkv, page_size, D]")
-    sshape = k_scales.shape if isinstance(k_scales, torch.Tensor) else ()
-    page = shape[-2]
-    if len(sshape) != lead + 3 or sshape[:-1] != shape[:-2] or not 0 < sshape[-1] <= page or page % sshape[-1]:
+    *front, page, _ = shape
+    *sfront, blocks = k_scales.shape if isinstance(k_scales, torch.Tensor) and k_scales.dim() else (0,)
+    if sfront != front or not 0 < blocks <= page or page % blocks:
         raise ValueError("k_scales: [" + "n_layers, " * lead + "n_pages, Hkv, page_size / block]")
     return (_dev(k_pages, "k_pages", _FP8), _dev(v_pages, "v_pages", _FP8, k_pages.numel()),
-            _dev(k_scales, "k_scales", torch.float32), _dev(v_scales, "v_scales", torch.float32, k_scales.numel()), shape[-4], page,
-            page // sshape[-1])
+            _dev(k_scales, "k_scales", _F32), _dev(v_scales, "v_scales", _F32, k_scales.numel()), front[-2], page, page // blocks)
 
 
 def ssm_tree_attention_fp8_workspace_size(n_seq: int, n_nodes: int, Hq: int, Hkv: int, D: int, max_cache_len: int) -> int:
