@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(Few<D, NT, CUT, BLOCKS>::THREADS, BLOCKS)
   next_page = page_of(1);
   float ks = 1.f, lv = 0.f, rv = 1.f, v0 = 1.f;
 
-  // One lane asks for a step's rows (box of them at a time, all in one page); swizzled, as they land, a warp's reads have no bank conflicts.
+  // One lane asks for a step's rows, box of them at a time, all in one page.  As they land swizzled, a warp's reads have no bank
+  // conflicts (two ways where a lane has eight columns of V, in heads of 64).
   unsigned char* ring = smem + warp * Sh::STAGES * Sh::STEP;
   const int box = min(1 << a.page_shift, 16);
   auto ask = [&](int i, int stage, int rows_at) {  // step i of the sixteen whose rows these are
