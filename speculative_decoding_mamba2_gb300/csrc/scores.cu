@@ -228,8 +228,9 @@ __global__ void __launch_bounds__(STHREADS, sblocks(sizeof(T) == 4)) scores_kern
   const Row<T> row(reinterpret_cast<const T*>(a.x) + (long long)t * a.ld, a.V);
   const int per = (row.vecs + parts - 1) / parts, j0 = min(part * per, row.vecs), j1 = min(j0 + per, row.vecs);
   const float c = a.scale * 1.4426950408889634f;
-  // Nothing below this has a weight, and (x - m) c stays finite from it on, which 0 times minus infinity would not be.  (With m
-  // itself as far from 0 on either side logits are taken one by one.)
+  // Beside a maximum m of half its size or less, nothing below this has a weight (it is 5e37 min(c, 1) powers of two below m, and c is at
+  // least 2^-100), so what is below counts as this: (x - m) c then stays finite, which 0 times minus infinity would not be.  (With m
+  // farther from 0, on either side, logits are taken one by one.)
   const float low = __uint_as_float(__float_as_uint(-1e38f / fmaxf(c, 1.f)) & 0xffff0000u);
   const uint32_t low2 = __float_as_uint(low) >> 16 | __float_as_uint(low);
   if (parts > 1) cluster.barrier_arrive();  // (awaited before another block's shared memory is written)
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(STHREADS, sblocks(sizeof(T) == 4)) scores_kern
     l += p, s = fmaf(p, fmaxf(d, -200.f), s);
   };
   auto add = [&](const Vec& u, float ref) {  // a vector's logits
-    if (__builtin_expect(fabsf(ref) > -low, 0)) {
+    if (__builtin_expect(fabsf(ref) > -0.5f * low, 0)) {
       float v[E];
       values(u, v);
 #pragma unroll 1

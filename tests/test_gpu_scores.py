@@ -205,3 +205,31 @@ def test_token_scores_past_32_bit_offsets():
 
 def test_token_scores_none():
     assert run(torch.empty(0, 50, device="cuda"), np.zeros((0, 2), int), 3)[4] == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -60, 0.5, 1.0, 5.0, 2.0 ** 100])
+def test_token_scores_largest_logit_near_a_mask(scale, dtype):
+    """Rows whose largest logits, far inside the row, are -1e38 over max(1, scale log2 e), with the lower half of its bits cleared, a step
+    or a few either side of it, or half of it, beside minus infinity and -3e38: those below count as little as they should."""
+    V = 9001
+    c = np.float32(scale) * np.float32(1.4426950408889634)
+    low = (np.float32(-1e38) / np.maximum(c, np.float32(1))).reshape(1).view(np.uint32) & np.uint32(0xFFFF0000)
+    unit = 1 if dtype == torch.float32 else 1 << 16
+    steps = [-2 * unit, -unit, 0, unit, 2 * unit, 1 << 16, -(1 << 23), -(1 << 23) - unit, unit - (1 << 23)]  # (2^23: a factor of two)
+    x = np.full((2 * len(steps), V), -np.inf, np.float32)
+    for i, step in enumerate(steps):
+        top = (low.astype(np.int64) + step).astype(np.uint32).view(np.float32)[0]
+        x[2 * i:2 * i + 2, 4000:4011] = top
+        x[2 * i + 1, ::2] = np.minimum(x[2 * i + 1, ::2], np.float32(-3e38))
+        x[2 * i + 1, 1::2] = np.maximum(x[2 * i + 1, 1::2], np.where(top < -3e38, -np.inf, np.float32(-3e38)))
+    x = torch.from_numpy(x).to(dtype).cuda()
+    tok = np.tile([4000, 1, 4010], (2 * len(steps), 1))
+    lp, h, top, tlp, status = run(x, tok, 12, scale)
+    want = oracle.token_scores(x.double().cpu().numpy(), tok, 12, scale)
+    far = lambda v: np.where(v < -float(np.finfo(np.float32).max), -np.inf, v)  # noqa: E731
+    E = (V / 512 + 64) * 2.0 ** -24 + (np.log(V) + 32) * 2.0 ** -22 + 2.0 ** -20
+    assert status == 0
+    np.testing.assert_array_equal(top, want[2])
+    for got, ref, e in ((lp, far(want[0]), E), (tlp, far(want[3]), E), (h, want[1], E * (1 + np.log(V)))):
+        np.testing.assert_allclose(got, ref, rtol=2.0 ** -22, atol=e)
