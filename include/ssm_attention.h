@@ -89,10 +89,14 @@ int ssm_kv_commit(int32_t n_layers, int32_t n_seq, int32_t n_nodes, int32_t Hkv,
  *                       sequence has such rows, and set SSM_STATUS_SCALE
  *   block               a power of two, 8 .. page_size
  * q that is not finite, and values of k that are not, make scores that are NaN.  scale from 2^-40 to 2^40.  The other arguments,
- * workspace and rounding as for ssm_tree_attention: q loses what is below 2^-18 of its row's largest magnitude, weights are held
- * in fp16 to 2^-11 of themselves and 2^-31 of a row's largest.
- * A row of q * scale whose largest magnitude is below 2^-52, and a block of k below 2^-58, may count as that large.  Scales of v
- * are to lie within 2^100 of each other, and values of v below 2^100: the sums before the division are fp32.
+ * workspace and rounding as for ssm_tree_attention: q loses what is below 2^-18 of its row's largest magnitude (with up to 16 query
+ * rows of a key/value head, n_nodes * Hq / Hkv, 2^-38: a node's last bits may differ with the number of nodes).  The weights of the
+ * nodes' own rows are rounded to bf16.  A cached row's weight is held in fp16 together with its scale of v, to 2^-11 of their product
+ * and 2^-31 of the query row's largest such product; the nodes' own rows count there as if their scale were the least among up to 256
+ * of the first cached rows, taken as 2^-60 .. 2^60.
+ * A row of q * scale whose largest magnitude is below 2^-52, and a block of k below 2^-58, may count as that large.  The sums before
+ * the division are fp32: scales of v are to lie within 2^100 of each other (those below 2^-60 count as that here), values of v below
+ * 2^100, and the nodes' own below 2^110 times the least scale above.
  */
 int ssm_tree_attention_fp8(int32_t n_seq, int32_t n_nodes, int32_t Hq, int32_t Hkv, int32_t D, const ssm_node *layout,
                            const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,

@@ -19,10 +19,12 @@ namespace {
 //    softmax's own warps converting it: 8 trees 50 us and not 40, wide trees 149 and not 113.)
 //  * A block's scale of K multiplies its scores in the softmax's own multiply-add.  Its scale of V is part of the weight: m is the
 //    maximum of S + log2 vs, so the weight w = 2^(S + log2 vs - m) fits fp16 whatever the scales, and the row's sum adds w / vs.  Scales
-//    of V count relative to one of them, so that neither sum leaves fp32.
+//    of V count relative to one of them, v0, so that neither sum leaves fp32.
 // Weights are 2^7 times as large (at most 2^15 with a maximum that lags by 2^8), so that fp16 holds them to 2^-31 of the largest.
 // The tree's own rows are bf16 and the first tile of a sequence's first run: their products are bf16's, with Q as it came in the columns
-// that O will take, and their K and V in the places of the first two fp16 tiles of V.
+// that O will take, and their K and V in the places of the first two fp16 tiles of V.  O is in units of v0, which is there the least of
+// the first scales of V: the tree's weights 2^(S - m) go into the sum as they are and into the product divided by v0, in bf16, whose
+// range is fp32's.  (With 1 for v0, weights of cached rows lost all bits where values were 2^-16 or less.)
 //
 // In a CUDA graph, 32 query and 8 (wide trees: 4) key/value heads of 128: 8 trees of 16 nodes over up to 8117 rows 40 us (84 MB of
 // cache at 2.1 TB/s), 4 of 40 over up to 40009 rows 113 us (750 TFLOP/s with Q's terms counted once); with heads of 64 36 and 96.
@@ -62,7 +64,7 @@ struct TileInfo {  // of each 8 keys: scale of k, log2 of the scale of v and its
 struct Attend8Misc {
   TileInfo info[INFOS];        // of tile i, at i % INFOS
   unsigned long long anc[64];  // ancestors and self of each node
-  unsigned long long k_full[6], k_free[6], v_full[6], v_free[6], v16_full[2], v16_free[2], info_full[INFOS], q_full, s_full[2], p_full[2], o_done[2], all_done, tree_full, drain[2];
+  unsigned long long k_full[6], k_free[6], v_full[6], v_free[6], v16_full[2], v16_free[2], info_full[INFOS], q_full, s_full[2], p_full[2], o_done[2], all_done, tree_full, v0_full, drain[2];
   SplitScratch split;
   unsigned int odd[2];         // tree rows with a value of v that is not finite
   float qs[128];               // a row's scale of Q
@@ -132,6 +134,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
     mbar_init(smem_u32(&ms->q_full), 8);
     mbar_init(smem_u32(&ms->all_done), 1);
     mbar_init(smem_u32(&ms->tree_full), 1);
+    mbar_init(smem_u32(&ms->v0_full), 1);
     ms->stop = 0;
     ms->odd[0] = ms->odd[1] = 0;
     fence_barrier_init();
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
 #pragma unroll
       for (int c = 0; c < KT; c += 16) tmem_wait_ld16(reinterpret_cast<float(&)[16]>(sv[c]));
       if (__builtin_expect(tree, 0)) {  // rows of V that are not to be multiplied, and values that are not finite, become zeros
-        ok = wait_bar(&ms->tree_full, 0, stop);
+        ok = wait_bar(&ms->tree_full, 0, stop) && wait_bar(&ms->v0_full, 0, stop);
         unsigned char* vt = smem + Sh::OFF_V16;
         // (a warp that gives up here still meets the others below)
 #pragma unroll 1
@@ -374,26 +377,22 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         }
       }
       l = pair_sum(l2[0]) + pair_sum(l2[1]);
-#pragma unroll
-      for (int c = 0; c < KT / 2; c += 8) tmem_st8(st + c, reinterpret_cast<const uint32_t(&)[8]>(u[c]));
-      if (__builtin_expect(tree, 0)) {
-        tmem_wait_st();
+      if (__builtin_expect(tree, 0)) {  // over S, in columns that have been read
+        const float up = 1.f / ms->v0;
 #pragma unroll 1
-        for (int c = 0; c < KT / 2; c += 16) {
+        for (int c = 0; c < KT; c += 16) {
           float x[16];
           uint32_t y[8];
           tmem_ld16_async(st + c, x);
           tmem_wait_ld16(x);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 w = f16x2_f32(__float_as_uint(x[8 * h + j]));
-              y[j] = pack_bf16x2(w.x, w.y);
-            }
-            tmem_st8(st + c + 8 * h, y);
-          }
+          for (int j = 0; j < 8; ++j)
+            y[j] = pack_bf16x2(exp2_sfu(fmaf(x[2 * j], by, -ref)) * up, exp2_sfu(fmaf(x[2 * j + 1], by, -ref)) * up);
+          tmem_st8(st + c / 2, y);
         }
+      } else {
+#pragma unroll
+        for (int c = 0; c < KT / 2; c += 8) tmem_st8(st + c, reinterpret_cast<const uint32_t(&)[8]>(u[c]));
       }
       tmem_wait_st();
       tc_fence_before();
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       const unsigned long long odd = has_tree ? (ms->odd[0] | (unsigned long long)ms->odd[1] << 32) & ms->anc[node] : 0ull;
       const long long tok = (long long)s * a.n + node;
       const int head = kvh * a.g + qh;
-      const float inv = 1.f / l, v0 = ms->v0;
+      const float v0 = ms->v0, inv = v0 / l;
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         float o[16];
@@ -427,7 +426,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
           }
         }
         if (row >= rows) {
-        } else if (splits == 1) {  // (the run has the tree: v0 is 1)
+        } else if (splits == 1) {
           uint32_t u[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) u[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
@@ -551,13 +550,25 @@ __global__ void __launch_bounds__(A8THREADS, 2)
       int pg = page_of(0);
       int pg1 = page_of(1);
       float2 sc = scales_of(0, pg);
-      float v0 = 1.f;
       if (has_tree) {
         TileInfo* in = &ms->info[0];
         if (lane < 8) in->ks[lane] = 1.f, in->lv[lane] = 0.f, in->rv[lane] = 1.f;
-        if (lane == 0) in->mask = a.n < 64 ? (1ull << a.n) - 1 : ~0ull, ms->v0 = 1.f;
+        if (lane == 0) in->mask = a.n < 64 ? (1ull << a.n) - 1 : ~0ull;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ms->info_full[0]));
+      }
+      // What scales of v are relative to, a power of two: the largest of the first tile; beside the tree the least of the first four, within
+      // 2^60 of 1 (at least, so that what the tree's rows of v add stays in fp32 beside a cache of zeros, whose scale is 2^-100)
+      float v0;
+      {
+        const bool there = pg >= 0 && good_scale(sc.x) && good_scale(sc.y);
+        const unsigned int e = __float_as_uint(sc.y) & 0x7f800000u, of = __ballot_sync(0xffffffffu, there) & (has_tree ? ~0u : 0xffu);
+        const bool counts = of >> lane & 1;
+        const unsigned int least = __reduce_min_sync(0xffffffffu, counts ? e : 0x7f800000u), top = __reduce_max_sync(0xffffffffu, counts ? e : 0u);
+        v0 = of == 0 ? 1.f : has_tree ? fminf(fmaxf(__uint_as_float(least), 0x1p-60f), 0x1p60f) : __uint_as_float(top);
+        if (lane == 0) ms->v0 = v0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->v0_full));  // (others see it with the first tile's info)
       }
       bool ok = true;
 #pragma unroll 1
@@ -568,11 +579,6 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         if (__any_sync(0xffffffffu, pg >= 0 && !good) && lane == 0) flag(a.status, SSM_STATUS_SCALE);
         const bool there = pg >= 0 && good;
         if (!there) sc = make_float2(1.f, 1.f);
-        if (c == 0 && !has_tree) {  // what scales of v are relative to: the largest of the first tile, as a power of two
-          const unsigned int top = __reduce_max_sync(0xffffffffu, lane < 8 && there ? __float_as_uint(sc.y) & 0x7f800000u : 0u);
-          v0 = top ? __uint_as_float(top) : 1.f;
-          if (lane == 0) ms->v0 = v0;
-        }
         const int left = min(max(len - (t0 + 4 * c + (lane >> 3)) * KT - 8 * grp, 0), 8);
         const unsigned long long keys = there ? (unsigned long long)((1u << left) - 1) << 8 * grp : 0ull;
         const float rel = fminf(fmaxf(sc.y / v0, 0x1p-120f), 0x1p120f), lv = log2f(rel), rv = 1.f / rel;

@@ -310,9 +310,16 @@ __global__ void __launch_bounds__(Few<D, NT, CUT, BLOCKS>::THREADS, BLOCKS)
         x[t][e] = ms.anc[node] >> (g + (e >> 1) * 8) & 1 ? x[t][e] * a.scale_log2 : -INFINITY;
       }
     st.weigh(x, 1.f, 1.f);
+    {  // what this warp's scales of v are relative to: the least of its first ones, as a power of two within 2^60 of 1
+      const bool counts = at_row >= 0 && good_scale(sc.x) && good_scale(sc.y);
+      const unsigned int least = __reduce_min_sync(0xffffffffu, counts ? __float_as_uint(sc.y) & 0x7f800000u : 0x7f800000u);
+      v0 = least == 0x7f800000u ? 1.f : fminf(fmaxf(__uint_as_float(least), 0x1p-60f), 0x1p60f);
+    }
+    const float up = 1.f / v0;
     uint32_t p[NT][2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) p[t][0] = transposed(pack_bf16x2(x[t][0], x[t][1])), p[t][1] = transposed(pack_bf16x2(x[t][2], x[t][3]));
+    for (int t = 0; t < NT; ++t)
+      p[t][0] = transposed(pack_bf16x2(x[t][0] * up, x[t][1] * up)), p[t][1] = transposed(pack_bf16x2(x[t][2] * up, x[t][3] * up));
 #pragma unroll
     for (int h = 0; h < KI; ++h) {  // eight of a lane's columns
       uint32_t w[4][4];

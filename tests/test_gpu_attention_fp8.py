@@ -566,3 +566,48 @@ def test_tree_attention_fp8_without_a_cache(n, g, D):
     assert rc == B.SSM_OK and int(status) == 0
     for s in range(3):
         check(c, host(o).reshape(3, n, Hq, D), s, length=0)
+
+
+def _own_key_over_a_flat_cache(n, g, D, length, nats):
+    """A cache of nearly equal scores, `nats` below those of a node's own row and its ancestors'."""
+    c = case(28, 1, n, g, 1, D, [length], 64, 32)
+    u = np.random.default_rng([28, n, D]).choice([-1.0, 1.0], D)
+    c["q"], c["q64"] = bf(np.broadcast_to(np.tile(u, g), (n, g * D)))
+    c["k"], c["k64"] = bf(np.broadcast_to(u * nats / np.sqrt(D), (n, D)))
+    c["q64"], c["k64"] = c["q64"].reshape(1, n, g, D), c["k64"].reshape(1, n, 1, D)
+    c["ks"], c["kp64"] = c["ks"] * 2.0 ** -4, c["kp64"] * 2.0 ** -4
+    return c
+
+
+@pytest.mark.parametrize("length,nats", [(320, 6.0), (16384, 10.0)])  # not cut into runs; cut
+@pytest.mark.parametrize("n,g,D", [(1, 4, 128), (1, 8, 64), (12, 1, 128), (16, 4, 128), (40, 2, 64)])
+def test_tree_attention_fp8_values_of_any_size(n, g, D, length, nats):
+    """Values of the cache and of the nodes' rows, all multiplied by a power of two: o is, and nothing else of it changes.  (The
+    cache's weights are half of a root's, however small its values are beside 1.)"""
+    c = _own_key_over_a_flat_cache(n, g, D, length, nats)
+    o0, status = run(c)
+    assert status == 0
+    check(c, o0, 0)
+    for by in (2.0 ** -10, 2.0 ** -16, 2.0 ** -30, 2.0 ** 20):
+        d = dict(c, v=c["v"] * by, v64=c["v64"] * by, vs=c["vs"] * by, vp64=c["vp64"] * by)
+        o, status = run(d)
+        assert status == 0
+        check(d, o, 0)
+        np.testing.assert_array_equal(o, o0 * by)
+
+
+@pytest.mark.parametrize("first,own", [(2.0 ** -100, 1.0), (2.0 ** -100, 2.0 ** 12), (2.0 ** -20, 2.0 ** 40), (2.0 ** 30, 1.0), (2.0 ** 90, 2.0 ** 30),
+                                       (2.0 ** -100, 2.0 ** 48), (1.0, 2.0 ** 96)])
+@pytest.mark.parametrize("n,g,length", [(1, 4, 700), (16, 4, 700), (3, 4, 300), (40, 2, 300)])
+def test_tree_attention_fp8_first_blocks_of_another_size(n, g, length, first, own):
+    """The cache's first 64 rows, zeros under the least scale among them, and the nodes' own rows far larger or smaller than the rest."""
+    c = _own_key_over_a_flat_cache(n, g, 128, length, 6.0)
+    pg = c["table"][0, 0]
+    if first == 2.0 ** -100:
+        c["vp"].view(torch.uint8)[pg] = 0
+    held = c["vp"][pg].double().cpu().numpy()
+    c["vs"][pg], c["vp64"][pg] = first, held * first
+    c["v"], c["v64"] = c["v"] * own, c["v64"] * own
+    o, status = run(c)
+    assert status == 0
+    check(c, o, 0)
