@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         ok = wait_bar(&ms->o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, stop);
         if (!ok) break;
         tc_fence_after();
-        const float to = fmaxf(m, mx), g = to == m ? 1.f : exp2_sfu(m - to);
+        const float to = mx > m + 8.f ? mx : m, g = to == m ? 1.f : exp2_sfu(m - to);  // (a row's weights do not depend on the other rows)
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           float o[16];

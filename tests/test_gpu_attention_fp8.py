@@ -611,3 +611,23 @@ def test_tree_attention_fp8_first_blocks_of_another_size(n, g, length, first, ow
     o, status = run(c)
     assert status == 0
     check(c, o, 0)
+
+
+@pytest.mark.parametrize("n,g,D", [(8, 4, 128), (40, 2, 64), (6, 2, 128)])
+def test_tree_attention_fp8_rows_do_not_depend_on_each_other(n, g, D):
+    """Children of one root, whose scores over the cache are 4 (in powers of two) above those of their own rows, and one whose are 12
+    above: whether its k, far larger, hides the cache from it changes no bit of the others."""
+    c = case(29, 1, n, g, 1, D, [300], 64, 16)
+    u = np.random.default_rng([29, D]).choice([-1.0, 1.0], D)
+    q = np.tile(u, (n, g))
+    q[-1] *= 3.0
+    c["q"], _ = bf(q)
+    c["k"].zero_()
+    c["par"][0] = [-1] + [0] * (n - 1)
+    held = (c["kp64"] * 0.3 + u * 2.8 / np.sqrt(D)) * 64.0
+    c["kp"], c["ks"] = torch.from_numpy(held).to(F8).cuda(), torch.full_like(c["ks"], 2.0 ** -6)
+    o0, _ = run(c)
+    c["k"][-1] = torch.from_numpy(u * 8.0)
+    o, status = run(c)
+    assert status == 0 and not np.array_equal(o[0][-1], o0[0][-1])
+    np.testing.assert_array_equal(o[0][:-1], o0[0][:-1])
