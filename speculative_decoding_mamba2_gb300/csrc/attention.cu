@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(ATHREADS, 2)
         tc_fence_after();
       }
       if (i > 0 && __any_sync(0xffffffffu, mx > m + 8.f)) {
-        const float to = fmaxf(m, mx), f = to == m ? 1.f : exp2_sfu(m - to);
+        const float to = mx > m + 8.f ? mx : m, f = to == m ? 1.f : exp2_sfu(m - to);  // (a row's weights do not depend on the other rows)
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           float o[16];

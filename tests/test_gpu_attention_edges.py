@@ -42,3 +42,20 @@ def test_kv_commit_lengths_up_to_an_int32(room):
             pages[0, 2, :, (length + i) % page] = rows[0, i].reshape(Hkv, D)
     np.testing.assert_array_equal(host(kp), kp64)
     np.testing.assert_array_equal(host(vp), vp64)
+
+
+@pytest.mark.parametrize("n,g,D", [(8, 4, 128), (40, 2, 64), (6, 2, 128)])
+def test_tree_attention_rows_do_not_depend_on_each_other(n, g, D):
+    """Children of one root, whose own rows score 4 (in powers of two) above the cache: whether one of them has a far larger k, and
+    its rows' maximum grows, changes no bit of the others."""
+    c = case(62, 1, n, g, 1, D, [100], 64)
+    u = np.random.default_rng([62, D]).choice([-1.0, 1.0], D)
+    c["q"], _ = bf(np.tile(u, (n, g)))
+    c["k"], _ = bf(np.tile(u * 2.8 / np.sqrt(D), (n, 1)))
+    c["par"][0] = [-1] + [0] * (n - 1)
+    c["kp"], _ = bf(c["kp64"] * 0.3)
+    o0, _ = run(c)
+    c["k"][-1] = torch.from_numpy(u * 8.0)
+    o, status = run(c)
+    assert status == 0 and not np.array_equal(o[0][-1], o0[0][-1])
+    np.testing.assert_array_equal(o[0][:-1], o0[0][:-1])
