@@ -631,3 +631,32 @@ def test_tree_attention_fp8_rows_do_not_depend_on_each_other(n, g, D):
     o, status = run(c)
     assert status == 0 and not np.array_equal(o[0][-1], o0[0][-1])
     np.testing.assert_array_equal(o[0][:-1], o0[0][:-1])
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), -float("inf")])
+@pytest.mark.parametrize("n,g", [(7, 1), (16, 4), (40, 8)])
+def test_tree_attention_fp8_a_bad_row_reaches_all_its_descendants(n, g, value):
+    """A row of k and v that is not finite: no value of any node that descends from it is."""
+    c = case(7, 2, n, g, 1, 128, [75, 130], 64, 16)
+    c["k"][2].fill_(value)
+    c["v"][2].fill_(value)
+    o, _ = run(c)
+    below = [v for v in range(n) if 2 in _chain(c["par"][0], v)]
+    assert below and not np.isfinite(o[0][below]).any()
+
+
+@pytest.mark.parametrize("n,g,D,lens", [(1, 4, 128, [3000, 65]), (12, 1, 64, [900, 7]), (16, 4, 128, [3000, 129]), (40, 8, 64, [700, 64])])
+def test_tree_attention_fp8_weights_of_cached_rows(n, g, D, lens):
+    """Weights of cached rows are held to 11 bits, not 8.  Tolerance: the output's rounding U|ref|, the fp32 part 2^-11 of all (as above),
+    U of what the nodes' own rows add, 2^-11 of what the cache adds, and, for weights below fp16's normal numbers, 2^-32 of the largest
+    product of a weight and its scale for each cached row, times its value of at most 448 of that scale."""
+    c = case(30, 2, n, g, 2, D, lens, 64, 16)
+    o, status = run(c)
+    assert status == 0
+    for s in range(2):
+        kc, vc = cache(c, s, lens[s])
+        args = c["q64"][s], c["k64"][s]
+        ref, mag = oracle.tree_attention(*args, c["v64"][s], c["par"][s], kc, vc, c["scale"])
+        own = oracle.tree_attention(*args, c["v64"][s], c["par"][s], kc, np.zeros_like(vc), c["scale"])[1]
+        tail = lens[s] * 2.0 ** -32 * 448.0 * float(c["vs"].max())
+        assert (np.abs(o[s] - ref) <= U * np.abs(ref) + 2.0 ** -11 * mag + U * own + 2.0 ** -11 * (mag - own) + tail).all()
