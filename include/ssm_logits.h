@@ -30,7 +30,7 @@ extern "C" {
  *   logits           device fp32 (f32 = 1) or bf16 (f32 = 0) [n_rows][ld], ld >= n_vocab, rows of any alignment
  *   scale            1 / temperature, from 2^-100 to 2^100
  *   m, tokens        tokens device int32 [n_rows][m]; -1: none, its logprob is 0; others outside [0, n_vocab): NaN and
- *                    SSM_STATUS_TOKEN_RANGE.  logprob device fp32 [n_rows][m].  m = 0: neither is read or written
+ *                    SSM_STATUS_TOKEN_RANGE.  logprob device fp32 [n_rows][m].  m = 0: neither is read or written; m <= 2^31 - 256
  *   entropy          device fp32 [n_rows], or NULL
  *   k, top, top_logprob  0 <= k <= SSM_MAX_TOP, k <= n_vocab; device int32 and fp32 [n_rows][k]; top_logprob may be NULL
  * Logits of minus infinity have probability 0.  A row with a NaN or plus infinity, or with nothing above minus infinity, has NaN for

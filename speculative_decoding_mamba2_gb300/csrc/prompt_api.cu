@@ -437,6 +437,7 @@ extern "C" int ssm_token_scores(int32_t n_rows, int32_t n_vocab, const void* log
   if (n_vocab < 1 || ld < n_vocab) return pfail(SSM_ERR_INVALID_ARG, fn, "n_vocab must be >= 1, ld at least that");
   if (!(scale >= 0x1p-100f && scale <= 0x1p100f)) return pfail(SSM_ERR_RANGE, fn, "scale must be in [2^-100, 2^100]");
   if (m < 0 || k < 0) return pfail(SSM_ERR_INVALID_ARG, fn, "m and k must be >= 0");
+  if (m > INT32_MAX - 255) return pfail(SSM_ERR_CAPACITY, fn, "m above 2^31 - 256");  // 256 threads step over them in an int
   if (k > SSM_MAX_TOP) return pfail(SSM_ERR_CAPACITY, fn, "k above SSM_MAX_TOP");
   if (k > n_vocab) return pfail(SSM_ERR_INVALID_ARG, fn, "k above n_vocab");
   if (n_rows > 0 && (!logits || (m > 0 && (!tokens || !logprob)) || (k > 0 && !top)))

@@ -147,3 +147,9 @@ def test_binding_checks_tensors(L):
         B.ssm_rope(64, i, torch.zeros(32, dtype=torch.int64), None, None)
     with pytest.raises(ValueError):
         B.ssm_token_scores(torch.zeros(2, 9), None, None, None, None)
+
+
+def test_token_scores_refuses_more_tokens_than_it_counts(L):
+    """256 threads step over a row's tokens in an int32: the last step ends below 2^31 for up to 2^31 - 256 of them."""
+    assert L.ssm_token_scores(*dict(SCORES, m=(1 << 31) - 255).values()) == CAP
+    assert L.ssm_token_scores(*dict(SCORES, T=0, m=(1 << 31) - 256).values()) == B.SSM_OK
