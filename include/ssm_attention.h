@@ -143,7 +143,8 @@ int ssm_kv_commit_fp8(int32_t n_layers, int32_t n_seq, int32_t n_nodes, int32_t 
  *                      kept, those between divided in part (linearly in the turns); 0 <= low < high
  *
  * ssm_rope_turns -- host-only.  The kernels' table of any frequencies: f / (2 pi) in units of 2^-64 of a turn, modulo one.  A
- * position times it, modulo 2^64, is the angle at any position up to 2^31 without a rounding that grows with it.
+ * position times an entry, modulo 2^64, is exact; what grows with the position is the entry's own rounding alone, 2^-55 of a turn
+ * for f up to 1.
  */
 #define SSM_ROPE_PLAIN 0
 #define SSM_ROPE_LINEAR 1
@@ -161,7 +162,8 @@ int ssm_rope_turns(int32_t n, const double *freq, uint64_t *turns);
  *   positions    device int32 [n_tok]; a negative one turns backwards
  *   q, k         device bf16 [n_tok][ldq], [n_tok][ldk]: Hq*D and Hkv*D columns
  *   q_out, k_out device bf16, strides ldqo, ldko; each may be its input (it may not overlap it in part)
- * Pointers 16-byte aligned, row strides multiples of 8.  Angles to 2^-24 of a turn; products in fp32, rounded once.
+ * Pointers 16-byte aligned, row strides multiples of 8.  Angles to 2^-25 of a turn up to position 2^29, to 2^-23 at any (f up to 1);
+ * products in fp32, rounded once.
  *
  * ssm_tree_rope -- the same for row s*n + v at position cache_len[s] + depth of node v.  A depth outside [0, n_nodes) counts as
  * 0 and sets SSM_STATUS_BAD_LAYOUT, a negative length counts as 0 and sets SSM_STATUS_SEQ_RANGE.

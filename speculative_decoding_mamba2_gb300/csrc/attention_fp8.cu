@@ -36,7 +36,6 @@ constexpr int A8THREADS = 384;  // 4 softmax warps; copies, MMAs of S, MMAs of P
 constexpr int R_SOFTMAX = 136, R_MMA = 48, R_CONVERT = 56;
 static_assert(R_SOFTMAX + R_MMA + R_CONVERT == 3 * 80, "what the block is launched with");
 constexpr int BLK = KT * 128;   // 64 rows x 64 columns of 16 bits
-constexpr float kShift = 7.f;
 // tensor memory columns: S of even and of odd tiles, each then overwritten by its P; O
 constexpr int A_S = 0, A_O = 128, A_COLS = 256;
 
@@ -78,11 +77,6 @@ static_assert(Attend8Smem<64>::VU + 2 <= INFOS && Attend8Smem<128>::VU + 2 <= IN
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {  // fp16 x fp16 -> fp32
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ float least_scale(uint32_t most) {  // of a largest magnitude's bits: 448 is 1.75 * 2^8
   const int e = (int)(most >> 23) - 127 - 8 + ((most & 0x7fffffu) > 0x600000u);
   return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
@@ -90,9 +84,6 @@ __device__ __forceinline__ float least_scale(uint32_t most) {  // of a largest m
 __device__ __forceinline__ uint32_t finite_bits(float x) {  // |x|, 0 where it is not finite
   const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
   return b < 0x7f800000u ? b : 0u;
-}
-__device__ __forceinline__ float nan_unless_finite(float x) {
-  return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x;
 }
 
 template <int D>

@@ -1,15 +1,15 @@
 // Tree attention over an 8-bit paged cache for up to 16 query rows of a key/value head (ssm_attention.h): single tokens, small trees.
 //
 // The plan of attention_fp8.cu has 128 rows and tiles of 64 keys that pass from warp to warp; a few rows want the cache read as
-// fast as memory gives it instead.  Here each warp takes 16 keys at a time by itself, with no barrier before the end (a few rows use
-// little of any tensor core, so its products are warp-level ones):
+// fast as memory gives it instead.  Here each warp takes 16 keys at a time by itself, with no barrier between its first row and the join (a few
+// rows use little of any tensor core, so its products are warp-level ones):
 //     S^T = K . Q^T,   P^T = 2^(S^T + log2 vs - m),   O^T += V^T . P^T
 // with K and V made fp16 (exact) in registers, Q fp16 under a row scale that is a power of two (exact down to 2^-38 of a row's
 // largest).  The columns of K's rows may stand in any order along a product's inner axis, and those of V's rows in any order along
 // its outer one: a lane reads 16 bytes of a row of either and has fragments; two keys' bytes of V are put side by side by byte
 // permutes before they are converted.  P^T goes from accumulators to operands by transposing 8 x 8 of fp16.  A lane of each warp asks
-// for its rows, three steps ahead, by tensor copies into a ring of the warp's own.  Scales, weights and sums are those of
-// attention_fp8.cu; the warps' sums are joined in shared memory, runs of a cache as there.
+// for its rows, three to eight steps ahead (STAGES), by tensor copies into a ring of the warp's own.  Scales, weights and sums are those
+// of attention_fp8.cu; the warps' sums are joined in shared memory, runs of a cache as there.
 //
 // Bound by HBM where caches are long: 76 tokens over up to 16000 rows 252 us (1.32 GB: 5.2 TB/s).  Else by what a block does before
 // its first and after its last row (lengths, pages, rows one after the other, the join): in a CUDA graph, 32 query and 8 key/value
@@ -22,8 +22,6 @@
 
 namespace ssmtree {
 namespace {
-
-constexpr float kShift = 7.f;  // weights are 2^7 times as large, so that fp16 holds them to 2^-31 of the largest
 
 template <int D, int NT, bool CUT, int BLOCKS>  // NT: eights of rows; BLOCKS: blocks on an SM, which share 16 or 12 warps
 struct Few {
@@ -60,14 +58,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
   return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float nan_unless_finite(float x) {
-  return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x;
 }
 template <int WORDS>
 __device__ __forceinline__ void load_words(uint32_t (&x)[WORDS], const unsigned char* p) {

@@ -58,10 +58,17 @@ struct ScoreArgs {
 };
 cudaError_t launch_token_scores(const ScoreArgs& a, cudaStream_t s);
 
+constexpr float kShift = 7.f;  // weights are 2^7 times as large, so that fp16 holds them to 2^-31 of the largest
+
 // two e4m3 values (the lower half of v) as two of fp16 (exact)
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   uint32_t r;
   asm("{\n .reg .b16 h, g;\n mov.b32 {h, g}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 __device__ __forceinline__ float2 f16x2_f32(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
@@ -86,6 +93,9 @@ __device__ __forceinline__ uint32_t f16x2_sub(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
+}
+__device__ __forceinline__ float nan_unless_finite(float x) {
+  return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x;
 }
 __device__ __forceinline__ bool good_scale(float s) { return s >= 0x1p-100f && s <= 0x1p120f; }
 

@@ -1,8 +1,8 @@
 // Rotary positions of q and k rows (ssm_attention.h).
 //
 // A pair (a, b) of a row at position p becomes (a cos - b sin, b cos + a sin) at the angle p f.  The angle is taken in turns, as
-// a 64-bit fraction: p times the table's f / (2 pi) 2^64 modulo 2^64 is exact, so a position of 2^30 costs no precision, and its upper
-// 32 bits are the angle of a sine and cosine in half turns.
+// a 64-bit fraction: p times the table's f / (2 pi) 2^64 modulo 2^64 is exact (the table's own rounding, 2^-55 of a turn, is all that
+// grows with the position), and its upper 32 bits are the angle of a sine and cosine in half turns.
 // One thread has eight columns (and their eight partners, half a rotated part on) of a row, makes their sines once and turns
 // a run of eight heads with them; where there are few rows a run is one head, so that all heads are under way at once.  Bound by
 // HBM where there are many rows: 8191 rows of 40 heads of 128 in 31 us (168 MB: 5.3 TB/s; runs of 4 or 20 heads 33 and 32).
