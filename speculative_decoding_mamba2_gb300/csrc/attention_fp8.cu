@@ -26,8 +26,8 @@ namespace {
 // the first scales of V: the tree's weights 2^(S - m) go into the sum as they are and into the product divided by v0, in bf16, whose
 // range is fp32's.  (With 1 for v0, weights of cached rows lost all bits where values were 2^-16 or less.)
 //
-// In a CUDA graph, 32 query and 8 (wide trees: 4) key/value heads of 128: 8 trees of 16 nodes over up to 8117 rows 40 us (84 MB of
-// cache at 2.1 TB/s), 4 of 40 over up to 40009 rows 113 us (750 TFLOP/s with Q's terms counted once); with heads of 64 36 and 96.
+// In a CUDA graph, 32 query and 8 (wide trees: 4) key/value heads of 128: 8 trees of 16 nodes over up to 8117 rows 41 us (84 MB of
+// cache at 2.0 TB/s), 4 of 40 over up to 40009 rows 113 us (760 TFLOP/s with Q's terms counted once); with heads of 64 37 and 99.
 // (Up to 16 query rows of a key/value head are attention_fp8_few.cu's.)  Wide trees are bound by the round trips of the two tiles under
 // way (P to P . V to S to the softmax) on top of the products: without copies, conversion or Q's lower terms they take as long; with
 // an idle softmax 15 % less, with that and no products a third less.
@@ -699,7 +699,8 @@ static_assert(2 * 2 * kSMs * 4 <= 2 * Attend8Smem<64>::TILE16, "the lengths stan
 // Commit.  A cluster of 8 CTAs for each sequence, a warp for each block of tokens of a layer, head and K or V: the largest of its new
 // rows gives the scale that they need, the block takes that or its own, rows that it holds are rounded again if it grew.  The
 // sequence's length is written by one of the CTAs once all eight have read it, so len_out may be cache_len.  Bound by latency:
-// 4.2 us for one sequence's path of 5 in 4 layers of 8 heads of 128 (in a CUDA graph; its bytes 0.02), 7.7 for 32 sequences' in 8 layers.
+// 4.3 us for one sequence's path of 5 in 4 layers of 8 heads of 128 (in a CUDA graph; its bytes 0.02), 9.2 for 32 sequences' in 8 layers
+// (7.6 where L2 holds the pages).
 constexpr int CCTAS = 8, CTHREADS = 512;
 
 template <int D>
@@ -834,7 +835,7 @@ __global__ void __cluster_dims__(CCTAS, 1, 1) __launch_bounds__(CTHREADS) kv_com
 
 // The plan of the 16-bit kernel; but few rows, whose blocks are half as large, are not cut either where their blocks fill half of the
 // SMs' places and no cache is so long that one block's walk of it takes more than cutting: 64 tokens of 8 heads over up to 1000 rows
-// 20.6 us, cut 32.3, over up to 400 rows 11 and 21.
+// 21 us, cut 32, over up to 400 rows 11 and 21.
 AttendPlan plan_attend_fp8(int S, int n, int Hq, int Hkv, int max_len) {
   AttendPlan p = plan_attend(S, n, Hq, Hkv, max_len);
   if (n * (Hq / Hkv) <= kFewRows && S * Hkv >= 2 * kSMs && max_len <= 2048) p.max_runs = 0;

@@ -1,8 +1,8 @@
 // Tree attention over an 8-bit paged cache for up to 16 query rows of a key/value head (ssm_attention.h): single tokens, small trees.
 //
 // The plan of attention_fp8.cu has 128 rows and tiles of 64 keys that pass from warp to warp; a few rows want the cache read as
-// fast as memory gives it instead.  Here each warp takes 16 keys at a time by itself, with no barrier between its first row and the join (a few
-// rows use little of any tensor core, so its products are warp-level ones):
+// fast as memory gives it instead.  Here each warp takes 16 keys at a time by itself, with no barrier between its first row and
+// the join (a few rows use little of any tensor core, so its products are warp-level ones):
 //     S^T = K . Q^T,   P^T = 2^(S^T + log2 vs - m),   O^T += V^T . P^T
 // with K and V made fp16 (exact) in registers, Q fp16 under a row scale that is a power of two (exact down to 2^-38 of a row's
 // largest).  The columns of K's rows may stand in any order along a product's inner axis, and those of V's rows in any order along
@@ -11,12 +11,12 @@
 // for its rows, three to eight steps ahead (STAGES), by tensor copies into a ring of the warp's own.  Scales, weights and sums are those
 // of attention_fp8.cu; the warps' sums are joined in shared memory, runs of a cache as there.
 //
-// Bound by HBM where caches are long: 76 tokens over up to 16000 rows 252 us (1.32 GB: 5.2 TB/s).  Else by what a block does before
+// Bound by HBM where caches are long: 76 tokens over up to 16000 rows 253 us (1.32 GB: 5.2 TB/s).  Else by what a block does before
 // its first and after its last row (lengths, pages, rows one after the other, the join): in a CUDA graph, 32 query and 8 key/value
-// heads of 128, one token over 16411 rows takes 16.4 us (the 128-row kernel 21.7), 16 over up to 4099 rows 25 (41), 64 over up to
-// 1000 rows 20.6 (65), 128 of them 31.6 (86); 16 query rows, one sequence of 16411 rows 22.6 (25.3), 8 of up to 8117 rows and 4 heads
-// 25.9 (26.2); one token with heads of 64 12.5 (19.4).  Rows straight into registers, one step ahead: one token 16.9, 128 39.6; by
-// asynchronous copies of 16 bytes: 19.1, 52.
+// heads of 128, one token over 16411 rows takes 18.1 us (16.4 where L2 holds the cache; the 128-row kernel 21.7 there), 16 over up to
+// 4099 rows 25 (41), 64 over up to 1000 rows 21 (65), 128 of them 32.5 (86); 16 query rows, one sequence of 16411 rows 24 (in L2 23;
+// 25.3), 8 of up to 8117 rows and 4 heads 26 (26.2); one token with heads of 64 13.9 (in L2 12.4; 19.4).  In L2, rows straight into
+// registers, one step ahead: one token 16.9, 128 39.6; by asynchronous copies of 16 bytes: 19.1, 52.
 #include "attend.cuh"
 #include "decode.cuh"
 
@@ -505,8 +505,8 @@ cudaError_t run_few(const AttendFp8Args& f, int max_runs, cudaStream_t s) {
 }
 
 // Where sequences and heads give each SM two blocks or more, blocks are half as large and four to an SM, so that one's beginning and
-// end pass under the others' rows (128 tokens over up to 1000 rows 31.6 us, with two to an SM 36.5; 64 of them, cut into runs, 32.3 and
-// 37.5; 76 over up to 16000 rows 252 and 240); below that a larger block takes a run in less time (one token 16.4 us).
+// end pass under the others' rows (128 tokens over up to 1000 rows 32 us, with two to an SM 36.5; 64 of them, cut into runs, 32.3 and
+// 37.5; 76 over up to 16000 rows 252 and 240); below that a larger block takes a run in less time (one token 18.1 us).
 template <int D>
 cudaError_t run_few(const AttendFp8Args& f, int max_runs, cudaStream_t s) {
   const bool many = f.a.S * f.a.Hkv >= 2 * kSMs;
