@@ -18,8 +18,8 @@
 // Rows of V that no key of the tile owns, and values of V in tree rows that are not finite, are zeroed in shared memory
 // (a weight of 0 would spread them); the latter are added to the rows that see them at the end.
 // Measured, both kernels, back to back in a graph (32 query heads, D = 128): one token of one sequence over 16411 rows, 8 heads
-// of K and V, 22.6 us (67 MB: 3.0 TB/s; 18 where L2 holds the cache; latency: seven tiles to a CTA); 8 trees of 16 nodes over up to 8117 rows 41 us (163 MB:
-// 4.0 TB/s of HBM); 4 trees of 40 nodes over up to 40009 rows, 4 heads, 86 us (85 GFLOP: 0.99 PFLOP/s, 1.19 with the rows
+// of K and V, 22.6 us (67 MB: 3.0 TB/s; 18 where L2 holds the cache; latency: seven tiles to a CTA); 8 trees of 16 nodes over up
+// to 8117 rows 41 us (163 MB: 4.0 TB/s of HBM); 4 trees of 40 nodes over up to 40009 rows, 4 heads, 86 us (85 GFLOP: 0.99 PFLOP/s, 1.19 with the rows
 // that fill up the third row tile; tensor pipe 52 % of the time, shared memory the rest).  D = 64, the same rows: 16, 28 and 73 us.
 #include "attend.cuh"
 

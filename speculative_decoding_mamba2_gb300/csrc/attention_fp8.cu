@@ -24,7 +24,8 @@ namespace {
 // The tree's own rows are bf16 and the first tile of a sequence's first run: their products are bf16's, with Q as it came in the columns
 // that O will take, and their K and V in the places of the first two fp16 tiles of V.  O is in units of v0, which is there the least of
 // the first scales of V: the tree's weights 2^(S - m) go into the sum as they are and into the product divided by v0, in bf16, whose
-// range is fp32's.  (With 1 for v0, weights of cached rows lost all bits where values were 2^-16 or less.)
+// range is fp32's.  (With 1 for v0, wide trees over a flat cache of 320 rows that has half of the weights were off by 4 % of o at values of
+// 2^-16, by half at 2^-20.)
 //
 // In a CUDA graph, 32 query and 8 (wide trees: 4) key/value heads of 128: 8 trees of 16 nodes over up to 8117 rows 41 us (84 MB of
 // cache at 2.0 TB/s), 4 of 40 over up to 40009 rows 113 us (760 TFLOP/s with Q's terms counted once); with heads of 64 37 and 99.
@@ -548,14 +549,15 @@ __global__ void __launch_bounds__(A8THREADS, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ms->info_full[0]));
       }
-      // What scales of v are relative to, a power of two: the largest of the first tile; beside the tree the least of the first four, within
-      // 2^60 of 1 (at least, so that what the tree's rows of v add stays in fp32 beside a cache of zeros, whose scale is 2^-100)
+      // What scales of v are relative to, a power of two: the largest of the first tile; beside the tree the least of the first four,
+      // within 2^60 of 1 (so that what the tree's rows of v add stays in fp32 beside a cache of zeros, whose scale is 2^-100)
       float v0;
       {
         const bool there = pg >= 0 && good_scale(sc.x) && good_scale(sc.y);
         const unsigned int e = __float_as_uint(sc.y) & 0x7f800000u, of = __ballot_sync(0xffffffffu, there) & (has_tree ? ~0u : 0xffu);
         const bool counts = of >> lane & 1;
-        const unsigned int least = __reduce_min_sync(0xffffffffu, counts ? e : 0x7f800000u), top = __reduce_max_sync(0xffffffffu, counts ? e : 0u);
+        const unsigned int least = __reduce_min_sync(0xffffffffu, counts ? e : 0x7f800000u);
+        const unsigned int top = __reduce_max_sync(0xffffffffu, counts ? e : 0u);
         v0 = of == 0 ? 1.f : has_tree ? fminf(fmaxf(__uint_as_float(least), 0x1p-60f), 0x1p60f) : __uint_as_float(top);
         if (lane == 0) ms->v0 = v0;
         __syncwarp();

@@ -660,3 +660,16 @@ def test_tree_attention_fp8_weights_of_cached_rows(n, g, D, lens):
         own = oracle.tree_attention(*args, c["v64"][s], c["par"][s], kc, np.zeros_like(vc), c["scale"])[1]
         tail = lens[s] * 2.0 ** -32 * 448.0 * float(c["vs"].max())
         assert (np.abs(o[s] - ref) <= U * np.abs(ref) + 2.0 ** -11 * mag + U * own + 2.0 ** -11 * (mag - own) + tail).all()
+
+
+@pytest.mark.parametrize("by", [2.0 ** -6, 2.0 ** -10, 2.0 ** -13, 2.0 ** -30])
+@pytest.mark.parametrize("n,g,D,length,nats", [(1, 4, 128, 16384, 10.0), (1, 8, 64, 320, 6.0), (16, 4, 128, 16384, 10.0), (40, 2, 64, 320, 6.0)])
+def test_tree_attention_fp8_small_values_of_one_sign(n, g, D, length, nats, by):
+    """The same with values of the cache that are all positive, so that what a flat cache adds to a root's o is half of it and nothing of
+    that averages out."""
+    c = _own_key_over_a_flat_cache(n, g, D, length, nats)
+    c["vp"].view(torch.uint8).bitwise_and_(0x7F)
+    d = dict(c, v=c["v"] * by, v64=c["v64"] * by, vs=c["vs"] * by, vp64=np.abs(c["vp64"]) * by)
+    o, status = run(d)
+    assert status == 0
+    check(d, o, 0)
